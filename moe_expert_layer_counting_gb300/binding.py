@@ -1,7 +1,7 @@
 """ctypes binding of libmoe_mxq.so -- argument marshalling only.
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
-include/moe_bfp8.h)
+include/moe_bfp8.h, include/moe_grouped.h)
 and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
@@ -43,12 +43,14 @@ PHASE_TOKEN_SCALES, PHASE_GEMM1, PHASE_GEMM2, PHASE_H_SCALES, PHASE_RESET = 1, 2
 SCHEDULE_DEFAULT, SCHEDULE_SEPARATE, SCHEDULE_EXPERT_WAVES = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID, ROUTE_RAW, ROUTE_NO_RENORM = 0, 1, 2, 4
 BFP8_LAYOUT_CANONICAL, BFP8_LAYOUT_TILED = 0, 1
+BF16, F32 = 0, 1                                         # enum moe_dtype
 
 EXPORTED = ["mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_route_topk_ex",
             "moe_permute_workspace_size",
             "moe_permute", "moe_permute_noalloc", "moe_expert_workspace_size", "moe_expert_forward", "moe_combine",
             "moe_workspace_size", "moe_forward", "moe_get_device_status", "moe_status_string", "moe_version",
-            "bfp8_quantize_act", "bfp8_quantize_weight", "moe_bfp8_workspace_size", "moe_forward_bfp8"]
+            "bfp8_quantize_act", "bfp8_quantize_weight", "moe_bfp8_workspace_size", "moe_forward_bfp8",
+            "moe_grouped_workspace_size", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"]
 
 
 class MoeExpertArgs(ctypes.Structure):
@@ -108,6 +110,11 @@ lib.bfp8_quantize_weight.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p,
 lib.moe_bfp8_workspace_size.argtypes = [_i64, _i64, _i64, _i32, _i32]
 lib.moe_bfp8_workspace_size.restype = _sz
 lib.moe_forward_bfp8.argtypes = [ctypes.POINTER(MoeBfp8Args), _p]
+lib.moe_grouped_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+lib.moe_grouped_workspace_size.restype = _sz
+lib.moe_grouped_forward.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _sz, _p]
+lib.moe_grouped_dgrad.argtypes = lib.moe_grouped_forward.argtypes
+lib.moe_grouped_wgrad.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _p, _i32, _i32, _p, _sz, _p]
 lib.moe_get_device_status.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_int)]
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
@@ -116,7 +123,7 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_permute_noalloc",
               "moe_expert_forward",
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
-              "moe_forward_bfp8"):
+              "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -304,4 +311,75 @@ def moe_forward_bfp8(x, logits, w1q, w1s, w2q, w2s, k: int, y, workspace, topk_i
     rc = lib.moe_forward_bfp8(ctypes.byref(a), _stream(stream))
     if check:
         _check(rc, "moe_forward_bfp8")
+    return rc
+
+
+# ---------------------------------------------------------------- BF16 products grouped by expert (include/moe_grouped.h)
+
+def _invalid(where: str, check: bool) -> int:
+    if check:
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return MOE_ERR_INVALID_ARG
+
+
+def _is_rows(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> bool:
+    """A [rows, cols] tensor whose rows are contiguous (any row stride)."""
+    return t.dtype == dtype and t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _is_offsets(t: torch.Tensor, E: int) -> bool:
+    return t.dtype == torch.int32 and t.shape == (E + 1,) and t.is_contiguous()
+
+
+def moe_grouped_workspace_size(P: int, N: int, K: int, E: int) -> int:
+    return int(lib.moe_grouped_workspace_size(P, N, K, E))
+
+
+def moe_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor,
+                        workspace: torch.Tensor, stream=None, check=True) -> int:
+    """y [P, N] = x [P, K] @ w[e] [N, K]^T for the rows offsets[e] .. offsets[e+1] of expert e (all bf16)."""
+    E, N, K = w.shape
+    P = x.shape[0]
+    if not (_is_rows(x, P, K) and _is_rows(y, P, N) and w.dtype == torch.bfloat16 and w.is_contiguous()
+            and _is_offsets(offsets, E)):
+        return _invalid("moe_grouped_forward", check)
+    rc = lib.moe_grouped_forward(x.data_ptr(), _row_stride(x), w.data_ptr(), offsets.data_ptr(), P, N, K, E,
+                                 y.data_ptr(), _row_stride(y), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if check:
+        _check(rc, "moe_grouped_forward")
+    return rc
+
+
+def moe_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dx: torch.Tensor,
+                      workspace: torch.Tensor, stream=None, check=True) -> int:
+    """dx [P, K] = dy [P, N] @ w[e] [N, K] for the rows offsets[e] .. offsets[e+1] of expert e (all bf16)."""
+    E, N, K = w.shape
+    P = dy.shape[0]
+    if not (_is_rows(dy, P, N) and _is_rows(dx, P, K) and w.dtype == torch.bfloat16 and w.is_contiguous()
+            and _is_offsets(offsets, E)):
+        return _invalid("moe_grouped_dgrad", check)
+    rc = lib.moe_grouped_dgrad(dy.data_ptr(), _row_stride(dy), w.data_ptr(), offsets.data_ptr(), P, N, K, E,
+                               dx.data_ptr(), _row_stride(dx), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if check:
+        _check(rc, "moe_grouped_dgrad")
+    return rc
+
+
+def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, dw: torch.Tensor,
+                      workspace: torch.Tensor, accumulate: bool = False, stream=None, check=True) -> int:
+    """dw [E, N, K] (bf16 or float32) = dy[rows of e]^T @ x[rows of e]; accumulate adds to a float32 dw."""
+    E, N, K = dw.shape
+    P = dy.shape[0]
+    if not (_is_rows(dy, P, N) and _is_rows(x, P, K) and dw.dtype in (torch.bfloat16, torch.float32)
+            and dw.is_contiguous() and _is_offsets(offsets, E)):
+        return _invalid("moe_grouped_wgrad", check)
+    rc = lib.moe_grouped_wgrad(dy.data_ptr(), _row_stride(dy), x.data_ptr(), _row_stride(x), offsets.data_ptr(), P, N, K,
+                               E, dw.data_ptr(), F32 if dw.dtype == torch.float32 else BF16, 1 if accumulate else 0,
+                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if check:
+        _check(rc, "moe_grouped_wgrad")
     return rc

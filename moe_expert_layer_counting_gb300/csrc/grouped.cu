@@ -1,0 +1,703 @@
+// grouped.cu -- BF16 products grouped by expert with ragged sizes, and their
+// gradients, on CTA pairs: one tcgen05.mma.cta_group::2 (M = 256, N up to 256,
+// K = 16, kind::f16, float32 accumulators in TMEM) drives two SMs.
+//
+// With R_e the rows of expert e (offsets[e] <= r < offsets[e+1]):
+//   forward  y[r][n]     = sum_k x[r][k] w[e][n][k]      A = w  (K-major),  B = x  (K-major)
+//   dgrad    dx[r][k]    = sum_n dy[r][n] w[e][n][k]     A = w  (M-major),  B = dy (K-major)
+//   wgrad    dw[e][n][k] = sum_{r in R_e} dy[r][n] x[r][k]  A = dy (M-major), B = x (N-major)
+// One kernel: the weight's rows (forward, wgrad) or columns (dgrad) fill the
+// M = 256 slots, the ragged rows (wgrad: the weight's columns) the N slots,
+// which an item uses in steps of 32, so a short segment costs little.  No
+// operand is transposed in memory: the MMA reads either major from the
+// 128-byte-swizzled boxes that TMA writes.
+//
+// Ragged ends.  forward / dgrad: rows past a segment's end are other experts'
+// (or no one's); they fill N slots of their own and are not stored.  wgrad
+// sums over rows, so the rows of the last 16-row step that lie past the end
+// are zeroed in shared memory, in both operands (0 x NaN of a neighbour would
+// not be 0): the block's copies land on a barrier of their own CTA, a warp
+// zeroes those rows, and the MMA waits for both CTAs' warps.
+//
+// Roles per CTA (384 threads): warp 0 loads (TMA), warp 1 of the leader issues
+// the MMAs, warp 2 allocates TMEM and zeroes ragged ends, warps 4-11 drain the
+// accumulators (two per TMEM lane quadrant, each with a 2 KB staging tile of
+// its own, so that the stores are 64-byte row pieces).  Two accumulators
+// alternate, so an item's drain overlaps the next item's MMAs.  Every wait is
+// bounded (see moe_get_device_status).
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cstdlib>
+#include <mutex>
+
+#include "../../include/moe_grouped.h"
+#include "host_common.h"
+#include "ptx.cuh"
+#include "ptx_f16.cuh"
+
+namespace mxq {
+
+namespace {
+
+enum : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+struct GP {
+  static constexpr int kM = 256;                       // M of a pair's MMA (128 per CTA)
+  static constexpr int kN = 256;                       // most N slots of an item
+  static constexpr int kBK = 64;                       // reduction values per stage (128 bytes of BF16)
+  static constexpr int kStages = 6;
+  static constexpr int kATile = 128 * kBK * 2;
+  static constexpr int kBTile = (kN / 2) * kBK * 2;
+  static constexpr int kHalfBox = 64 * kBK * 2;        // a 64 x 64 box (M- / N-major operands)
+  static constexpr int kFirstEpiWarp = 4;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+  static constexpr int kStageTile = 2048;              // staging per epilogue warp
+  static constexpr int kOffA = 0;
+  static constexpr int kOffB = kOffA + kStages * kATile;
+  static constexpr int kOffEpi = kOffB + kStages * kBTile;
+  static constexpr int kOffBar = kOffEpi + kEpiWarps * kStageTile;
+  // full, empty, tail_full, tail_fixed [kStages] each, tmem_full[2], tmem_empty[2], mma_done, never
+  static constexpr int kNumBars = 4 * kStages + 6;
+  static constexpr int kOffTmemPtr = (kOffBar + 8 * kNumBars + 63) & ~63;
+  static constexpr int kOffTab = kOffTmemPtr + 64;     // off[E+1], tile_off[E+1]
+};
+
+constexpr long long kLimit = 2000000000LL;              // ~1 s
+constexpr long long kInjectedLimit = 20000000LL;        // ~10 ms: the debug wait's budget
+constexpr int kMaxExperts = 1024;
+constexpr size_t kSmemMax = 1024 + GP::kOffTab + 8 * (kMaxExperts + 1);
+static_assert(kSmemMax <= 232448, "shared memory of one CTA");
+
+struct GMaps {
+  CUtensorMap a;        // w (3-D) or dy
+  CUtensorMap b[4];     // row operand with boxes of 16, 32, 64, 128 rows; wgrad: b[0] = x, 64 x 64 boxes
+};
+
+struct GArgs {
+  const int32_t *offsets;
+  int64_t P;
+  int E;
+  int M, R, C;          // M extent, reduction length (forward, dgrad), N extent (wgrad)
+  int64_t ld_out;       // forward / dgrad: row stride of the output
+  void *out;
+  int f32, accumulate;  // wgrad
+  int inject_wait;
+  int *status;
+};
+
+struct GItem {
+  int e, m, c;          // expert, pair of 128-row M tiles, wgrad: 256-column N tile
+  int row0, rows;       // forward / dgrad: first row and rows of the tile; wgrad: of the expert
+  int kb;               // reduction blocks
+  uint32_t n_mma;       // N slots of the MMA (a multiple of 32)
+};
+
+template <int OP>
+__device__ __forceinline__ GItem decode_item(int w, const GArgs &g, const int *off, const int *tile_off) {
+  GItem it;
+  const int mt = (g.M + GP::kM - 1) / GP::kM;
+  if (OP == kWgrad) {
+    const int ct = (g.C + GP::kN - 1) / GP::kN;
+    it.e = w / (mt * ct);
+    const int r = w - it.e * (mt * ct);
+    it.c = r / mt;
+    it.m = r - it.c * mt;
+    it.row0 = off[it.e];
+    it.rows = off[it.e + 1] - it.row0;
+    it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
+    it.n_mma = (uint32_t)min(GP::kN, (g.C - it.c * GP::kN + 31) & ~31);
+  } else {
+    const int t = w / mt;
+    it.m = w - t * mt;
+    it.c = 0;
+    int lo = 0, hi = g.E;                 // tile_off[lo] <= t < tile_off[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile_off[mid] <= t) lo = mid; else hi = mid;
+    }
+    it.e = lo;
+    it.row0 = off[lo] + (t - tile_off[lo]) * GP::kN;
+    it.rows = min(GP::kN, off[lo + 1] - it.row0);
+    it.kb = (g.R + GP::kBK - 1) / GP::kBK;
+    it.n_mma = (uint32_t)((it.rows + 31) & ~31);
+  }
+  return it;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// forward / dgrad: 32 N slots (rows c0 .. c0 + 31 of the item) of this warp's
+// 32 output columns: TMEM lanes are output columns, so lanes l and l ^ 1 swap
+// one value of each slot pair, which gives packed column pairs; staged as
+// [row][32 columns], stored as one 64-byte piece per row.
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int c0, int col0, const GItem &it, const GArgs &g,
+                                           int lane, uint32_t *stage) {
+  const bool odd = (lane & 1) != 0;
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) {
+    const float a = __uint_as_float(v[t]), b = __uint_as_float(v[t + 1]);
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    stage[(t + (odd ? 1 : 0)) * 16 + (lane >> 1)] = odd ? pack_bf16(got, b) : pack_bf16(a, got);
+  }
+  __syncwarp();
+  uint16_t *out = reinterpret_cast<uint16_t *>(g.out);
+  const int col = col0 + 8 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 piece = *reinterpret_cast<const uint4 *>(stage + r * 16 + 4 * (lane & 3));
+    if (c0 + r < it.rows && col < g.M)
+      *reinterpret_cast<uint4 *>(out + (int64_t)(it.row0 + c0 + r) * g.ld_out + col) = piece;
+  }
+  __syncwarp();
+}
+
+// wgrad: 32 columns of this warp's 32 rows of dw (TMEM lanes are rows).
+__device__ __forceinline__ void store_block(const uint32_t (&v)[32], int c0, int row0, const GItem &it, const GArgs &g,
+                                            int lane, uint4 *stage) {
+  const int64_t base = (int64_t)it.e * g.M;
+  const int swz = (lane >> 1) & 3;                // 16-byte pieces of a 64-byte row, spread over the banks
+  const int r_out = lane >> 2, p_out = lane & 3;
+  if (!g.f32) {
+    uint16_t *out = reinterpret_cast<uint16_t *>(g.out);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16(__uint_as_float(v[8 * p + 2 * i]), __uint_as_float(v[8 * p + 2 * i + 1]));
+      stage[lane * 4 + (p ^ swz)] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int col = c0 + 8 * p_out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + r_out;
+      const uint4 piece = stage[r * 4 + (p_out ^ ((r >> 1) & 3))];
+      if (row0 + r < g.M && col < g.C) *reinterpret_cast<uint4 *>(out + (base + row0 + r) * g.C + col) = piece;
+    }
+    __syncwarp();
+  } else {
+    float *out = reinterpret_cast<float *>(g.out);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        stage[lane * 4 + (p ^ swz)] = make_uint4(v[16 * h + 4 * p], v[16 * h + 4 * p + 1], v[16 * h + 4 * p + 2],
+                                                 v[16 * h + 4 * p + 3]);
+      __syncwarp();
+      const int col = c0 + 16 * h + 4 * p_out;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + r_out;
+        const uint4 piece = stage[r * 4 + (p_out ^ ((r >> 1) & 3))];
+        if (row0 + r < g.M && col < g.C) {
+          float4 f = make_float4(__uint_as_float(piece.x), __uint_as_float(piece.y), __uint_as_float(piece.z),
+                                 __uint_as_float(piece.w));
+          float4 *dst = reinterpret_cast<float4 *>(out + (base + row0 + r) * g.C + col);
+          if (g.accumulate) {
+            const float4 o = *dst;
+            f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+          }
+          *dst = f;
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_constant__ GMaps maps, const GArgs g) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + GP::kOffBar);
+  uint64_t *full = bars;                               // leader: both CTAs' copies of a stage
+  uint64_t *empty = full + GP::kStages;                // each CTA: stage consumed
+  uint64_t *tail_full = empty + GP::kStages;           // each CTA: its own copies of a ragged block
+  uint64_t *tail_fixed = tail_full + GP::kStages;      // leader: both CTAs zeroed the block's end
+  uint64_t *tmem_full = tail_fixed + GP::kStages;      // each CTA: accumulator ready
+  uint64_t *tmem_empty = tmem_full + 2;                // leader: both CTAs drained the accumulator
+  uint64_t *mma_done = tmem_empty + 2;
+  uint64_t *never = mma_done + 1;
+  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + GP::kOffTmemPtr);
+  int *off = reinterpret_cast<int *>(smem + GP::kOffTab);
+  int *tile_off = off + g.E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = (int)blockIdx.x >> 1, nclusters = (int)gridDim.x >> 1;
+  int *status = g.status;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.a);
+      for (int i = 0; i < (OP == kWgrad ? 1 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      for (int s = 0; s < GP::kStages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+        mbar_init(&tail_full[s], 1);
+        mbar_init(&tail_fixed[s], 2);
+      }
+      for (int a = 0; a < 2; ++a) {
+        mbar_init(&tmem_full[a], 1);
+        mbar_init(&tmem_empty[a], 2 * GP::kEpiWarps);
+      }
+      mbar_init(mma_done, 1);
+      mbar_init(never, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc_2sm(tmem_ptr, 512);
+    tmem_relinquish_2sm();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 16) status[threadIdx.x] = 0;
+  int bad = 0;
+  for (int e = threadIdx.x; e <= g.E; e += GP::kThreads) {
+    const int o = __ldg(g.offsets + e);
+    const int before = e > 0 ? __ldg(g.offsets + e - 1) : 0;
+    off[e] = o;
+    bad |= o < before || (int64_t)o > g.P;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) report_status(status, kStatusBadIndex);
+  const int mt = (g.M + GP::kM - 1) / GP::kM;
+  int total;
+  if (OP == kWgrad) {
+    total = g.E * mt * ((g.C + GP::kN - 1) / GP::kN);
+  } else {
+    if (warp == 0) {
+      int base = 0;
+      for (int e0 = 0; e0 < g.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = !bad && e < g.E ? (off[e + 1] - off[e] + GP::kN - 1) / GP::kN : 0;
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += up;
+        }
+        if (e < g.E) tile_off[e] = base + s - n;
+        base += __shfl_sync(0xffffffffu, s, 31);
+      }
+      if (lane == 0) tile_off[g.E] = base;
+    }
+    __syncthreads();
+    total = tile_off[g.E] * mt;
+  }
+  if (bad) total = 0;
+  const uint32_t tmem_base = *tmem_ptr;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0, tails = 0, tail_phase = 0;
+    bool ok = true;
+    for (int w = cluster; w < total && ok; w += nclusters) {
+      const GItem it = decode_item<OP>(w, g, off, tile_off);
+      const int half = (int)it.n_mma >> 1;
+      const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+      const int boxes = half <= 64 ? 1 : 2;                       // wgrad: 64-column boxes of B
+      const uint32_t bytes = GP::kATile + (OP == kWgrad ? boxes * GP::kHalfBox : (16 << box) * GP::kBK * 2);
+      const int m0 = it.m * GP::kM + (int)rank * 128;
+      for (int kb = 0; kb < it.kb; ++kb) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_reset(&empty[stage], phase ^ 1, status, kLimit, kWaitProducerEmpty, kb))) {
+          ok = false;
+          break;
+        }
+        const bool tail = OP == kWgrad && kb == it.kb - 1 && (it.rows & 15) != 0;
+        if (lane == 0) {
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          unsigned char *a = smem + GP::kOffA + stage * GP::kATile, *b = smem + GP::kOffB + stage * GP::kBTile;
+          if (tail) {
+            // the ragged block: onto this CTA's own barrier, for warp 2
+            if (rank == 0) mbar_arrive(&full[stage]);
+            mbar_arrive_expect_tx(&tail_full[stage], bytes);
+            for (int j = 0; j < 2; ++j)
+              tma_load_2d(a + j * GP::kHalfBox, &maps.a, &tail_full[stage], m0 + 64 * j, it.row0 + kb * GP::kBK);
+            for (int j = 0; j < boxes; ++j)
+              tma_load_2d(b + j * GP::kHalfBox, &maps.b[0], &tail_full[stage],
+                          it.c * GP::kN + (int)rank * half + 64 * j, it.row0 + kb * GP::kBK);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            if (OP == kForward) {
+              tma_load_3d_2sm(a, &maps.a, bar, kb * GP::kBK, m0, it.e);
+            } else if (OP == kDgrad) {
+              for (int j = 0; j < 2; ++j)
+                tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, kb * GP::kBK, it.e);
+            } else {
+              for (int j = 0; j < 2; ++j)
+                tma_load_2d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, it.row0 + kb * GP::kBK);
+            }
+            if (OP == kWgrad) {
+              for (int j = 0; j < boxes; ++j)
+                tma_load_2d_2sm(b + j * GP::kHalfBox, &maps.b[0], bar, it.c * GP::kN + (int)rank * half + 64 * j,
+                                it.row0 + kb * GP::kBK);
+            } else {
+              tma_load_2d_2sm(b, &maps.b[box], bar, kb * GP::kBK, it.row0 + (int)rank * half);
+            }
+          }
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (tail) {
+          tails |= 1u << stage;
+          tail_phase ^= 1u << stage;               // parity of the next use of tail_full[stage]
+        }
+        if (++stage == GP::kStages) { stage = 0; phase ^= 1; }
+      }
+    }
+    // no CTA leaves with copies in flight: the leader waits for both CTAs'
+    // copies (the final cluster barrier holds the other until then)
+    for (int s = 0; s < GP::kStages; ++s) {
+      if (rank == 0 && (issued & (1u << s)))
+        mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
+      if (tails & (1u << s))
+        mbar_wait_reset(&tail_full[s], ((tail_phase >> s) & 1u) ^ 1u, status, kLimit, kWaitProducerDrain, s, false);
+    }
+    // after a wait gave up the other CTA may have copies in flight for a stage
+    // that the leader never armed: give them time to land (~100 us)
+    if (lane == 0 && *reinterpret_cast<volatile int *>(status + 1) != 0) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 200000) __nanosleep(1000);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (rank == 0) {
+      int stage = 0, j = 0;
+      uint32_t phase = 0, fixed_phase = 0;
+      bool ok = true;
+      for (int w = cluster; w < total && ok; w += nclusters) {
+        const GItem it = decode_item<OP>(w, g, off, tile_off);
+        if (OP == kWgrad && it.kb == 0) continue;
+        const int acc = j & 1;
+        const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
+        ++j;
+        if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit,
+                                                     kWaitMmaTmemEmpty, w)))
+          break;
+        if (g.inject_wait == 1 && j == 1 &&
+            !__all_sync(0xffffffffu, mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, w)))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
+        const uint32_t idesc = make_idesc_bf16(GP::kM, it.n_mma, OP != kForward, OP == kWgrad);
+        const int len = OP == kWgrad ? it.rows : g.R;
+        for (int kb = 0; kb < it.kb; ++kb) {
+          const int left = len - kb * GP::kBK;                  // reduction values from here on
+          const bool tail = OP == kWgrad && kb == it.kb - 1 && (it.rows & 15) != 0;
+          bool got = mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb);
+          if (tail) {
+            got = got && mbar_wait_reset(&tail_fixed[stage], (fixed_phase >> stage) & 1u, status, kLimit, kWaitMmaFull, kb);
+            fixed_phase ^= 1u << stage;
+          }
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t a = smem_u32(smem + GP::kOffA + stage * GP::kATile);
+            const uint32_t b = smem_u32(smem + GP::kOffB + stage * GP::kBTile);
+            const int steps = left >= GP::kBK ? 4 : (left + 15) >> 4;
+            for (int kk = 0; kk < steps; ++kk) {
+              // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row
+              // groups 1024 bytes apart; M- / N-major: 16 K rows of 128 bytes,
+              // 8-row groups 1024 bytes apart, 64-wide boxes kHalfBox apart
+              const uint64_t ad = OP == kForward ? make_smem_desc(a + kk * 32, 16, 1024, kSwizzle128B)
+                                                 : make_smem_desc(a + kk * 2048, GP::kHalfBox, 1024, kSwizzle128B);
+              const uint64_t bd = OP == kWgrad ? make_smem_desc(b + kk * 2048, GP::kHalfBox, 1024, kSwizzle128B)
+                                               : make_smem_desc(b + kk * 32, 16, 1024, kSwizzle128B);
+              tc_mma_2sm_f16(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+            tc_commit_2sm(&empty[stage], 3);
+          }
+          __syncwarp();
+          if (++stage == GP::kStages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit_2sm(&tmem_full[acc], 3);
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit_2sm(mma_done, 1);
+      __syncwarp();
+      mbar_wait_reset(mma_done, 0, status, kLimit, kWaitMmaDone, 0, false);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ ragged ends (both CTAs)
+    if (OP == kWgrad) {
+      int block = 0;                                           // blocks of the items before, modulo the ring
+      uint32_t tail_phase = 0;
+      for (int w = cluster; w < total; w += nclusters) {
+        const GItem it = decode_item<OP>(w, g, off, tile_off);
+        if (it.kb > 0 && (it.rows & 15) != 0) {
+          const int stage = (block + it.kb - 1) % GP::kStages;
+          if (!__all_sync(0xffffffffu, mbar_wait_reset(&tail_full[stage], (tail_phase >> stage) & 1u, status, kLimit,
+                                                       kWaitMmaFull, w)))
+            break;
+          tail_phase ^= 1u << stage;
+          const int rem = it.rows - (it.kb - 1) * GP::kBK;       // 1 .. 63 rows of the block
+          const int rows = ((rem + 15) & ~15) - rem;             // rows to zero, 128 bytes in each box
+          for (int i = lane; i < rows * 32; i += 32) {
+            const int box = i / (rows * 8), r = i - box * (rows * 8);
+            unsigned char *p = box < 2 ? smem + GP::kOffA + stage * GP::kATile + box * GP::kHalfBox
+                                       : smem + GP::kOffB + stage * GP::kBTile + (box - 2) * GP::kHalfBox;
+            *reinterpret_cast<uint4 *>(p + rem * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_fixed[stage]), 0));
+        }
+        block = (block + it.kb) % GP::kStages;
+      }
+    }
+  } else if (warp >= GP::kFirstEpiWarp) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;
+    const int ew = warp - GP::kFirstEpiWarp;
+    uint32_t *stage_tile = reinterpret_cast<uint32_t *>(smem + GP::kOffEpi + ew * GP::kStageTile);
+    int j = 0;
+    for (int w = cluster; w < total; w += nclusters) {
+      const GItem it = decode_item<OP>(w, g, off, tile_off);
+      const int first = it.m * GP::kM + (int)rank * 128 + 32 * q;  // this warp's M rows
+      const bool none = OP == kWgrad && it.kb == 0;
+      const int acc = j & 1;
+      if (!none) {
+        const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
+        ++j;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_reset(&tmem_full[acc], acc_phase, status, kLimit, kWaitEpiTmemFull, w)))
+          break;
+        tc_fence_after();
+      } else if (g.accumulate) {
+        continue;
+      }
+      const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN);
+      const int cols = OP == kWgrad ? min(GP::kN, g.C - it.c * GP::kN) : it.rows;
+      if (first < g.M) {
+        for (int c0 = 32 * (ew >> 2); c0 < cols; c0 += 64) {
+          uint32_t v[32];
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          } else {
+            tmem_ld_32x32b_x32(t_row + (uint32_t)c0, v);
+            tmem_ld_wait();
+          }
+          if (OP == kWgrad)
+            store_block(v, it.c * GP::kN + c0, first, it, g, lane, reinterpret_cast<uint4 *>(stage_tile));
+          else
+            store_rows(v, c0, first, it, g, lane, stage_tile);
+        }
+      }
+      if (!none) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_2sm(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  return fn;
+}
+
+// A BF16 tensor of rank 2 or 3 (strides in elements, innermost 1) with boxes
+// of box0 x box1 (x 1), 128-byte swizzled; what lies outside reads as zero.
+bool encode_bf16(CUtensorMap *map, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                 uint64_t s2, uint32_t box0, uint32_t box1) {
+  EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {s1 * 2, s2 * 2};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t smem_bytes(int E) { return 1024 + GP::kOffTab + (size_t)8 * (E + 1); }
+
+template <int OP>
+int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};                // devices whose kernel attribute is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(grouped_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  const int64_t clusters = std::min<int64_t>(num_sms() / 2, most_items);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * clusters));
+  cfg.blockDim = dim3(GP::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(g.E);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<OP>, maps, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int check_grouped(int64_t P, int64_t N, int64_t K, int32_t E, const void *offsets, const void *workspace,
+                  size_t workspace_bytes) {
+  if (P < 0 || N <= 0 || K <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+  if (P > 0x7fffffffLL || N > 0x7fffff00LL || K > 0x7fffff00LL || N % 8 != 0 || K % 8 != 0 || E > kMaxExperts)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || !aligned(offsets, 4)) return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < moe_grouped_workspace_size(P, N, K, E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return MOE_OK;
+}
+
+int check_rows(const void *p, int64_t ld, int64_t cols) {
+  if (!p || ld < cols) return MOE_ERR_INVALID_ARG;
+  if (ld % 8 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return aligned(p, 16) ? MOE_OK : MOE_ERR_MISALIGNED;
+}
+
+int injected_wait() {
+  const char *env = getenv("MOE_MXQ_DEBUG_INJECT_WAIT");
+  return env ? atoi(env) : 0;
+}
+
+// forward (OP kForward): in = x [P][K], out = y [P][N]; dgrad: in = dy [P][N],
+// out = dx [P][K].
+template <int OP>
+int rows_product(const uint16_t *in, int64_t ld_in, const uint16_t *w, const int32_t *offsets, int64_t P, int64_t N,
+                 int64_t K, int32_t E, uint16_t *out, int64_t ld_out, void *workspace, size_t workspace_bytes,
+                 cudaStream_t st) {
+  int rc = check_grouped(P, N, K, E, offsets, workspace, workspace_bytes);
+  if (rc != MOE_OK) return rc;
+  if (P == 0)
+    return cudaMemsetAsync(workspace, 0, 64, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int64_t R = OP == kForward ? K : N, M = OP == kForward ? N : K;
+  if ((rc = check_rows(in, ld_in, R)) != MOE_OK || (rc = check_rows(out, ld_out, M)) != MOE_OK) return rc;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (!aligned(w, 16)) return MOE_ERR_MISALIGNED;
+  GMaps maps;
+  bool ok = OP == kForward ? encode_bf16(&maps.a, w, 3, K, N, E, K, N * K, GP::kBK, 128)
+                           : encode_bf16(&maps.a, w, 3, K, N, E, K, N * K, 64, GP::kBK);
+  for (int i = 0; i < 4; ++i) ok = ok && encode_bf16(&maps.b[i], in, 2, R, P, 1, ld_in, 0, GP::kBK, 16u << i);
+  if (!ok) return MOE_ERR_CUDA;
+  GArgs g{};
+  g.offsets = offsets;
+  g.P = P;
+  g.E = E;
+  g.M = (int)M;
+  g.R = (int)R;
+  g.ld_out = ld_out;
+  g.out = out;
+  g.inject_wait = injected_wait();
+  g.status = reinterpret_cast<int *>(workspace);
+  const int64_t tiles = std::min<int64_t>(P, P / GP::kN + E);      // most row tiles of any offsets
+  return launch_grouped<OP>(maps, g, tiles * ceil_div(M, GP::kM), st);
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" size_t moe_grouped_workspace_size(int64_t P, int64_t N, int64_t K, int32_t E) {
+  if (P < 0 || N <= 0 || K <= 0 || E <= 0) return 0;
+  return kStatusBytes;
+}
+
+extern "C" int moe_grouped_forward(const uint16_t *x, int64_t ldx, const uint16_t *w, const int32_t *offsets,
+                                   int64_t P, int64_t N, int64_t K, int32_t E, uint16_t *y, int64_t ldy,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return rows_product<kForward>(x, ldx, w, offsets, P, N, K, E, y, ldy, workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_grouped_dgrad(const uint16_t *dy, int64_t ldy, const uint16_t *w, const int32_t *offsets, int64_t P,
+                                 int64_t N, int64_t K, int32_t E, uint16_t *dx, int64_t ldx, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+  return rows_product<kDgrad>(dy, ldy, w, offsets, P, N, K, E, dx, ldx, workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_grouped_wgrad(const uint16_t *dy, int64_t ldy, const uint16_t *x, int64_t ldx,
+                                 const int32_t *offsets, int64_t P, int64_t N, int64_t K, int32_t E, void *dw,
+                                 int32_t dw_dtype, int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+  int rc = check_grouped(P, N, K, E, offsets, workspace, workspace_bytes);
+  if (rc != MOE_OK) return rc;
+  if ((dw_dtype != MOE_BF16 && dw_dtype != MOE_F32) || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
+  if (accumulate && dw_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (!dw) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dw, 16)) return MOE_ERR_MISALIGNED;
+  if (P == 0) {
+    const size_t bytes = (size_t)E * N * K * (dw_dtype == MOE_F32 ? 4 : 2);
+    if (cudaMemsetAsync(workspace, 0, 64, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    return accumulate || cudaMemsetAsync(dw, 0, bytes, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if ((rc = check_rows(dy, ldy, N)) != MOE_OK || (rc = check_rows(x, ldx, K)) != MOE_OK) return rc;
+  GMaps maps;
+  if (!encode_bf16(&maps.a, dy, 2, N, P, 1, ldy, 0, 64, GP::kBK) ||
+      !encode_bf16(&maps.b[0], x, 2, K, P, 1, ldx, 0, 64, GP::kBK))
+    return MOE_ERR_CUDA;
+  for (int i = 1; i < 4; ++i) maps.b[i] = maps.b[0];
+  GArgs g{};
+  g.offsets = offsets;
+  g.P = P;
+  g.E = E;
+  g.M = (int)N;
+  g.C = (int)K;
+  g.out = dw;
+  g.f32 = dw_dtype == MOE_F32;
+  g.accumulate = accumulate;
+  g.inject_wait = injected_wait();
+  g.status = reinterpret_cast<int *>(workspace);
+  return launch_grouped<kWgrad>(maps, g, (int64_t)E * ceil_div(N, GP::kM) * ceil_div(K, GP::kN), stream);
+}

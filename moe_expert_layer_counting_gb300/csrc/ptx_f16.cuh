@@ -1,0 +1,110 @@
+// ptx_f16.cuh -- inline-PTX wrappers of the BF16 products (grouped.cu) beyond
+// those of ptx.cuh: 3-D TMA loads of a CTA pair, tcgen05.mma kind::f16 with
+// operands of either major, wide TMEM reads, and bounded waits of kernels
+// that reset their own status words.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+
+#include "ptx.cuh"
+
+namespace mxq {
+
+// TMA tile load into this CTA's shared memory, counted on an mbarrier of
+// either CTA of the pair (`bar_cluster`: shared::cluster address).
+__device__ __forceinline__ void tma_load_3d_2sm(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t x,
+                                                int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16: BF16 x BF16 -> float32, M = m, N = n;
+// a_mn / b_mn: the operand's M (N) index is the contiguous one in shared
+// memory (else its K index is).
+__device__ __forceinline__ uint32_t make_idesc_bf16(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
+  uint32_t d = 0;
+  d |= 1u << 4;                        // D: float32
+  d |= 1u << 7;                        // A: BF16
+  d |= 1u << 10;                       // B: BF16
+  d |= (a_mn ? 1u : 0u) << 15;
+  d |= (b_mn ? 1u : 0u) << 16;
+  d |= ((n >> 3) & 0x3Fu) << 17;
+  d |= ((m >> 4) & 0x1Fu) << 24;
+  return d;
+}
+
+// D[tmem] (+)= A x B on the tensor cores of both SMs of the pair.
+__device__ __forceinline__ void tc_mma_2sm_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Each thread of the warp reads its own TMEM lane, 32 consecutive columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Orders this thread's generic-proxy shared-memory writes before later
+// async-proxy (tensor core) reads of them.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// As mbar_try_wait, ordered after arrivals of the other CTA of the pair too.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait for a kernel whose first CTA resets the status words when it
+// starts (no launch before it does): the abort flag is looked at only after
+// kAbortDelay cycles of waiting (~1 ms), when that CTA, the first of the grid
+// to be placed, has long done so; a flag left by an earlier call is not seen.
+constexpr long long kAbortDelay = 2000000LL;
+__device__ __forceinline__ bool mbar_wait_reset(uint64_t *bar, uint32_t parity, int *ws_status, long long limit,
+                                                int site, int pos, bool honor_abort = true) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  volatile int *abort_flag = ws_status + 1;
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const long long waited = clock64() - t0;
+    if (honor_abort && waited > kAbortDelay && *abort_flag) return false;
+    if (waited > limit) {
+      if (atomicCAS(ws_status + 2, 0, site) == 0) {
+        ws_status[3] = (int)blockIdx.x;
+        ws_status[4] = pos;
+      }
+      report_status(ws_status, kStatusTimeout);
+      atomicExch(ws_status + 1, 1);
+      return false;
+    }
+  }
+}
+
+}  // namespace mxq
