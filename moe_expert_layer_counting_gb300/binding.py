@@ -1,8 +1,8 @@
 """ctypes binding of libmoe_mxq.so -- argument marshalling only.
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
-include/moe_bfp8.h, include/moe_grouped.h)
-and takes torch tensors for the device buffers; all work runs in the
+include/moe_bfp8.h, include/moe_grouped.h,
+include/moe_norm.h) and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
 There is no CPU fallback: importing this module without the built library
@@ -44,13 +44,15 @@ SCHEDULE_DEFAULT, SCHEDULE_SEPARATE, SCHEDULE_EXPERT_WAVES = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID, ROUTE_RAW, ROUTE_NO_RENORM = 0, 1, 2, 4
 BFP8_LAYOUT_CANONICAL, BFP8_LAYOUT_TILED = 0, 1
 BF16, F32 = 0, 1                                         # enum moe_dtype
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
 
 EXPORTED = ["mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_route_topk_ex",
             "moe_permute_workspace_size",
             "moe_permute", "moe_permute_noalloc", "moe_expert_workspace_size", "moe_expert_forward", "moe_combine",
             "moe_workspace_size", "moe_forward", "moe_get_device_status", "moe_status_string", "moe_version",
             "bfp8_quantize_act", "bfp8_quantize_weight", "moe_bfp8_workspace_size", "moe_forward_bfp8",
-            "moe_grouped_workspace_size", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"]
+            "moe_grouped_workspace_size", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
+            "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward"]
 
 
 class MoeExpertArgs(ctypes.Structure):
@@ -90,6 +92,22 @@ class MoeBfp8Args(ctypes.Structure):
                 ("workspace", _p), ("workspace_bytes", _sz), ("weight_layout", _i32), ("phases", _i32)]
 
 
+class MoeNormArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32),
+                ("x_dtype", _i32), ("w_dtype", _i32), ("gate_dtype", _i32), ("gate_kind", _i32), ("gate_sigmoid", _i32),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
+                ("T", _i64), ("H", _i64), ("x", _p), ("ldx", _i64), ("b", _p), ("ldb", _i64),
+                ("gate", _p), ("ld_gate", _i64), ("w_post", _p), ("w_pre", _p),
+                ("y", _p), ("ldy", _i64), ("n", _p), ("ldn", _i64)]
+
+
+class MoeNormGrads(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32),
+                ("dy", _p), ("ld_dy", _i64), ("dn", _p), ("ld_dn", _i64), ("dx", _p), ("ld_dx", _i64),
+                ("db", _p), ("ld_db", _i64), ("dgate", _p), ("ld_dgate", _i64), ("dw_post", _p), ("dw_pre", _p),
+                ("workspace", _p), ("workspace_bytes", _sz)]
+
+
 lib.mxq_quantize_act.argtypes = [_p, _i64, _i64, _p, _p, _p]
 lib.mxq_quantize_weight.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]
 lib.moe_route_topk.argtypes = [_p, _i64, _i32, _i32, _p, _p, _p]
@@ -115,6 +133,10 @@ lib.moe_grouped_workspace_size.restype = _sz
 lib.moe_grouped_forward.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _sz, _p]
 lib.moe_grouped_dgrad.argtypes = lib.moe_grouped_forward.argtypes
 lib.moe_grouped_wgrad.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _p, _i32, _i32, _p, _sz, _p]
+lib.moe_norm_forward.argtypes = [ctypes.POINTER(MoeNormArgs), _p]
+lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
+lib.moe_norm_workspace_size.restype = _sz
+lib.moe_norm_backward.argtypes = [ctypes.POINTER(MoeNormArgs), ctypes.POINTER(MoeNormGrads), _p]
 lib.moe_get_device_status.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_int)]
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
@@ -123,7 +145,8 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_permute_noalloc",
               "moe_expert_forward",
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
-              "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"):
+              "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
+              "moe_norm_forward", "moe_norm_backward"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -382,4 +405,99 @@ def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
                                workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if check:
         _check(rc, "moe_grouped_wgrad")
+    return rc
+
+
+# ---------------------------------------------------------------- norms around the layer (include/moe_norm.h)
+
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid):
+    """MoeNormArgs of these tensors, or None if a type, shape or stride does not fit."""
+    T, H = x.shape
+    xt = _DTYPES.get(x.dtype)
+    if xt is None or not _is_rows(x, T, H, x.dtype):
+        return None
+    if b is not None and not _is_rows(b, T, H):
+        return None
+    if y is not None and not _is_rows(y, T, H, x.dtype):
+        return None
+    if n is not None and not _is_rows(n, T, H):
+        return None
+    w = w_pre if w_pre is not None else w_post
+    wt = BF16 if w is None else _DTYPES.get(w.dtype)
+    for t in (w_post, w_pre):
+        if t is not None and (wt is None or t.dtype != w.dtype or t.shape != (H,) or not t.is_contiguous()):
+            return None
+    kind, gt, ld_gate = GATE_NONE, BF16, H
+    if gate is not None:
+        gt = _DTYPES.get(gate.dtype)
+        if gt is None or gate.dim() != 2:
+            return None
+        if gate.shape == (T, 1) and H != 1:
+            kind = GATE_TOKEN
+            if not gate.is_contiguous():
+                return None
+        elif gate.shape == (1, H):
+            kind = GATE_CHANNEL
+            if H > 1 and gate.stride(1) != 1:
+                return None
+        elif _is_rows(gate, T, H, gate.dtype):
+            kind, ld_gate = GATE_FULL, _row_stride(gate)
+        else:
+            return None
+    return MoeNormArgs(ctypes.sizeof(MoeNormArgs), xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale,
+                       weight_offset, eps, T, H, x.data_ptr(), _row_stride(x),
+                       None if b is None else b.data_ptr(), H if b is None else _row_stride(b),
+                       None if gate is None else gate.data_ptr(), ld_gate,
+                       None if w_post is None else w_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
+                       None if y is None else y.data_ptr(), H if y is None else _row_stride(y),
+                       None if n is None else n.data_ptr(), H if n is None else _row_stride(n))
+
+
+def moe_norm_forward(x, b, gate, w_post, w_pre, y, n, residual_scale: float = 1.0, weight_offset: float = 0.0,
+                     eps: float = 1e-6, gate_sigmoid: bool = False, stream=None, check=True) -> int:
+    """y = residual_scale x + g norm(b; w_post), n = norm(y; w_pre); b, gate, w_post, w_pre, y and n may be None as
+    include/moe_norm.h says.  gate [T, 1], [1, H] or [T, H]; x and y bf16 or float32, b and n bf16."""
+    a = _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid)
+    if a is None:
+        return _invalid("moe_norm_forward", check)
+    rc = lib.moe_norm_forward(ctypes.byref(a), _stream(stream))
+    if check:
+        _check(rc, "moe_norm_forward")
+    return rc
+
+
+def moe_norm_workspace_size(T: int, H: int) -> int:
+    return int(lib.moe_norm_workspace_size(T, H))
+
+
+def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=None, dgate=None, dw_post=None, dw_pre=None,
+                      residual_scale: float = 1.0, weight_offset: float = 0.0, eps: float = 1e-6,
+                      gate_sigmoid: bool = False, stream=None, check=True) -> int:
+    """Gradients of moe_norm_forward from dy and dn; y is its y (without b: its x).  Outputs that are None are not
+    computed; dgate has the gate's shape and type, dw_post and dw_pre are float32 [H]."""
+    a = _norm_args(y, b, gate, w_post, w_pre, None, None, residual_scale, weight_offset, eps, gate_sigmoid)
+    T, H = y.shape
+    ok = a is not None
+    for t, dtype in ((dy, y.dtype), (dx, y.dtype), (dn, torch.bfloat16), (db, torch.bfloat16)):
+        ok = ok and (t is None or _is_rows(t, T, H, dtype))
+    for t in (dw_post, dw_pre):
+        ok = ok and (t is None or (t.dtype == torch.float32 and t.shape == (H,) and t.is_contiguous()))
+    if dgate is not None:
+        ok = ok and gate is not None and dgate.dtype == gate.dtype and dgate.shape == gate.shape and \
+            (dgate.is_contiguous() or (a.gate_kind == GATE_FULL and dgate.stride(1) == 1))
+    if not ok:
+        return _invalid("moe_norm_backward", check)
+
+    def rows(t):
+        return (None, H) if t is None else (t.data_ptr(), _row_stride(t))
+
+    g = MoeNormGrads(ctypes.sizeof(MoeNormGrads), *rows(dy), *rows(dn), *rows(dx), *rows(db), *rows(dgate),
+                     None if dw_post is None else dw_post.data_ptr(), None if dw_pre is None else dw_pre.data_ptr(),
+                     workspace.data_ptr(), workspace.nbytes)
+    rc = lib.moe_norm_backward(ctypes.byref(a), ctypes.byref(g), _stream(stream))
+    if check:
+        _check(rc, "moe_norm_backward")
     return rc

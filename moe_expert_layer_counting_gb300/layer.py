@@ -3,9 +3,19 @@ layer object that owns its workspace.  Allocation uses torch; every
 computation is a call into libmoe_mxq.so."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as B
+
+
+def _on(stream):
+    """Allocations made inside belong to `stream` (None: the current one), so that their memory is not handed on
+    while work of that stream still uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 class QuantizedExperts:
@@ -129,3 +139,42 @@ class MoELayerBfp8:
 
     def device_status(self, stream=None) -> int:
         return B.moe_get_device_status(self.workspace, stream)
+
+
+class BlockNorm:
+    """The norms around the layer with its gate and residual scale, forward and backward (include/moe_norm.h).
+
+    w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.
+    """
+
+    def __init__(self, w_post: torch.Tensor = None, w_pre: torch.Tensor = None, residual_scale: float = 1.0,
+                 weight_offset: float = 0.0, eps: float = 1e-6, gate_sigmoid: bool = False):
+        self.w_post, self.w_pre = w_post, w_pre
+        self.how = (residual_scale, weight_offset, eps, gate_sigmoid)
+
+    def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
+        """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
+        with _on(stream):
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if b is not None else None
+            n = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if self.w_pre is not None else None
+        B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, stream=stream)
+        return (x if y is None else y), n
+
+    def backward(self, y: torch.Tensor, b: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, dn: torch.Tensor,
+                 stream=None) -> dict:
+        """Gradients dx, db, dgate, dw_post, dw_pre (None where there is nothing to differentiate) from those of
+        forward's y and n (either may be None); y, b and gate are what forward returned and took."""
+        T, H = y.shape
+        dev = y.device
+        w_post = self.w_post if b is not None else None
+        with _on(stream):
+            out = {"dx": torch.empty(T, H, dtype=y.dtype, device=dev),
+                   "db": None if b is None else torch.empty(T, H, dtype=torch.bfloat16, device=dev),
+                   "dgate": None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dev),
+                   "dw_post": None if w_post is None else torch.empty(H, dtype=torch.float32, device=dev),
+                   "dw_pre": None if dn is None else torch.empty(H, dtype=torch.float32, device=dev)}
+            ws = torch.empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8, device=dev)
+        s, o, e, sig = self.how
+        B.moe_norm_backward(y, b, gate, w_post, None if dn is None else self.w_pre, dy, dn, ws, residual_scale=s,
+                            weight_offset=o, eps=e, gate_sigmoid=sig, stream=stream, **out)
+        return out
