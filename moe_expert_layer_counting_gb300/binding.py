@@ -2,7 +2,7 @@
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
 include/moe_bfp8.h, include/moe_grouped.h,
-include/moe_norm.h) and takes torch tensors for the device buffers; all work runs in the
+include/moe_norm.h, include/moe_adamw.h) and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
 There is no CPU fallback: importing this module without the built library
@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 # MOE_MXQ_LIB may point at another build of the same library (e.g. one built
@@ -52,7 +53,7 @@ EXPORTED = ["mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_ro
             "moe_workspace_size", "moe_forward", "moe_get_device_status", "moe_status_string", "moe_version",
             "bfp8_quantize_act", "bfp8_quantize_weight", "moe_bfp8_workspace_size", "moe_forward_bfp8",
             "moe_grouped_workspace_size", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
-            "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward"]
+            "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward", "moe_adamw_step"]
 
 
 class MoeExpertArgs(ctypes.Structure):
@@ -108,6 +109,17 @@ class MoeNormGrads(ctypes.Structure):
                 ("workspace", _p), ("workspace_bytes", _sz)]
 
 
+# moe_adamw_tensor, for host tables (numpy structured arrays)
+ADAMW_TENSOR = np.dtype([(f, np.int64) for f in ("n", "p", "g", "m", "v", "m_scale", "v_scale", "copy")])
+
+
+class MoeAdamwArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("n_tensors", _i32), ("tensors", _p),
+                ("p_dtype", _i32), ("g_dtype", _i32), ("state_bits", _i32), ("grad_scale", _p),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", _i64)]
+
+
 lib.mxq_quantize_act.argtypes = [_p, _i64, _i64, _p, _p, _p]
 lib.mxq_quantize_weight.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]
 lib.moe_route_topk.argtypes = [_p, _i64, _i32, _i32, _p, _p, _p]
@@ -137,6 +149,7 @@ lib.moe_norm_forward.argtypes = [ctypes.POINTER(MoeNormArgs), _p]
 lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
 lib.moe_norm_workspace_size.restype = _sz
 lib.moe_norm_backward.argtypes = [ctypes.POINTER(MoeNormArgs), ctypes.POINTER(MoeNormGrads), _p]
+lib.moe_adamw_step.argtypes = [ctypes.POINTER(MoeAdamwArgs), _p]
 lib.moe_get_device_status.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_int)]
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
@@ -146,7 +159,7 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_expert_forward",
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
               "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
-              "moe_norm_forward", "moe_norm_backward"):
+              "moe_norm_forward", "moe_norm_backward", "moe_adamw_step"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -500,4 +513,21 @@ def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=
     rc = lib.moe_norm_backward(ctypes.byref(a), ctypes.byref(g), _stream(stream))
     if check:
         _check(rc, "moe_norm_backward")
+    return rc
+
+
+# ---------------------------------------------------------------- AdamW over many tensors (include/moe_adamw.h)
+
+def moe_adamw_step(table: np.ndarray, p_dtype: int, g_dtype: int, state_bits: int, lr: float, beta1: float, beta2: float,
+                   eps: float, weight_decay: float, step: int, grad_scale: torch.Tensor = None, stream=None,
+                   check=True) -> int:
+    """One step over the tensors of ``table`` (a contiguous array of ADAMW_TENSOR: sizes and device pointers)."""
+    if table.dtype != ADAMW_TENSOR or not table.flags.c_contiguous or \
+            (grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1)):
+        return _invalid("moe_adamw_step", check)
+    a = MoeAdamwArgs(ctypes.sizeof(MoeAdamwArgs), table.size, table.ctypes.data, p_dtype, g_dtype, state_bits,
+                     None if grad_scale is None else grad_scale.data_ptr(), lr, beta1, beta2, eps, weight_decay, step)
+    rc = lib.moe_adamw_step(ctypes.byref(a), _stream(stream))
+    if check:
+        _check(rc, "moe_adamw_step")
     return rc

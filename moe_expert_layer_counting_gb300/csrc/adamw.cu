@@ -1,0 +1,320 @@
+// adamw.cu -- one AdamW step over many tensors (include/moe_adamw.h has the
+// formulas and the 8-bit states' format).
+//
+// Bound by HBM: 28 bytes a value with float32 states (p read and written, BF16
+// gradient and copy, m and v read and written), 14.1 with 8-bit states.  The
+// table of tensors travels in the kernel's parameters (no copy to the device,
+// nothing kept between calls), up to kTensors per launch; a block finds its
+// tensor by bisection of the tensors' first blocks.  A thread owns 8
+// consecutive values, four neighbours a 32-value group of the 8-bit states.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "../../include/moe_adamw.h"
+#include "host_common.h"
+#include "ptx.cuh"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRounds = 2;                                   // vectors per thread
+constexpr int64_t kChunk = (int64_t)kThreads * 8 * kRounds;  // values per block
+
+struct AdamEntry {
+  int64_t n;
+  void *p;
+  const void *g;
+  void *m, *v;
+  uint8_t *ms, *vs;
+  uint16_t *copy;
+};
+
+template <int TENSORS>
+struct AdamTable {
+  AdamEntry t[TENSORS];
+  int first[TENSORS + 1];          // first block of each tensor
+  int count;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, keep, rate, root_scale, eps;
+  const float *grad_scale;
+};
+
+struct V8 {
+  float v[8];
+};
+
+__device__ __forceinline__ V8 load8(const float *p) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  return V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ V8 load8(const uint16_t *p) {
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[2 * i] = bf16_bits_to_float(w[i] & 0xFFFFu);
+    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(f);
+  return *reinterpret_cast<const uint16_t *>(&b);
+}
+__device__ __forceinline__ void put(float *p, float f) { *p = f; }
+__device__ __forceinline__ void put(uint16_t *p, float f) { *p = to_bf16(f); }
+__device__ __forceinline__ float get(const float *p) { return *p; }
+__device__ __forceinline__ float get(const uint16_t *p) { return bf16_bits_to_float(*p); }
+__device__ __forceinline__ void store8(float *p, const V8 &f) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+}
+__device__ __forceinline__ void store8(uint16_t *p, const V8 &f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)to_bf16(f.v[2 * i]) | ((uint32_t)to_bf16(f.v[2 * i + 1]) << 16);
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// `live` (1 .. 8) of 8 values; the others read as zero and are not written.
+template <typename T>
+__device__ __forceinline__ V8 load_some(const T *p, int live) {
+  if (live == 8) return load8(p);
+  V8 r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.v[j] = j < live ? get(p + j) : 0.f;
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T *p, const V8 &f, int live) {
+  if (live == 8) {
+    store8(p, f);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < live) put(p + j, f.v[j]);
+}
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p, int live) {
+  if (live == 8) return *reinterpret_cast<const uint2 *>(p);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < live) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint2 &c, int live) {
+  if (live == 8) {
+    *reinterpret_cast<uint2 *>(p) = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < live) p[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+}
+
+// 2^(byte - 127) (byte 0: a float32 subnormal).
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+__device__ __forceinline__ V8 decode8(const uint2 &c, uint32_t byte) {
+  const float s = scale_of(byte);
+  const uint32_t w[2] = {c.x, c.y};
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    r.v[2 * i] = f.x * s;
+    r.v[2 * i + 1] = f.y * s;
+  }
+  return r;
+}
+
+// Codes and scale byte of a 32-value group spread over four lanes; kRoot: a
+// value above zero takes at least the smallest code, 2^-9.
+template <bool kRoot>
+__device__ __forceinline__ uint2 encode8(const V8 &f, uint8_t *byte) {
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f.v[j]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int e = ue8m0_exponent<true>(amax);
+  const float inv = pow2_neg(e);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = f.v[2 * i] * inv, b = f.v[2 * i + 1] * inv;
+    if (kRoot) {
+      if (f.v[2 * i] > 0.f) a = fmaxf(a, 0.001953125f);
+      if (f.v[2 * i + 1] > 0.f) b = fmaxf(b, 0.001953125f);
+    }
+    c[i] = cvt_e4m3x2(a, b);
+  }
+  *byte = (uint8_t)(e + 127);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+template <typename PT, typename GT, bool kSmall, int TENSORS>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<TENSORS> a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  int lo = 0, hi = a.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.first[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
+  }
+  const AdamEntry &t = a.t[lo];
+  const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk;
+  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = base + ((int64_t)r * kThreads + threadIdx.x) * 8;
+    if (kSmall ? i - 8 * (threadIdx.x & 31) >= n : i >= n) break;      // 8-bit states: whole warps go on
+    const int live = (int)(n - i < 0 ? 0 : n - i < 8 ? n - i : 8);
+    V8 p, g, m, v, root;
+    if (!kSmall || live > 0) {
+      p = load_some(static_cast<const PT *>(t.p) + i, live);
+      g = load_some(static_cast<const GT *>(t.g) + i, live);
+      if (kSmall) {
+        m = decode8(load_codes(static_cast<const uint8_t *>(t.m) + i, live), t.ms[i >> 5]);
+        v = decode8(load_codes(static_cast<const uint8_t *>(t.v) + i, live), t.vs[i >> 5]);
+      } else {
+        m = load_some(static_cast<const float *>(t.m) + i, live);
+        v = load_some(static_cast<const float *>(t.v) + i, live);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // each product and sum of m and v rounded by itself (no fused
+        // multiply-add), so that the 8-bit codes have one right answer
+        const float gj = __fmul_rn(g.v[j], gs);
+        const float old = kSmall ? __fmul_rn(v.v[j], v.v[j]) : v.v[j];
+        m.v[j] = __fadd_rn(__fmul_rn(m.v[j], a.beta1), __fmul_rn(gj, a.one_minus_beta1));
+        v.v[j] = __fadd_rn(__fmul_rn(old, a.beta2), __fmul_rn(__fmul_rn(gj, gj), a.one_minus_beta2));
+        root.v[j] = __fsqrt_rn(v.v[j]);
+        p.v[j] = p.v[j] * a.keep - a.rate * __fdividef(m.v[j], fmaf(root.v[j], a.root_scale, a.eps));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p.v[j] = m.v[j] = root.v[j] = 0.f;
+    }
+    if (kSmall) {
+      uint8_t mb, vb;
+      const uint2 mc = encode8<false>(m, &mb), vc = encode8<true>(root, &vb);
+      if (live > 0) {
+        store_codes(static_cast<uint8_t *>(t.m) + i, mc, live);
+        store_codes(static_cast<uint8_t *>(t.v) + i, vc, live);
+        if ((i & 31) == 0) {
+          t.ms[i >> 5] = mb;
+          t.vs[i >> 5] = vb;
+        }
+      }
+    } else {
+      store_some(static_cast<float *>(t.m) + i, m, live);
+      store_some(static_cast<float *>(t.v) + i, v, live);
+    }
+    if (!kSmall || live > 0) {
+      store_some(static_cast<PT *>(t.p) + i, p, live);
+      if (t.copy) store_some(t.copy + i, p, live);
+    }
+  }
+}
+
+template <typename PT, typename GT, bool kSmall, int TENSORS>
+int launch_some(const moe_adamw_args &a, int from, int to, cudaStream_t st) {
+  AdamTable<TENSORS> t;
+  t.count = 0;
+  int64_t blocks = 0;
+  for (int i = from; i < to; ++i) {
+    const moe_adamw_tensor &x = a.tensors[i];
+    if (x.n == 0) continue;
+    t.t[t.count] = AdamEntry{x.n, x.p, x.g, x.m, x.v, x.m_scale, x.v_scale, x.copy};
+    t.first[t.count++] = (int)blocks;
+    blocks += ceil_div(x.n, kChunk);
+  }
+  if (blocks == 0) return MOE_OK;
+  t.first[t.count] = (int)blocks;
+  t.beta1 = (float)a.beta1;
+  t.one_minus_beta1 = (float)(1.0 - a.beta1);
+  t.beta2 = (float)a.beta2;
+  t.one_minus_beta2 = (float)(1.0 - a.beta2);
+  t.keep = (float)(1.0 - a.lr * a.weight_decay);
+  t.rate = (float)(a.lr / (1.0 - std::pow(a.beta1, (double)a.step)));
+  t.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, (double)a.step)));
+  t.eps = (float)a.eps;
+  t.grad_scale = a.grad_scale;
+  return launch_pdl(adamw_kernel<PT, GT, kSmall, TENSORS>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t);
+}
+
+constexpr int kFew = 40, kMany = 400;       // tensors per launch: 3 KB or 28 KB of kernel parameters
+static_assert(sizeof(AdamTable<kFew>) <= 4000 && sizeof(AdamTable<kMany>) <= 32000, "kernel parameter space");
+
+// Launches of at most kMany tensors and less than 2^31 blocks each.
+template <typename PT, typename GT, bool kSmall>
+int step_all(const moe_adamw_args &a, cudaStream_t st) {
+  for (int from = 0; from < a.n_tensors;) {
+    int to = from;
+    int64_t blocks = 0;
+    while (to < a.n_tensors && to - from < kMany) {
+      const int64_t more = ceil_div(a.tensors[to].n, kChunk);
+      if (to > from && blocks + more > 0x7fffffffLL) break;
+      blocks += more;
+      ++to;
+    }
+    const int rc = to - from <= kFew ? launch_some<PT, GT, kSmall, kFew>(a, from, to, st)
+                                     : launch_some<PT, GT, kSmall, kMany>(a, from, to, st);
+    if (rc != MOE_OK) return rc;
+    from = to;
+  }
+  return MOE_OK;
+}
+
+template <typename PT, typename GT>
+int step_bits(const moe_adamw_args &a, cudaStream_t st) {
+  return a.state_bits == 8 ? step_all<PT, GT, true>(a, st) : step_all<PT, GT, false>(a, st);
+}
+
+template <typename PT>
+int step_grad(const moe_adamw_args &a, cudaStream_t st) {
+  return a.g_dtype == MOE_F32 ? step_bits<PT, float>(a, st) : step_bits<PT, uint16_t>(a, st);
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" int moe_adamw_step(const moe_adamw_args *a, cudaStream_t stream) {
+  if (!a || a->struct_size != sizeof(moe_adamw_args) || a->n_tensors < 0) return MOE_ERR_INVALID_ARG;
+  if ((a->p_dtype != MOE_BF16 && a->p_dtype != MOE_F32) || (a->g_dtype != MOE_BF16 && a->g_dtype != MOE_F32))
+    return MOE_ERR_INVALID_ARG;
+  if ((a->state_bits != 32 && a->state_bits != 8) || a->step < 1) return MOE_ERR_INVALID_ARG;
+  if (!(a->beta1 >= 0 && a->beta1 < 1 && a->beta2 >= 0 && a->beta2 < 1 && a->eps >= 0) || !std::isfinite(a->eps) ||
+      !std::isfinite(a->lr) || !std::isfinite(a->weight_decay))
+    return MOE_ERR_INVALID_ARG;
+  if (a->n_tensors == 0) return MOE_OK;
+  if (!a->tensors) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a->grad_scale, 4)) return MOE_ERR_MISALIGNED;
+  for (int i = 0; i < a->n_tensors; ++i) {
+    const moe_adamw_tensor &t = a->tensors[i];
+    if (t.n < 0) return MOE_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (ceil_div(t.n, kChunk) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!t.p || !t.g || !t.m || !t.v || (a->state_bits == 8 && (!t.m_scale || !t.v_scale)) ||
+        (t.copy && a->p_dtype == MOE_BF16))
+      return MOE_ERR_INVALID_ARG;
+    if (!aligned(t.p, 16) || !aligned(t.g, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) || !aligned(t.copy, 16))
+      return MOE_ERR_MISALIGNED;
+  }
+  return a->p_dtype == MOE_F32 ? step_grad<float>(*a, stream) : step_grad<uint16_t>(*a, stream);
+}

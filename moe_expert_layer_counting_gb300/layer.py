@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import contextlib
 
+import numpy as np
 import torch
 
 from . import binding as B
@@ -178,3 +179,54 @@ class BlockNorm:
         B.moe_norm_backward(y, b, gate, w_post, None if dn is None else self.w_pre, dy, dn, ws, residual_scale=s,
                             weight_offset=o, eps=e, gate_sigmoid=sig, stream=stream, **out)
         return out
+
+
+class AdamW:
+    """AdamW over a list of tensors, all updated by one call (include/moe_adamw.h).
+
+    params: contiguous, all bf16 or all float32.  copies: a bf16 copy of each float32 parameter, written by every step
+    (what the next forward pass reads).  state_bits 32: float32 states m, v; 8: E4M3 codes m, v (of sqrt v) with one
+    UE8M0 byte per 32 values, m_scale, v_scale.  step and state resume a run: the steps taken so far and the lists
+    (m, v) or (m, v, m_scale, v_scale) as an earlier object's ``state``; they are used in place.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
+                 state_bits: int = 32, copies=None, step: int = 0, state=None):
+        self.params, self.copies = list(params), None if copies is None else list(copies)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.steps = state_bits, step
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits is 32 or 8")
+        kinds = {p.dtype for p in self.params}
+        if len(kinds) > 1 or not kinds <= set(B._DTYPES):
+            raise ValueError("parameters are all bf16 or all float32")
+        self.p_dtype = B._DTYPES[kinds.pop()] if kinds else B.F32
+        if state is None:
+            kind = torch.float32 if state_bits == 32 else torch.uint8
+            m, v = ([torch.zeros(p.numel(), dtype=kind, device=p.device) for p in self.params] for _ in range(2))
+            scales = ([torch.zeros(-(-p.numel() // 32), dtype=torch.uint8, device=p.device) for p in self.params]
+                      for _ in range(2)) if state_bits == 8 else (None, None)
+            state = (m, v, *scales)
+        names = ("m", "v", "m_scale", "v_scale") if state_bits == 8 else ("m", "v")
+        self.state = {k: list(s) for k, s in zip(names, state)}
+        self.table = np.zeros(len(self.params), B.ADAMW_TENSOR)
+        self.table["n"] = self.sizes = [p.numel() for p in self.params]
+        for name, tensors in (("p", self.params), *self.state.items(), ("copy", self.copies)):
+            if tensors is None:
+                continue
+            want = {"p": None, "copy": torch.bfloat16}.get(name, torch.float32 if state_bits == 32 else torch.uint8)
+            sizes = [-(-n // 32) for n in self.sizes] if name.endswith("scale") else self.sizes
+            if [t.numel() for t in tensors] != sizes or not all(t.is_contiguous() and want in (None, t.dtype) for t in tensors):
+                raise ValueError(f"{name}: sizes, types or strides do not fit the parameters")
+            self.table[name] = [t.data_ptr() for t in tensors]
+
+    def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
+        """One step with these gradients (contiguous, all bf16 or all float32), each times grad_scale (a device float)."""
+        kind = grads[0].dtype if grads else torch.float32
+        if [g.numel() for g in grads] != self.sizes or kind not in B._DTYPES or \
+                not all(g.dtype == kind and g.is_contiguous() for g in grads):
+            raise ValueError("gradients: sizes, types or strides do not fit the parameters")
+        self.table["g"] = [g.data_ptr() for g in grads]
+        B.moe_adamw_step(self.table, self.p_dtype, B._DTYPES[kind], self.state_bits, self.lr, *self.betas, self.eps,
+                         self.weight_decay, self.steps + 1, grad_scale, stream=stream)
+        self.steps += 1
