@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -45,6 +46,7 @@ SCHEDULE_DEFAULT, SCHEDULE_SEPARATE, SCHEDULE_EXPERT_WAVES = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID, ROUTE_RAW, ROUTE_NO_RENORM = 0, 1, 2, 4
 BFP8_LAYOUT_CANONICAL, BFP8_LAYOUT_TILED = 0, 1
 BF16, F32 = 0, 1                                         # enum moe_dtype
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
 
 EXPORTED = ["mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_route_topk_ex",
@@ -145,11 +147,11 @@ lib.moe_grouped_workspace_size.restype = _sz
 lib.moe_grouped_forward.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _sz, _p]
 lib.moe_grouped_dgrad.argtypes = lib.moe_grouped_forward.argtypes
 lib.moe_grouped_wgrad.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _p, _i32, _i32, _p, _sz, _p]
-lib.moe_norm_forward.argtypes = [ctypes.POINTER(MoeNormArgs), _p]
+lib.moe_norm_forward.argtypes = [_p, _p]                # packed structures (below) or byref of the ctypes ones
 lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
 lib.moe_norm_workspace_size.restype = _sz
-lib.moe_norm_backward.argtypes = [ctypes.POINTER(MoeNormArgs), ctypes.POINTER(MoeNormGrads), _p]
-lib.moe_adamw_step.argtypes = [ctypes.POINTER(MoeAdamwArgs), _p]
+lib.moe_norm_backward.argtypes = [_p, _p, _p]
+lib.moe_adamw_step.argtypes = [_p, _p]
 lib.moe_get_device_status.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_int)]
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
@@ -182,9 +184,10 @@ def _ptr(t):
 
 
 def _stream(stream):
+    """The stream's handle; None: the current stream (asked for without making a torch.cuda.Stream, which costs 3 us)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(rc: int, where: str):
@@ -358,21 +361,25 @@ def _invalid(where: str, check: bool) -> int:
     return MOE_ERR_INVALID_ARG
 
 
-def _is_rows(t: torch.Tensor, rows: int, cols: int, dtype=torch.bfloat16) -> bool:
-    """A [rows, cols] tensor whose rows are contiguous (any row stride)."""
-    return t.dtype == dtype and t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1)
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t: torch.Tensor, shape: tuple, dtype=torch.bfloat16):
+    """(pointer, row stride) of a tensor of this shape and type whose rows are contiguous; None if it is not."""
+    if t.dtype is not dtype or t.shape != shape:
+        return None
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    return (t.data_ptr(), t.stride(0)) if t.stride(1) == 1 else None
 
 
 def _is_offsets(t: torch.Tensor, E: int) -> bool:
-    return t.dtype == torch.int32 and t.shape == (E + 1,) and t.is_contiguous()
+    return t.dtype is torch.int32 and t.shape == (E + 1,) and t.is_contiguous()
 
 
 def moe_grouped_workspace_size(P: int, N: int, K: int, E: int) -> int:
     return int(lib.moe_grouped_workspace_size(P, N, K, E))
+
+
+def _is_weight(t: torch.Tensor) -> bool:
+    return t.dtype is torch.bfloat16 and t.is_contiguous()
 
 
 def moe_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor,
@@ -380,11 +387,11 @@ def moe_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     """y [P, N] = x [P, K] @ w[e] [N, K]^T for the rows offsets[e] .. offsets[e+1] of expert e (all bf16)."""
     E, N, K = w.shape
     P = x.shape[0]
-    if not (_is_rows(x, P, K) and _is_rows(y, P, N) and w.dtype == torch.bfloat16 and w.is_contiguous()
-            and _is_offsets(offsets, E)):
+    xr, yr = _rows(x, (P, K)), _rows(y, (P, N))
+    if xr is None or yr is None or not _is_weight(w) or not _is_offsets(offsets, E):
         return _invalid("moe_grouped_forward", check)
-    rc = lib.moe_grouped_forward(x.data_ptr(), _row_stride(x), w.data_ptr(), offsets.data_ptr(), P, N, K, E,
-                                 y.data_ptr(), _row_stride(y), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    rc = lib.moe_grouped_forward(*xr, w.data_ptr(), offsets.data_ptr(), P, N, K, E, *yr, workspace.data_ptr(),
+                                 workspace.nbytes, _stream(stream))
     if check:
         _check(rc, "moe_grouped_forward")
     return rc
@@ -395,11 +402,11 @@ def moe_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, 
     """dx [P, K] = dy [P, N] @ w[e] [N, K] for the rows offsets[e] .. offsets[e+1] of expert e (all bf16)."""
     E, N, K = w.shape
     P = dy.shape[0]
-    if not (_is_rows(dy, P, N) and _is_rows(dx, P, K) and w.dtype == torch.bfloat16 and w.is_contiguous()
-            and _is_offsets(offsets, E)):
+    yr, xr = _rows(dy, (P, N)), _rows(dx, (P, K))
+    if xr is None or yr is None or not _is_weight(w) or not _is_offsets(offsets, E):
         return _invalid("moe_grouped_dgrad", check)
-    rc = lib.moe_grouped_dgrad(dy.data_ptr(), _row_stride(dy), w.data_ptr(), offsets.data_ptr(), P, N, K, E,
-                               dx.data_ptr(), _row_stride(dx), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    rc = lib.moe_grouped_dgrad(*yr, w.data_ptr(), offsets.data_ptr(), P, N, K, E, *xr, workspace.data_ptr(),
+                               workspace.nbytes, _stream(stream))
     if check:
         _check(rc, "moe_grouped_dgrad")
     return rc
@@ -410,11 +417,10 @@ def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
     """dw [E, N, K] (bf16 or float32) = dy[rows of e]^T @ x[rows of e]; accumulate adds to a float32 dw."""
     E, N, K = dw.shape
     P = dy.shape[0]
-    if not (_is_rows(dy, P, N) and _is_rows(x, P, K) and dw.dtype in (torch.bfloat16, torch.float32)
-            and dw.is_contiguous() and _is_offsets(offsets, E)):
+    yr, xr, kind = _rows(dy, (P, N)), _rows(x, (P, K)), _DTYPES.get(dw.dtype)
+    if xr is None or yr is None or kind is None or not dw.is_contiguous() or not _is_offsets(offsets, E):
         return _invalid("moe_grouped_wgrad", check)
-    rc = lib.moe_grouped_wgrad(dy.data_ptr(), _row_stride(dy), x.data_ptr(), _row_stride(x), offsets.data_ptr(), P, N, K,
-                               E, dw.data_ptr(), F32 if dw.dtype == torch.float32 else BF16, 1 if accumulate else 0,
+    rc = lib.moe_grouped_wgrad(*yr, *xr, offsets.data_ptr(), P, N, K, E, dw.data_ptr(), kind, 1 if accumulate else 0,
                                workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if check:
         _check(rc, "moe_grouped_wgrad")
@@ -423,50 +429,48 @@ def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
 
 # ---------------------------------------------------------------- norms around the layer (include/moe_norm.h)
 
-_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+# MoeNormArgs, MoeNormGrads and MoeAdamwArgs as bytes: packing costs a fifth of filling a ctypes structure
+_NORM_ARGS = struct.Struct("@I5i3fqqPqPqPqPPPqPq")
+_NORM_GRADS = struct.Struct("@IPqPqPqPqPqPPPN")
+_ADAMW_ARGS = struct.Struct("@IiPiiiP5dq")
+assert (_NORM_ARGS.size, _NORM_GRADS.size, _ADAMW_ARGS.size) == tuple(
+    ctypes.sizeof(c) for c in (MoeNormArgs, MoeNormGrads, MoeAdamwArgs))
+_NONE = (0, 0)
 
 
 def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid):
-    """MoeNormArgs of these tensors, or None if a type, shape or stride does not fit."""
-    T, H = x.shape
+    """The bytes of MoeNormArgs for these tensors, or None if a type, shape or stride does not fit."""
+    shape = T, H = x.shape
     xt = _DTYPES.get(x.dtype)
-    if xt is None or not _is_rows(x, T, H, x.dtype):
+    xr = _rows(x, shape, x.dtype)
+    br = _NONE if b is None else _rows(b, shape)
+    yr = _NONE if y is None else _rows(y, shape, x.dtype)
+    nr = _NONE if n is None else _rows(n, shape)
+    if xt is None or xr is None or br is None or yr is None or nr is None:
         return None
-    if b is not None and not _is_rows(b, T, H):
-        return None
-    if y is not None and not _is_rows(y, T, H, x.dtype):
-        return None
-    if n is not None and not _is_rows(n, T, H):
-        return None
-    w = w_pre if w_pre is not None else w_post
-    wt = BF16 if w is None else _DTYPES.get(w.dtype)
-    for t in (w_post, w_pre):
-        if t is not None and (wt is None or t.dtype != w.dtype or t.shape != (H,) or not t.is_contiguous()):
+    wt, post, pre = BF16, 0, 0
+    if w_pre is not None:
+        wt, pre = _DTYPES.get(w_pre.dtype), w_pre.data_ptr()
+        if wt is None or w_pre.shape != (H,) or not w_pre.is_contiguous():
             return None
-    kind, gt, ld_gate = GATE_NONE, BF16, H
+    if w_post is not None:
+        wt, post = _DTYPES.get(w_post.dtype), w_post.data_ptr()
+        if wt is None or w_post.shape != (H,) or not w_post.is_contiguous() or (w_pre is not None and w_pre.dtype is not w_post.dtype):
+            return None
+    kind, gt, gr = GATE_NONE, BF16, _NONE
     if gate is not None:
-        gt = _DTYPES.get(gate.dtype)
-        if gt is None or gate.dim() != 2:
+        gt, gs = _DTYPES.get(gate.dtype), gate.shape
+        if gt is None or len(gs) != 2:
             return None
-        if gate.shape == (T, 1) and H != 1:
-            kind = GATE_TOKEN
-            if not gate.is_contiguous():
-                return None
-        elif gate.shape == (1, H):
-            kind = GATE_CHANNEL
-            if H > 1 and gate.stride(1) != 1:
-                return None
-        elif _is_rows(gate, T, H, gate.dtype):
-            kind, ld_gate = GATE_FULL, _row_stride(gate)
+        kind = GATE_TOKEN if gs == (T, 1) else GATE_CHANNEL if gs == (1, H) else GATE_FULL
+        if kind != GATE_FULL:
+            gr = (gate.data_ptr(), 0) if gate.is_contiguous() else None
         else:
+            gr = _rows(gate, shape, gate.dtype)
+        if gr is None:
             return None
-    return MoeNormArgs(ctypes.sizeof(MoeNormArgs), xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale,
-                       weight_offset, eps, T, H, x.data_ptr(), _row_stride(x),
-                       None if b is None else b.data_ptr(), H if b is None else _row_stride(b),
-                       None if gate is None else gate.data_ptr(), ld_gate,
-                       None if w_post is None else w_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
-                       None if y is None else y.data_ptr(), H if y is None else _row_stride(y),
-                       None if n is None else n.data_ptr(), H if n is None else _row_stride(n))
+    return _NORM_ARGS.pack(_NORM_ARGS.size, xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale, weight_offset, eps,
+                           T, H, *xr, *br, *gr, post, pre, *yr, *nr)
 
 
 def moe_norm_forward(x, b, gate, w_post, w_pre, y, n, residual_scale: float = 1.0, weight_offset: float = 0.0,
@@ -476,7 +480,7 @@ def moe_norm_forward(x, b, gate, w_post, w_pre, y, n, residual_scale: float = 1.
     a = _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid)
     if a is None:
         return _invalid("moe_norm_forward", check)
-    rc = lib.moe_norm_forward(ctypes.byref(a), _stream(stream))
+    rc = lib.moe_norm_forward(a, _stream(stream))
     if check:
         _check(rc, "moe_norm_forward")
     return rc
@@ -492,25 +496,23 @@ def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=
     """Gradients of moe_norm_forward from dy and dn; y is its y (without b: its x).  Outputs that are None are not
     computed; dgate has the gate's shape and type, dw_post and dw_pre are float32 [H]."""
     a = _norm_args(y, b, gate, w_post, w_pre, None, None, residual_scale, weight_offset, eps, gate_sigmoid)
-    T, H = y.shape
-    ok = a is not None
-    for t, dtype in ((dy, y.dtype), (dx, y.dtype), (dn, torch.bfloat16), (db, torch.bfloat16)):
-        ok = ok and (t is None or _is_rows(t, T, H, dtype))
-    for t in (dw_post, dw_pre):
-        ok = ok and (t is None or (t.dtype == torch.float32 and t.shape == (H,) and t.is_contiguous()))
+    shape = y.shape
+    rows = [_NONE if t is None else _rows(t, shape, dtype) for t, dtype in
+            ((dy, y.dtype), (dn, torch.bfloat16), (dx, y.dtype), (db, torch.bfloat16))]
     if dgate is not None:
-        ok = ok and gate is not None and dgate.dtype == gate.dtype and dgate.shape == gate.shape and \
-            (dgate.is_contiguous() or (a.gate_kind == GATE_FULL and dgate.stride(1) == 1))
-    if not ok:
+        if gate is None or dgate.dtype is not gate.dtype or dgate.shape != gate.shape:
+            return _invalid("moe_norm_backward", check)
+        rows.append(_rows(dgate, shape, dgate.dtype) if dgate.shape == shape else
+                    (dgate.data_ptr(), 0) if dgate.is_contiguous() else None)
+    else:
+        rows.append(_NONE)
+    sums = [0 if t is None else t.data_ptr() if t.dtype is torch.float32 and t.shape == shape[1:] and t.is_contiguous() else None
+            for t in (dw_post, dw_pre)]
+    if a is None or None in rows or None in sums:
         return _invalid("moe_norm_backward", check)
-
-    def rows(t):
-        return (None, H) if t is None else (t.data_ptr(), _row_stride(t))
-
-    g = MoeNormGrads(ctypes.sizeof(MoeNormGrads), *rows(dy), *rows(dn), *rows(dx), *rows(db), *rows(dgate),
-                     None if dw_post is None else dw_post.data_ptr(), None if dw_pre is None else dw_pre.data_ptr(),
-                     workspace.data_ptr(), workspace.nbytes)
-    rc = lib.moe_norm_backward(ctypes.byref(a), ctypes.byref(g), _stream(stream))
+    g = _NORM_GRADS.pack(_NORM_GRADS.size, *rows[0], *rows[1], *rows[2], *rows[3], *rows[4], *sums, workspace.data_ptr(),
+                         workspace.nbytes)
+    rc = lib.moe_norm_backward(a, g, _stream(stream))
     if check:
         _check(rc, "moe_norm_backward")
     return rc
@@ -525,9 +527,9 @@ def moe_adamw_step(table: np.ndarray, p_dtype: int, g_dtype: int, state_bits: in
     if table.dtype != ADAMW_TENSOR or not table.flags.c_contiguous or \
             (grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1)):
         return _invalid("moe_adamw_step", check)
-    a = MoeAdamwArgs(ctypes.sizeof(MoeAdamwArgs), table.size, table.ctypes.data, p_dtype, g_dtype, state_bits,
-                     None if grad_scale is None else grad_scale.data_ptr(), lr, beta1, beta2, eps, weight_decay, step)
-    rc = lib.moe_adamw_step(ctypes.byref(a), _stream(stream))
+    a = _ADAMW_ARGS.pack(_ADAMW_ARGS.size, table.size, table.ctypes.data, p_dtype, g_dtype, state_bits,
+                         0 if grad_scale is None else grad_scale.data_ptr(), lr, beta1, beta2, eps, weight_decay, step)
+    rc = lib.moe_adamw_step(a, _stream(stream))
     if check:
         _check(rc, "moe_adamw_step")
     return rc

@@ -156,8 +156,10 @@ class BlockNorm:
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
         """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
         with _on(stream):
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if b is not None else None
-            n = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if self.w_pre is not None else None
+            y = torch.empty_like(x, memory_format=torch.contiguous_format) if b is not None else None
+            n = None
+            if self.w_pre is not None:
+                n = torch.empty_like(x if b is None else b, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
         B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, stream=stream)
         return (x if y is None else y), n
 
@@ -166,15 +168,16 @@ class BlockNorm:
         """Gradients dx, db, dgate, dw_post, dw_pre (None where there is nothing to differentiate) from those of
         forward's y and n (either may be None); y, b and gate are what forward returned and took."""
         T, H = y.shape
-        dev = y.device
         w_post = self.w_post if b is not None else None
         with _on(stream):
-            out = {"dx": torch.empty(T, H, dtype=y.dtype, device=dev),
-                   "db": None if b is None else torch.empty(T, H, dtype=torch.bfloat16, device=dev),
-                   "dgate": None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dev),
-                   "dw_post": None if w_post is None else torch.empty(H, dtype=torch.float32, device=dev),
-                   "dw_pre": None if dn is None else torch.empty(H, dtype=torch.float32, device=dev)}
-            ws = torch.empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8, device=dev)
+            new = torch.empty_like
+            flat = torch.contiguous_format
+            out = {"dx": new(y, memory_format=flat),
+                   "db": None if b is None else new(b, memory_format=flat),
+                   "dgate": None if gate is None else new(gate, memory_format=flat),
+                   "dw_post": None if w_post is None else new(w_post, dtype=torch.float32),
+                   "dw_pre": None if dn is None else new(self.w_pre, dtype=torch.float32)}
+            ws = y.new_empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8)
         s, o, e, sig = self.how
         B.moe_norm_backward(y, b, gate, w_post, None if dn is None else self.w_pre, dy, dn, ws, residual_scale=s,
                             weight_offset=o, eps=e, gate_sigmoid=sig, stream=stream, **out)
@@ -223,8 +226,8 @@ class AdamW:
     def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
         """One step with these gradients (contiguous, all bf16 or all float32), each times grad_scale (a device float)."""
         kind = grads[0].dtype if grads else torch.float32
-        if [g.numel() for g in grads] != self.sizes or kind not in B._DTYPES or \
-                not all(g.dtype == kind and g.is_contiguous() for g in grads):
+        flat = [g.dtype is kind and g.is_contiguous() for g in grads]
+        if kind not in B._DTYPES or not all(flat) or [g.numel() for g in grads] != self.sizes:
             raise ValueError("gradients: sizes, types or strides do not fit the parameters")
         self.table["g"] = [g.data_ptr() for g in grads]
         B.moe_adamw_step(self.table, self.p_dtype, B._DTYPES[kind], self.state_bits, self.lr, *self.betas, self.eps,
