@@ -21,8 +21,8 @@
 //
 // Roles per CTA (384 threads): warp 0 loads (TMA), warp 1 of the leader issues
 // the MMAs, warp 2 allocates TMEM and zeroes ragged ends, warps 4-11 drain the
-// accumulators (two per TMEM lane quadrant, each with a 2 KB staging tile of
-// its own, so that the stores are 64-byte row pieces).  Two accumulators
+// accumulators (two per TMEM lane quadrant, each with staging of its own: row
+// pieces of 64 bytes, wgrad boxes of 32 rows x 128 bytes for TMA).  Two accumulators
 // alternate, so an item's drain overlaps the next item's MMAs.  Every wait is
 // bounded (see moe_get_device_status).
 #include <cuda_bf16.h>
@@ -46,33 +46,41 @@ struct GP {
   static constexpr int kM = 256;                       // M of a pair's MMA (128 per CTA)
   static constexpr int kN = 256;                       // most N slots of an item
   static constexpr int kBK = 64;                       // reduction values per stage (128 bytes of BF16)
-  static constexpr int kStages = 6;
   static constexpr int kATile = 128 * kBK * 2;
   static constexpr int kBTile = (kN / 2) * kBK * 2;
   static constexpr int kHalfBox = 64 * kBK * 2;        // a 64 x 64 box (M- / N-major operands)
   static constexpr int kFirstEpiWarp = 4;
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
-  static constexpr int kStageTile = 2048;              // staging per epilogue warp
+  static constexpr int kMaxStages = 6;
+  static constexpr int kNumBars = 4 * kMaxStages + 6;
+};
+
+// Shared memory of one direction.  wgrad stages its output for TMA stores
+// (4 KB boxes, two per epilogue warp), forward / dgrad 2 KB per warp.
+template <int OP>
+struct Layout {
+  static constexpr int kStages = OP == kWgrad ? 4 : 6;
+  static constexpr int kEpiBytes = OP == kWgrad ? 8192 : 2048;   // per epilogue warp
   static constexpr int kOffA = 0;
-  static constexpr int kOffB = kOffA + kStages * kATile;
-  static constexpr int kOffEpi = kOffB + kStages * kBTile;
-  static constexpr int kOffBar = kOffEpi + kEpiWarps * kStageTile;
-  // full, empty, tail_full, tail_fixed [kStages] each, tmem_full[2], tmem_empty[2], mma_done, never
-  static constexpr int kNumBars = 4 * kStages + 6;
-  static constexpr int kOffTmemPtr = (kOffBar + 8 * kNumBars + 63) & ~63;
-  static constexpr int kOffTab = kOffTmemPtr + 64;     // off[E+1], tile_off[E+1]
+  static constexpr int kOffB = kOffA + kStages * GP::kATile;
+  static constexpr int kOffEpi = kOffB + kStages * GP::kBTile;
+  static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
+  static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
+  static constexpr int kOffTab = kOffTmemPtr + 64;     // off[E+1], forward / dgrad also tile_off[E+1]
+  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (size_t)(OP == kWgrad ? 4 : 8) * (E + 1); }
 };
 
 constexpr long long kLimit = 2000000000LL;              // ~1 s
 constexpr long long kInjectedLimit = 20000000LL;        // ~10 ms: the debug wait's budget
 constexpr int kMaxExperts = 1024;
-constexpr size_t kSmemMax = 1024 + GP::kOffTab + 8 * (kMaxExperts + 1);
-static_assert(kSmemMax <= 232448, "shared memory of one CTA");
+static_assert(Layout<kForward>::bytes(kMaxExperts) <= 232448 && Layout<kWgrad>::bytes(kMaxExperts) <= 232448,
+              "shared memory of one CTA");
 
 struct GMaps {
   CUtensorMap a;        // w (3-D) or dy
-  CUtensorMap b[4];     // row operand with boxes of 16, 32, 64, 128 rows; wgrad: b[0] = x, 64 x 64 boxes
+  CUtensorMap b[4];     // row operand with boxes of 16, 32, 64, 128 rows; wgrad: b[0] = x in 64 x 64 boxes,
+                        // b[1] = dw in boxes of 32 rows x 128 bytes
 };
 
 struct GArgs {
@@ -157,77 +165,75 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int c0, int 
   __syncwarp();
 }
 
-// wgrad: 32 columns of this warp's 32 rows of dw (TMEM lanes are rows).
-__device__ __forceinline__ void store_block(const uint32_t (&v)[32], int c0, int row0, const GItem &it, const GArgs &g,
-                                            int lane, uint4 *stage) {
-  const int64_t base = (int64_t)it.e * g.M;
-  const int swz = (lane >> 1) & 3;                // 16-byte pieces of a 64-byte row, spread over the banks
-  const int r_out = lane >> 2, p_out = lane & 3;
-  if (!g.f32) {
-    uint16_t *out = reinterpret_cast<uint16_t *>(g.out);
+// wgrad: this warp's 32 rows (TMEM lanes) x 128 columns of dw, in boxes of 32
+// rows x 128 bytes (64 BF16 or 32 float32 columns), each written to one of two
+// swizzled staging buffers and stored by TMA, which leaves out what lies
+// outside dw.  `none`: no rows, zeros.
+template <bool kF32>
+__device__ __forceinline__ void store_block(uint32_t t_row, bool none, int row0, int col0, const GItem &it, const GArgs &g,
+                                            const CUtensorMap *map, int lane, unsigned char *stage, int &turn) {
+  constexpr int kCols = kF32 ? 32 : 64;
+#pragma unroll 2
+  for (int i = 0; i < 128 / kCols; ++i) {
+    const int c0 = i * kCols;
+    if (col0 + c0 >= g.C) break;
+    unsigned char *buf = stage + turn * 4096;
+    turn ^= 1;
+    uint4 piece[8];
+    if (none) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint32_t w[4];
+      for (int p = 0; p < 8; ++p) piece[p] = make_uint4(0, 0, 0, 0);
+    } else {
+      uint32_t v[kCols];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = pack_bf16(__uint_as_float(v[8 * p + 2 * i]), __uint_as_float(v[8 * p + 2 * i + 1]));
-      stage[lane * 4 + (p ^ swz)] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-    const int col = c0 + 8 * p_out;
+      for (int h = 0; h < kCols / 32; ++h) tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+      tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + r_out;
-      const uint4 piece = stage[r * 4 + (p_out ^ ((r >> 1) & 3))];
-      if (row0 + r < g.M && col < g.C) *reinterpret_cast<uint4 *>(out + (base + row0 + r) * g.C + col) = piece;
-    }
-    __syncwarp();
-  } else {
-    float *out = reinterpret_cast<float *>(g.out);
+      for (int p = 0; p < 8; ++p) {
+        if (kF32) {
+          piece[p] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+        } else {
+          uint32_t w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        stage[lane * 4 + (p ^ swz)] = make_uint4(v[16 * h + 4 * p], v[16 * h + 4 * p + 1], v[16 * h + 4 * p + 2],
-                                                 v[16 * h + 4 * p + 3]);
-      __syncwarp();
-      const int col = c0 + 16 * h + 4 * p_out;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + r_out;
-        const uint4 piece = stage[r * 4 + (p_out ^ ((r >> 1) & 3))];
-        if (row0 + r < g.M && col < g.C) {
-          float4 f = make_float4(__uint_as_float(piece.x), __uint_as_float(piece.y), __uint_as_float(piece.z),
-                                 __uint_as_float(piece.w));
-          float4 *dst = reinterpret_cast<float4 *>(out + (base + row0 + r) * g.C + col);
-          if (g.accumulate) {
-            const float4 o = *dst;
-            f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
-          }
-          *dst = f;
+          for (int j = 0; j < 4; ++j)
+            w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
+          piece[p] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_read<1>();               // the store that last used this buffer has read it
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4 *>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = piece[p];
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (kF32 && g.accumulate)
+        tma_add_3d(map, buf, col0 + c0, row0, it.e);
+      else
+        tma_store_3d(map, buf, col0 + c0, row0, it.e);
+      bulk_commit();
     }
   }
 }
 
 template <int OP>
 __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_constant__ GMaps maps, const GArgs g) {
+  using L = Layout<OP>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + GP::kOffBar);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   uint64_t *full = bars;                               // leader: both CTAs' copies of a stage
-  uint64_t *empty = full + GP::kStages;                // each CTA: stage consumed
-  uint64_t *tail_full = empty + GP::kStages;           // each CTA: its own copies of a ragged block
-  uint64_t *tail_fixed = tail_full + GP::kStages;      // leader: both CTAs zeroed the block's end
-  uint64_t *tmem_full = tail_fixed + GP::kStages;      // each CTA: accumulator ready
+  uint64_t *empty = full + L::kStages;                // each CTA: stage consumed
+  uint64_t *tail_full = empty + L::kStages;           // each CTA: its own copies of a ragged block
+  uint64_t *tail_fixed = tail_full + L::kStages;      // leader: both CTAs zeroed the block's end
+  uint64_t *tmem_full = tail_fixed + L::kStages;      // each CTA: accumulator ready
   uint64_t *tmem_empty = tmem_full + 2;                // leader: both CTAs drained the accumulator
   uint64_t *mma_done = tmem_empty + 2;
   uint64_t *never = mma_done + 1;
-  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + GP::kOffTmemPtr);
-  int *off = reinterpret_cast<int *>(smem + GP::kOffTab);
+  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
+  int *off = reinterpret_cast<int *>(smem + L::kOffTab);
   int *tile_off = off + g.E + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -238,11 +244,11 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&maps.a);
-      for (int i = 0; i < (OP == kWgrad ? 1 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
+      for (int i = 0; i < (OP == kWgrad ? 2 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
     }
   } else if (warp == 2) {
     if (lane == 0) {
-      for (int s = 0; s < GP::kStages; ++s) {
+      for (int s = 0; s < L::kStages; ++s) {
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], 1);
         mbar_init(&tail_full[s], 1);
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         const bool tail = OP == kWgrad && kb == it.kb - 1 && (it.rows & 15) != 0;
         if (lane == 0) {
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-          unsigned char *a = smem + GP::kOffA + stage * GP::kATile, *b = smem + GP::kOffB + stage * GP::kBTile;
+          unsigned char *a = smem + L::kOffA + stage * GP::kATile, *b = smem + L::kOffB + stage * GP::kBTile;
           if (tail) {
             // the ragged block: onto this CTA's own barrier, for warp 2
             if (rank == 0) mbar_arrive(&full[stage]);
@@ -361,12 +367,12 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           tails |= 1u << stage;
           tail_phase ^= 1u << stage;               // parity of the next use of tail_full[stage]
         }
-        if (++stage == GP::kStages) { stage = 0; phase ^= 1; }
+        if (++stage == L::kStages) { stage = 0; phase ^= 1; }
       }
     }
     // no CTA leaves with copies in flight: the leader waits for both CTAs'
     // copies (the final cluster barrier holds the other until then)
-    for (int s = 0; s < GP::kStages; ++s) {
+    for (int s = 0; s < L::kStages; ++s) {
       if (rank == 0 && (issued & (1u << s)))
         mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
       if (tails & (1u << s))
@@ -414,8 +420,8 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
             break;
           }
           if (elect_one()) {
-            const uint32_t a = smem_u32(smem + GP::kOffA + stage * GP::kATile);
-            const uint32_t b = smem_u32(smem + GP::kOffB + stage * GP::kBTile);
+            const uint32_t a = smem_u32(smem + L::kOffA + stage * GP::kATile);
+            const uint32_t b = smem_u32(smem + L::kOffB + stage * GP::kBTile);
             const int steps = left >= GP::kBK ? 4 : (left + 15) >> 4;
             for (int kk = 0; kk < steps; ++kk) {
               // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
             tc_commit_2sm(&empty[stage], 3);
           }
           __syncwarp();
-          if (++stage == GP::kStages) { stage = 0; phase ^= 1; }
+          if (++stage == L::kStages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
         if (elect_one()) tc_commit_2sm(&tmem_full[acc], 3);
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       for (int w = cluster; w < total; w += nclusters) {
         const GItem it = decode_item<OP>(w, g, off, tile_off);
         if (it.kb > 0 && (it.rows & 15) != 0) {
-          const int stage = (block + it.kb - 1) % GP::kStages;
+          const int stage = (block + it.kb - 1) % L::kStages;
           if (!__all_sync(0xffffffffu, mbar_wait_reset(&tail_full[stage], (tail_phase >> stage) & 1u, status, kLimit,
                                                        kWaitMmaFull, w)))
             break;
@@ -457,23 +463,23 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           const int rows = ((rem + 15) & ~15) - rem;             // rows to zero, 128 bytes in each box
           for (int i = lane; i < rows * 32; i += 32) {
             const int box = i / (rows * 8), r = i - box * (rows * 8);
-            unsigned char *p = box < 2 ? smem + GP::kOffA + stage * GP::kATile + box * GP::kHalfBox
-                                       : smem + GP::kOffB + stage * GP::kBTile + (box - 2) * GP::kHalfBox;
+            unsigned char *p = box < 2 ? smem + L::kOffA + stage * GP::kATile + box * GP::kHalfBox
+                                       : smem + L::kOffB + stage * GP::kBTile + (box - 2) * GP::kHalfBox;
             *reinterpret_cast<uint4 *>(p + rem * 128 + r * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_fixed[stage]), 0));
         }
-        block = (block + it.kb) % GP::kStages;
+        block = (block + it.kb) % L::kStages;
       }
     }
   } else if (warp >= GP::kFirstEpiWarp) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;
     const int ew = warp - GP::kFirstEpiWarp;
-    uint32_t *stage_tile = reinterpret_cast<uint32_t *>(smem + GP::kOffEpi + ew * GP::kStageTile);
-    int j = 0;
+    unsigned char *stage_tile = smem + L::kOffEpi + ew * L::kEpiBytes;
+    int j = 0, turn = 0;
     for (int w = cluster; w < total; w += nclusters) {
       const GItem it = decode_item<OP>(w, g, off, tile_off);
       const int first = it.m * GP::kM + (int)rank * 128 + 32 * q;  // this warp's M rows
@@ -490,21 +496,20 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         continue;
       }
       const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN);
-      const int cols = OP == kWgrad ? min(GP::kN, g.C - it.c * GP::kN) : it.rows;
       if (first < g.M) {
-        for (int c0 = 32 * (ew >> 2); c0 < cols; c0 += 64) {
-          uint32_t v[32];
-          if (none) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0;
-          } else {
+        if (OP == kWgrad) {
+          const int c0 = 128 * (ew >> 2);
+          if (g.f32)
+            store_block<true>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile, turn);
+          else
+            store_block<false>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile, turn);
+        } else {
+          for (int c0 = 32 * (ew >> 2); c0 < it.rows; c0 += 64) {
+            uint32_t v[32];
             tmem_ld_32x32b_x32(t_row + (uint32_t)c0, v);
             tmem_ld_wait();
+            store_rows(v, c0, first, it, g, lane, reinterpret_cast<uint32_t *>(stage_tile));
           }
-          if (OP == kWgrad)
-            store_block(v, it.c * GP::kN + c0, first, it, g, lane, reinterpret_cast<uint4 *>(stage_tile));
-          else
-            store_rows(v, c0, first, it, g, lane, stage_tile);
         }
       }
       if (!none) {
@@ -513,6 +518,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
       }
     }
+    if (OP == kWgrad && lane == 0) bulk_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -542,22 +548,21 @@ EncodeFn encoder() {
   return fn;
 }
 
-// A BF16 tensor of rank 2 or 3 (strides in elements, innermost 1) with boxes
+// A BF16 (or float32) tensor of rank 2 or 3 (strides in elements, innermost 1) with boxes
 // of box0 x box1 (x 1), 128-byte swizzled; what lies outside reads as zero.
-bool encode_bf16(CUtensorMap *map, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                 uint64_t s2, uint32_t box0, uint32_t box1) {
+bool encode_map(CUtensorMap *map, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                uint64_t s2, uint32_t box0, uint32_t box1, bool f32 = false) {
   EncodeFn fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {s1 * 2, s2 * 2};
+  const uint64_t size = f32 ? 4 : 2;
+  const cuuint64_t strides[2] = {s1 * size, s2 * size};
   const cuuint32_t box[3] = {box0, box1, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-size_t smem_bytes(int E) { return 1024 + GP::kOffTab + (size_t)8 * (E + 1); }
 
 template <int OP>
 int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaStream_t st) {
@@ -566,7 +571,7 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(grouped_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) !=
+    if (cudaFuncSetAttribute(grouped_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<OP>::bytes(kMaxExperts)) !=
         cudaSuccess)
       return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
@@ -582,7 +587,7 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * clusters));
   cfg.blockDim = dim3(GP::kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(g.E);
+  cfg.dynamicSmemBytes = Layout<OP>::bytes(g.E);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -626,9 +631,9 @@ int rows_product(const uint16_t *in, int64_t ld_in, const uint16_t *w, const int
   if (!w) return MOE_ERR_INVALID_ARG;
   if (!aligned(w, 16)) return MOE_ERR_MISALIGNED;
   GMaps maps;
-  bool ok = OP == kForward ? encode_bf16(&maps.a, w, 3, K, N, E, K, N * K, GP::kBK, 128)
-                           : encode_bf16(&maps.a, w, 3, K, N, E, K, N * K, 64, GP::kBK);
-  for (int i = 0; i < 4; ++i) ok = ok && encode_bf16(&maps.b[i], in, 2, R, P, 1, ld_in, 0, GP::kBK, 16u << i);
+  bool ok = OP == kForward ? encode_map(&maps.a, w, 3, K, N, E, K, N * K, GP::kBK, 128)
+                           : encode_map(&maps.a, w, 3, K, N, E, K, N * K, 64, GP::kBK);
+  for (int i = 0; i < 4; ++i) ok = ok && encode_map(&maps.b[i], in, 2, R, P, 1, ld_in, 0, GP::kBK, 16u << i);
   if (!ok) return MOE_ERR_CUDA;
   GArgs g{};
   g.offsets = offsets;
@@ -684,10 +689,10 @@ extern "C" int moe_grouped_wgrad(const uint16_t *dy, int64_t ldy, const uint16_t
   }
   if ((rc = check_rows(dy, ldy, N)) != MOE_OK || (rc = check_rows(x, ldx, K)) != MOE_OK) return rc;
   GMaps maps;
-  if (!encode_bf16(&maps.a, dy, 2, N, P, 1, ldy, 0, 64, GP::kBK) ||
-      !encode_bf16(&maps.b[0], x, 2, K, P, 1, ldx, 0, 64, GP::kBK))
+  if (!encode_map(&maps.a, dy, 2, N, P, 1, ldy, 0, 64, GP::kBK) ||
+      !encode_map(&maps.b[0], x, 2, K, P, 1, ldx, 0, 64, GP::kBK) ||
+      !encode_map(&maps.b[1], dw, 3, K, N, E, K, N * K, dw_dtype == MOE_F32 ? 32 : 64, 32, dw_dtype == MOE_F32))
     return MOE_ERR_CUDA;
-  for (int i = 1; i < 4; ++i) maps.b[i] = maps.b[0];
   GArgs g{};
   g.offsets = offsets;
   g.P = P;
