@@ -57,18 +57,21 @@ struct GP {
 };
 
 // Shared memory of one direction.  wgrad stages its output for TMA stores
-// (4 KB boxes, two per epilogue warp), forward / dgrad 2 KB per warp.
+// (a 4 KB box per epilogue warp; two would cost a stage, and the loads' latency
+// counts for more: 348 instead of 312 us for 32 experts of 128 rows, N = 4096,
+// K = 7168), forward / dgrad 2 KB per warp; wgrad's items need no table of row
+// tiles, and its offsets are read where they lie.
 template <int OP>
 struct Layout {
-  static constexpr int kStages = OP == kWgrad ? 4 : 6;
-  static constexpr int kEpiBytes = OP == kWgrad ? 8192 : 2048;   // per epilogue warp
+  static constexpr int kStages = 6;
+  static constexpr int kEpiBytes = OP == kWgrad ? 4096 : 2048;   // per epilogue warp
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + kStages * GP::kATile;
   static constexpr int kOffEpi = kOffB + kStages * GP::kBTile;
   static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
-  static constexpr int kOffTab = kOffTmemPtr + 64;     // off[E+1], forward / dgrad also tile_off[E+1]
-  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (size_t)(OP == kWgrad ? 4 : 8) * (E + 1); }
+  static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: off[E+1], tile_off[E+1]
+  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (OP == kWgrad ? 0 : (size_t)8 * (E + 1)); }
 };
 
 constexpr long long kLimit = 2000000000LL;              // ~1 s
@@ -102,37 +105,68 @@ struct GItem {
   uint32_t n_mma;       // N slots of the MMA (a multiple of 32)
 };
 
+// The items w, w + step, ... of one cluster, in order.  wgrad: expert-major,
+// then 256-row tiles, 256-column tiles fastest (so that the items in flight
+// write whole rows of dw), advanced without divisions.
 template <int OP>
-__device__ __forceinline__ GItem decode_item(int w, const GArgs &g, const int *off, const int *tile_off) {
-  GItem it;
-  const int mt = (g.M + GP::kM - 1) / GP::kM;
-  if (OP == kWgrad) {
-    const int ct = (g.C + GP::kN - 1) / GP::kN;
-    it.e = w / (mt * ct);
-    const int r = w - it.e * (mt * ct);
-    it.c = r / mt;
-    it.m = r - it.c * mt;
-    it.row0 = off[it.e];
-    it.rows = off[it.e + 1] - it.row0;
-    it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
-    it.n_mma = (uint32_t)min(GP::kN, (g.C - it.c * GP::kN + 31) & ~31);
-  } else {
-    const int t = w / mt;
-    it.m = w - t * mt;
-    it.c = 0;
-    int lo = 0, hi = g.E;                 // tile_off[lo] <= t < tile_off[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tile_off[mid] <= t) lo = mid; else hi = mid;
+struct Items {
+  const GArgs &g;
+  const int *off, *tile_off;
+  int mt, ct;
+  int w, step, total;
+  int e, m, c;                // wgrad: of w
+  int dm, dc;                 // wgrad: step in (m, c)
+
+  __device__ __forceinline__ Items(const GArgs &g, const int *off, const int *tile_off, int first, int step, int total)
+      : g(g), off(off), tile_off(tile_off), mt((g.M + GP::kM - 1) / GP::kM), ct((g.C + GP::kN - 1) / GP::kN), w(first),
+        step(step), total(total), e(0), m(0), c(0), dm(0), dc(0) {
+    if (OP == kWgrad) {
+      m = w / ct;
+      c = w - m * ct;
+      dm = step / ct;
+      dc = step - dm * ct;
+      e = m / mt;
+      m -= e * mt;
     }
-    it.e = lo;
-    it.row0 = off[lo] + (t - tile_off[lo]) * GP::kN;
-    it.rows = min(GP::kN, off[lo + 1] - it.row0);
-    it.kb = (g.R + GP::kBK - 1) / GP::kBK;
-    it.n_mma = (uint32_t)((it.rows + 31) & ~31);
   }
-  return it;
-}
+  __device__ __forceinline__ bool more() const { return w < total; }
+  __device__ __forceinline__ void next() {
+    w += step;
+    if (OP == kWgrad) {
+      c += dc;
+      m += dm;
+      if (c >= ct) { c -= ct; ++m; }
+      while (m >= mt) { m -= mt; ++e; }
+    }
+  }
+  __device__ __forceinline__ GItem get() const {
+    GItem it;
+    if (OP == kWgrad) {
+      it.e = e;
+      it.m = m;
+      it.c = c;
+      it.row0 = __ldg(off + e);
+      it.rows = __ldg(off + e + 1) - it.row0;
+      it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
+      it.n_mma = (uint32_t)min(GP::kN, (g.C - c * GP::kN + 31) & ~31);
+    } else {
+      const int t = w / mt;
+      it.m = w - t * mt;
+      it.c = 0;
+      int lo = 0, hi = g.E;                 // tile_off[lo] <= t < tile_off[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tile_off[mid] <= t) lo = mid; else hi = mid;
+      }
+      it.e = lo;
+      it.row0 = off[lo] + (t - tile_off[lo]) * GP::kN;
+      it.rows = min(GP::kN, off[lo + 1] - it.row0);
+      it.kb = (g.R + GP::kBK - 1) / GP::kBK;
+      it.n_mma = (uint32_t)((it.rows + 31) & ~31);
+    }
+    return it;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -166,42 +200,40 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int c0, int 
 }
 
 // wgrad: this warp's 32 rows (TMEM lanes) x 128 columns of dw, in boxes of 32
-// rows x 128 bytes (64 BF16 or 32 float32 columns), each written to one of two
-// swizzled staging buffers and stored by TMA, which leaves out what lies
-// outside dw.  `none`: no rows, zeros.
+// rows x 128 bytes (64 BF16 or 32 float32 columns), each written to swizzled
+// staging and stored by TMA, which leaves out what lies outside dw.  `none`: no
+// rows, zeros.
 template <bool kF32>
 __device__ __forceinline__ void store_block(uint32_t t_row, bool none, int row0, int col0, const GItem &it, const GArgs &g,
-                                            const CUtensorMap *map, int lane, unsigned char *stage, int &turn) {
+                                            const CUtensorMap *map, int lane, unsigned char *buf) {
   constexpr int kCols = kF32 ? 32 : 64;
-#pragma unroll 2
-  for (int i = 0; i < 128 / kCols; ++i) {
-    const int c0 = i * kCols;
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += kCols) {
     if (col0 + c0 >= g.C) break;
-    unsigned char *buf = stage + turn * 4096;
-    turn ^= 1;
-    uint4 piece[8];
+    uint32_t v[kCols];
     if (none) {
 #pragma unroll
-      for (int p = 0; p < 8; ++p) piece[p] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kCols; ++i) v[i] = 0;
     } else {
-      uint32_t v[kCols];
 #pragma unroll
-      for (int h = 0; h < kCols / 32; ++h) tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+      for (int h = 0; h < kCols / 32; ++h)
+        tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
       tmem_ld_wait();
+    }
+    uint4 piece[8];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        if (kF32) {
-          piece[p] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-        } else {
-          uint32_t w[4];
+    for (int p = 0; p < 8; ++p) {
+      if (kF32) {
+        piece[p] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+      } else {
+        uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
-          piece[p] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int j = 0; j < 4; ++j)
+          w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
+        piece[p] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    if (lane == 0) bulk_wait_read<1>();               // the store that last used this buffer has read it
+    if (lane == 0) bulk_wait_read<0>();               // the store before has read the staging
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4 *>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = piece[p];
@@ -233,8 +265,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   uint64_t *mma_done = tmem_empty + 2;
   uint64_t *never = mma_done + 1;
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
-  int *off = reinterpret_cast<int *>(smem + L::kOffTab);
-  int *tile_off = off + g.E + 1;
+  int *off_sm = reinterpret_cast<int *>(smem + L::kOffTab);
+  int *tile_off = off_sm + g.E + 1;
+  const int *off = OP == kWgrad ? g.offsets : off_sm;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -277,7 +310,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   for (int e = threadIdx.x; e <= g.E; e += GP::kThreads) {
     const int o = __ldg(g.offsets + e);
     const int before = e > 0 ? __ldg(g.offsets + e - 1) : 0;
-    off[e] = o;
+    if (OP != kWgrad) off_sm[e] = o;
     bad |= o < before || (int64_t)o > g.P;
   }
   bad = __syncthreads_or(bad);
@@ -308,14 +341,15 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   }
   if (bad) total = 0;
   const uint32_t tmem_base = *tmem_ptr;
+  Items<OP> items(g, off, tile_off, cluster, nclusters, total);
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads (both CTAs)
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_phase = 0, tails = 0, tail_phase = 0;
     bool ok = true;
-    for (int w = cluster; w < total && ok; w += nclusters) {
-      const GItem it = decode_item<OP>(w, g, off, tile_off);
+    for (; items.more() && ok; items.next()) {
+      const GItem it = items.get();
       const int half = (int)it.n_mma >> 1;
       const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
       const int boxes = half <= 64 ? 1 : 2;                       // wgrad: 64-column boxes of B
@@ -388,11 +422,20 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
+      // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row groups 1024
+      // bytes apart; M- / N-major: 16 K rows of 128 bytes, 8-row groups 1024
+      // bytes apart, 64-wide boxes kHalfBox apart
+      constexpr uint64_t kAStep = (OP == kForward ? 32 : 2048) >> 4, kBStep = (OP == kWgrad ? 2048 : 32) >> 4;
+      const uint64_t a_desc =
+          make_smem_desc(smem_u32(smem + L::kOffA), OP == kForward ? 16 : GP::kHalfBox, 1024, kSwizzle128B);
+      const uint64_t b_desc =
+          make_smem_desc(smem_u32(smem + L::kOffB), OP == kWgrad ? GP::kHalfBox : 16, 1024, kSwizzle128B);
       int stage = 0, j = 0;
       uint32_t phase = 0, fixed_phase = 0;
       bool ok = true;
-      for (int w = cluster; w < total && ok; w += nclusters) {
-        const GItem it = decode_item<OP>(w, g, off, tile_off);
+      for (; items.more() && ok; items.next()) {
+        const int w = items.w;
+        const GItem it = items.get();
         if (OP == kWgrad && it.kb == 0) continue;
         const int acc = j & 1;
         const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
@@ -420,18 +463,15 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
             break;
           }
           if (elect_one()) {
-            const uint32_t a = smem_u32(smem + L::kOffA + stage * GP::kATile);
-            const uint32_t b = smem_u32(smem + L::kOffB + stage * GP::kBTile);
-            const int steps = left >= GP::kBK ? 4 : (left + 15) >> 4;
-            for (int kk = 0; kk < steps; ++kk) {
-              // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row
-              // groups 1024 bytes apart; M- / N-major: 16 K rows of 128 bytes,
-              // 8-row groups 1024 bytes apart, 64-wide boxes kHalfBox apart
-              const uint64_t ad = OP == kForward ? make_smem_desc(a + kk * 32, 16, 1024, kSwizzle128B)
-                                                 : make_smem_desc(a + kk * 2048, GP::kHalfBox, 1024, kSwizzle128B);
-              const uint64_t bd = OP == kWgrad ? make_smem_desc(b + kk * 2048, GP::kHalfBox, 1024, kSwizzle128B)
-                                               : make_smem_desc(b + kk * 32, 16, 1024, kSwizzle128B);
-              tc_mma_2sm_f16(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            const uint64_t ad = a_desc + (uint64_t)((stage * GP::kATile) >> 4);
+            const uint64_t bd = b_desc + (uint64_t)((stage * GP::kBTile) >> 4);
+            if (left > GP::kBK - 16) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
+            } else {
+              for (int kk = 0; 16 * kk < left; ++kk)
+                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
             }
             tc_commit_2sm(&empty[stage], 3);
           }
@@ -451,25 +491,31 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
     if (OP == kWgrad) {
       int block = 0;                                           // blocks of the items before, modulo the ring
       uint32_t tail_phase = 0;
-      for (int w = cluster; w < total; w += nclusters) {
-        const GItem it = decode_item<OP>(w, g, off, tile_off);
+      for (; items.more(); items.next()) {
+        const GItem it = items.get();
         if (it.kb > 0 && (it.rows & 15) != 0) {
           const int stage = (block + it.kb - 1) % L::kStages;
           if (!__all_sync(0xffffffffu, mbar_wait_reset(&tail_full[stage], (tail_phase >> stage) & 1u, status, kLimit,
-                                                       kWaitMmaFull, w)))
+                                                       kWaitMmaFull, items.w)))
             break;
           tail_phase ^= 1u << stage;
           const int rem = it.rows - (it.kb - 1) * GP::kBK;       // 1 .. 63 rows of the block
           const int rows = ((rem + 15) & ~15) - rem;             // rows to zero, 128 bytes in each box
-          for (int i = lane; i < rows * 32; i += 32) {
-            const int box = i / (rows * 8), r = i - box * (rows * 8);
-            unsigned char *p = box < 2 ? smem + L::kOffA + stage * GP::kATile + box * GP::kHalfBox
-                                       : smem + L::kOffB + stage * GP::kBTile + (box - 2) * GP::kHalfBox;
-            *reinterpret_cast<uint4 *>(p + rem * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+          unsigned char *p = smem + L::kOffA + stage * GP::kATile + rem * 128 + lane * 16;
+#pragma unroll
+          for (int box = 0; box < 4; ++box) {
+            if (box == 2) p += L::kOffB + stage * GP::kBTile - (L::kOffA + stage * GP::kATile) - 2 * GP::kHalfBox;
+            for (int i = lane; i < rows * 8; i += 32) *reinterpret_cast<uint4 *>(p + (i - lane) * 16) = make_uint4(0, 0, 0, 0);
+            p += GP::kHalfBox;
           }
           fence_proxy_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_fixed[stage]), 0));
+          // the zeros lie in this SM's shared memory and are ordered before its
+          // tensor core's reads by the proxy fence: the arrival itself has
+          // nothing to publish (released at cluster scope it took the warp
+          // ~2000 cycles an item and held the MMAs up: 378 instead of 312 us
+          // for 32 experts of 128 rows, N = 4096, K = 7168)
+          if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tail_fixed[stage]), 0));
         }
         block = (block + it.kb) % L::kStages;
       }
@@ -479,9 +525,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
     const int q = warp & 3;
     const int ew = warp - GP::kFirstEpiWarp;
     unsigned char *stage_tile = smem + L::kOffEpi + ew * L::kEpiBytes;
-    int j = 0, turn = 0;
-    for (int w = cluster; w < total; w += nclusters) {
-      const GItem it = decode_item<OP>(w, g, off, tile_off);
+    int j = 0;
+    for (; items.more(); items.next()) {
+      const int w = items.w;
+      const GItem it = items.get();
       const int first = it.m * GP::kM + (int)rank * 128 + 32 * q;  // this warp's M rows
       const bool none = OP == kWgrad && it.kb == 0;
       const int acc = j & 1;
@@ -500,9 +547,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         if (OP == kWgrad) {
           const int c0 = 128 * (ew >> 2);
           if (g.f32)
-            store_block<true>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile, turn);
+            store_block<true>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile);
           else
-            store_block<false>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile, turn);
+            store_block<false>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile);
         } else {
           for (int c0 = 32 * (ew >> 2); c0 < it.rows; c0 += 64) {
             uint32_t v[32];
@@ -515,7 +562,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       if (!none) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+        if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
       }
     }
     if (OP == kWgrad && lane == 0) bulk_wait<0>();

@@ -94,6 +94,15 @@ __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Arrival on an mbarrier of either CTA of the pair by a thread that has no
+// memory writes to publish to the other CTA's threads (its TMEM loads are
+// complete, tcgen05.wait::ld; or its own shared memory is ordered for the
+// tensor core by a proxy fence).  Releasing at cluster scope instead waits for
+// every store of the thread to be performed: ~2000 cycles, measured.
+__device__ __forceinline__ void mbar_arrive_done(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // As mbar_try_wait, ordered after arrivals of the other CTA of the pair too.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
