@@ -40,7 +40,7 @@ namespace mxq {
 
 namespace {
 
-enum : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
+enum : int { kForward = 0, kDgrad = 1, kWgrad = 2, kWgradF32 = 3 };
 
 struct GP {
   static constexpr int kM = 256;                       // M of a pair's MMA (128 per CTA)
@@ -56,28 +56,39 @@ struct GP {
   static constexpr int kNumBars = 4 * kMaxStages + 6;
 };
 
-// Shared memory of one direction.  wgrad stages its output for TMA stores
-// (a 4 KB box per epilogue warp; two would cost a stage, and the loads' latency
-// counts for more: 348 instead of 312 us for 32 experts of 128 rows, N = 4096,
-// K = 7168), forward / dgrad 2 KB per warp; wgrad's items need no table of row
-// tiles, and its offsets are read where they lie.
+// Shared memory of one direction.  forward / dgrad stage 2 KB of output per
+// epilogue warp.  wgrad stages it for TMA stores: a 4 KB box per warp for BF16
+// (two would cost a stage, and the loads' latency counts for more: 348 instead
+// of 312 us for 32 experts of 128 rows, N = 4096, K = 7168), two for float32,
+// whose twice as many boxes bound the drain (256 experts of 31 rows, N = 1024,
+// K = 2048: 381 us with one and six stages).  wgrad's items need no table of
+// row tiles, and its offsets are read where they lie.
 template <int OP>
 struct Layout {
-  static constexpr int kStages = 6;
-  static constexpr int kEpiBytes = OP == kWgrad ? 4096 : 2048;   // per epilogue warp
+  static constexpr bool kW = OP >= kWgrad;
+  static constexpr int kStages = OP == kWgradF32 ? 5 : 6;
+  static constexpr int kBoxes = OP == kWgradF32 ? 2 : 1;
+  static constexpr int kEpiBytes = kW ? kBoxes * 4096 : 2048;    // per epilogue warp
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + kStages * GP::kATile;
   static constexpr int kOffEpi = kOffB + kStages * GP::kBTile;
   static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
   static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: off[E+1], tile_off[E+1]
-  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (OP == kWgrad ? 0 : (size_t)8 * (E + 1)); }
+  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (kW ? 0 : (size_t)8 * (E + 1)); }
 };
+
+// float32 gradients: reduction blocks whose sum the tensor core holds before it
+// is added to the item's float32 sum.  The tensor core truncates each addition to its
+// accumulator, an error that grows with the length (1e-9 of the result per
+// row, measured); past 1024 rows it would pass float32's own.
+constexpr int kPartBlocks = 16;
 
 constexpr long long kLimit = 2000000000LL;              // ~1 s
 constexpr long long kInjectedLimit = 20000000LL;        // ~10 ms: the debug wait's budget
 constexpr int kMaxExperts = 1024;
-static_assert(Layout<kForward>::bytes(kMaxExperts) <= 232448 && Layout<kWgrad>::bytes(kMaxExperts) <= 232448,
+static_assert(Layout<kForward>::bytes(kMaxExperts) <= 232448 && Layout<kWgrad>::bytes(kMaxExperts) <= 232448 &&
+                  Layout<kWgradF32>::bytes(kMaxExperts) <= 232448,
               "shared memory of one CTA");
 
 struct GMaps {
@@ -93,7 +104,7 @@ struct GArgs {
   int M, R, C;          // M extent, reduction length (forward, dgrad), N extent (wgrad)
   int64_t ld_out;       // forward / dgrad: row stride of the output
   void *out;
-  int f32, accumulate;  // wgrad
+  int accumulate;       // wgrad in float32
   int inject_wait;
   int *status;
 };
@@ -110,6 +121,7 @@ struct GItem {
 // write whole rows of dw), advanced without divisions.
 template <int OP>
 struct Items {
+  static constexpr bool kW = OP >= kWgrad;
   const GArgs &g;
   const int *off, *tile_off;
   int mt, ct;
@@ -120,7 +132,7 @@ struct Items {
   __device__ __forceinline__ Items(const GArgs &g, const int *off, const int *tile_off, int first, int step, int total)
       : g(g), off(off), tile_off(tile_off), mt((g.M + GP::kM - 1) / GP::kM), ct((g.C + GP::kN - 1) / GP::kN), w(first),
         step(step), total(total), e(0), m(0), c(0), dm(0), dc(0) {
-    if (OP == kWgrad) {
+    if (kW) {
       m = w / ct;
       c = w - m * ct;
       dm = step / ct;
@@ -132,7 +144,7 @@ struct Items {
   __device__ __forceinline__ bool more() const { return w < total; }
   __device__ __forceinline__ void next() {
     w += step;
-    if (OP == kWgrad) {
+    if (kW) {
       c += dc;
       m += dm;
       if (c >= ct) { c -= ct; ++m; }
@@ -141,7 +153,7 @@ struct Items {
   }
   __device__ __forceinline__ GItem get() const {
     GItem it;
-    if (OP == kWgrad) {
+    if (kW) {
       it.e = e;
       it.m = m;
       it.c = c;
@@ -199,59 +211,70 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int c0, int 
   __syncwarp();
 }
 
-// wgrad: this warp's 32 rows (TMEM lanes) x 128 columns of dw, in boxes of 32
-// rows x 128 bytes (64 BF16 or 32 float32 columns), each written to swizzled
-// staging and stored by TMA, which leaves out what lies outside dw.  `none`: no
-// rows, zeros.
-template <bool kF32>
-__device__ __forceinline__ void store_block(uint32_t t_row, bool none, int row0, int col0, const GItem &it, const GArgs &g,
+// wgrad: BOXES boxes of 32 rows (TMEM lanes) x 128 bytes (64 BF16 or 32 float32
+// columns) of dw, from this lane's values `v`, through swizzled staging to a
+// TMA store (`add`: addition), which leaves out what lies outside dw.
+template <bool kF32, int BOXES>
+__device__ __forceinline__ void store_boxes(const uint32_t *v, bool add, int row, int col, int e, int C,
                                             const CUtensorMap *map, int lane, unsigned char *buf) {
   constexpr int kCols = kF32 ? 32 : 64;
+  if (lane == 0) bulk_wait_read<0>();               // the stores before have read the staging
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 8 * BOXES; ++p) {
+    uint4 piece;
+    if (kF32) {
+      piece = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
+      piece = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *reinterpret_cast<uint4 *>(buf + (p >> 3) * 4096 + lane * 128 + (((p & 7) ^ (lane & 7)) << 4)) = piece;
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+#pragma unroll
+    for (int b = 0; b < BOXES; ++b) {
+      if (col + b * kCols >= C) break;
+      if (kF32 && add)
+        tma_add_3d(map, buf + b * 4096, col + b * kCols, row, e);
+      else
+        tma_store_3d(map, buf + b * 4096, col + b * kCols, row, e);
+    }
+    bulk_commit();
+  }
+}
+
+// This warp's 32 rows x 128 columns of dw from the accumulator; `none`: no
+// rows, zeros.
+template <bool kF32, int BOXES>
+__device__ __forceinline__ void store_block(uint32_t t_row, bool none, bool add, int row, int col, int e, int C,
+                                            const CUtensorMap *map, int lane, unsigned char *buf) {
+  constexpr int kCols = (kF32 ? 32 : 64) * BOXES;
 #pragma unroll
   for (int c0 = 0; c0 < 128; c0 += kCols) {
-    if (col0 + c0 >= g.C) break;
+    if (col + c0 >= C) break;
     uint32_t v[kCols];
     if (none) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) v[i] = 0;
     } else {
 #pragma unroll
-      for (int h = 0; h < kCols / 32; ++h)
-        tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+      for (int h = 0; h < kCols; h += 32)
+        tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + h), *reinterpret_cast<uint32_t(*)[32]>(v + h));
       tmem_ld_wait();
     }
-    uint4 piece[8];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if (kF32) {
-        piece[p] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
-        piece[p] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    if (lane == 0) bulk_wait_read<0>();               // the store before has read the staging
-    __syncwarp();
-#pragma unroll
-    for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4 *>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = piece[p];
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      if (kF32 && g.accumulate)
-        tma_add_3d(map, buf, col0 + c0, row0, it.e);
-      else
-        tma_store_3d(map, buf, col0 + c0, row0, it.e);
-      bulk_commit();
-    }
+    store_boxes<kF32, BOXES>(v, add, row, col + c0, e, C, map, lane, buf);
   }
 }
 
 template <int OP>
 __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_constant__ GMaps maps, const GArgs g) {
   using L = Layout<OP>;
+  constexpr bool kW = L::kW;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -267,7 +290,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
   int *off_sm = reinterpret_cast<int *>(smem + L::kOffTab);
   int *tile_off = off_sm + g.E + 1;
-  const int *off = OP == kWgrad ? g.offsets : off_sm;
+  const int *off = kW ? g.offsets : off_sm;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -277,7 +300,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&maps.a);
-      for (int i = 0; i < (OP == kWgrad ? 2 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
+      for (int i = 0; i < (kW ? 2 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
     }
   } else if (warp == 2) {
     if (lane == 0) {
@@ -310,14 +333,14 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   for (int e = threadIdx.x; e <= g.E; e += GP::kThreads) {
     const int o = __ldg(g.offsets + e);
     const int before = e > 0 ? __ldg(g.offsets + e - 1) : 0;
-    if (OP != kWgrad) off_sm[e] = o;
+    if (!kW) off_sm[e] = o;
     bad |= o < before || (int64_t)o > g.P;
   }
   bad = __syncthreads_or(bad);
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) report_status(status, kStatusBadIndex);
   const int mt = (g.M + GP::kM - 1) / GP::kM;
   int total;
-  if (OP == kWgrad) {
+  if (kW) {
     total = g.E * mt * ((g.C + GP::kN - 1) / GP::kN);
   } else {
     if (warp == 0) {
@@ -353,7 +376,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       const int half = (int)it.n_mma >> 1;
       const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
       const int boxes = half <= 64 ? 1 : 2;                       // wgrad: 64-column boxes of B
-      const uint32_t bytes = GP::kATile + (OP == kWgrad ? boxes * GP::kHalfBox : (16 << box) * GP::kBK * 2);
+      const uint32_t bytes = GP::kATile + (kW ? boxes * GP::kHalfBox : (16 << box) * GP::kBK * 2);
       const int m0 = it.m * GP::kM + (int)rank * 128;
       for (int kb = 0; kb < it.kb; ++kb) {
         if (!__all_sync(0xffffffffu,
@@ -361,7 +384,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           ok = false;
           break;
         }
-        const bool tail = OP == kWgrad && kb == it.kb - 1 && (it.rows & 15) != 0;
+        const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
         if (lane == 0) {
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
           unsigned char *a = smem + L::kOffA + stage * GP::kATile, *b = smem + L::kOffB + stage * GP::kBTile;
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
               for (int j = 0; j < 2; ++j)
                 tma_load_2d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, it.row0 + kb * GP::kBK);
             }
-            if (OP == kWgrad) {
+            if (kW) {
               for (int j = 0; j < boxes; ++j)
                 tma_load_2d_2sm(b + j * GP::kHalfBox, &maps.b[0], bar, it.c * GP::kN + (int)rank * half + 64 * j,
                                 it.row0 + kb * GP::kBK);
@@ -425,20 +448,20 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row groups 1024
       // bytes apart; M- / N-major: 16 K rows of 128 bytes, 8-row groups 1024
       // bytes apart, 64-wide boxes kHalfBox apart
-      constexpr uint64_t kAStep = (OP == kForward ? 32 : 2048) >> 4, kBStep = (OP == kWgrad ? 2048 : 32) >> 4;
+      constexpr uint64_t kAStep = (OP == kForward ? 32 : 2048) >> 4, kBStep = (kW ? 2048 : 32) >> 4;
       const uint64_t a_desc =
           make_smem_desc(smem_u32(smem + L::kOffA), OP == kForward ? 16 : GP::kHalfBox, 1024, kSwizzle128B);
       const uint64_t b_desc =
-          make_smem_desc(smem_u32(smem + L::kOffB), OP == kWgrad ? GP::kHalfBox : 16, 1024, kSwizzle128B);
+          make_smem_desc(smem_u32(smem + L::kOffB), kW ? GP::kHalfBox : 16, 1024, kSwizzle128B);
       int stage = 0, j = 0;
       uint32_t phase = 0, fixed_phase = 0;
       bool ok = true;
       for (; items.more() && ok; items.next()) {
         const int w = items.w;
         const GItem it = items.get();
-        if (OP == kWgrad && it.kb == 0) continue;
-        const int acc = j & 1;
-        const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
+        if (kW && it.kb == 0) continue;
+        int acc = j & 1;
+        uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
         ++j;
         if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit,
                                                      kWaitMmaTmemEmpty, w)))
@@ -447,12 +470,28 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
             !__all_sync(0xffffffffu, mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, w)))
           break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
-        const uint32_t idesc = make_idesc_bf16(GP::kM, it.n_mma, OP != kForward, OP == kWgrad);
-        const int len = OP == kWgrad ? it.rows : g.R;
+        uint32_t d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
+        const uint32_t idesc = make_idesc_bf16(GP::kM, it.n_mma, OP != kForward, kW);
+        const int len = kW ? it.rows : g.R;
+        int first = 0;                                          // first block of the accumulator's sum
         for (int kb = 0; kb < it.kb; ++kb) {
+          if (OP == kWgradF32 && kb == first + kPartBlocks) {   // hand the part over, go on in the other accumulator
+            if (elect_one()) tc_commit_2sm(&tmem_full[acc], 3);
+            __syncwarp();
+            acc = j & 1;
+            acc_phase = (uint32_t)(j >> 1) & 1u;
+            ++j;
+            if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit,
+                                                         kWaitMmaTmemEmpty, w))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
+            first = kb;
+          }
           const int left = len - kb * GP::kBK;                  // reduction values from here on
-          const bool tail = OP == kWgrad && kb == it.kb - 1 && (it.rows & 15) != 0;
+          const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
           bool got = mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb);
           if (tail) {
             got = got && mbar_wait_reset(&tail_fixed[stage], (fixed_phase >> stage) & 1u, status, kLimit, kWaitMmaFull, kb);
@@ -468,10 +507,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
             if (left > GP::kBK - 16) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
+                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, kb != first || kk != 0 ? 1u : 0u);
             } else {
               for (int kk = 0; 16 * kk < left; ++kk)
-                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
+                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, kb != first || kk != 0 ? 1u : 0u);
             }
             tc_commit_2sm(&empty[stage], 3);
           }
@@ -488,7 +527,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ ragged ends (both CTAs)
-    if (OP == kWgrad) {
+    if (kW) {
       int block = 0;                                           // blocks of the items before, modulo the ring
       uint32_t tail_phase = 0;
       for (; items.more(); items.next()) {
@@ -530,26 +569,63 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       const int w = items.w;
       const GItem it = items.get();
       const int first = it.m * GP::kM + (int)rank * 128 + 32 * q;  // this warp's M rows
-      const bool none = OP == kWgrad && it.kb == 0;
-      const int acc = j & 1;
-      if (!none) {
-        const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
-        ++j;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait_reset(&tmem_full[acc], acc_phase, status, kLimit, kWaitEpiTmemFull, w)))
-          break;
-        tc_fence_after();
-      } else if (g.accumulate) {
+      const int col = it.c * GP::kN + 128 * (ew >> 2);             // wgrad: this warp's columns
+      if (kW && it.kb == 0) {                                      // an expert without rows
+        if (first < g.M && !g.accumulate)
+          store_block<OP == kWgradF32, L::kBoxes>(0, true, false, first, col, it.e, g.C, &maps.b[1], lane, stage_tile);
         continue;
       }
-      const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN);
+      const uint32_t t_lane = tmem_base + ((uint32_t)(32 * q) << 16);
+      auto wait_full = [&](int acc) {
+        const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
+        ++j;
+        const bool got =
+            __all_sync(0xffffffffu, mbar_wait_reset(&tmem_full[acc], acc_phase, status, kLimit, kWaitEpiTmemFull, w));
+        tc_fence_after();
+        return got;
+      };
+      auto release = [&](int acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      };
+      if (OP == kWgradF32 && it.kb > kPartBlocks) {
+        // a long sum: its parts added up in registers, in order
+        float sum[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        bool got = true;
+        for (int kb = 0; kb < it.kb; kb += kPartBlocks) {
+          const int acc = j & 1;
+          got = wait_full(acc);
+          if (!got) break;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t_lane + (uint32_t)(acc * GP::kN + 128 * (ew >> 2) + c), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+          }
+          release(acc);
+        }
+        if (!got) break;
+        if (first < g.M) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 32 * L::kBoxes)
+            if (col + c < g.C)
+              store_boxes<true, L::kBoxes>(reinterpret_cast<uint32_t *>(sum) + c, g.accumulate, first, col + c, it.e, g.C,
+                                           &maps.b[1], lane, stage_tile);
+        }
+        continue;
+      }
+      const int acc = j & 1;
+      if (!wait_full(acc)) break;
+      const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
       if (first < g.M) {
-        if (OP == kWgrad) {
-          const int c0 = 128 * (ew >> 2);
-          if (g.f32)
-            store_block<true>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile);
-          else
-            store_block<false>(t_row + c0, none, first, it.c * GP::kN + c0, it, g, &maps.b[1], lane, stage_tile);
+        if (kW) {
+          store_block<OP == kWgradF32, L::kBoxes>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
+                                                  &maps.b[1], lane, stage_tile);
         } else {
           for (int c0 = 32 * (ew >> 2); c0 < it.rows; c0 += 64) {
             uint32_t v[32];
@@ -559,13 +635,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           }
         }
       }
-      if (!none) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
-      }
+      release(acc);
     }
-    if (OP == kWgrad && lane == 0) bulk_wait<0>();
+    if (kW && lane == 0) bulk_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -747,9 +819,10 @@ extern "C" int moe_grouped_wgrad(const uint16_t *dy, int64_t ldy, const uint16_t
   g.M = (int)N;
   g.C = (int)K;
   g.out = dw;
-  g.f32 = dw_dtype == MOE_F32;
   g.accumulate = accumulate;
   g.inject_wait = injected_wait();
   g.status = reinterpret_cast<int *>(workspace);
-  return launch_grouped<kWgrad>(maps, g, (int64_t)E * ceil_div(N, GP::kM) * ceil_div(K, GP::kN), stream);
+  const int64_t items = (int64_t)E * ceil_div(N, GP::kM) * ceil_div(K, GP::kN);
+  return dw_dtype == MOE_F32 ? launch_grouped<kWgradF32>(maps, g, items, stream)
+                             : launch_grouped<kWgrad>(maps, g, items, stream);
 }

@@ -119,6 +119,18 @@ def test_weights_accumulate(B, counts):
             assert torch.equal(dw[e], base[e])
 
 
+def test_long_segment_in_float32(B):
+    """16 384 rows of one expert: a float32 gradient keeps float32's precision over a long sum (error in norm at
+    most 2e-6, which truncation over the whole length would pass several times over)."""
+    P, N, K = 16384, 128, 256
+    dy, x = randn(P, N, seed=7), randn(P, K, seed=8)
+    dw = torch.empty(1, N, K, device="cuda")
+    ws = workspace(B, P, N, K, 1)
+    B.moe_grouped_wgrad(dy, x, offsets_of([P]), dw, ws)
+    ref = dy.double().T @ x.double()
+    assert float((dw[0].double() - ref).norm() / ref.norm()) <= 2e-6
+
+
 @pytest.mark.parametrize("first,last", [(0, 9), (6, 0), (5, 4)])
 def test_rows_of_no_expert_are_left_alone(B, first, last):
     """Rows outside [offsets[0], offsets[E]) are not written, whatever they hold (NaN here), and reach no result."""
