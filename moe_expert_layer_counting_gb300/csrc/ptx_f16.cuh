@@ -70,10 +70,13 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 
 // TMA tile store / float32 addition of a box in this CTA's shared memory
 // (values outside the tensor are left out), one bulk group per commit.
+// The store's lines are the first to leave L2.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
