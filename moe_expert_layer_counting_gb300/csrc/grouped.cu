@@ -21,8 +21,8 @@
 //
 // Roles per CTA (384 threads): warp 0 loads (TMA), warp 1 of the leader issues
 // the MMAs, warp 2 allocates TMEM and zeroes ragged ends, warps 4-11 drain the
-// accumulators (two per TMEM lane quadrant, each with staging of its own: row
-// pieces of 64 bytes, wgrad boxes of 32 rows x 128 bytes for TMA).  Two accumulators
+// accumulators (two per TMEM lane quadrant: forward / dgrad 64-byte row pieces
+// from registers, wgrad boxes of 32 rows x 128 bytes through TMA).  Two accumulators
 // alternate, so an item's drain overlaps the next item's MMAs.  Every wait is
 // bounded (see moe_get_device_status).
 #include <cuda_bf16.h>
@@ -30,6 +30,7 @@
 #include <atomic>
 #include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/moe_grouped.h"
 #include "host_common.h"
@@ -47,7 +48,6 @@ struct GP {
   static constexpr int kN = 256;                       // most N slots of an item
   static constexpr int kBK = 64;                       // reduction values per stage (128 bytes of BF16)
   static constexpr int kATile = 128 * kBK * 2;
-  static constexpr int kBTile = (kN / 2) * kBK * 2;
   static constexpr int kHalfBox = 64 * kBK * 2;        // a 64 x 64 box (M- / N-major operands)
   static constexpr int kFirstEpiWarp = 4;
   static constexpr int kEpiWarps = 8;
@@ -56,26 +56,31 @@ struct GP {
   static constexpr int kNumBars = 4 * kMaxStages + 6;
 };
 
-// Shared memory of one direction.  forward / dgrad stage 2 KB of output per
-// epilogue warp.  wgrad stages it for TMA stores: a 4 KB box per warp for BF16
-// (two would cost a stage, and the loads' latency counts for more: 348 instead
-// of 312 us for 32 experts of 128 rows, N = 4096, K = 7168), two for float32,
-// whose twice as many boxes bound the drain (256 experts of 31 rows, N = 1024,
-// K = 2048: 381 us with one and six stages).  wgrad's items need no table of
-// row tiles, and its offsets are read where they lie.
+// Shared memory of one direction: a ring of slots (stages), staging of the
+// output, barriers, tables.
+// forward / dgrad: a slot holds, by the item's rows,
+//   up to 32:   two reduction blocks (A, A, B, B: 16 + 16 + 2 + 2 KB): such
+//               items are bound by HBM, and 192 KB in flight per SM hide its
+//               latency;
+//   up to 320:  one block (A 16 KB, B 20 KB).
+// Six slots: with five, 16 384 rows of one expert (N = 4096, K = 7168) took 539
+// instead of 494 us.  The output goes from registers to memory.
+// wgrad: one block (A 16 KB, B 16 KB).  It stages its output for TMA stores: a
+// 4 KB box per warp for BF16 (two would cost a stage: 348 instead of 312 us for
+// 32 experts of 128 rows), two for float32, whose twice as many boxes bound the
+// drain.  Its items need no table.
 template <int OP>
 struct Layout {
   static constexpr bool kW = OP >= kWgrad;
+  static constexpr int kSlot = kW ? 32768 : 36864;
   static constexpr int kStages = OP == kWgradF32 ? 5 : 6;
   static constexpr int kBoxes = OP == kWgradF32 ? 2 : 1;
-  static constexpr int kEpiBytes = kW ? kBoxes * 4096 : 2048;    // per epilogue warp
-  static constexpr int kOffA = 0;
-  static constexpr int kOffB = kOffA + kStages * GP::kATile;
-  static constexpr int kOffEpi = kOffB + kStages * GP::kBTile;
+  static constexpr int kEpiBytes = kW ? kBoxes * 4096 : 0;       // per epilogue warp
+  static constexpr int kOffEpi = kStages * kSlot;
   static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
-  static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: off[E+1], Tiles::first[2][E+1]
-  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (kW ? 0 : (size_t)12 * (E + 1)); }
+  static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: Lists::first[2][E+1]
+  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (kW ? 0 : (size_t)8 * (E + 1)); }
 };
 
 // float32 gradients: reduction blocks whose sum the tensor core holds before it
@@ -83,6 +88,8 @@ struct Layout {
 // accumulator, an error that grows with the length (1e-9 of the result per
 // row, measured); past 1024 rows it would pass float32's own.
 constexpr int kPartBlocks = 16;
+
+constexpr int kSmallB = 2048;       // forward / dgrad: B of one of a slot's two blocks
 
 constexpr long long kLimit = 2000000000LL;              // ~1 s
 constexpr long long kInjectedLimit = 20000000LL;        // ~10 ms: the debug wait's budget
@@ -93,7 +100,7 @@ static_assert(Layout<kForward>::bytes(kMaxExperts) <= 232448 && Layout<kWgrad>::
 
 struct GMaps {
   CUtensorMap a;        // w (3-D) or dy
-  CUtensorMap b[4];     // row operand with boxes of 16, 32, 64, 128 rows; wgrad: b[0] = x in 64 x 64 boxes,
+  CUtensorMap b[5];     // row operand with boxes of kBoxRows rows; wgrad: b[0] = x in 64 x 64 boxes,
                         // b[1] = dw in boxes of 32 rows x 128 bytes
 };
 
@@ -109,104 +116,140 @@ struct GArgs {
   int *status;
 };
 
+constexpr int kBoxRows[5] = {16, 32, 64, 80, 128};
+__device__ __forceinline__ int box_of(int rows) {
+  return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 80 ? 3 : 4;
+}
+__device__ __forceinline__ int box_rows(int box) { return box < 3 ? 16 << box : box == 3 ? 80 : 128; }
+
 struct GItem {
   int e, m, c;          // expert, pair of 128-row M tiles, wgrad: 256-column N tile
   int row0, rows;       // forward / dgrad: first row and rows of the tile; wgrad: of the expert
-  int kb;               // reduction blocks
-  uint32_t n_mma;       // N slots of the MMA (a multiple of 32)
+  int kb, per;          // reduction blocks, in all and per stage
+  int n, n2;            // N slots (multiples of 32) of the MMA, of a second one for the rows after the first n
 };
 
-// The items w, w + step, ... of one cluster, in order.  forward / dgrad: row
-// tiles in the order of Tiles, the M tiles of a row tile fastest.  wgrad:
-// expert-major, then 256-row tiles, 256-column tiles fastest (so that the items
-// in flight write whole rows of dw), advanced without divisions.
-//
-// Row tiles fall in two lists, each expert-major: those of experts with more
-// than one tile, bound by the tensor cores (their weights come from L2 after
-// the first tile), and those of experts with one, bound by HBM where it has few
-// rows.  The lists are merged in proportion, so that both are busy all along.
-struct Tiles {
-  const int *off;        // [E+1]
-  const int *first;      // [2][E+1]: first tile of each expert in the two lists (many, one)
-  int E, n[2];
+// forward / dgrad: where the items of a launch lie.  An item is a tile of an
+// expert's rows times a 256-wide M tile.  An expert's rows are cut into equal
+// tiles of up to 256, or 320 where that saves one: up to 256 fill one accumulator, so that its
+// drain overlaps the next item's MMAs; more take both (two MMAs per A tile),
+// which costs that overlap but not a second pass over the weights (an expert of
+// 264 rows as 256 + 8 took 1.2 times as long).
+// Items fall in two lists, each expert-major: those of experts with more than
+// one tile, bound by the tensor cores, and those of experts with one, bound by
+// HBM where it has few rows.  The lists are merged in proportion, kRun items at
+// a time, so that both are busy all along.  Within an expert, groups of kGroup
+// tiles are walked tiles first: the items in flight then share rows as well as
+// weights in L2 (64 experts, 16 384 rows, skewed, N = 4096, K = 7168: HBM reads
+// 4.6 GB instead of 5.2, of which 4.0 are each operand once).
+constexpr int kRun = 16;
+constexpr int kGroup = 8;
 
-  __device__ __forceinline__ int total() const { return n[0] + n[1]; }
-  // Expert, first row and rows of the t-th tile.
-  __device__ __forceinline__ void at(int t, int &e, int &row0, int &rows) const {
-    const unsigned nt = (unsigned)total(), na = (unsigned)n[0];
-    unsigned before, upto;                                   // tiles of the first list before / up to t
-    if (nt < 65536u) {
-      before = (unsigned)t * na / nt;
-      upto = ((unsigned)t + 1) * na / nt;
+__device__ __forceinline__ int tiles_of(int rows) { return rows <= 320 ? (rows > 0) : rows <= 576 ? 2 : (rows + 255) / 256; }
+
+struct Lists {
+  const int32_t *offsets;
+  const int *first;      // [2][E+1]: first tile of each expert in the two lists (many, one)
+  int E, mt;             // experts, M tiles
+  int items0, items1, runs0, runs1;
+
+  __device__ __forceinline__ int total() const { return (runs0 + runs1) * kRun; }
+  // The w-th place: false where a list's last run has no item left.
+  __device__ __forceinline__ bool at(int w, GItem &it) const {
+    int list, i = w;
+    if (runs0 == 0 || runs1 == 0) {
+      list = runs0 == 0 ? 1 : 0;
     } else {
-      before = (unsigned)((uint64_t)t * na / nt);
-      upto = (unsigned)(((uint64_t)t + 1) * na / nt);
+      const unsigned run = (unsigned)w / kRun, n = (unsigned)(runs0 + runs1), a = (unsigned)runs0;
+      unsigned before, upto;                                 // runs of the first list before / up to this one
+      if (n < 65536u) {
+        before = run * a / n;
+        upto = (run + 1) * a / n;
+      } else {
+        before = (unsigned)((uint64_t)run * a / n);
+        upto = (unsigned)((uint64_t)(run + 1) * a / n);
+      }
+      list = upto > before ? 0 : 1;
+      i = (int)(list == 0 ? before : run - before) * kRun + w % kRun;
     }
-    const bool many = upto > before;
-    const int i = many ? (int)before : t - (int)before;
-    const int *f = first + (many ? 0 : E + 1);
-    int lo = 0, hi = E;                                      // f[lo] <= i < f[hi]
+    if (i >= (list == 0 ? items0 : items1)) return false;
+    const int *f = first + list * (E + 1);
+    const int tile = i / mt;
+    int lo = 0, hi = E;                                      // f[lo] <= tile < f[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (f[mid] <= i) lo = mid; else hi = mid;
+      if (f[mid] <= tile) lo = mid; else hi = mid;
     }
-    e = lo;
-    row0 = off[lo] + (i - f[lo]) * GP::kN;
-    rows = min(GP::kN, off[lo + 1] - row0);
+    it.e = lo;
+    it.c = 0;
+    it.m = i - f[lo] * mt;
+    it.row0 = __ldg(offsets + lo);
+    it.rows = __ldg(offsets + lo + 1) - it.row0;
+    if (list == 0) {
+      const int tiles = f[lo + 1] - f[lo];
+      const int group = it.m / (kGroup * mt), r = it.m - group * (kGroup * mt);
+      const int in_group = min(kGroup, tiles - group * kGroup);
+      it.m = r / in_group;
+      // equal tiles: the first `longer` have a row more
+      const int t = group * kGroup + r - it.m * in_group;
+      const int size = it.rows / tiles, longer = it.rows - size * tiles;
+      it.row0 += t * size + min(t, longer);
+      it.rows = size + (t < longer ? 1 : 0);
+    }
+    it.per = it.rows <= 32 ? 2 : 1;
+    it.n = it.rows <= GP::kN ? (it.rows + 31) & ~31 : ((it.rows + 1) / 2 + 31) & ~31;
+    it.n2 = it.rows <= GP::kN ? 0 : (it.rows - it.n + 31) & ~31;
+    return true;
   }
 };
 
+// The items at places w, w + step, ... of one cluster, in order.  wgrad: every
+// place has one, expert-major, then 256-row tiles, 256-column tiles fastest (so
+// that the items in flight write whole rows of dw), advanced without divisions.
 template <int OP>
 struct Items {
   static constexpr bool kW = OP >= kWgrad;
   const GArgs &g;
-  const Tiles &tiles;         // forward / dgrad
-  int mt, ct;
+  const Lists &lists;         // forward / dgrad
   int w, step, total;
-  int e, m, c;                // wgrad: of w
-  int dm, dc;                 // wgrad: step in (m, c)
+  int mt, ct, dm, dc;         // wgrad: tiles of dw, step in (it.m, it.c)
+  GItem it;
 
-  __device__ __forceinline__ Items(const GArgs &g, const Tiles &tiles, int first, int step, int total)
-      : g(g), tiles(tiles), mt((g.M + GP::kM - 1) / GP::kM), ct((g.C + GP::kN - 1) / GP::kN), w(first),
-        step(step), total(total), e(0), m(0), c(0), dm(0), dc(0) {
+  __device__ __forceinline__ Items(const GArgs &g, const Lists &lists, int first, int step, int total)
+      : g(g), lists(lists), w(first), step(step), total(total), mt(lists.mt), ct((g.C + GP::kN - 1) / GP::kN), dm(0), dc(0) {
     if (kW) {
-      m = w / ct;
-      c = w - m * ct;
+      it.m = w / ct;
+      it.c = w - it.m * ct;
       dm = step / ct;
       dc = step - dm * ct;
-      e = m / mt;
-      m -= e * mt;
+      it.e = it.m / mt;
+      it.m -= it.e * mt;
+      if (w < total) set();
+    } else {
+      it.kb = (g.R + GP::kBK - 1) / GP::kBK;
+      while (w < total && !lists.at(w, it)) w += step;
     }
+  }
+  __device__ __forceinline__ void set() {
+    it.row0 = __ldg(g.offsets + it.e);
+    it.rows = __ldg(g.offsets + it.e + 1) - it.row0;
+    it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
+    it.per = 1;
+    it.n = min(GP::kN, (g.C - it.c * GP::kN + 31) & ~31);
+    it.n2 = 0;
   }
   __device__ __forceinline__ bool more() const { return w < total; }
   __device__ __forceinline__ void next() {
     w += step;
     if (kW) {
-      c += dc;
-      m += dm;
-      if (c >= ct) { c -= ct; ++m; }
-      while (m >= mt) { m -= mt; ++e; }
-    }
-  }
-  __device__ __forceinline__ GItem get() const {
-    GItem it;
-    if (kW) {
-      it.e = e;
-      it.m = m;
-      it.c = c;
-      it.row0 = __ldg(g.offsets + e);
-      it.rows = __ldg(g.offsets + e + 1) - it.row0;
-      it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
-      it.n_mma = (uint32_t)min(GP::kN, (g.C - c * GP::kN + 31) & ~31);
+      it.c += dc;
+      it.m += dm;
+      if (it.c >= ct) { it.c -= ct; ++it.m; }
+      while (it.m >= mt) { it.m -= mt; ++it.e; }
+      if (w < total) set();
     } else {
-      const int t = w / mt;
-      it.m = w - t * mt;
-      it.c = 0;
-      tiles.at(t, it.e, it.row0, it.rows);
-      it.kb = (g.R + GP::kBK - 1) / GP::kBK;
-      it.n_mma = (uint32_t)((it.rows + 31) & ~31);
+      while (w < total && !lists.at(w, it)) w += step;
     }
-    return it;
   }
 };
 
@@ -215,30 +258,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// forward / dgrad: 32 N slots (rows c0 .. c0 + 31 of the item) of this warp's
-// 32 output columns: TMEM lanes are output columns, so lanes l and l ^ 1 swap
-// one value of each slot pair, which gives packed column pairs; staged as
-// [row][32 columns], stored as one 64-byte piece per row.
-__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int c0, int col0, const GItem &it, const GArgs &g,
-                                           int lane, uint32_t *stage) {
-  const bool odd = (lane & 1) != 0;
+// forward / dgrad: 32 N slots (`rows` of them rows, from row0) of this warp's
+// 32 output columns.  TMEM lanes are output columns; three exchanges between
+// lanes (of one value, one word, two words) turn them so that lane l holds
+// columns 8 (l / 8) .. + 7 of rows l % 8 + 8 r as 16 bytes, and a store writes
+// 64-byte pieces of 8 rows.
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int64_t row0, int rows, int col0, const GArgs &g,
+                                           int lane) {
+  const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0, b2 = (lane & 4) != 0;
+  uint32_t w[16];                      // rows 2 p + b0, two columns
 #pragma unroll
-  for (int t = 0; t < 32; t += 2) {
-    const float a = __uint_as_float(v[t]), b = __uint_as_float(v[t + 1]);
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-    stage[(t + (odd ? 1 : 0)) * 16 + (lane >> 1)] = odd ? pack_bf16(got, b) : pack_bf16(a, got);
+  for (int p = 0; p < 16; ++p) {
+    const float a = __uint_as_float(v[2 * p]), b = __uint_as_float(v[2 * p + 1]);
+    const float got = __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
+    w[p] = b0 ? pack_bf16(got, b) : pack_bf16(a, got);
   }
-  __syncwarp();
+  uint32_t u[8][2];                    // rows 4 q + 2 b1 + b0, four columns
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? w[2 * q] : w[2 * q + 1], 2);
+    u[q][0] = b1 ? got : w[2 * q];
+    u[q][1] = b1 ? w[2 * q + 1] : got;
+  }
   uint16_t *out = reinterpret_cast<uint16_t *>(g.out);
-  const int col = col0 + 8 * (lane & 3);
+  const int col = col0 + 8 * (lane >> 3);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const uint4 piece = *reinterpret_cast<const uint4 *>(stage + r * 16 + 4 * (lane & 3));
-    if (c0 + r < it.rows && col < g.M)
-      *reinterpret_cast<uint4 *>(out + (int64_t)(it.row0 + c0 + r) * g.ld_out + col) = piece;
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t got0 = __shfl_xor_sync(0xffffffffu, b2 ? u[2 * r][0] : u[2 * r + 1][0], 4);
+    const uint32_t got1 = __shfl_xor_sync(0xffffffffu, b2 ? u[2 * r][1] : u[2 * r + 1][1], 4);
+    const uint4 piece = b2 ? make_uint4(got0, got1, u[2 * r + 1][0], u[2 * r + 1][1])
+                           : make_uint4(u[2 * r][0], u[2 * r][1], got0, got1);
+    const int row = 8 * r + (lane & 7);
+    if (row < rows && col < g.M) *reinterpret_cast<uint4 *>(out + (row0 + row) * g.ld_out + col) = piece;
   }
-  __syncwarp();
 }
 
 // wgrad: BOXES boxes of 32 rows (TMEM lanes) x 128 bytes (64 BF16 or 32 float32
@@ -320,8 +372,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   uint64_t *mma_done = tmem_empty + 2;
   uint64_t *never = mma_done + 1;
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
-  int *off = reinterpret_cast<int *>(smem + L::kOffTab);
-  int *tile_first = off + g.E + 1;
+  int *tile_first = reinterpret_cast<int *>(smem + L::kOffTab);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -331,7 +382,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&maps.a);
-      for (int i = 0; i < (kW ? 2 : 4); ++i) tma_prefetch_desc(&maps.b[i]);
+      for (int i = 0; i < (kW ? 2 : 5); ++i) tma_prefetch_desc(&maps.b[i]);
     }
   } else if (warp == 2) {
     if (lane == 0) {
@@ -364,13 +415,12 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   for (int e = threadIdx.x; e <= g.E; e += GP::kThreads) {
     const int o = __ldg(g.offsets + e);
     const int before = e > 0 ? __ldg(g.offsets + e - 1) : 0;
-    if (!kW) off[e] = o;
     bad |= o < before || (int64_t)o > g.P;
   }
   bad = __syncthreads_or(bad);
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) report_status(status, kStatusBadIndex);
   const int mt = (g.M + GP::kM - 1) / GP::kM;
-  Tiles tiles{off, tile_first, g.E, {0, 0}};
+  Lists lists{g.offsets, tile_first, g.E, mt, 0, 0, 0, 0};
   int total;
   if (kW) {
     total = g.E * mt * ((g.C + GP::kN - 1) / GP::kN);
@@ -380,7 +430,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       int base = 0;
       for (int e0 = 0; e0 < g.E; e0 += 32) {
         const int e = e0 + lane;
-        int n = !bad && e < g.E ? (off[e + 1] - off[e] + GP::kN - 1) / GP::kN : 0;
+        int n = !bad && e < g.E ? tiles_of(__ldg(g.offsets + e + 1) - __ldg(g.offsets + e)) : 0;
         if ((n > 1) != (warp == 0)) n = 0;
         int s = n;
 #pragma unroll
@@ -394,180 +444,230 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       if (lane == 0) first[g.E] = base;
     }
     __syncthreads();
-    tiles.n[0] = tile_first[g.E];
-    tiles.n[1] = tile_first[2 * g.E + 1];
-    total = tiles.total() * mt;
+    lists.items0 = tile_first[g.E] * mt;
+    lists.items1 = tile_first[2 * g.E + 1] * mt;
+    lists.runs0 = (lists.items0 + kRun - 1) / kRun;
+    lists.runs1 = (lists.items1 + kRun - 1) / kRun;
+    total = lists.total();
   }
   if (bad) total = 0;
   const uint32_t tmem_base = *tmem_ptr;
-  Items<OP> items(g, tiles, cluster, nclusters, total);
+  Items<OP> items(g, lists, cluster, nclusters, total);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ loads (both CTAs)
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, issued_phase = 0, tails = 0, tail_phase = 0;
-    bool ok = true;
-    for (; items.more() && ok; items.next()) {
-      const GItem it = items.get();
-      const int half = (int)it.n_mma >> 1;
-      const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-      const int boxes = half <= 64 ? 1 : 2;                       // wgrad: 64-column boxes of B
-      const uint32_t bytes = GP::kATile + (kW ? boxes * GP::kHalfBox : (16 << box) * GP::kBK * 2);
-      const int m0 = it.m * GP::kM + (int)rank * 128;
-      for (int kb = 0; kb < it.kb; ++kb) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait_reset(&empty[stage], phase ^ 1, status, kLimit, kWaitProducerEmpty, kb))) {
-          ok = false;
-          break;
+    // ------------------------------------------------------------ loads (both CTAs), one thread
+    // The ring's slots are few for the loads' latency, so the way from a free
+    // slot to its copies is kept short: everything but the slot is worked out
+    // beforehand.
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0, tails = 0, tail_phase = 0;
+      bool ok = true;
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+      while (items.more() && ok) {
+        const GItem it = items.it;
+        if (kW && it.kb == 0) {
+          items.next();
+          continue;
         }
-        const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
-        if (lane == 0) {
-          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-          unsigned char *a = smem + L::kOffA + stage * GP::kATile, *b = smem + L::kOffB + stage * GP::kBTile;
-          if (tail) {
-            // the ragged block: onto this CTA's own barrier, for warp 2
-            if (rank == 0) mbar_arrive(&full[stage]);
-            mbar_arrive_expect_tx(&tail_full[stage], bytes);
-            for (int j = 0; j < 2; ++j)
-              tma_load_2d(a + j * GP::kHalfBox, &maps.a, &tail_full[stage], m0 + 64 * j, it.row0 + kb * GP::kBK);
-            for (int j = 0; j < boxes; ++j)
-              tma_load_2d(b + j * GP::kHalfBox, &maps.b[0], &tail_full[stage],
-                          it.c * GP::kN + (int)rank * half + 64 * j, it.row0 + kb * GP::kBK);
-          } else {
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
-            if (OP == kForward) {
-              tma_load_3d_2sm(a, &maps.a, bar, kb * GP::kBK, m0, it.e);
-            } else if (OP == kDgrad) {
+        const int half = it.n >> 1, half2 = it.n2 >> 1;
+        const int box = box_of(half), box2 = box_of(half2);
+        const int boxes = half <= 64 ? 1 : 2;                     // wgrad: 64-column boxes of B
+        const int b_bytes = kW ? boxes * GP::kHalfBox : box_rows(box) * GP::kBK * 2;
+        const int m0 = it.m * GP::kM + (int)rank * 128;
+        const CUtensorMap *map_b = &maps.b[box], *map_b2 = &maps.b[box2];
+        const int b_row = it.row0 + (int)rank * half, b2_row = it.row0 + it.n + (int)rank * half2;
+        const int b_col = it.c * GP::kN + (int)rank * half;
+        // kPer blocks a stage, kTwo: rows in two MMAs
+        auto blocks_of = [&](auto per_c, auto two_c) {
+          constexpr int kPer = decltype(per_c)::value;
+          constexpr bool kTwo = decltype(two_c)::value;
+          const uint32_t block_bytes = (uint32_t)(GP::kATile + b_bytes);
+          const uint32_t bytes = kPer * block_bytes + (kTwo ? (uint32_t)(box_rows(box2) * GP::kBK * 2) : 0u);
+          for (int kb = 0; kb < it.kb; kb += kPer) {
+            const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
+            const bool one = kPer == 2 && kb + 1 >= it.kb;        // the last of an odd number of blocks
+            unsigned char *slot = smem + stage * L::kSlot;
+            const uint32_t bar = full0 + 8 * (uint32_t)stage;
+            if (!mbar_wait_reset(&empty[stage], phase ^ 1, status, kLimit, kWaitProducerEmpty, kb)) return false;
+            if (tail) {
+              // the ragged block: onto this CTA's own barrier, for warp 2
+              if (rank == 0) mbar_arrive(&full[stage]);
+              mbar_arrive_expect_tx(&tail_full[stage], bytes);
               for (int j = 0; j < 2; ++j)
-                tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, kb * GP::kBK, it.e);
-            } else {
-              for (int j = 0; j < 2; ++j)
-                tma_load_2d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, it.row0 + kb * GP::kBK);
-            }
-            if (kW) {
+                tma_load_2d(slot + j * GP::kHalfBox, &maps.a, &tail_full[stage], m0 + 64 * j, it.row0 + kb * GP::kBK);
               for (int j = 0; j < boxes; ++j)
-                tma_load_2d_2sm(b + j * GP::kHalfBox, &maps.b[0], bar, it.c * GP::kN + (int)rank * half + 64 * j,
-                                it.row0 + kb * GP::kBK);
+                tma_load_2d(slot + GP::kATile + j * GP::kHalfBox, &maps.b[0], &tail_full[stage], b_col + 64 * j,
+                            it.row0 + kb * GP::kBK);
+              tails |= 1u << stage;
+              tail_phase ^= 1u << stage;             // parity of the next use of tail_full[stage]
             } else {
-              tma_load_2d_2sm(b, &maps.b[box], bar, kb * GP::kBK, it.row0 + (int)rank * half);
+              if (rank == 0) mbar_arrive_expect_tx(&full[stage], one ? 2 * block_bytes : 2 * bytes);
+              if (kW) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  tma_load_2d_2sm(slot + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, it.row0 + kb * GP::kBK);
+                tma_load_2d_2sm(slot + GP::kATile, &maps.b[0], bar, b_col, it.row0 + kb * GP::kBK);
+                if (boxes == 2)
+                  tma_load_2d_2sm(slot + GP::kATile + GP::kHalfBox, &maps.b[0], bar, b_col + 64, it.row0 + kb * GP::kBK);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                  if (i > 0 && one) break;
+                  unsigned char *a = slot + i * GP::kATile, *b = slot + kPer * GP::kATile + i * kSmallB;
+                  const int k0 = (kb + i) * GP::kBK;
+                  if (OP == kForward) {
+                    tma_load_3d_2sm(a, &maps.a, bar, k0, m0, it.e);
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, k0, it.e);
+                  }
+                  tma_load_2d_2sm(b, map_b, bar, k0, b_row);
+                  if (kTwo) tma_load_2d_2sm(b + b_bytes, map_b2, bar, k0, b2_row);
+                }
+              }
             }
+            issued |= 1u << stage;
+            issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == L::kStages) { stage = 0; phase ^= 1; }
+            if (kb == 0) items.next();               // while the first blocks are on their way
           }
-        }
-        __syncwarp();
-        issued |= 1u << stage;
-        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-        if (tail) {
-          tails |= 1u << stage;
-          tail_phase ^= 1u << stage;               // parity of the next use of tail_full[stage]
-        }
-        if (++stage == L::kStages) { stage = 0; phase ^= 1; }
+          return true;
+        };
+        using std::integral_constant;
+        if (kW || (it.per == 1 && it.n2 == 0))
+          ok = blocks_of(integral_constant<int, 1>{}, integral_constant<bool, false>{});
+        else if (it.per == 1)
+          ok = blocks_of(integral_constant<int, 1>{}, integral_constant<bool, true>{});
+        else
+          ok = blocks_of(integral_constant<int, 2>{}, integral_constant<bool, false>{});
       }
-    }
-    // no CTA leaves with copies in flight: the leader waits for both CTAs'
-    // copies (the final cluster barrier holds the other until then)
-    for (int s = 0; s < L::kStages; ++s) {
-      if (rank == 0 && (issued & (1u << s)))
-        mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
-      if (tails & (1u << s))
-        mbar_wait_reset(&tail_full[s], ((tail_phase >> s) & 1u) ^ 1u, status, kLimit, kWaitProducerDrain, s, false);
-    }
-    // after a wait gave up the other CTA may have copies in flight for a stage
-    // that the leader never armed: give them time to land (~100 us)
-    if (lane == 0 && *reinterpret_cast<volatile int *>(status + 1) != 0) {
-      const long long t0 = clock64();
-      while (clock64() - t0 < 200000) __nanosleep(1000);
+      // no CTA leaves with copies in flight: the leader waits for both CTAs'
+      // copies (the final cluster barrier holds the other until then)
+      for (int s = 0; s < L::kStages; ++s) {
+        if (rank == 0 && (issued & (1u << s)))
+          mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
+        if (tails & (1u << s))
+          mbar_wait_reset(&tail_full[s], ((tail_phase >> s) & 1u) ^ 1u, status, kLimit, kWaitProducerDrain, s, false);
+      }
+      // after a wait gave up the other CTA may have copies in flight for a stage
+      // that the leader never armed: give them time to land (~100 us)
+      if (*reinterpret_cast<volatile int *>(status + 1) != 0) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) __nanosleep(1000);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader)
-    if (rank == 0) {
+    // ------------------------------------------------------------ MMA issuer (leader), one thread
+    if (rank == 0 && elect_one()) {
       // K-major: 16 K values are 32 bytes of a 128-byte row, 8-row groups 1024
       // bytes apart; M- / N-major: 16 K rows of 128 bytes, 8-row groups 1024
       // bytes apart, 64-wide boxes kHalfBox apart
       constexpr uint64_t kAStep = (OP == kForward ? 32 : 2048) >> 4, kBStep = (kW ? 2048 : 32) >> 4;
-      const uint64_t a_desc =
-          make_smem_desc(smem_u32(smem + L::kOffA), OP == kForward ? 16 : GP::kHalfBox, 1024, kSwizzle128B);
-      const uint64_t b_desc =
-          make_smem_desc(smem_u32(smem + L::kOffB), kW ? GP::kHalfBox : 16, 1024, kSwizzle128B);
+      const uint64_t a_desc = make_smem_desc(smem_u32(smem), OP == kForward ? 16 : GP::kHalfBox, 1024, kSwizzle128B);
+      const uint64_t b_desc = make_smem_desc(smem_u32(smem), kW ? GP::kHalfBox : 16, 1024, kSwizzle128B);
       int stage = 0, j = 0;
       uint32_t phase = 0, fixed_phase = 0;
       bool ok = true;
-      for (; items.more() && ok; items.next()) {
+      while (items.more() && ok) {
         const int w = items.w;
-        const GItem it = items.get();
-        if (kW && it.kb == 0) continue;
-        int acc = j & 1;
-        uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
-        ++j;
-        if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit,
-                                                     kWaitMmaTmemEmpty, w)))
+        const GItem it = items.it;
+        if (kW && it.kb == 0) {
+          items.next();
+          continue;
+        }
+        auto next_acc = [&](int &acc) {                         // the accumulator after the last, drained
+          acc = j & 1;
+          const uint32_t acc_phase = (uint32_t)(j >> 1) & 1u;
+          ++j;
+          const bool got = mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit, kWaitMmaTmemEmpty, w);
+          tc_fence_after();
+          return got;
+        };
+        int acc, acc2 = 0;
+        if (!next_acc(acc) || (it.n2 && !next_acc(acc2))) break;
+        if (g.inject_wait == 1 && j <= 2 && w == cluster &&
+            !mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, w))
           break;
-        if (g.inject_wait == 1 && j == 1 &&
-            !__all_sync(0xffffffffu, mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, w)))
-          break;
-        tc_fence_after();
-        uint32_t d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
-        const uint32_t idesc = make_idesc_bf16(GP::kM, it.n_mma, OP != kForward, kW);
+        const uint32_t idesc = make_idesc_bf16(GP::kM, (uint32_t)it.n, OP != kForward, kW);
+        const uint32_t idesc2 = make_idesc_bf16(GP::kM, (uint32_t)it.n2, OP != kForward, kW);
+        const int b2_off = box_rows(box_of(it.n >> 1)) * GP::kBK * 2;
         const int len = kW ? it.rows : g.R;
         int first = 0;                                          // first block of the accumulator's sum
-        for (int kb = 0; kb < it.kb; ++kb) {
-          if (OP == kWgradF32 && kb == first + kPartBlocks) {   // hand the part over, go on in the other accumulator
-            if (elect_one()) tc_commit_2sm(&tmem_full[acc], 3);
-            __syncwarp();
-            acc = j & 1;
-            acc_phase = (uint32_t)(j >> 1) & 1u;
-            ++j;
-            if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_empty[acc], acc_phase ^ 1u, status, kLimit,
-                                                         kWaitMmaTmemEmpty, w))) {
-              ok = false;
-              break;
+        // kPer blocks a stage, kTwo: rows in two MMAs
+        auto blocks_of = [&](auto per_c, auto two_c) {
+          constexpr int kPer = decltype(per_c)::value;
+          constexpr bool kTwo = decltype(two_c)::value;
+          const uint32_t d = tmem_base + (uint32_t)(acc * GP::kN), d2 = tmem_base + (uint32_t)(acc2 * GP::kN);
+          uint32_t d_now = d;
+          for (int kb = 0; kb < it.kb; kb += kPer) {
+            if (OP == kWgradF32 && kb == first + kPartBlocks) { // hand the part over, go on in the other accumulator
+              tc_commit_2sm(&tmem_full[acc], 3);
+              if (!next_acc(acc)) return false;
+              d_now = tmem_base + (uint32_t)(acc * GP::kN);
+              first = kb;
             }
-            tc_fence_after();
-            d_tmem = tmem_base + (uint32_t)(acc * GP::kN);
-            first = kb;
-          }
-          const int left = len - kb * GP::kBK;                  // reduction values from here on
-          const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
-          bool got = mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb);
-          if (tail) {
-            got = got && mbar_wait_reset(&tail_fixed[stage], (fixed_phase >> stage) & 1u, status, kLimit, kWaitMmaFull, kb);
-            fixed_phase ^= 1u << stage;
-          }
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            const uint64_t ad = a_desc + (uint64_t)((stage * GP::kATile) >> 4);
-            const uint64_t bd = b_desc + (uint64_t)((stage * GP::kBTile) >> 4);
-            if (left > GP::kBK - 16) {
+            const bool tail = kW && kb == it.kb - 1 && (it.rows & 15) != 0;
+            bool got = mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb);
+            if (tail) {
+              got = got &&
+                    mbar_wait_reset(&tail_fixed[stage], (fixed_phase >> stage) & 1u, status, kLimit, kWaitMmaFull, kb);
+              fixed_phase ^= 1u << stage;
+            }
+            if (!got) return false;
+            {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, kb != first || kk != 0 ? 1u : 0u);
-            } else {
-              for (int kk = 0; 16 * kk < left; ++kk)
-                tc_mma_2sm_f16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, kb != first || kk != 0 ? 1u : 0u);
+              for (int i = 0; i < kPer; ++i) {
+                if (i > 0 && kb + i >= it.kb) break;
+                const uint64_t ad = a_desc + (uint64_t)((stage * L::kSlot + i * GP::kATile) >> 4);
+                const uint64_t bd = b_desc + (uint64_t)((stage * L::kSlot + kPer * GP::kATile + i * kSmallB) >> 4);
+                const uint64_t bd2 = bd + (uint64_t)(b2_off >> 4);
+                const int left = len - (kb + i) * GP::kBK;       // reduction values from here on
+                if (left > GP::kBK - 16) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t more = i > 0 || kk > 0 || kb != first ? 1u : 0u;
+                    tc_mma_2sm_f16(d_now, ad + kk * kAStep, bd + kk * kBStep, idesc, more);
+                    if (kTwo) tc_mma_2sm_f16(d2, ad + kk * kAStep, bd2 + kk * kBStep, idesc2, more);
+                  }
+                } else {
+                  for (int kk = 0; 16 * kk < left; ++kk) {
+                    const uint32_t more = i > 0 || kk > 0 || kb != first ? 1u : 0u;
+                    tc_mma_2sm_f16(d_now, ad + kk * kAStep, bd + kk * kBStep, idesc, more);
+                    if (kTwo) tc_mma_2sm_f16(d2, ad + kk * kAStep, bd2 + kk * kBStep, idesc2, more);
+                  }
+                }
+              }
+              tc_commit_2sm(&empty[stage], 3);
             }
-            tc_commit_2sm(&empty[stage], 3);
+            if (++stage == L::kStages) { stage = 0; phase ^= 1; }
+            if (kb == 0) items.next();                         // while the tensor cores are busy
           }
-          __syncwarp();
-          if (++stage == L::kStages) { stage = 0; phase ^= 1; }
-        }
+          return true;
+        };
+        using std::integral_constant;
+        if (kW || (it.per == 1 && it.n2 == 0))
+          ok = blocks_of(integral_constant<int, 1>{}, integral_constant<bool, false>{});
+        else if (it.per == 1)
+          ok = blocks_of(integral_constant<int, 1>{}, integral_constant<bool, true>{});
+        else
+          ok = blocks_of(integral_constant<int, 2>{}, integral_constant<bool, false>{});
         if (!ok) break;
-        if (elect_one()) tc_commit_2sm(&tmem_full[acc], 3);
-        __syncwarp();
+        tc_commit_2sm(&tmem_full[acc], 3);
+        if (it.n2) tc_commit_2sm(&tmem_full[acc2], 3);
       }
-      if (elect_one()) tc_commit_2sm(mma_done, 1);
-      __syncwarp();
+      tc_commit_2sm(mma_done, 1);
       mbar_wait_reset(mma_done, 0, status, kLimit, kWaitMmaDone, 0, false);
     }
+    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ ragged ends (both CTAs)
     if (kW) {
       int block = 0;                                           // blocks of the items before, modulo the ring
       uint32_t tail_phase = 0;
       for (; items.more(); items.next()) {
-        const GItem it = items.get();
+        const GItem it = items.it;
         if (it.kb > 0 && (it.rows & 15) != 0) {
           const int stage = (block + it.kb - 1) % L::kStages;
           if (!__all_sync(0xffffffffu, mbar_wait_reset(&tail_full[stage], (tail_phase >> stage) & 1u, status, kLimit,
@@ -576,10 +676,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           tail_phase ^= 1u << stage;
           const int rem = it.rows - (it.kb - 1) * GP::kBK;       // 1 .. 63 rows of the block
           const int rows = ((rem + 15) & ~15) - rem;             // rows to zero, 128 bytes in each box
-          unsigned char *p = smem + L::kOffA + stage * GP::kATile + rem * 128 + lane * 16;
+          unsigned char *p = smem + stage * L::kSlot + rem * 128 + lane * 16;
 #pragma unroll
           for (int box = 0; box < 4; ++box) {
-            if (box == 2) p += L::kOffB + stage * GP::kBTile - (L::kOffA + stage * GP::kATile) - 2 * GP::kHalfBox;
             for (int i = lane; i < rows * 8; i += 32) *reinterpret_cast<uint4 *>(p + (i - lane) * 16) = make_uint4(0, 0, 0, 0);
             p += GP::kHalfBox;
           }
@@ -601,9 +700,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
     const int ew = warp - GP::kFirstEpiWarp;
     unsigned char *stage_tile = smem + L::kOffEpi + ew * L::kEpiBytes;
     int j = 0;
-    for (; items.more(); items.next()) {
+    while (items.more()) {
       const int w = items.w;
-      const GItem it = items.get();
+      const GItem it = items.it;
+      items.next();                                                // before the wait
       const int first = it.m * GP::kM + (int)rank * 128 + 32 * q;  // this warp's M rows
       const int col = it.c * GP::kN + 128 * (ew >> 2);             // wgrad: this warp's columns
       if (kW && it.kb == 0) {                                      // an expert without rows
@@ -655,23 +755,29 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         }
         continue;
       }
-      const int acc = j & 1;
-      if (!wait_full(acc)) break;
-      const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
-      if (first < g.M) {
-        if (kW) {
-          store_block<OP == kWgradF32, L::kBoxes>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
-                                                  &maps.b[1], lane, stage_tile);
-        } else {
-          for (int c0 = 32 * (ew >> 2); c0 < it.rows; c0 += 64) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_row + (uint32_t)c0, v);
-            tmem_ld_wait();
-            store_rows(v, c0, first, it, g, lane, reinterpret_cast<uint32_t *>(stage_tile));
+      bool got = true;
+      for (int part = 0; part < (it.n2 ? 2 : 1); ++part) {
+        const int acc = j & 1;
+        got = wait_full(acc);
+        if (!got) break;
+        const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
+        if (first < g.M) {
+          if (kW) {
+            store_block<OP == kWgradF32, L::kBoxes>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
+                                                    &maps.b[1], lane, stage_tile);
+          } else {
+            const int row0 = it.row0 + part * it.n, rows = part == 0 ? min(it.rows, it.n) : it.rows - it.n;
+            for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 64) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_row + (uint32_t)c0, v);
+              tmem_ld_wait();
+              store_rows(v, (int64_t)row0 + c0, rows - c0, first, g, lane);
+            }
           }
         }
+        release(acc);
       }
-      release(acc);
+      if (!got) break;
     }
     if (kW && lane == 0) bulk_wait<0>();
   }
@@ -788,7 +894,7 @@ int rows_product(const uint16_t *in, int64_t ld_in, const uint16_t *w, const int
   GMaps maps;
   bool ok = OP == kForward ? encode_map(&maps.a, w, 3, K, N, E, K, N * K, GP::kBK, 128)
                            : encode_map(&maps.a, w, 3, K, N, E, K, N * K, 64, GP::kBK);
-  for (int i = 0; i < 4; ++i) ok = ok && encode_map(&maps.b[i], in, 2, R, P, 1, ld_in, 0, GP::kBK, 16u << i);
+  for (int i = 0; i < 5; ++i) ok = ok && encode_map(&maps.b[i], in, 2, R, P, 1, ld_in, 0, GP::kBK, kBoxRows[i]);
   if (!ok) return MOE_ERR_CUDA;
   GArgs g{};
   g.offsets = offsets;

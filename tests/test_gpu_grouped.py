@@ -69,6 +69,8 @@ CASES = [
     ([16, 32, 64, 128, 256], 256, 256),
     ([15, 17, 31, 33, 63, 65, 127, 129, 255, 257], 264, 200),
     ([0, 0, 700, 0, 1, 1025], 520, 1032),
+    ([256, 257, 288, 289, 320, 321, 384, 512, 513, 576, 577, 640, 641, 768, 769], 136, 328),
+    ([2300, 64, 65, 1], 392, 456),
     ([3] * 100 + [0] * 28, 128, 72),
     ([40] * 16, 1024, 512),
     ([2, 0, 5] * 341 + [1], 16, 64),          # 1024 experts
