@@ -82,7 +82,8 @@ typedef struct moe_norm_grads {
     int64_t ld_dgate;
     float *dw_post;            /* [H] float32 */
     float *dw_pre;             /* [H] float32 */
-    void *workspace;           /* moe_norm_workspace_size bytes, 256-byte aligned (sums of parts of the rows) */
+    void *workspace;           /* moe_norm_workspace_size bytes, 256-byte aligned: device status (moe_get_device_status,
+                                  reset by the call), sums of parts of the rows */
     size_t workspace_bytes;
 } moe_norm_grads;
 

@@ -1,10 +1,23 @@
 // norm.cu -- the norms before and after the expert layer with its gate and
 // residual scale, and their gradients (include/moe_norm.h has the formulas).
 //
-// Both directions are bound by HBM: every row is read once, kept in registers
-// over its reductions and written once.  A block owns a row; its threads own
-// 16-byte vectors of 8 values.
+// Both directions are bound by HBM if the SM keeps up: every row is read once
+// and written once, but a row needs two sums over its columns one after the
+// other, and ~17 operations a value in the backward pass.  So, up to H = 8192:
+//   - a group of H / 16 threads owns a row at a time, a thread 16 columns (with 8,
+//     the instructions that do not depend on the columns are as many as those
+//     that do: 149 instead of 127 us for the gradients of 8192 x 7168);
+//   - the rows to come are copied (bulk copies) into a ring in shared memory; a
+//     row is taken into registers, and its slot has its next row on the way
+//     before the row's first sum is used;
+//   - arithmetic on pairs (f32x2 instructions), and column constants (the
+//     weights with their offset, the channel gate) made once per block;
+//   - the gradients of w_post and of a channel gate are the same column sum
+//     sum_t d b rsqrt(mean b^2 + eps), times a constant of the column.
+// Longer rows are loaded into registers directly (the *_wide kernels).
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "../../include/moe_norm.h"
 #include "host_common.h"
@@ -17,11 +30,47 @@ namespace {
 constexpr int kMaxH = 16384;
 constexpr int kMaxWarps = 32;
 constexpr int kBackwardThreads = 512;
-constexpr int kMaxParts = 304;         // blocks whose column sums the backward keeps apart
 
 struct F8 {
   float v[8];
 };
+
+// Two floats that one f32x2 instruction works on.
+struct P2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ P2 pair(float lo, float hi) {
+  P2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ P2 twice(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 split(P2 p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+  return f;
+}
+__device__ __forceinline__ P2 operator*(P2 a, P2 b) {
+  P2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ P2 operator+(P2 a, P2 b) {
+  P2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ P2 fma2(P2 a, P2 b, P2 c) {
+  P2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ P2 from_bf16x2(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t to_bf16x2(P2 p) {
+  const float2 f = split(p);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
 
 __device__ __forceinline__ F8 unpack_bf16x8(const uint4 &q) {
   F8 f;
@@ -50,6 +99,7 @@ template <> struct Raw8<uint16_t> {
   uint4 q;
   __device__ __forceinline__ void load(const uint16_t *p) { q = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ F8 get() const { return unpack_bf16x8(q); }
+  __device__ __forceinline__ P2 two(int i) const { return from_bf16x2(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w); }
 };
 template <> struct Raw8<float> {
   float4 a, b;
@@ -58,12 +108,24 @@ template <> struct Raw8<float> {
     b = reinterpret_cast<const float4 *>(p)[1];
   }
   __device__ __forceinline__ F8 get() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+  __device__ __forceinline__ P2 two(int i) const {
+    return i == 0 ? pair(a.x, a.y) : i == 1 ? pair(a.z, a.w) : i == 2 ? pair(b.x, b.y) : pair(b.z, b.w);
+  }
 };
 
 __device__ __forceinline__ void store8(uint16_t *p, const F8 &f) { *reinterpret_cast<uint4 *>(p) = pack_bf16x8(f); }
 __device__ __forceinline__ void store8(float *p, const F8 &f) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+}
+
+__device__ __forceinline__ void store_pairs(uint16_t *p, const P2 (&v)[4]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
+}
+__device__ __forceinline__ void store_pairs(float *p, const P2 (&v)[4]) {
+  const float2 a = split(v[0]), b = split(v[1]), c = split(v[2]), d = split(v[3]);
+  reinterpret_cast<float4 *>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
 }
 
 // Eight values of a weight or gate, of either type (the same branch for the
@@ -86,32 +148,582 @@ __device__ __forceinline__ void store1_any(void *p, int dtype, int64_t i, float 
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 
-// Sums of N values over the block, the same bits in every thread (each adds
-// the warps' sums in the same order).  One barrier; a buffer `red`
-// [N][kMaxWarps] may be used again after another sum in another buffer.
+// Sums of up to four values over `warps` warps (at most 32), the same bits in
+// every thread.  Lanes hand values on as they add (6 shuffles for four values
+// instead of 20), every warp adds the warps' sums in the same tree; the result
+// of value k is in `v[k]`.  `sync` joins the warps, once; `red` [4][32] may be
+// used again after another sum in another buffer.
+template <int N, typename Sync>
+__device__ __forceinline__ void group_sum(float (&v)[N], int warps, int warp, float *red, Sync sync) {
+  static_assert(N >= 1 && N <= 4, "one to four values");
+  const int lane = (int)(threadIdx.x & 31);
+  float s;
+  if (N == 1) {
+    s = v[0];
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+  } else {
+    // lanes with bit 4 keep values 2 and 3, then lanes with bit 3 the odd one
+    const float v1 = v[1 % N], v2 = N > 2 ? v[2 % N] : 0.f, v3 = N > 3 ? v[3 % N] : 0.f;
+    const bool up = (lane & 16) != 0;
+    float a = (up ? v2 : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v2, 16);
+    float b = (up ? v3 : v1) + __shfl_xor_sync(0xffffffffu, up ? v1 : v3, 16);
+    const bool odd = (lane & 8) != 0;
+    s = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+  }
+  s += __shfl_xor_sync(0xffffffffu, s, 4);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  if (warps > 1) {
+    // [value][warp]; absent warps were zeroed once
+    if ((lane & 7) == 0 && (N > 1 || lane == 0)) red[(lane >> 3) * 32 + warp] = s;
+    sync();
+    const float4 q = *reinterpret_cast<const float4 *>(red + (N == 1 ? 0 : (lane >> 3) * 32) + 4 * (lane & 7));
+    s = (q.x + q.y) + (q.z + q.w);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+  } else {
+    sync();
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, s, N == 1 ? 0 : 8 * k);
+}
+
+// ---------------------------------------------------------------- rows through a ring in shared memory
+
+// A launch: `group` threads a row (a multiple of 32), `groups` rows at a time
+// in a block, `stages` slots a group.
+struct RingShape {
+  int group, groups, stages;
+};
+constexpr int kThreads = 512;                           // of a block, at most
+constexpr int V = 2;                                    // 8-column vectors of a thread
+constexpr int kMaxGroups = 4, kMaxStages = 8;
+constexpr long long kRingLimit = 2000000000LL;          // ~1 s
+
+// One row tensor of a launch: where its row t is, its bytes, its place in a slot.
+struct RowSource {
+  const char *base;
+  int64_t stride;              // bytes
+  int bytes;                   // of a row; 0: not read
+  int at;
+};
+
+struct RingSmem {
+  uint64_t full[kMaxGroups][kMaxStages];
+  float red[kMaxGroups][2][2][4 * 32];                  // of even and odd rows, two sums each
+};
+
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int warps = (int)(blockDim.x >> 5);
-  if (warps == 1) return;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[i * kMaxWarps + (threadIdx.x >> 5)] = v[i];
-  __syncthreads();
+__device__ __forceinline__ int place_rows(RowSource (&src)[N]) {
+  int at = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += red[i * kMaxWarps + w];
-    v[i] = s;
+    src[i].at = at;
+    at += src[i].bytes;
+  }
+  return at;
+}
+
+template <int N>
+__device__ __forceinline__ void ring_init(RingSmem &sm, const RingShape &sh, const RowSource (&src)[N]) {
+  for (int i = (int)threadIdx.x; i < kMaxGroups * 2 * 2 * 4 * 32; i += (int)blockDim.x) (&sm.red[0][0][0][0])[i] = 0.f;
+  if (threadIdx.x == 0) {
+    uint32_t copies = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) copies += src[i].bytes > 0 ? 1u : 0u;
+    for (int g = 0; g < sh.groups; ++g)
+      for (int s = 0; s < sh.stages; ++s) mbar_init(&sm.full[g][s], copies);
+    fence_mbar_init();
+  }
+  __syncthreads();
+}
+
+// Which tensors' copies this thread issues: each by the first lane of a warp of
+// its own (a thread's copies issue one after another), as far as the group has
+// warps.
+template <int N>
+__device__ __forceinline__ uint32_t my_copies(const RowSource (&src)[N], int warps, int warp) {
+  uint32_t mask = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (src[i].bytes > 0 && i % warps == warp && (threadIdx.x & 31) == 0) mask |= 1u << i;
+  return mask;
+}
+
+// Row t into a slot.
+template <int N>
+__device__ __forceinline__ void ring_copy(uint32_t mask, const RowSource (&src)[N], unsigned char *slot, uint64_t *bar,
+                                          int64_t t) {
+  if (mask == 0) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!(mask >> i & 1u)) continue;
+    mbar_arrive_expect_tx(bar, (uint32_t)src[i].bytes);
+    bulk_load(slot + src[i].at, src[i].base + t * src[i].stride, (uint32_t)src[i].bytes, bar);
   }
 }
 
+// Waits for this block's own copies.  One that gives up is reported, and the
+// caller begins no other.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (clock64() - t0 < kRingLimit)
+    if (mbar_try_wait(bar, parity)) return true;
+  report_status(status, kStatusTimeout);
+  return false;
+}
+
+// Column constants in shared memory: 8 columns of vector c in two planes, so
+// that neighbouring threads' 16-byte reads do not share banks.
+__device__ __forceinline__ void put_columns(float4 *plane, int vecs, int c, const F8 &f) {
+  plane[c] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+  plane[vecs + c] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+}
+__device__ __forceinline__ void get_columns(const float4 *plane, int vecs, int c, P2 (&w)[4]) {
+  const float4 a = plane[c], b = plane[vecs + c];
+  w[0] = pair(a.x, a.y);
+  w[1] = pair(a.z, a.w);
+  w[2] = pair(b.x, b.y);
+  w[3] = pair(b.z, b.w);
+}
+
+// weight_offset + w, or 1 without a weight.
+__device__ __forceinline__ F8 offset_weight(const void *w, int dtype, int c, float offset) {
+  F8 f;
+  if (w) {
+    f = load8_any(w, dtype, 8 * c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] += offset;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = 1.0f;
+  }
+  return f;
+}
+__device__ __forceinline__ F8 gate8(const void *gate, int dtype, bool sig, int64_t i) {
+  F8 f = load8_any(gate, dtype, i);
+  if (sig)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = sigmoid(f.v[j]);
+  return f;
+}
+// A full gate's 8 values from the ring.
+__device__ __forceinline__ F8 ring_gate8(const unsigned char *row, int c, int dtype, bool sig) {
+  F8 f;
+  if (dtype == MOE_BF16) {
+    f = unpack_bf16x8(*reinterpret_cast<const uint4 *>(row + 16 * c));
+  } else {
+    Raw8<float> r;
+    r.load(reinterpret_cast<const float *>(row) + 8 * c);
+    f = r.get();
+  }
+  if (sig)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = sigmoid(f.v[j]);
+  return f;
+}
+__device__ __forceinline__ void to_pairs(const F8 &f, P2 (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pair(f.v[2 * i], f.v[2 * i + 1]);
+}
+__device__ __forceinline__ float total(P2 p) {
+  const float2 f = split(p);
+  return f.x + f.y;
+}
+
+// FULL: a gate of each value.  ALL: a layer's answer, both norms and both outputs
+// are there (the branches on them cost as much as the arithmetic).
+template <typename XT, bool FULL, bool ALL>
+__global__ void __launch_bounds__(kThreads, 1)
+    norm_forward_kernel(const __grid_constant__ moe_norm_args a, const RingShape sh) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ RingSmem sm;
+  const int H = (int)a.H, vecs = H >> 3;
+  const bool sig = a.gate_sigmoid != 0;
+  const bool has_b = ALL || a.b, post = ALL || a.w_post, out_y = ALL || (a.b && a.y), out_n = ALL || a.n;
+  const int gate_size = a.gate_dtype == MOE_F32 ? 4 : 2;
+  RowSource src[3] = {{static_cast<const char *>(a.x), a.ldx * (int64_t)sizeof(XT), H * (int)sizeof(XT), 0},
+                      {reinterpret_cast<const char *>(a.b), a.ldb * 2, has_b ? H * 2 : 0, 0},
+                      {static_cast<const char *>(a.gate), a.ld_gate * gate_size, FULL ? H * gate_size : 0, 0}};
+  const int row_bytes = place_rows(src);
+  const int group = (int)threadIdx.x / sh.group, tid = (int)threadIdx.x - group * sh.group;
+  const int warps = sh.group >> 5, warp = tid >> 5;
+  const unsigned T = (unsigned)a.T, first = blockIdx.x * (unsigned)sh.groups + (unsigned)group,
+                 n = gridDim.x * (unsigned)sh.groups, ahead = (unsigned)sh.stages * n;
+  unsigned char *ring = ring_smem + (size_t)group * sh.stages * row_bytes;
+  const uint32_t copies = my_copies(src, warps, warp);
+  ring_init(sm, sh, src);
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int s = 0; s < sh.stages; ++s)
+    if (first + s * n < T) ring_copy(copies, src, ring + s * row_bytes, &sm.full[group][s], first + s * n);
+  const float inv_h = 1.0f / (float)H;
+  auto sync = [&] {
+    if (warps == 1) __syncwarp(); else named_bar_sync(1 + group, sh.group);
+  };
+  // the weight after the layer times a channel gate; the weight before the next
+  P2 c_post[V][4], c_pre[V][4];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * sh.group;
+    if (c >= vecs) continue;
+    F8 f = offset_weight(a.w_post, a.w_dtype, c, a.weight_offset);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f.v[j] *= z.v[j];
+    }
+    to_pairs(f, c_post[i]);
+    to_pairs(offset_weight(a.w_pre, a.w_dtype, c, a.weight_offset), c_pre[i]);
+  }
+  const P2 scale = twice(a.b ? a.residual_scale : 1.0f);
+  XT *py = static_cast<XT *>(a.y) + first * a.ldy + 8 * tid;
+  uint16_t *pn = a.n + first * a.ldn + 8 * tid;
+  const int64_t step_y = n * a.ldy, step_n = n * a.ldn;
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (unsigned t = first; t < T; t += n, turn ^= 1) {
+    unsigned char *row = ring + stage * row_bytes;
+    if (ok) ok = ring_wait(&sm.full[group][stage], phase, nullptr);
+    P2 y[V][4], u[V][4], sq = twice(0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * sh.group;
+      if (c >= vecs) continue;
+      Raw8<XT> x;
+      x.load(reinterpret_cast<const XT *>(row) + 8 * c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[i][k] = scale * x.two(k);
+      if (has_b) {
+        Raw8<uint16_t> b;
+        b.load(reinterpret_cast<const uint16_t *>(row + src[1].at) + 8 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          u[i][k] = b.two(k);
+          sq = fma2(u[i][k], u[i][k], sq);
+          u[i][k] = u[i][k] * c_post[i][k];
+        }
+        if (FULL) {
+          P2 z[4];
+          to_pairs(ring_gate8(row + src[2].at, c, a.gate_dtype, sig), z);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[i][k] = u[i][k] * z[k];
+        }
+      }
+    }
+    float rb = 1.0f;
+    if (post) {
+      float s[1] = {total(sq)};
+      group_sum(s, warps, warp, sm.red[group][turn][0], sync);
+      rb = rsqrtf(s[0] * inv_h + a.eps);
+    } else {
+      sync();
+    }
+    // the row is in registers: its slot takes the row after the ring's
+    if (T - t > ahead) ring_copy(copies, src, row, &sm.full[group][stage], t + ahead);
+    if (++stage == sh.stages) { stage = 0; phase ^= 1; }
+    if (a.gate_kind == MOE_GATE_TOKEN) {
+      const float z = load1_any(a.gate, a.gate_dtype, t);
+      rb *= sig ? sigmoid(z) : z;
+    }
+    sq = twice(0.f);
+    const P2 rb2 = twice(rb);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (tid + i * sh.group >= vecs) continue;
+      if (has_b) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[i][k] = fma2(u[i][k], rb2, y[i][k]);
+        if (out_y) store_pairs(py + 8 * i * sh.group, y[i]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sq = fma2(y[i][k], y[i][k], sq);
+    }
+    py += step_y;
+    if (!out_n) continue;
+    float s[1] = {total(sq)};
+    group_sum(s, warps, warp, sm.red[group][turn][1], sync);
+    const P2 r2 = twice(rsqrtf(s[0] * inv_h + a.eps));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (tid + i * sh.group >= vecs) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[i][k] = y[i][k] * r2 * c_pre[i][k];
+      store_pairs(pn + 8 * i * sh.group, y[i]);
+    }
+    pn += step_n;
+  }
+}
+
+// Column sums over rows: of dn h (dw_pre) and of S = d b rsqrt(mean b^2 + eps)
+// (times a token's or a value's gate), from which norm_parts_kernel makes
+// dw_post and a channel gate's dgate.  Each thread adds up its group's rows in
+// registers, in row order, a block adds its groups' sums in order and leaves one
+// part; norm_parts_kernel adds the parts in block order.
+enum : int { kSumPre = 0, kSumPost = 1 };
+
+// FULL, ALL as above (ALL: and all gradients of rows).  Values stay in
+// registers as they lie in memory: a spilled register goes through the little
+// L1 that the ring leaves, and costs more than unpacking twice.  A float32 dy is
+// loaded directly, from L2 where its row was brought one row before: with it in
+// the ring, a slot of 7168 columns fits only once.  With a full gate or a
+// float32 stream the row is read again from its slot after the first sum
+// (kLate), and the slot is free after the second.
+template <typename XT, bool FULL, bool ALL>
+__global__ void __launch_bounds__(kThreads, 1)
+    norm_backward_kernel(const __grid_constant__ moe_norm_args a, const __grid_constant__ moe_norm_grads g,
+                         const RingShape sh, int *status, float *parts) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ RingSmem sm;
+  const int H = (int)a.H, vecs = H >> 3;
+  const bool token = a.gate_kind == MOE_GATE_TOKEN, sig = a.gate_sigmoid != 0;
+  const bool has_b = ALL || a.b, post = ALL || a.w_post, pre = ALL || a.w_pre, has_dy = ALL || g.dy, out_dx = ALL || g.dx,
+             out_db = ALL || g.db;
+  constexpr bool kDirect = sizeof(XT) == 4, kLate = FULL || kDirect;
+  const int xb = H * (int)sizeof(XT), gate_size = a.gate_dtype == MOE_F32 ? 4 : 2;
+  RowSource src[5] = {
+      {static_cast<const char *>(a.x), a.ldx * (int64_t)sizeof(XT), pre ? xb : 0, 0},
+      {reinterpret_cast<const char *>(g.dn), g.ld_dn * 2, pre ? H * 2 : 0, 0},
+      {static_cast<const char *>(g.dy), g.ld_dy * (int64_t)sizeof(XT), has_dy && !kDirect ? xb : 0, 0},
+      {reinterpret_cast<const char *>(a.b), a.ldb * 2, has_b ? H * 2 : 0, 0},
+      {static_cast<const char *>(a.gate), a.ld_gate * gate_size, FULL ? H * gate_size : 0, 0}};
+  const int row_bytes = place_rows(src);
+  const int group = (int)threadIdx.x / sh.group, tid = (int)threadIdx.x - group * sh.group;
+  const int warps = sh.group >> 5, warp = tid >> 5;
+  const unsigned T = (unsigned)a.T, first = blockIdx.x * (unsigned)sh.groups + (unsigned)group,
+                 n = gridDim.x * (unsigned)sh.groups, ahead = (unsigned)sh.stages * n;
+  // column constants, then the rings
+  float4 *c_pre = reinterpret_cast<float4 *>(ring_smem), *c_post = c_pre + 2 * vecs;
+  unsigned char *ring = ring_smem + 2 * H * 4 + (size_t)group * sh.stages * row_bytes;
+  const uint32_t copies = my_copies(src, warps, warp);
+  ring_init(sm, sh, src);
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int s = 0; s < sh.stages; ++s)
+    if (first + s * n < T) ring_copy(copies, src, ring + s * row_bytes, &sm.full[group][s], first + s * n);
+  if (blockIdx.x == 0 && threadIdx.x < 16) status[threadIdx.x] = 0;
+  for (int c = (int)threadIdx.x; c < vecs; c += (int)blockDim.x) {
+    put_columns(c_pre, vecs, c, offset_weight(a.w_pre, a.w_dtype, c, a.weight_offset));
+    F8 f = offset_weight(a.w_post, a.w_dtype, c, a.weight_offset);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f.v[j] *= z.v[j];
+    }
+    put_columns(c_post, vecs, c, f);
+  }
+  __syncthreads();
+  const float inv_h = 1.0f / (float)H;
+  auto sync = [&] {
+    if (warps == 1) __syncwarp(); else named_bar_sync(1 + group, sh.group);
+  };
+  P2 sum_pre[V][4], sum_post[V][4];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum_pre[i][k] = sum_post[i][k] = twice(0.f);
+  const P2 scale = twice(a.b ? a.residual_scale : 1.0f);
+  XT *px = static_cast<XT *>(g.dx) + first * g.ld_dx + 8 * tid;
+  uint16_t *pb = g.db + first * g.ld_db + 8 * tid;
+  const int64_t step_x = n * g.ld_dx, step_b = n * g.ld_db;
+  const XT *pd = static_cast<const XT *>(g.dy) + first * g.ld_dy + 8 * tid;
+  const int64_t step_d = n * g.ld_dy;
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (unsigned t = first; t < T; t += n, turn ^= 1) {
+    unsigned char *row = ring + stage * row_bytes;
+    uint64_t *full = &sm.full[group][stage];
+    Raw8<XT> y[V], dy[V];
+    Raw8<uint16_t> dn[V], b[V];
+    if (kDirect && has_dy) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (tid + i * sh.group < vecs) dy[i].load(pd + 8 * i * sh.group);
+      pd += step_d;
+      if (tid == 0 && T - t > n) prefetch_l2_bulk(pd, (uint32_t)xb);
+    }
+    if (ok) ok = ring_wait(full, phase, status);
+    // sums of y^2, dn w y and b^2
+    P2 s0 = twice(0.f), s1 = s0, s2 = s0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * sh.group;
+      if (c >= vecs) continue;
+      if (pre) {
+        y[i].load(reinterpret_cast<const XT *>(row) + 8 * c);
+        dn[i].load(reinterpret_cast<const uint16_t *>(row + src[1].at) + 8 * c);
+        P2 w[4];
+        get_columns(c_pre, vecs, c, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s0 = fma2(y[i].two(k), y[i].two(k), s0);
+          s1 = fma2(dn[i].two(k) * w[k], y[i].two(k), s1);
+        }
+      }
+      if (!kDirect && has_dy) dy[i].load(reinterpret_cast<const XT *>(row + src[2].at) + 8 * c);
+      if (has_b) {
+        b[i].load(reinterpret_cast<const uint16_t *>(row + src[3].at) + 8 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s2 = fma2(b[i].two(k), b[i].two(k), s2);
+      }
+    }
+    float s[3] = {total(s0), total(s1), total(s2)};
+    group_sum(s, warps, warp, sm.red[group][turn][0], sync);
+    // the row is in registers: its slot takes the row after the ring's
+    if (!kLate && T - t > ahead) ring_copy(copies, src, row, full, t + ahead);
+    if (++stage == sh.stages) { stage = 0; phase ^= 1; }
+    const float r = rsqrtf(s[0] * inv_h + a.eps);
+    const float rb = post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
+    float gate_t = 1.0f;
+    if (token) {
+      gate_t = load1_any(a.gate, a.gate_dtype, t);
+      if (sig) gate_t = sigmoid(gate_t);
+    }
+    const P2 rs = twice(rb * gate_t);
+    const P2 r2 = twice(r), back = twice(-r * r * r * s[1] * inv_h);
+    P2 d[V][4], q2 = twice(0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * sh.group;
+      if (c >= vecs) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[i][k] = has_dy ? dy[i].two(k) : twice(0.f);
+      if (pre) {
+        // d += r dn w - y r^2 mean(dn w h)
+        if (kLate) {
+          y[i].load(reinterpret_cast<const XT *>(row) + 8 * c);
+          dn[i].load(reinterpret_cast<const uint16_t *>(row + src[1].at) + 8 * c);
+        }
+        P2 w[4];
+        get_columns(c_pre, vecs, c, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const P2 m = dn[i].two(k) * r2, f = y[i].two(k);
+          d[i][k] = fma2(m, w[k], d[i][k]);
+          d[i][k] = fma2(f, back, d[i][k]);
+          sum_pre[i][k] = fma2(m, f, sum_pre[i][k]);
+        }
+      }
+      if (out_dx) {
+        P2 o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = d[i][k] * scale;
+        store_pairs(px + 8 * i * sh.group, o);
+      }
+      if (has_b) {
+        P2 w[4];
+        get_columns(c_post, vecs, c, w);
+        if (FULL) {
+          P2 dz[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            P2 v;
+            if (a.gate_dtype == MOE_BF16) {
+              v = from_bf16x2(reinterpret_cast<const uint32_t *>(row + src[4].at)[4 * c + k]);
+            } else {
+              const float2 z = reinterpret_cast<const float2 *>(row + src[4].at)[4 * c + k];
+              v = pair(z.x, z.y);
+            }
+            dz[k] = d[i][k] * b[i].two(k) * w[k] * rs;
+            if (sig) {
+              const float2 z = split(v);
+              const float z0 = sigmoid(z.x), z1 = sigmoid(z.y);
+              v = pair(z0, z1);
+              dz[k] = dz[k] * pair(z0 * (1.0f - z0), z1 * (1.0f - z1));
+            }
+            d[i][k] = d[i][k] * v;
+          }
+          if (g.dgate) {
+            if (a.gate_dtype == MOE_BF16)
+              store_pairs(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
+            else
+              store_pairs(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const P2 p = d[i][k] * b[i].two(k);
+          sum_post[i][k] = fma2(p, rs, sum_post[i][k]);
+          q2 = fma2(p, w[k], q2);
+          d[i][k] = d[i][k] * w[k];
+        }
+      }
+    }
+    px += step_x;
+    if (!has_b) {
+      if (kLate) {
+        sync();
+        if (T - t > ahead) ring_copy(copies, src, row, full, t + ahead);
+      }
+      continue;
+    }
+    // q: the sum of d g w b (token gates: without g)
+    float q[1] = {total(q2)};
+    if (post || token) group_sum(q, warps, warp, sm.red[group][turn][1], sync);
+    if (kLate) {
+      if (!(post || token)) sync();
+      if (T - t > ahead) ring_copy(copies, src, row, full, t + ahead);
+    }
+    if (token && g.dgate && tid == 0)
+      store1_any(g.dgate, a.gate_dtype, t, (sig ? gate_t * (1.0f - gate_t) : 1.0f) * q[0] * rb);
+    if (out_db) {
+      // db = rb (g d w - h mean(g d w h)) = rs d w - b g rb^3 q / H
+      const P2 back_b = twice(post ? -rb * rb * rb * q[0] * gate_t * inv_h : 0.f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (tid + i * sh.group >= vecs) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[i][k] = fma2(b[i].two(k), back_b, d[i][k] * rs);
+        store_pairs(pb + 8 * i * sh.group, d[i]);
+      }
+    }
+    pb += step_b;
+  }
+  // the block's part: its groups' sums, in group order, by way of the ring's
+  // memory (no copy is in flight: every row that was asked for was waited for)
+  float *part = parts + (int64_t)blockIdx.x * 2 * H;
+  float *join = reinterpret_cast<float *>(ring_smem + 2 * H * 4);
+  const bool wanted[2] = {g.dw_pre != nullptr, g.dw_post != nullptr || (a.gate_kind == MOE_GATE_CHANNEL && g.dgate)};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!wanted[k]) continue;
+    for (int from = 0; from < sh.groups; ++from) {
+      if (sh.groups > 1) __syncthreads();
+      if (group != from) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * sh.group;
+        if (c >= vecs) continue;
+        P2(&sum)[4] = k == kSumPre ? sum_pre[i] : sum_post[i];
+        if (from > 0) {
+          Raw8<float> before;
+          before.load(join + 8 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[j] = before.two(j) + sum[j];
+        }
+        store_pairs(from + 1 < sh.groups ? join + 8 * c : part + k * H + 8 * c, sum);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- wide rows, in registers
+
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
+  group_sum(v, (int)(blockDim.x >> 5), (int)(threadIdx.x >> 5), red, [] { __syncthreads(); });
+}
+
 template <typename XT, int V>
-__global__ void norm_forward_kernel(const moe_norm_args a) {
+__global__ void norm_forward_wide_kernel(const moe_norm_args a) {
   __shared__ float red[2][kMaxWarps];
+  if (threadIdx.x < 2 * kMaxWarps) red[0][threadIdx.x] = 0.f;     // a row has at least 1024 / 4 threads here
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
   const int64_t t = blockIdx.x;
@@ -193,23 +805,20 @@ __global__ void norm_forward_kernel(const moe_norm_args a) {
   }
 }
 
-// Column sums over rows (dw_pre, dw_post, dgate of a channel gate): each block
-// adds up its rows' values in registers, in row order, and leaves one part;
-// norm_parts_kernel adds the parts in block order.
-enum : int { kSumPre = 0, kSumPost = 1, kSumGate = 2 };
-
 template <typename XT, int V>
-__global__ void __launch_bounds__(kBackwardThreads) norm_backward_kernel(const moe_norm_args a, const moe_norm_grads g,
-                                                                         float *parts) {
-  __shared__ float red_buf[2][4 * kMaxWarps];      // of even and odd rows
+__global__ void __launch_bounds__(kBackwardThreads) norm_backward_wide_kernel(const moe_norm_args a,
+                                                                              const moe_norm_grads g, float *parts) {
+  __shared__ float red_buf[2][5 * kMaxWarps];      // of even and odd rows
   int turn = 0;
+  for (int i = (int)threadIdx.x; i < 10 * kMaxWarps; i += (int)blockDim.x) red_buf[0][i] = 0.f;
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
   const int H = (int)a.H, vecs = H >> 3;
   const float inv_h = 1.0f / (float)H;
-  F8 sums[3][V];
+  F8 sums[2][V];
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -309,28 +918,28 @@ __global__ void __launch_bounds__(kBackwardThreads) norm_backward_kernel(const m
             for (int j = 0; j < 8; ++j) {
               const float gv = a.gate_sigmoid ? sigmoid(z.v[j]) : z.v[j];
               dz.v[j] = d[i].v[j] * f.v[j] * w.v[j];
-              if (full && a.gate_sigmoid) dz.v[j] *= gv * (1.0f - gv);
+              if (a.gate_sigmoid) dz.v[j] *= gv * (1.0f - gv);
+              if (!full) sums[kSumPost][i].v[j] = fmaf(d[i].v[j], f.v[j] * rb, sums[kSumPost][i].v[j]);
               d[i].v[j] *= gv;
             }
-            if (full) {
-              if (g.dgate) {
-                if (a.gate_dtype == MOE_BF16)
-                  store8(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
-                else
-                  store8(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) sums[kSumGate][i].v[j] += dz.v[j];
+            if (full && g.dgate) {
+              if (a.gate_dtype == MOE_BF16)
+                store8(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
+              else
+                store8(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
             }
           }
+          if (a.gate_kind != MOE_GATE_CHANNEL)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              sums[kSumPost][i].v[j] = fmaf(d[i].v[j] * gate_t, f.v[j] * rb, sums[kSumPost][i].v[j]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) q[0] = fmaf(d[i].v[j] * w.v[j], f.v[j], q[0]);
         }
       }
     }
     if (!a.b) continue;
-    if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) block_sum(q, red + 3 * kMaxWarps);
+    if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) block_sum(q, red + 4 * kMaxWarps);
     if (a.gate_kind == MOE_GATE_TOKEN && g.dgate && threadIdx.x == 0)
       store1_any(g.dgate, a.gate_dtype, t, a.gate_sigmoid ? q[0] * gate_t * (1.0f - gate_t) : q[0]);
     // db = rb (g d w - h mean(g d w h)); w above carries rb once, so with
@@ -348,7 +957,6 @@ __global__ void __launch_bounds__(kBackwardThreads) norm_backward_kernel(const m
           const F8 w = load8_any(a.w_post, a.w_dtype, 8 * c);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            sums[kSumPost][i].v[j] = fmaf(o.v[j], f.v[j] * rb, sums[kSumPost][i].v[j]);
             o.v[j] = o.v[j] * (w.v[j] + a.weight_offset) * rb - f.v[j] * back_b;
           }
         }
@@ -356,14 +964,13 @@ __global__ void __launch_bounds__(kBackwardThreads) norm_backward_kernel(const m
       }
     }
   }
-  float *part = parts + (int64_t)blockIdx.x * 3 * H;
+  float *part = parts + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (int)threadIdx.x + i * (int)blockDim.x;
     if (c < vecs) {
-      if (g.dw_pre) store8(part + kSumPre * H + 8 * c, sums[kSumPre][i]);
-      if (g.dw_post) store8(part + kSumPost * H + 8 * c, sums[kSumPost][i]);
-      if (a.gate_kind == MOE_GATE_CHANNEL && g.dgate) store8(part + kSumGate * H + 8 * c, sums[kSumGate][i]);
+      store8(part + kSumPre * H + 8 * c, sums[kSumPre][i]);
+      store8(part + kSumPost * H + 8 * c, sums[kSumPost][i]);
     }
   }
 }
@@ -375,14 +982,14 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const moe_norm_args a, 
   pdl_launch_dependents();
   pdl_wait();
   const int H = (int)a.H, which = blockIdx.y;
-  const bool wanted = which == kSumPre ? g.dw_pre != nullptr
-                      : which == kSumPost ? g.dw_post != nullptr
-                                          : a.gate_kind == MOE_GATE_CHANNEL && g.dgate != nullptr;
-  if (!wanted) return;
+  const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+  if (which == kSumPre ? g.dw_pre == nullptr : g.dw_post == nullptr && !(channel && g.dgate)) return;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
   float s = 0.f;
-  if (c < H)
-    for (int p = k; p < n; p += 8) s += parts[((int64_t)p * 3 + which) * H + c];
+  if (c < H) {
+#pragma unroll 8
+    for (int p = k; p < n; p += 8) s += parts[((int64_t)p * 2 + which) * H + c];
+  }
   red[k][threadIdx.x & 31] = s;
   __syncthreads();
   if (k != 0 || c >= H) return;
@@ -390,15 +997,21 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const moe_norm_args a, 
   for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
   if (which == kSumPre) {
     g.dw_pre[c] = s;
-  } else if (which == kSumPost) {
-    g.dw_post[c] = s;
-  } else {
-    if (a.gate_sigmoid) {
-      const float v = sigmoid(load1_any(a.gate, a.gate_dtype, c));
-      s *= v * (1.0f - v);
-    }
-    store1_any(g.dgate, a.gate_dtype, c, s);
+    return;
   }
+  float gv = 1.0f, slope = 1.0f;
+  if (channel) {
+    gv = load1_any(a.gate, a.gate_dtype, c);
+    if (a.gate_sigmoid) {
+      gv = sigmoid(gv);
+      slope = gv * (1.0f - gv);
+    }
+    if (g.dgate) {
+      const float w = a.w_post ? load1_any(a.w_post, a.w_dtype, c) + a.weight_offset : 1.0f;
+      store1_any(g.dgate, a.gate_dtype, c, s * w * slope);
+    }
+  }
+  if (g.dw_post) g.dw_post[c] = s * gv;
 }
 
 // ---------------------------------------------------------------- host
@@ -432,37 +1045,121 @@ int check_norm(const moe_norm_args *a) {
   return rc;
 }
 
-struct Shape {
-  int threads, v;      // threads per row, vectors per thread (1, 2 or 4)
+// The most shared memory that a block's ring and column constants may have.
+constexpr int kMaxRingBytes = 208 * 1024;
+constexpr int kMaxRingH = 8192;
+
+struct RingLaunch {
+  RingShape shape;
+  int blocks, smem;
+  bool ok;
 };
 
-// Threads of a row: `v` vectors each, in whole warps.
+// Rows of up to 4096 columns share a block where there are `many`, more than
+// SMs; as many blocks per SM as have 512 threads (128 registers each).
+void block_shape(int64_t H, bool many, RingShape &s, int &per_sm) {
+  s.group = (int)round_up((size_t)ceil_div(H, 8 * V), 32);
+  s.groups = many ? std::max(1, std::min(kMaxGroups, kThreads / s.group)) : 1;
+  per_sm = std::min(4, std::max(1, kThreads / (s.group * s.groups)));
+}
+
+// Most blocks of a backward launch (parts in the workspace).
+int most_parts(int64_t T, int64_t H) {
+  RingShape s;
+  int per_sm;
+  block_shape(H, true, s, per_sm);
+  return (int)std::min<int64_t>(T, 160 * std::max(2, per_sm));
+}
+
+// As many stages as a block's share of the shared memory holds, but no more
+// than a group has rows.
+RingLaunch ring_launch(int64_t T, int64_t H, int row_bytes, int constants) {
+  RingLaunch l{};
+  int per_sm;
+  block_shape(H, T > num_sms(), l.shape, per_sm);
+  l.blocks = (int)std::min<int64_t>({ceil_div(T, l.shape.groups), (int64_t)per_sm * num_sms(), most_parts(T, H)});
+  const int ring = kMaxRingBytes / per_sm - (per_sm - 1) * 10 * 1024 - constants;
+  l.shape.stages = (int)std::min<int64_t>({kMaxStages, ring / (l.shape.groups * row_bytes),
+                                           ceil_div(T, (int64_t)l.blocks * l.shape.groups)});
+  l.smem = std::max(l.shape.stages * l.shape.groups * row_bytes, (int)H * 4) + constants;
+  l.ok = H <= kMaxRingH && ring > 0 && l.shape.stages > 0;
+  return l;
+}
+
+template <typename Kernel>
+bool allow_smem(Kernel kernel, std::atomic<uint64_t> &ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (ready.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRingBytes) != cudaSuccess) return false;
+  ready.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
+// Threads of a wide row: v vectors of 8 columns each, in whole warps.
+struct Shape {
+  int threads, v;
+};
 Shape row_shape(int64_t H, int v, int most) {
   const int vecs = (int)(H / 8);
   while (v < 4 && (vecs + v - 1) / v > most) v *= 2;
   return {(int)round_up((size_t)((vecs + v - 1) / v), 32), v};
 }
 
-template <typename XT>
-int forward_launch(const moe_norm_args &a, cudaStream_t st) {
-  const Shape s = row_shape(a.H, a.T <= 4 * num_sms() ? 1 : 4, 1024);
-  auto kernel = s.v == 1 ? norm_forward_kernel<XT, 1> : s.v == 2 ? norm_forward_kernel<XT, 2> : norm_forward_kernel<XT, 4>;
-  return launch_pdl(kernel, dim3((unsigned)a.T), dim3(s.threads), 0, st, a);
+int gate_row_bytes(const moe_norm_args &a) {
+  return a.gate_kind == MOE_GATE_FULL ? (int)a.H * (a.gate_dtype == MOE_F32 ? 4 : 2) : 0;
 }
 
-int backward_parts(int64_t T) { return (int)std::min<int64_t>(T, std::min(2 * num_sms(), kMaxParts)); }
+template <typename XT>
+int forward_launch(const moe_norm_args &a, cudaStream_t st) {
+  const RingLaunch l = ring_launch(a.T, a.H, (int)a.H * ((int)sizeof(XT) + (a.b ? 2 : 0)) + gate_row_bytes(a), 0);
+  if (l.ok) {
+    const int threads = l.shape.group * l.shape.groups;
+    static std::atomic<uint64_t> ready[3];
+    auto run = [&](auto kernel, std::atomic<uint64_t> &r) -> int {
+      return allow_smem(kernel, r) ? launch_pdl(kernel, dim3(l.blocks), dim3(threads), l.smem, st, a, l.shape) : MOE_ERR_CUDA;
+    };
+    const bool all = a.b && a.w_post && a.w_pre && a.y;
+    if (a.gate_kind == MOE_GATE_FULL) return run(norm_forward_kernel<XT, true, false>, ready[0]);
+    return all ? run(norm_forward_kernel<XT, false, true>, ready[1]) : run(norm_forward_kernel<XT, false, false>, ready[2]);
+  }
+  const Shape s = row_shape(a.H, 2, 1024);
+  return launch_pdl(s.v == 2 ? norm_forward_wide_kernel<XT, 2> : norm_forward_wide_kernel<XT, 4>, dim3((unsigned)a.T),
+                    dim3(s.threads), 0, st, a);
+}
 
 template <typename XT>
 int backward_launch(const moe_norm_args &a, const moe_norm_grads &g, cudaStream_t st) {
-  const Shape s = row_shape(a.H, 2, kBackwardThreads);
-  float *parts = static_cast<float *>(g.workspace);
-  auto kernel = s.v == 2 ? norm_backward_kernel<XT, 2> : norm_backward_kernel<XT, 4>;
-  const int n = backward_parts(a.T);
-  const int rc = launch_pdl(kernel, dim3(n), dim3(s.threads), 0, st, a, g, parts);
+  int *status = static_cast<int *>(g.workspace);
+  float *parts = reinterpret_cast<float *>(static_cast<char *>(g.workspace) + kStatusBytes);
+  const int x = (int)sizeof(XT), H = (int)a.H;
+  const RingLaunch l = ring_launch(a.T, a.H, H * ((a.w_pre ? x + 2 : 0) + (g.dy && x == 2 ? x : 0) + (a.b ? 2 : 0)) + gate_row_bytes(a),
+                                   8 * H);
+  int n = l.blocks, rc;
+  if (l.ok) {
+    const int threads = l.shape.group * l.shape.groups;
+    static std::atomic<uint64_t> ready[3];
+    auto run = [&](auto kernel, std::atomic<uint64_t> &r) -> int {
+      return allow_smem(kernel, r) ? launch_pdl(kernel, dim3(n), dim3(threads), l.smem, st, a, g, l.shape, status, parts)
+                                   : MOE_ERR_CUDA;
+    };
+    const bool all = a.b && a.w_post && a.w_pre && g.dy && g.dx && g.db;
+    if (a.gate_kind == MOE_GATE_FULL)
+      rc = run(norm_backward_kernel<XT, true, false>, ready[0]);
+    else
+      rc = all ? run(norm_backward_kernel<XT, false, true>, ready[1]) : run(norm_backward_kernel<XT, false, false>, ready[2]);
+  } else {
+    if (cudaMemsetAsync(status, 0, 64, st) != cudaSuccess) return MOE_ERR_CUDA;
+    n = std::min(most_parts(a.T, a.H), 2 * num_sms());
+    const Shape s = row_shape(a.H, 2, kBackwardThreads);
+    rc = launch_pdl(s.v == 2 ? norm_backward_wide_kernel<XT, 2> : norm_backward_wide_kernel<XT, 4>, dim3(n),
+                    dim3(s.threads), 0, st, a, g, parts);
+  }
   if (rc != MOE_OK) return rc;
   const bool gate = a.gate_kind == MOE_GATE_CHANNEL && g.dgate;
   if (!g.dw_pre && !g.dw_post && !gate) return MOE_OK;
-  return launch_pdl(norm_parts_kernel, dim3((unsigned)ceil_div(a.H, 32), gate ? 3 : g.dw_post ? 2 : 1), dim3(256), 0, st,
+  return launch_pdl(norm_parts_kernel, dim3((unsigned)ceil_div(a.H, 32), g.dw_post || gate ? 2 : 1), dim3(256), 0, st,
                     a, g, static_cast<const float *>(parts), n);
 }
 
@@ -483,7 +1180,7 @@ extern "C" int moe_norm_forward(const moe_norm_args *a, cudaStream_t stream) {
 
 extern "C" size_t moe_norm_workspace_size(int64_t T, int64_t H) {
   if (T < 0 || H <= 0 || H > kMaxH) return 0;
-  return round_up((size_t)std::min<int64_t>(T, kMaxParts) * 3 * (size_t)H * 4, 256) + 256;
+  return kStatusBytes + round_up((size_t)most_parts(T, H) * 2 * (size_t)H * 4, 256);
 }
 
 extern "C" int moe_norm_backward(const moe_norm_args *a, const moe_norm_grads *g, cudaStream_t stream) {
@@ -496,6 +1193,7 @@ extern "C" int moe_norm_backward(const moe_norm_args *a, const moe_norm_grads *g
   if (g->workspace_bytes < moe_norm_workspace_size(a->T, a->H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (a->T == 0) {
     const size_t w = (size_t)a->H * 4;
+    if (cudaMemsetAsync(g->workspace, 0, 64, stream) != cudaSuccess) return MOE_ERR_CUDA;
     if (g->dw_pre && cudaMemsetAsync(g->dw_pre, 0, w, stream) != cudaSuccess) return MOE_ERR_CUDA;
     if (g->dw_post && cudaMemsetAsync(g->dw_post, 0, w, stream) != cudaSuccess) return MOE_ERR_CUDA;
     if (g->dgate && a->gate_kind == MOE_GATE_CHANNEL &&
