@@ -139,29 +139,25 @@ __device__ __forceinline__ V8 decode8(const uint2 &c, uint32_t byte) {
   return r;
 }
 
-// Codes and scale byte of a 32-value group spread over four lanes; kRoot: a
-// value above zero takes at least the smallest code, 2^-9.
-template <bool kRoot>
-__device__ __forceinline__ uint2 encode8(const V8 &f, uint8_t *byte) {
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f.v[j]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const int e = ue8m0_exponent<true>(amax);
+// The largest of four lanes' values (a group's 32).
+__device__ __forceinline__ float group_max(float a) {
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+// Codes of eight values under the scale 2^e.
+__device__ __forceinline__ uint2 encode8(const V8 &f, int e) {
   const float inv = pow2_neg(e);
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = f.v[2 * i] * inv, b = f.v[2 * i + 1] * inv;
-    if (kRoot) {
-      if (f.v[2 * i] > 0.f) a = fmaxf(a, 0.001953125f);
-      if (f.v[2 * i + 1] > 0.f) b = fmaxf(b, 0.001953125f);
-    }
-    c[i] = cvt_e4m3x2(a, b);
-  }
-  *byte = (uint8_t)(e + 127);
+  for (int i = 0; i < 4; ++i) c[i] = cvt_e4m3x2(f.v[2 * i] * inv, f.v[2 * i + 1] * inv);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {              // within 2 units in the last place
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <typename PT, typename GT, bool kSmall, int TENSORS>
@@ -200,16 +196,38 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const float old = kSmall ? __fmul_rn(v.v[j], v.v[j]) : v.v[j];
         m.v[j] = __fadd_rn(__fmul_rn(m.v[j], a.beta1), __fmul_rn(gj, a.one_minus_beta1));
         v.v[j] = __fadd_rn(__fmul_rn(old, a.beta2), __fmul_rn(__fmul_rn(gj, gj), a.one_minus_beta2));
-        root.v[j] = __fsqrt_rn(v.v[j]);
+        root.v[j] = sqrt_approx(v.v[j]);
         p.v[j] = p.v[j] * a.keep - a.rate * __fdividef(m.v[j], fmaf(root.v[j], a.root_scale, a.eps));
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.v[j] = m.v[j] = root.v[j] = 0.f;
+      for (int j = 0; j < 8; ++j) p.v[j] = m.v[j] = v.v[j] = root.v[j] = 0.f;
     }
     if (kSmall) {
-      uint8_t mb, vb;
-      const uint2 mc = encode8<false>(m, &mb), vc = encode8<true>(root, &vb);
+      // scales: the root of the largest v is the largest root
+      float m_max = 0.f, v_max = 0.f;
+      // a code changes where a root passes a multiple of 2^19 units of its last
+      // place; the approximate root decides unless it is that near (about one
+      // value in 100 000)
+      uint32_t near = 0xffffffffu;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m_max = fmaxf(m_max, fabsf(m.v[j]));
+        v_max = fmaxf(v_max, v.v[j]);
+        near = min(near, (__float_as_uint(root.v[j]) + 2u) & 0x7ffffu);
+      }
+      const int me = ue8m0_exponent<true>(group_max(m_max)), ve = ue8m0_exponent<true>(__fsqrt_rn(group_max(v_max)));
+      const uint8_t mb = (uint8_t)(me + 127), vb = (uint8_t)(ve + 127);
+      if (near <= 4u) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) root.v[j] = __fsqrt_rn(v.v[j]);
+      }
+      // a root above zero takes at least the smallest code
+      const float least = scale_of(vb) * 0.001953125f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (root.v[j] > 0.f) root.v[j] = fmaxf(root.v[j], least);
+      const uint2 mc = encode8(m, me), vc = encode8(root, ve);
       if (live > 0) {
         store_codes(static_cast<uint8_t *>(t.m) + i, mc, live);
         store_codes(static_cast<uint8_t *>(t.v) + i, vc, live);

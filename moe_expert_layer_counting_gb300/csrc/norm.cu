@@ -21,6 +21,7 @@
 
 #include "../../include/moe_norm.h"
 #include "host_common.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace mxq {
@@ -34,43 +35,6 @@ constexpr int kBackwardThreads = 512;
 struct F8 {
   float v[8];
 };
-
-// Two floats that one f32x2 instruction works on.
-struct P2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ P2 pair(float lo, float hi) {
-  P2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ P2 twice(float x) { return pair(x, x); }
-__device__ __forceinline__ float2 split(P2 p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
-  return f;
-}
-__device__ __forceinline__ P2 operator*(P2 a, P2 b) {
-  P2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ P2 operator+(P2 a, P2 b) {
-  P2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ P2 fma2(P2 a, P2 b, P2 c) {
-  P2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ P2 from_bf16x2(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
-__device__ __forceinline__ uint32_t to_bf16x2(P2 p) {
-  const float2 f = split(p);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
 
 __device__ __forceinline__ F8 unpack_bf16x8(const uint4 &q) {
   F8 f;
