@@ -2,9 +2,9 @@
 // formulas and the 8-bit states' format).
 //
 // Bound by HBM: 28 bytes a value with float32 states (p read and written, BF16
-// gradient and copy, m and v read and written), 14.1 with 8-bit states.  The
+// gradient and copy, m and v read and written), 16.1 with 8-bit states.  The
 // table of tensors travels in the kernel's parameters (no copy to the device,
-// nothing kept between calls), up to kTensors per launch; a block finds its
+// nothing kept between calls), up to kMany per launch; a block finds its
 // tensor by bisection of the tensors' first blocks.  A thread owns 8
 // consecutive values, four neighbours a 32-value group of the 8-bit states.
 #include <cuda_bf16.h>
@@ -46,18 +46,50 @@ struct V8 {
   float v[8];
 };
 
-__device__ __forceinline__ V8 load8(const float *p) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  return V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ V8 load8(const uint16_t *p) {
-  const uint4 q = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  V8 r;
+// Eight values as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ V8 get() const { return V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
+template <> struct Raw8<uint16_t> {
+  uint4 q;
+  __device__ __forceinline__ V8 get() const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    V8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = bf16_bits_to_float(w[i] & 0xFFFFu);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      r.v[2 * i] = bf16_bits_to_float(w[i] & 0xFFFFu);
+      r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    return r;
+  }
+};
+// `live` (1 .. 8) of them; the others read as zero.
+__device__ __forceinline__ Raw8<float> load_raw(const float *p, int live) {
+  Raw8<float> r;
+  if (live == 8) {
+    r.a = reinterpret_cast<const float4 *>(p)[0];
+    r.b = reinterpret_cast<const float4 *>(p)[1];
+  } else {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < live ? p[j] : 0.f;
+    r.a = make_float4(f[0], f[1], f[2], f[3]);
+    r.b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  return r;
+}
+__device__ __forceinline__ Raw8<uint16_t> load_raw(const uint16_t *p, int live) {
+  Raw8<uint16_t> r;
+  if (live == 8) {
+    r.q = *reinterpret_cast<const uint4 *>(p);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < live ? p[2 * i] : 0u) | (2 * i + 1 < live ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    r.q = make_uint4(w[0], w[1], w[2], w[3]);
   }
   return r;
 }
@@ -67,8 +99,6 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
 }
 __device__ __forceinline__ void put(float *p, float f) { *p = f; }
 __device__ __forceinline__ void put(uint16_t *p, float f) { *p = to_bf16(f); }
-__device__ __forceinline__ float get(const float *p) { return *p; }
-__device__ __forceinline__ float get(const uint16_t *p) { return bf16_bits_to_float(*p); }
 __device__ __forceinline__ void store8(float *p, const V8 &f) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
@@ -80,15 +110,7 @@ __device__ __forceinline__ void store8(uint16_t *p, const V8 &f) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// `live` (1 .. 8) of 8 values; the others read as zero and are not written.
-template <typename T>
-__device__ __forceinline__ V8 load_some(const T *p, int live) {
-  if (live == 8) return load8(p);
-  V8 r;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r.v[j] = j < live ? get(p + j) : 0.f;
-  return r;
-}
+// `live` (1 .. 8) of 8 values.
 template <typename T>
 __device__ __forceinline__ void store_some(T *p, const V8 &f, int live) {
   if (live == 8) {
@@ -172,22 +194,48 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const AdamEntry &t = a.t[lo];
   const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk;
   const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
+  // a round's loads are issued before the round before is worked on (352 M
+  // values with 8-bit states: 871 us instead of 1104; four rounds 1038, fewer
+  // registers for more blocks 1003 or worse)
+  struct Loaded {
+    Raw8<PT> p;
+    Raw8<GT> g;
+    Raw8<float> m, v;           // float32 states
+    uint2 mc, vc;               // 8-bit states
+    uint32_t ms, vs;
+  };
+  auto load = [&](int64_t i) {
+    Loaded x;
+    const int live = (int)(n - i < 0 ? 0 : n - i < 8 ? n - i : 8);
+    if (live > 0) {
+      x.p = load_raw(static_cast<const PT *>(t.p) + i, live);
+      x.g = load_raw(static_cast<const GT *>(t.g) + i, live);
+      if (kSmall) {
+        x.mc = load_codes(static_cast<const uint8_t *>(t.m) + i, live);
+        x.vc = load_codes(static_cast<const uint8_t *>(t.v) + i, live);
+        x.ms = t.ms[i >> 5];
+        x.vs = t.vs[i >> 5];
+      } else {
+        x.m = load_raw(static_cast<const float *>(t.m) + i, live);
+        x.v = load_raw(static_cast<const float *>(t.v) + i, live);
+      }
+    }
+    return x;
+  };
+  int64_t i = base + (int64_t)threadIdx.x * 8;
+  Loaded ahead = load(i);
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + ((int64_t)r * kThreads + threadIdx.x) * 8;
+  for (int r = 0; r < kRounds; ++r, i += 8 * kThreads) {
     if (kSmall ? i - 8 * (threadIdx.x & 31) >= n : i >= n) break;      // 8-bit states: whole warps go on
     const int live = (int)(n - i < 0 ? 0 : n - i < 8 ? n - i : 8);
+    const Loaded x = ahead;
+    if (r + 1 < kRounds) ahead = load(i + 8 * kThreads);
     V8 p, g, m, v, root;
     if (!kSmall || live > 0) {
-      p = load_some(static_cast<const PT *>(t.p) + i, live);
-      g = load_some(static_cast<const GT *>(t.g) + i, live);
-      if (kSmall) {
-        m = decode8(load_codes(static_cast<const uint8_t *>(t.m) + i, live), t.ms[i >> 5]);
-        v = decode8(load_codes(static_cast<const uint8_t *>(t.v) + i, live), t.vs[i >> 5]);
-      } else {
-        m = load_some(static_cast<const float *>(t.m) + i, live);
-        v = load_some(static_cast<const float *>(t.v) + i, live);
-      }
+      p = x.p.get();
+      g = x.g.get();
+      m = kSmall ? decode8(x.mc, x.ms) : x.m.get();
+      v = kSmall ? decode8(x.vc, x.vs) : x.v.get();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // each product and sum of m and v rounded by itself (no fused
