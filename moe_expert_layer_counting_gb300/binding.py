@@ -441,32 +441,35 @@ _NONE = (0, 0)
 def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid):
     """The bytes of MoeNormArgs for these tensors, or None if a type, shape or stride does not fit."""
     shape = T, H = x.shape
-    xt = _DTYPES.get(x.dtype)
-    xr = _rows(x, shape, x.dtype)
+    dtype = x.dtype
+    xt = _DTYPES.get(dtype)
+    xr = _rows(x, shape, dtype)
     br = _NONE if b is None else _rows(b, shape)
-    yr = _NONE if y is None else _rows(y, shape, x.dtype)
+    yr = _NONE if y is None else _rows(y, shape, dtype)
     nr = _NONE if n is None else _rows(n, shape)
     if xt is None or xr is None or br is None or yr is None or nr is None:
         return None
-    wt, post, pre = BF16, 0, 0
+    wt, post, pre, kinds = BF16, 0, 0, None
     if w_pre is not None:
-        wt, pre = _DTYPES.get(w_pre.dtype), w_pre.data_ptr()
+        kinds, pre = w_pre.dtype, w_pre.data_ptr()
+        wt = _DTYPES.get(kinds)
         if wt is None or w_pre.shape != (H,) or not w_pre.is_contiguous():
             return None
     if w_post is not None:
-        wt, post = _DTYPES.get(w_post.dtype), w_post.data_ptr()
-        if wt is None or w_post.shape != (H,) or not w_post.is_contiguous() or (w_pre is not None and w_pre.dtype is not w_post.dtype):
+        kind, post = w_post.dtype, w_post.data_ptr()
+        wt = _DTYPES.get(kind)
+        if wt is None or kinds not in (None, kind) or w_post.shape != (H,) or not w_post.is_contiguous():
             return None
     kind, gt, gr = GATE_NONE, BF16, _NONE
     if gate is not None:
         gt, gs = _DTYPES.get(gate.dtype), gate.shape
         if gt is None or len(gs) != 2:
             return None
-        kind = GATE_TOKEN if gs == (T, 1) else GATE_CHANNEL if gs == (1, H) else GATE_FULL
-        if kind != GATE_FULL:
+        if gs == (T, 1) or gs == (1, H):
+            kind = GATE_TOKEN if gs == (T, 1) else GATE_CHANNEL
             gr = (gate.data_ptr(), 0) if gate.is_contiguous() else None
         else:
-            gr = _rows(gate, shape, gate.dtype)
+            kind, gr = GATE_FULL, _rows(gate, shape, gate.dtype)
         if gr is None:
             return None
     return _NORM_ARGS.pack(_NORM_ARGS.size, xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale, weight_offset, eps,

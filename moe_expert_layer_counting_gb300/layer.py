@@ -145,43 +145,63 @@ class MoELayerBfp8:
 class BlockNorm:
     """The norms around the layer with its gate and residual scale, forward and backward (include/moe_norm.h).
 
-    w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.
+    w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.  The object keeps
+    a workspace for each stream that it is used on.
     """
 
     def __init__(self, w_post: torch.Tensor = None, w_pre: torch.Tensor = None, residual_scale: float = 1.0,
                  weight_offset: float = 0.0, eps: float = 1e-6, gate_sigmoid: bool = False):
         self.w_post, self.w_pre = w_post, w_pre
         self.how = (residual_scale, weight_offset, eps, gate_sigmoid)
+        self._workspaces = {}                       # stream handle -> (rows it is enough for, tensor)
 
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
         """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
-        with _on(stream):
-            y = torch.empty_like(x, memory_format=torch.contiguous_format) if b is not None else None
-            n = None
-            if self.w_pre is not None:
-                n = torch.empty_like(x if b is None else b, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-        B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, stream=stream)
+        if stream is not None:
+            with _on(stream):
+                return self._forward(x, b, gate, stream)
+        return self._forward(x, b, gate, None)
+
+    def _forward(self, x, b, gate, stream):
+        flat = torch.contiguous_format
+        y = torch.empty_like(x, memory_format=flat) if b is not None else None
+        n = None
+        if self.w_pre is not None:
+            n = torch.empty_like(x if b is None else b, dtype=torch.bfloat16, memory_format=flat)
+        B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, stream)
         return (x if y is None else y), n
 
     def backward(self, y: torch.Tensor, b: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, dn: torch.Tensor,
                  stream=None) -> dict:
         """Gradients dx, db, dgate, dw_post, dw_pre (None where there is nothing to differentiate) from those of
         forward's y and n (either may be None); y, b and gate are what forward returned and took."""
-        T, H = y.shape
+        if stream is not None:
+            with _on(stream):
+                return self._backward(y, b, gate, dy, dn, stream)
+        return self._backward(y, b, gate, dy, dn, None)
+
+    def _backward(self, y, b, gate, dy, dn, stream):
+        new, flat = torch.empty_like, torch.contiguous_format
         w_post = self.w_post if b is not None else None
-        with _on(stream):
-            new = torch.empty_like
-            flat = torch.contiguous_format
-            out = {"dx": new(y, memory_format=flat),
-                   "db": None if b is None else new(b, memory_format=flat),
-                   "dgate": None if gate is None else new(gate, memory_format=flat),
-                   "dw_post": None if w_post is None else new(w_post, dtype=torch.float32),
-                   "dw_pre": None if dn is None else new(self.w_pre, dtype=torch.float32)}
+        w_pre = self.w_pre if dn is not None else None
+        dx = new(y, memory_format=flat)
+        db = None if b is None else new(b, memory_format=flat)
+        dgate = None if gate is None else new(gate, memory_format=flat)
+        dw_post = None if w_post is None else new(w_post, dtype=torch.float32)
+        dw_pre = None if w_pre is None else new(w_pre, dtype=torch.float32)
+        handle = B._stream(stream)
+        rows, ws = self._workspaces.get(handle, (-1, None))
+        T, H = y.shape
+        if T > rows:
             ws = y.new_empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8)
-        s, o, e, sig = self.how
-        B.moe_norm_backward(y, b, gate, w_post, None if dn is None else self.w_pre, dy, dn, ws, residual_scale=s,
-                            weight_offset=o, eps=e, gate_sigmoid=sig, stream=stream, **out)
-        return out
+            self._workspaces[handle] = (T, ws)
+        B.moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, ws, dx, db, dgate, dw_post, dw_pre, *self.how, handle)
+        return {"dx": dx, "db": db, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
+
+    def device_status(self, stream=None) -> int:
+        """MOE_OK, or what the last backward call on this stream reported."""
+        rows, ws = self._workspaces.get(B._stream(stream), (-1, None))
+        return B.MOE_OK if ws is None else B.moe_get_device_status(ws, stream)
 
 
 class AdamW:
@@ -226,8 +246,7 @@ class AdamW:
     def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
         """One step with these gradients (contiguous, all bf16 or all float32), each times grad_scale (a device float)."""
         kind = grads[0].dtype if grads else torch.float32
-        flat = [g.dtype is kind and g.is_contiguous() for g in grads]
-        if kind not in B._DTYPES or not all(flat) or [g.numel() for g in grads] != self.sizes:
+        if kind not in B._DTYPES or [g.numel() for g in grads if g.dtype is kind and g.is_contiguous()] != self.sizes:
             raise ValueError("gradients: sizes, types or strides do not fit the parameters")
         self.table["g"] = [g.data_ptr() for g in grads]
         B.moe_adamw_step(self.table, self.p_dtype, B._DTYPES[kind], self.state_bits, self.lr, *self.betas, self.eps,
