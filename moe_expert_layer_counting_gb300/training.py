@@ -1,0 +1,89 @@
+"""The expert layer with BF16 weights, forward and backward: what trains the weights that ``QuantizedExperts`` and
+``Bfp8Experts`` are cast from.
+
+The products, the permute and the combine are the library's; the gathers of rows and the gated activation between the
+two products are plain torch operations (float32 inside, one rounding to BF16).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+class TrainableExperts:
+    """b = layer(n, topk_idx, topk_w) and its gradients, with the layer's weights l1 [E, 2I, H] (gate rows then up rows)
+    and l2 [E, H, I] in BF16.
+
+    The layer is that of ``MoELayer`` without its quantisation: h = silu(gate) * up * topk_w for each (token, slot) pair,
+    summed over a token's slots after the down product.  topk_idx < 0 marks a dropped pair.
+    """
+
+    def __init__(self, l1: torch.Tensor, l2: torch.Tensor):
+        E, twoI, H = l1.shape
+        if l2.shape != (E, H, twoI // 2):
+            raise ValueError("l1 [E, 2I, H] and l2 [E, H, I] do not fit")
+        self.l1, self.l2 = l1, l2
+        self.E, self.H, self.I = E, H, twoI // 2
+        dev = l1.device
+        # of the products (the size does not depend on the rows), each call's status checked by status()
+        self.workspaces = [torch.zeros(B.moe_grouped_workspace_size(1, H, 2 * self.I, E), dtype=torch.uint8, device=dev)
+                           for _ in range(6)]
+
+    def _permute(self, topk_idx):
+        T, k = topk_idx.shape
+        dev = topk_idx.device
+        counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+        offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+        perm = torch.zeros(T * k, dtype=torch.int32, device=dev)         # rows past offsets[E] belong to no expert
+        inv_perm = torch.empty(T * k, dtype=torch.int32, device=dev)
+        ws = torch.empty(B.moe_permute_workspace_size(T, self.E, k), dtype=torch.uint8, device=dev)
+        B.moe_permute(topk_idx, self.E, counts, offsets, perm, inv_perm, ws)
+        return offsets, perm.long(), inv_perm.long()
+
+    def _sum_slots(self, rows, s):
+        """Each token's sum over its slots of its pairs' rows (float32 inside; dropped slots are left out)."""
+        T, k = s["topk_idx"].shape
+        by_slot = rows[s["inv_perm"].clamp(min=0).view(T, k).T.reshape(-1)].view(k, T, -1)
+        out = torch.empty(T, rows.shape[1], dtype=torch.bfloat16, device=rows.device)
+        B.moe_combine(by_slot, s["topk_idx"], out)
+        return out
+
+    def forward(self, n: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor):
+        """(b [T, H], what backward needs); n [T, H] BF16, topk_idx [T, k] int32, topk_w [T, k] float32."""
+        T, k = topk_idx.shape
+        offsets, perm, inv_perm = self._permute(topk_idx)
+        s = {"topk_idx": topk_idx, "offsets": offsets, "perm": perm, "inv_perm": inv_perm, "token": perm // k,
+             "w": topk_w.reshape(-1)[perm][:, None]}
+        s["rows"] = n[s["token"]]
+        s["a"] = torch.zeros(T * k, 2 * self.I, dtype=torch.bfloat16, device=n.device)
+        B.moe_grouped_forward(s["rows"], self.l1, offsets, s["a"], self.workspaces[0])
+        gate, up = s["a"].float().split(self.I, 1)
+        s["h"] = (torch.nn.functional.silu(gate) * up * s["w"]).bfloat16()
+        o = torch.zeros(T * k, self.H, dtype=torch.bfloat16, device=n.device)
+        B.moe_grouped_forward(s["h"], self.l2, offsets, o, self.workspaces[1])
+        return self._sum_slots(o, s), s
+
+    def backward(self, db: torch.Tensor, s: dict, dl1: torch.Tensor, dl2: torch.Tensor, accumulate: bool = False):
+        """(dn [T, H], dtopk_w [T, k]); the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
+        T, k = s["topk_idx"].shape
+        do = db[s["token"]]
+        dh = torch.zeros_like(s["h"])
+        B.moe_grouped_dgrad(do, self.l2, s["offsets"], dh, self.workspaces[2])
+        B.moe_grouped_wgrad(do, s["h"], s["offsets"], dl2, self.workspaces[3], accumulate)
+        gate, up = s["a"].float().split(self.I, 1)
+        sig = torch.sigmoid(gate)
+        act = gate * sig
+        d = dh.float()
+        dw = (d * act * up).sum(1)
+        d = d * s["w"]
+        da = torch.cat([d * up * (sig + act * (1 - sig)), d * act], 1).bfloat16()
+        drows = torch.zeros_like(s["rows"])
+        B.moe_grouped_dgrad(da, self.l1, s["offsets"], drows, self.workspaces[4])
+        B.moe_grouped_wgrad(da, s["rows"], s["offsets"], dl1, self.workspaces[5], accumulate)
+        dtopk_w = torch.where(s["topk_idx"] < 0, 0.0, dw[s["inv_perm"].clamp(min=0)].view(T, k))
+        return self._sum_slots(drows, s), dtopk_w
+
+    def status(self) -> int:
+        """MOE_OK, or the first status that the last step's products reported (synchronises)."""
+        return next((c for c in (B.moe_get_device_status(w) for w in self.workspaces) if c), B.MOE_OK)
