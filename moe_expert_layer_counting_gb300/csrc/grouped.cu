@@ -126,6 +126,7 @@ struct GItem {
   int e, m, c;          // expert, pair of 128-row M tiles, wgrad: 256-column N tile
   int row0, rows;       // forward / dgrad: first row and rows of the tile; wgrad: of the expert
   int kb, per;          // reduction blocks, in all and per stage
+  bool once;            // forward / dgrad: no other tile reads these weights
   int n, n2;            // N slots (multiples of 32) of the MMA, of a second one for the rows after the first n
 };
 
@@ -182,6 +183,7 @@ struct Lists {
     }
     it.e = lo;
     it.c = 0;
+    it.once = list == 1;
     it.m = i - f[lo] * mt;
     it.row0 = __ldg(offsets + lo);
     it.rows = __ldg(offsets + lo + 1) - it.row0;
@@ -478,6 +480,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         const CUtensorMap *map_b = &maps.b[box], *map_b2 = &maps.b[box2];
         const int b_row = it.row0 + (int)rank * half, b2_row = it.row0 + it.n + (int)rank * half2;
         const int b_col = it.c * GP::kN + (int)rank * half;
+        // weights that one tile reads leave L2 first, and the others' stay (64
+        // experts, skewed, N = 4096, K = 7168: 4.39 GB from HBM instead of 4.56,
+        // 761 instead of 808 us)
+        const uint64_t policy = l2_policy(!kW && it.once);
         // kPer blocks a stage, kTwo: rows in two MMAs
         auto blocks_of = [&](auto per_c, auto two_c) {
           constexpr int kPer = decltype(per_c)::value;
@@ -517,10 +523,11 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
                   unsigned char *a = slot + i * GP::kATile, *b = slot + kPer * GP::kATile + i * kSmallB;
                   const int k0 = (kb + i) * GP::kBK;
                   if (OP == kForward) {
-                    tma_load_3d_2sm(a, &maps.a, bar, k0, m0, it.e);
+                    tma_load_3d_2sm(a, &maps.a, bar, k0, m0, it.e, policy);
                   } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, k0, it.e);
+                    for (int j = 0; j < 2; ++j) tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, m0 + 64 * j, k0, it.e,
+                                                                  policy);
                   }
                   tma_load_2d_2sm(b, map_b, bar, k0, b_row);
                   if (kTwo) tma_load_2d_2sm(b + b_bytes, map_b2, bar, k0, b2_row);

@@ -154,6 +154,7 @@ class BlockNorm:
         self.w_post, self.w_pre = w_post, w_pre
         self.how = (residual_scale, weight_offset, eps, gate_sigmoid)
         self._workspaces = {}                       # stream handle -> (rows it is enough for, tensor)
+        self._outgrown = []                         # kept, as a captured graph may still use one
 
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
         """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
@@ -193,6 +194,7 @@ class BlockNorm:
         rows, ws = self._workspaces.get(handle, (-1, None))
         T, H = y.shape
         if T > rows:
+            self._outgrown.append(ws)
             ws = y.new_empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8)
             self._workspaces[handle] = (T, ws)
         B.moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, ws, dx, db, dgate, dw_post, dw_pre, *self.how, handle)
