@@ -427,23 +427,30 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   if (kW) {
     total = g.E * mt * ((g.C + GP::kN - 1) / GP::kN);
   } else {
-    if (warp < 2) {                      // warp 0: the list of experts with more than one tile, warp 1: with one
+    if (warp < 2) {
+      // warp 0: the list of experts with more than one tile, warp 1: with one;
+      // a lane takes a run of experts, so that its loads are all in flight
       int *first = tile_first + warp * (g.E + 1);
-      int base = 0;
-      for (int e0 = 0; e0 < g.E; e0 += 32) {
-        const int e = e0 + lane;
-        int n = !bad && e < g.E ? tiles_of(__ldg(g.offsets + e + 1) - __ldg(g.offsets + e)) : 0;
-        if ((n > 1) != (warp == 0)) n = 0;
-        int s = n;
+      const int per = (g.E + 31) / 32, e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
+      auto tiles_in_list = [&](int e) {
+        const int n = bad ? 0 : tiles_of(__ldg(g.offsets + e + 1) - __ldg(g.offsets + e));
+        return (n > 1) == (warp == 0) ? n : 0;
+      };
+      int sum = 0;
+#pragma unroll 8
+      for (int e = e0; e < e1; ++e) sum += tiles_in_list(e);
+      int upto = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, s, o);
-          if (lane >= o) s += up;
-        }
-        if (e < g.E) first[e] = base + s - n;
-        base += __shfl_sync(0xffffffffu, s, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
       }
-      if (lane == 0) first[g.E] = base;
+      int at = upto - sum;
+      for (int e = e0; e < e1; ++e) {
+        first[e] = at;
+        at += tiles_in_list(e);
+      }
+      if (lane == 31) first[g.E] = upto;
     }
     __syncthreads();
     lists.items0 = tile_first[g.E] * mt;
