@@ -939,43 +939,52 @@ __global__ void __launch_bounds__(kBackwardThreads) norm_backward_wide_kernel(co
   }
 }
 
-// blockIdx.y: which sum; 32 columns per block, eight threads per column.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const moe_norm_args a, const moe_norm_grads g,
-                                                         const float *parts, int n) {
-  __shared__ float red[8][33];
+// blockIdx.y: which sum.  A block has 128 columns, four to a lane, and a warp
+// takes every kPartWarps-th part: a thread's loads (10 for 152 parts) are all
+// in flight at once, and wait for nothing else.
+constexpr int kPartWarps = 16;
+
+__global__ void __launch_bounds__(32 * kPartWarps) norm_parts_kernel(const moe_norm_args a, const moe_norm_grads g,
+                                                                     const float *parts, int n) {
+  __shared__ float4 red[kPartWarps][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int H = (int)a.H, which = blockIdx.y;
+  const int H = (int)a.H, which = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (which == kSumPre ? g.dw_pre == nullptr : g.dw_post == nullptr && !(channel && g.dgate)) return;
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
-  float s = 0.f;
-  if (c < H) {
-#pragma unroll 8
-    for (int p = k; p < n; p += 8) s += parts[((int64_t)p * 2 + which) * H + c];
+  const int c4 = blockIdx.x * 128 + 4 * lane;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c4 < H) {
+    const float *from = parts + (int64_t)which * H + c4;
+#pragma unroll 10
+    for (int p = warp; p < n; p += kPartWarps) {
+      const float4 v = *reinterpret_cast<const float4 *>(from + (int64_t)p * 2 * H);
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
   }
-  red[k][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (k != 0 || c >= H) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
-  if (which == kSumPre) {
-    g.dw_pre[c] = s;
-    return;
-  }
-  float gv = 1.0f, slope = 1.0f;
-  if (channel) {
+  red[warp][lane] = s;
+  const int c = blockIdx.x * 128 + (int)threadIdx.x;
+  const bool last = threadIdx.x < 128 && c < H;
+  float gv = 1.0f, slope = 1.0f, w = 1.0f;
+  if (last && which != kSumPre && channel) {
     gv = load1_any(a.gate, a.gate_dtype, c);
     if (a.gate_sigmoid) {
       gv = sigmoid(gv);
       slope = gv * (1.0f - gv);
     }
-    if (g.dgate) {
-      const float w = a.w_post ? load1_any(a.w_post, a.w_dtype, c) + a.weight_offset : 1.0f;
-      store1_any(g.dgate, a.gate_dtype, c, s * w * slope);
-    }
+    if (a.w_post) w = load1_any(a.w_post, a.w_dtype, c) + a.weight_offset;
   }
-  if (g.dw_post) g.dw_post[c] = s * gv;
+  __syncthreads();
+  if (!last) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPartWarps; ++i) sum += reinterpret_cast<const float *>(red[i])[threadIdx.x];
+  if (which == kSumPre) {
+    g.dw_pre[c] = sum;
+    return;
+  }
+  if (channel && g.dgate) store1_any(g.dgate, a.gate_dtype, c, sum * w * slope);
+  if (g.dw_post) g.dw_post[c] = sum * gv;
 }
 
 // ---------------------------------------------------------------- host
@@ -1123,7 +1132,7 @@ int backward_launch(const moe_norm_args &a, const moe_norm_grads &g, cudaStream_
   if (rc != MOE_OK) return rc;
   const bool gate = a.gate_kind == MOE_GATE_CHANNEL && g.dgate;
   if (!g.dw_pre && !g.dw_post && !gate) return MOE_OK;
-  return launch_pdl(norm_parts_kernel, dim3((unsigned)ceil_div(a.H, 32), g.dw_post || gate ? 2 : 1), dim3(256), 0, st,
+  return launch_pdl(norm_parts_kernel, dim3((unsigned)ceil_div(a.H, 128), g.dw_post || gate ? 2 : 1), dim3(32 * kPartWarps), 0, st,
                     a, g, static_cast<const float *>(parts), n);
 }
 

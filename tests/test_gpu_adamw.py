@@ -56,7 +56,7 @@ def expected(p, m, v, g, t, lr, betas, eps, weight_decay):
     return p * (1 - lr * weight_decay) - rate * m_new / root, p.abs() + rate * m_mag / root, m_new, m_mag, v_new
 
 
-@pytest.mark.parametrize("pt,gt,clip", itertools.product((F32, BF16), (F32, BF16), (False, True)))
+@pytest.mark.parametrize("pt,gt,clip", list(itertools.product((F32, BF16), (F32, BF16), (False, True))))
 def test_float32_states(M, pt, gt, clip):
     params, grads = tensors(SIZES, pt, 0.5, 1), [tensors(SIZES, gt, 1e-2, s) for s in (2, 3, 4)]
     copies = tensors(SIZES, BF16, 1.0, 5) if pt == F32 else None
