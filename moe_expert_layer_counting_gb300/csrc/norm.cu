@@ -3,10 +3,10 @@
 //
 // Both directions are bound by HBM if the SM keeps up: every row is read once
 // and written once, but a row needs two sums over its columns one after the
-// other, and ~17 operations a value in the backward pass.  So, up to H = 8192:
+// other, and ~17 operations a value in the backward pass.  So:
 //   - a group of H / 16 threads owns a row at a time, a thread 16 columns (with 8,
 //     the instructions that do not depend on the columns are as many as those
-//     that do: 149 instead of 127 us for the gradients of 8192 x 7168);
+//     that do: 149 instead of 127 us for the gradients of 8192 x 7168 in BF16);
 //   - the rows to come are copied (bulk copies) into a ring in shared memory; a
 //     row is taken into registers, and its slot has its next row on the way
 //     before the row's first sum is used;
@@ -14,7 +14,12 @@
 //     weights with their offset, the channel gate) made once per block;
 //   - the gradients of w_post and of a channel gate are the same column sum
 //     sum_t d b rsqrt(mean b^2 + eps), times a constant of the column.
-// Longer rows are loaded into registers directly (the *_wide kernels).
+// A row of more than 8192 columns is split over the two blocks of a cluster
+// (SPLIT), which add their sums through each other's shared memory (2048 x 16384:
+// 59 and 89 us; held in one block's registers it took 69 and 214).
+// Measured, BF16, channel gate: forward of 8192 x 7168 in 74 us (6.3 TB/s), the
+// gradients in 124 us (5.7 TB/s); 4096 x 7168 in 41 and 69 us, of which ~10 us
+// are the first rows' way in, the last ones' way out and the sums of the parts.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -29,8 +34,6 @@ namespace mxq {
 namespace {
 
 constexpr int kMaxH = 16384;
-constexpr int kMaxWarps = 32;
-constexpr int kBackwardThreads = 512;
 
 struct F8 {
   float v[8];
@@ -47,22 +50,11 @@ __device__ __forceinline__ F8 unpack_bf16x8(const uint4 &q) {
   return f;
 }
 
-__device__ __forceinline__ uint4 pack_bf16x8(const F8 &f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.v[2 * i], f.v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Eight values of a row as they lie in memory (registers until they are used).
 template <typename T> struct Raw8;
 template <> struct Raw8<uint16_t> {
   uint4 q;
   __device__ __forceinline__ void load(const uint16_t *p) { q = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ F8 get() const { return unpack_bf16x8(q); }
   __device__ __forceinline__ P2 two(int i) const { return from_bf16x2(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w); }
 };
 template <> struct Raw8<float> {
@@ -76,12 +68,6 @@ template <> struct Raw8<float> {
     return i == 0 ? pair(a.x, a.y) : i == 1 ? pair(a.z, a.w) : i == 2 ? pair(b.x, b.y) : pair(b.z, b.w);
   }
 };
-
-__device__ __forceinline__ void store8(uint16_t *p, const F8 &f) { *reinterpret_cast<uint4 *>(p) = pack_bf16x8(f); }
-__device__ __forceinline__ void store8(float *p, const F8 &f) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
-}
 
 __device__ __forceinline__ void store_pairs(uint16_t *p, const P2 (&v)[4]) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
@@ -177,6 +163,8 @@ struct RowSource {
 struct RingSmem {
   uint64_t full[kMaxGroups][kMaxStages];
   float red[kMaxGroups][2][2][4 * 32];                  // of even and odd rows, two sums each
+  float4 other[2][2];                                   // SPLIT: the other block's, the same four
+  uint64_t here[2][2];                                  //        and the arrival of each
 };
 
 template <int N>
@@ -190,7 +178,7 @@ __device__ __forceinline__ int place_rows(RowSource (&src)[N]) {
   return at;
 }
 
-template <int N>
+template <bool SPLIT, int N>
 __device__ __forceinline__ void ring_init(RingSmem &sm, const RingShape &sh, const RowSource (&src)[N]) {
   for (int i = (int)threadIdx.x; i < kMaxGroups * 2 * 2 * 4 * 32; i += (int)blockDim.x) (&sm.red[0][0][0][0])[i] = 0.f;
   if (threadIdx.x == 0) {
@@ -199,9 +187,12 @@ __device__ __forceinline__ void ring_init(RingSmem &sm, const RingShape &sh, con
     for (int i = 0; i < N; ++i) copies += src[i].bytes > 0 ? 1u : 0u;
     for (int g = 0; g < sh.groups; ++g)
       for (int s = 0; s < sh.stages; ++s) mbar_init(&sm.full[g][s], copies);
+    if (SPLIT)
+      for (int i = 0; i < 4; ++i) mbar_init(&sm.here[i >> 1][i & 1], 1);
     fence_mbar_init();
   }
   __syncthreads();
+  if (SPLIT) cluster_sync();
 }
 
 // Which tensors' copies this thread issues: each by the first lane of a warp of
@@ -214,6 +205,13 @@ __device__ __forceinline__ uint32_t my_copies(const RowSource (&src)[N], int war
   for (int i = 0; i < N; ++i)
     if (src[i].bytes > 0 && i % warps == warp && (threadIdx.x & 31) == 0) mask |= 1u << i;
   return mask;
+}
+
+// 16 bytes into another block's shared memory, counted by its barrier.
+__device__ __forceinline__ void send16(uint32_t to, uint32_t bar, const float4 &f) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(f.x), "f"(f.y), "f"(f.z), "f"(f.w), "r"(bar)
+               : "memory");
 }
 
 // Row t into a slot.
@@ -229,8 +227,11 @@ __device__ __forceinline__ void ring_copy(uint32_t mask, const RowSource (&src)[
   }
 }
 
-// Waits for this block's own copies.  One that gives up is reported, and the
-// caller begins no other.
+// Waits for this block's own copies (or the other's sums).  After one that gives
+// up, and is reported, the thread begins no other and no more copies (it has
+// none `ahead`), and gives those in flight time to land before it leaves.
+constexpr unsigned kGaveUp = ~0u;
+
 __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *status) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
@@ -238,6 +239,32 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *s
     if (mbar_try_wait(bar, parity)) return true;
   report_status(status, kStatusTimeout);
   return false;
+}
+__device__ __forceinline__ void let_land() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 200000) __nanosleep(1000);      // ~100 us
+}
+
+// Sums over a split row, from the sums over this block's columns: the first
+// thread of each block writes its own into the other's shared memory, and both
+// add the two in the order of the columns.  A place is written again two rows
+// later, after this block's sums of the row between, that is after all its
+// threads have read it.
+template <int N>
+__device__ __forceinline__ bool add_other(float (&v)[N], RingSmem &sm, int turn, int which, uint32_t parity, uint32_t rank,
+                                          int *status) {
+  uint64_t *bar = &sm.here[turn][which];
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, 16);
+    send16(mapa_shared(smem_u32(&sm.other[turn][which]), rank ^ 1), mapa_shared(smem_u32(bar), rank ^ 1),
+           make_float4(v[0], v[1 % N], v[2 % N], 0.f));
+  }
+  if (!ring_wait(bar, parity, status)) return false;
+  const float4 o = sm.other[turn][which];
+  const float f[3] = {o.x, o.y, o.z};
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = rank == 0 ? v[k] + f[k] : f[k] + v[k];
+  return true;
 }
 
 // Column constants in shared memory: 8 columns of vector c in two planes, so
@@ -300,26 +327,33 @@ __device__ __forceinline__ float total(P2 p) {
 
 // FULL: a gate of each value.  ALL: a layer's answer, both norms and both outputs
 // are there (the branches on them cost as much as the arithmetic).
-template <typename XT, bool FULL, bool ALL>
+template <typename XT, bool FULL, bool ALL, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_forward_kernel(const __grid_constant__ moe_norm_args a, const RingShape sh) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ RingSmem sm;
-  const int H = (int)a.H, vecs = H >> 3;
+  // this block's columns: 8 vecs of them, from 8 c0 on; the rows go by clusters
+  const int H = (int)a.H, half = (H + 8) >> 4;
+  const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
+  const int c0 = rank * half, vecs = SPLIT ? (rank == 0 ? half : (H >> 3) - half) : H >> 3, cols = SPLIT ? 8 * vecs : H;
+  const unsigned block = SPLIT ? blockIdx.x >> 1 : blockIdx.x, blocks = SPLIT ? gridDim.x >> 1 : gridDim.x;
   const bool sig = a.gate_sigmoid != 0;
   const bool has_b = ALL || a.b, post = ALL || a.w_post, out_y = ALL || (a.b && a.y), out_n = ALL || a.n;
   const int gate_size = a.gate_dtype == MOE_F32 ? 4 : 2;
-  RowSource src[3] = {{static_cast<const char *>(a.x), a.ldx * (int64_t)sizeof(XT), H * (int)sizeof(XT), 0},
-                      {reinterpret_cast<const char *>(a.b), a.ldb * 2, has_b ? H * 2 : 0, 0},
-                      {static_cast<const char *>(a.gate), a.ld_gate * gate_size, FULL ? H * gate_size : 0, 0}};
+  const int xb = cols * (int)sizeof(XT);
+  RowSource src[3] = {
+      {static_cast<const char *>(a.x) + 8 * c0 * (int)sizeof(XT), a.ldx * (int64_t)sizeof(XT), xb, 0},
+      {reinterpret_cast<const char *>(a.b) + 16 * c0, a.ldb * 2, has_b ? cols * 2 : 0, 0},
+      {static_cast<const char *>(a.gate) + 8 * c0 * gate_size, a.ld_gate * gate_size, FULL ? cols * gate_size : 0, 0}};
   const int row_bytes = place_rows(src);
   const int group = (int)threadIdx.x / sh.group, tid = (int)threadIdx.x - group * sh.group;
   const int warps = sh.group >> 5, warp = tid >> 5;
-  const unsigned T = (unsigned)a.T, first = blockIdx.x * (unsigned)sh.groups + (unsigned)group,
-                 n = gridDim.x * (unsigned)sh.groups, ahead = (unsigned)sh.stages * n;
+  const unsigned T = (unsigned)a.T, first = block * (unsigned)sh.groups + (unsigned)group,
+                 n = blocks * (unsigned)sh.groups;
+  unsigned ahead = (unsigned)sh.stages * n;
   unsigned char *ring = ring_smem + (size_t)group * sh.stages * row_bytes;
   const uint32_t copies = my_copies(src, warps, warp);
-  ring_init(sm, sh, src);
+  ring_init<SPLIT>(sm, sh, src);
   pdl_launch_dependents();
   pdl_wait();
   for (int s = 0; s < sh.stages; ++s)
@@ -334,25 +368,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = 0; i < V; ++i) {
     const int c = tid + i * sh.group;
     if (c >= vecs) continue;
-    F8 f = offset_weight(a.w_post, a.w_dtype, c, a.weight_offset);
+    F8 f = offset_weight(a.w_post, a.w_dtype, c0 + c, a.weight_offset);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
-      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * c);
+      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * (c0 + c));
 #pragma unroll
       for (int j = 0; j < 8; ++j) f.v[j] *= z.v[j];
     }
     to_pairs(f, c_post[i]);
-    to_pairs(offset_weight(a.w_pre, a.w_dtype, c, a.weight_offset), c_pre[i]);
+    to_pairs(offset_weight(a.w_pre, a.w_dtype, c0 + c, a.weight_offset), c_pre[i]);
   }
   const P2 scale = twice(a.b ? a.residual_scale : 1.0f);
-  XT *py = static_cast<XT *>(a.y) + first * a.ldy + 8 * tid;
-  uint16_t *pn = a.n + first * a.ldn + 8 * tid;
+  XT *py = static_cast<XT *>(a.y) + first * a.ldy + 8 * (c0 + tid);
+  uint16_t *pn = a.n + first * a.ldn + 8 * (c0 + tid);
   const int64_t step_y = n * a.ldy, step_n = n * a.ldn;
   int stage = 0, turn = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (unsigned t = first; t < T; t += n, turn ^= 1) {
+  uint32_t phase = 0, half_phase = 0;      // half_phase: of this turn's sums of a split row
+  for (unsigned t = first; t < T; t += n, half_phase ^= (uint32_t)turn, turn ^= 1) {
     unsigned char *row = ring + stage * row_bytes;
-    if (ok) ok = ring_wait(&sm.full[group][stage], phase, nullptr);
+    if (ahead != kGaveUp && !ring_wait(&sm.full[group][stage], phase, nullptr)) ahead = kGaveUp;
     P2 y[V][4], u[V][4], sq = twice(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -383,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (post) {
       float s[1] = {total(sq)};
       group_sum(s, warps, warp, sm.red[group][turn][0], sync);
+      if (SPLIT && ahead != kGaveUp && !add_other(s, sm, turn, 0, half_phase, rank, nullptr)) ahead = kGaveUp;
       rb = rsqrtf(s[0] * inv_h + a.eps);
     } else {
       sync();
@@ -411,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!out_n) continue;
     float s[1] = {total(sq)};
     group_sum(s, warps, warp, sm.red[group][turn][1], sync);
+    if (SPLIT && ahead != kGaveUp && !add_other(s, sm, turn, 1, half_phase, rank, nullptr)) ahead = kGaveUp;
     const P2 r2 = twice(rsqrtf(s[0] * inv_h + a.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -420,6 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_pairs(pn + 8 * i * sh.group, y[i]);
     }
     pn += step_n;
+  }
+  if (ahead == kGaveUp) let_land();
+  if (SPLIT) {                             // the other block may still write into this one's memory
+    __syncthreads();
+    cluster_sync();
   }
 }
 
@@ -437,44 +477,50 @@ enum : int { kSumPre = 0, kSumPost = 1 };
 // the ring, a slot of 7168 columns fits only once.  With a full gate or a
 // float32 stream the row is read again from its slot after the first sum
 // (kLate), and the slot is free after the second.
-template <typename XT, bool FULL, bool ALL>
+template <typename XT, bool FULL, bool ALL, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_backward_kernel(const __grid_constant__ moe_norm_args a, const __grid_constant__ moe_norm_grads g,
                          const RingShape sh, int *status, float *parts) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ RingSmem sm;
-  const int H = (int)a.H, vecs = H >> 3;
+  // this block's columns: 8 vecs of them, from 8 c0 on; the rows go by clusters
+  const int H = (int)a.H, half = (H + 8) >> 4;
+  const uint32_t rank = SPLIT ? cluster_ctarank() : 0;
+  const int c0 = rank * half, vecs = SPLIT ? (rank == 0 ? half : (H >> 3) - half) : H >> 3, cols = SPLIT ? 8 * vecs : H;
+  const unsigned block = SPLIT ? blockIdx.x >> 1 : blockIdx.x, blocks = SPLIT ? gridDim.x >> 1 : gridDim.x;
   const bool token = a.gate_kind == MOE_GATE_TOKEN, sig = a.gate_sigmoid != 0;
   const bool has_b = ALL || a.b, post = ALL || a.w_post, pre = ALL || a.w_pre, has_dy = ALL || g.dy, out_dx = ALL || g.dx,
              out_db = ALL || g.db;
   constexpr bool kDirect = sizeof(XT) == 4, kLate = FULL || kDirect;
-  const int xb = H * (int)sizeof(XT), gate_size = a.gate_dtype == MOE_F32 ? 4 : 2;
+  const int xb = cols * (int)sizeof(XT), gate_size = a.gate_dtype == MOE_F32 ? 4 : 2;
   RowSource src[5] = {
-      {static_cast<const char *>(a.x), a.ldx * (int64_t)sizeof(XT), pre ? xb : 0, 0},
-      {reinterpret_cast<const char *>(g.dn), g.ld_dn * 2, pre ? H * 2 : 0, 0},
-      {static_cast<const char *>(g.dy), g.ld_dy * (int64_t)sizeof(XT), has_dy && !kDirect ? xb : 0, 0},
-      {reinterpret_cast<const char *>(a.b), a.ldb * 2, has_b ? H * 2 : 0, 0},
-      {static_cast<const char *>(a.gate), a.ld_gate * gate_size, FULL ? H * gate_size : 0, 0}};
+      {static_cast<const char *>(a.x) + 8 * c0 * (int)sizeof(XT), a.ldx * (int64_t)sizeof(XT), pre ? xb : 0, 0},
+      {reinterpret_cast<const char *>(g.dn) + 16 * c0, g.ld_dn * 2, pre ? cols * 2 : 0, 0},
+      {static_cast<const char *>(g.dy) + 8 * c0 * (int)sizeof(XT), g.ld_dy * (int64_t)sizeof(XT),
+       has_dy && !kDirect ? xb : 0, 0},
+      {reinterpret_cast<const char *>(a.b) + 16 * c0, a.ldb * 2, has_b ? cols * 2 : 0, 0},
+      {static_cast<const char *>(a.gate) + 8 * c0 * gate_size, a.ld_gate * gate_size, FULL ? cols * gate_size : 0, 0}};
   const int row_bytes = place_rows(src);
   const int group = (int)threadIdx.x / sh.group, tid = (int)threadIdx.x - group * sh.group;
   const int warps = sh.group >> 5, warp = tid >> 5;
-  const unsigned T = (unsigned)a.T, first = blockIdx.x * (unsigned)sh.groups + (unsigned)group,
-                 n = gridDim.x * (unsigned)sh.groups, ahead = (unsigned)sh.stages * n;
+  const unsigned T = (unsigned)a.T, first = block * (unsigned)sh.groups + (unsigned)group,
+                 n = blocks * (unsigned)sh.groups;
+  unsigned ahead = (unsigned)sh.stages * n;
   // column constants, then the rings
   float4 *c_pre = reinterpret_cast<float4 *>(ring_smem), *c_post = c_pre + 2 * vecs;
-  unsigned char *ring = ring_smem + 2 * H * 4 + (size_t)group * sh.stages * row_bytes;
+  unsigned char *ring = ring_smem + 2 * cols * 4 + (size_t)group * sh.stages * row_bytes;
   const uint32_t copies = my_copies(src, warps, warp);
-  ring_init(sm, sh, src);
+  ring_init<SPLIT>(sm, sh, src);
   pdl_launch_dependents();
   pdl_wait();
   for (int s = 0; s < sh.stages; ++s)
     if (first + s * n < T) ring_copy(copies, src, ring + s * row_bytes, &sm.full[group][s], first + s * n);
   if (blockIdx.x == 0 && threadIdx.x < 16) status[threadIdx.x] = 0;
   for (int c = (int)threadIdx.x; c < vecs; c += (int)blockDim.x) {
-    put_columns(c_pre, vecs, c, offset_weight(a.w_pre, a.w_dtype, c, a.weight_offset));
-    F8 f = offset_weight(a.w_post, a.w_dtype, c, a.weight_offset);
+    put_columns(c_pre, vecs, c, offset_weight(a.w_pre, a.w_dtype, c0 + c, a.weight_offset));
+    F8 f = offset_weight(a.w_post, a.w_dtype, c0 + c, a.weight_offset);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
-      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * c);
+      const F8 z = gate8(a.gate, a.gate_dtype, sig, 8 * (c0 + c));
 #pragma unroll
       for (int j = 0; j < 8; ++j) f.v[j] *= z.v[j];
     }
@@ -491,15 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum_pre[i][k] = sum_post[i][k] = twice(0.f);
   const P2 scale = twice(a.b ? a.residual_scale : 1.0f);
-  XT *px = static_cast<XT *>(g.dx) + first * g.ld_dx + 8 * tid;
-  uint16_t *pb = g.db + first * g.ld_db + 8 * tid;
+  XT *px = static_cast<XT *>(g.dx) + first * g.ld_dx + 8 * (c0 + tid);
+  uint16_t *pb = g.db + first * g.ld_db + 8 * (c0 + tid);
   const int64_t step_x = n * g.ld_dx, step_b = n * g.ld_db;
-  const XT *pd = static_cast<const XT *>(g.dy) + first * g.ld_dy + 8 * tid;
+  const XT *pd = static_cast<const XT *>(g.dy) + first * g.ld_dy + 8 * (c0 + tid);
   const int64_t step_d = n * g.ld_dy;
   int stage = 0, turn = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (unsigned t = first; t < T; t += n, turn ^= 1) {
+  uint32_t phase = 0, half_phase = 0;      // half_phase: of this turn's sums of a split row
+  for (unsigned t = first; t < T; t += n, half_phase ^= (uint32_t)turn, turn ^= 1) {
     unsigned char *row = ring + stage * row_bytes;
     uint64_t *full = &sm.full[group][stage];
     Raw8<XT> y[V], dy[V];
@@ -511,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pd += step_d;
       if (tid == 0 && T - t > n) prefetch_l2_bulk(pd, (uint32_t)xb);
     }
-    if (ok) ok = ring_wait(full, phase, status);
+    if (ahead != kGaveUp && !ring_wait(full, phase, status)) ahead = kGaveUp;
     // sums of y^2, dn w y and b^2
     P2 s0 = twice(0.f), s1 = s0, s2 = s0;
 #pragma unroll
@@ -538,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float s[3] = {total(s0), total(s1), total(s2)};
     group_sum(s, warps, warp, sm.red[group][turn][0], sync);
+    if (SPLIT && ahead != kGaveUp && !add_other(s, sm, turn, 0, half_phase, rank, status)) ahead = kGaveUp;
     // the row is in registers: its slot takes the row after the ring's
     if (!kLate && T - t > ahead) ring_copy(copies, src, row, full, t + ahead);
     if (++stage == sh.stages) { stage = 0; phase ^= 1; }
@@ -604,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (g.dgate) {
             if (a.gate_dtype == MOE_BF16)
-              store_pairs(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
+              store_pairs(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * (c0 + c), dz);
             else
-              store_pairs(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
+              store_pairs(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * (c0 + c), dz);
           }
         }
 #pragma unroll
@@ -628,12 +674,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // q: the sum of d g w b (token gates: without g)
     float q[1] = {total(q2)};
-    if (post || token) group_sum(q, warps, warp, sm.red[group][turn][1], sync);
+    if (post || token) {
+      group_sum(q, warps, warp, sm.red[group][turn][1], sync);
+      if (SPLIT && ahead != kGaveUp && !add_other(q, sm, turn, 1, half_phase, rank, status)) ahead = kGaveUp;
+    }
     if (kLate) {
       if (!(post || token)) sync();
       if (T - t > ahead) ring_copy(copies, src, row, full, t + ahead);
     }
-    if (token && g.dgate && tid == 0)
+    if (token && g.dgate && tid == 0 && rank == 0)
       store1_any(g.dgate, a.gate_dtype, t, (sig ? gate_t * (1.0f - gate_t) : 1.0f) * q[0] * rb);
     if (out_db) {
       // db = rb (g d w - h mean(g d w h)) = rs d w - b g rb^3 q / H
@@ -650,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the block's part: its groups' sums, in group order, by way of the ring's
   // memory (no copy is in flight: every row that was asked for was waited for)
-  float *part = parts + (int64_t)blockIdx.x * 2 * H;
-  float *join = reinterpret_cast<float *>(ring_smem + 2 * H * 4);
+  float *part = parts + (int64_t)block * 2 * H + 8 * c0;
+  float *join = reinterpret_cast<float *>(ring_smem + 2 * cols * 4);
   const bool wanted[2] = {g.dw_pre != nullptr, g.dw_post != nullptr || (a.gate_kind == MOE_GATE_CHANNEL && g.dgate)};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -674,268 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-}
-
-// ---------------------------------------------------------------- wide rows, in registers
-
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
-  group_sum(v, (int)(blockDim.x >> 5), (int)(threadIdx.x >> 5), red, [] { __syncthreads(); });
-}
-
-template <typename XT, int V>
-__global__ void norm_forward_wide_kernel(const moe_norm_args a) {
-  __shared__ float red[2][kMaxWarps];
-  if (threadIdx.x < 2 * kMaxWarps) red[0][threadIdx.x] = 0.f;     // a row has at least 1024 / 4 threads here
-  __syncthreads();
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t t = blockIdx.x;
-  const int H = (int)a.H, vecs = H >> 3;
-  const float inv_h = 1.0f / (float)H;
-  const XT *x = static_cast<const XT *>(a.x) + t * a.ldx;
-  const uint16_t *b = a.b ? a.b + t * a.ldb : nullptr;
-  Raw8<XT> xr[V];
-  Raw8<uint16_t> br[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (int)threadIdx.x + i * (int)blockDim.x;
-    if (c < vecs) {
-      xr[i].load(x + 8 * c);
-      if (b) br[i].load(b + 8 * c);
-    }
-  }
-  float gate_t = 1.0f;
-  if (a.gate_kind == MOE_GATE_TOKEN) {
-    gate_t = load1_any(a.gate, a.gate_dtype, t);
-    if (a.gate_sigmoid) gate_t = sigmoid(gate_t);
-  }
-  float rb = 1.0f;
-  if (b && a.w_post) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if ((int)threadIdx.x + i * (int)blockDim.x < vecs) {
-        const F8 f = br[i].get();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(f.v[j], f.v[j], s[0]);
-      }
-    }
-    block_sum(s, red[0]);
-    rb = __frsqrt_rn(s[0] * inv_h + a.eps);
-  }
-  F8 y[V];
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (int)threadIdx.x + i * (int)blockDim.x;
-    if (c < vecs) {
-      y[i] = xr[i].get();
-      if (b) {
-        F8 u = br[i].get();
-        if (a.w_post) {
-          const F8 w = load8_any(a.w_post, a.w_dtype, 8 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u.v[j] = u.v[j] * rb * (a.weight_offset + w.v[j]);
-        }
-        if (a.gate_kind >= MOE_GATE_CHANNEL) {
-          const F8 g = load8_any(a.gate, a.gate_dtype, (a.gate_kind == MOE_GATE_FULL ? t * a.ld_gate : 0) + 8 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u.v[j] *= a.gate_sigmoid ? sigmoid(g.v[j]) : g.v[j];
-        } else if (a.gate_kind == MOE_GATE_TOKEN) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u.v[j] *= gate_t;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[i].v[j] = fmaf(a.residual_scale, y[i].v[j], u.v[j]);
-        if (a.y) store8(static_cast<XT *>(a.y) + t * a.ldy + 8 * c, y[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(y[i].v[j], y[i].v[j], s[0]);
-    }
-  }
-  if (!a.n) return;
-  block_sum(s, red[1]);
-  const float r = __frsqrt_rn(s[0] * inv_h + a.eps);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (int)threadIdx.x + i * (int)blockDim.x;
-    if (c < vecs) {
-      const F8 w = load8_any(a.w_pre, a.w_dtype, 8 * c);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i].v[j] = y[i].v[j] * r * (a.weight_offset + w.v[j]);
-      store8(a.n + t * a.ldn + 8 * c, y[i]);
-    }
-  }
-}
-
-template <typename XT, int V>
-__global__ void __launch_bounds__(kBackwardThreads) norm_backward_wide_kernel(const moe_norm_args a,
-                                                                              const moe_norm_grads g, float *parts) {
-  __shared__ float red_buf[2][5 * kMaxWarps];      // of even and odd rows
-  int turn = 0;
-  for (int i = (int)threadIdx.x; i < 10 * kMaxWarps; i += (int)blockDim.x) red_buf[0][i] = 0.f;
-  __syncthreads();
-  pdl_launch_dependents();
-  pdl_wait();
-  const int H = (int)a.H, vecs = H >> 3;
-  const float inv_h = 1.0f / (float)H;
-  F8 sums[2][V];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sums[k][i].v[j] = 0.f;
-
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    float *red = red_buf[turn];
-    const XT *y = static_cast<const XT *>(a.x) + t * a.ldx;
-    Raw8<XT> yr[V], dyr[V];
-    Raw8<uint16_t> br[V], dnr[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (int)threadIdx.x + i * (int)blockDim.x;
-      if (c < vecs) {
-        if (a.w_pre) {
-          yr[i].load(y + 8 * c);
-          dnr[i].load(g.dn + t * g.ld_dn + 8 * c);
-        }
-        if (g.dy) dyr[i].load(static_cast<const XT *>(g.dy) + t * g.ld_dy + 8 * c);
-        if (a.b) br[i].load(a.b + t * a.ldb + 8 * c);
-      }
-    }
-    float gate_t = 1.0f;
-    if (a.gate_kind == MOE_GATE_TOKEN) {
-      gate_t = load1_any(a.gate, a.gate_dtype, t);
-      if (a.gate_sigmoid) gate_t = sigmoid(gate_t);
-    }
-    // sums of y^2, dn w y and b^2
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (int)threadIdx.x + i * (int)blockDim.x;
-      if (c < vecs) {
-        if (a.w_pre) {
-          const F8 f = yr[i].get(), d = dnr[i].get(), w = load8_any(a.w_pre, a.w_dtype, 8 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            s[0] = fmaf(f.v[j], f.v[j], s[0]);
-            s[1] = fmaf(d.v[j] * (a.weight_offset + w.v[j]), f.v[j], s[1]);
-          }
-        }
-        if (a.b && a.w_post) {
-          const F8 f = br[i].get();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[2] = fmaf(f.v[j], f.v[j], s[2]);
-        }
-      }
-    }
-    block_sum(s, red);
-    const float r = __frsqrt_rn(s[0] * inv_h + a.eps);
-    const float rb = a.w_post ? __frsqrt_rn(s[2] * inv_h + a.eps) : 1.0f;
-    const float back = r * r * s[1] * inv_h;              // mean(dn w h) r
-    // d, and the sum of d g w_post b (token gates: without g)
-    F8 d[V];
-    float q[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (int)threadIdx.x + i * (int)blockDim.x;
-      if (c < vecs) {
-        if (g.dy) {
-          d[i] = dyr[i].get();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[i].v[j] = 0.f;
-        }
-        if (a.w_pre) {
-          const F8 f = yr[i].get(), n = dnr[i].get(), w = load8_any(a.w_pre, a.w_dtype, 8 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            d[i].v[j] += r * (n.v[j] * (a.weight_offset + w.v[j]) - f.v[j] * back);
-            sums[kSumPre][i].v[j] = fmaf(n.v[j], f.v[j] * r, sums[kSumPre][i].v[j]);
-          }
-        }
-        if (g.dx) {
-          F8 o = d[i];
-          if (a.b)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o.v[j] *= a.residual_scale;
-          store8(static_cast<XT *>(g.dx) + t * g.ld_dx + 8 * c, o);
-        }
-        if (a.b) {
-          const F8 f = br[i].get();
-          F8 w;
-          if (a.w_post) {
-            w = load8_any(a.w_post, a.w_dtype, 8 * c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w.v[j] = (w.v[j] + a.weight_offset) * rb;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w.v[j] = 1.0f;
-          }
-          if (a.gate_kind >= MOE_GATE_CHANNEL) {
-            const bool full = a.gate_kind == MOE_GATE_FULL;
-            F8 z = load8_any(a.gate, a.gate_dtype, (full ? t * a.ld_gate : 0) + 8 * c);
-            F8 dz;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float gv = a.gate_sigmoid ? sigmoid(z.v[j]) : z.v[j];
-              dz.v[j] = d[i].v[j] * f.v[j] * w.v[j];
-              if (a.gate_sigmoid) dz.v[j] *= gv * (1.0f - gv);
-              if (!full) sums[kSumPost][i].v[j] = fmaf(d[i].v[j], f.v[j] * rb, sums[kSumPost][i].v[j]);
-              d[i].v[j] *= gv;
-            }
-            if (full && g.dgate) {
-              if (a.gate_dtype == MOE_BF16)
-                store8(static_cast<uint16_t *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
-              else
-                store8(static_cast<float *>(g.dgate) + t * g.ld_dgate + 8 * c, dz);
-            }
-          }
-          if (a.gate_kind != MOE_GATE_CHANNEL)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              sums[kSumPost][i].v[j] = fmaf(d[i].v[j] * gate_t, f.v[j] * rb, sums[kSumPost][i].v[j]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) q[0] = fmaf(d[i].v[j] * w.v[j], f.v[j], q[0]);
-        }
-      }
-    }
-    if (!a.b) continue;
-    if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) block_sum(q, red + 4 * kMaxWarps);
-    if (a.gate_kind == MOE_GATE_TOKEN && g.dgate && threadIdx.x == 0)
-      store1_any(g.dgate, a.gate_dtype, t, a.gate_sigmoid ? q[0] * gate_t * (1.0f - gate_t) : q[0]);
-    // db = rb (g d w - h mean(g d w h)); w above carries rb once, so with
-    // q = sum(g d w rb b):  db = g d w rb - b rb^2 q / H
-    const float back_b = a.w_post ? rb * rb * q[0] * inv_h * (a.gate_kind == MOE_GATE_TOKEN ? gate_t : 1.0f) : 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (int)threadIdx.x + i * (int)blockDim.x;
-      if (c < vecs) {
-        const F8 f = br[i].get();
-        F8 o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = d[i].v[j] * gate_t;
-        if (a.w_post) {
-          const F8 w = load8_any(a.w_post, a.w_dtype, 8 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o.v[j] = o.v[j] * (w.v[j] + a.weight_offset) * rb - f.v[j] * back_b;
-          }
-        }
-        if (g.db) store8(g.db + t * g.ld_db + 8 * c, o);
-      }
-    }
-  }
-  float *part = parts + (int64_t)blockIdx.x * 2 * H;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (int)threadIdx.x + i * (int)blockDim.x;
-    if (c < vecs) {
-      store8(part + kSumPre * H + 8 * c, sums[kSumPre][i]);
-      store8(part + kSumPost * H + 8 * c, sums[kSumPost][i]);
-    }
+  if (ahead == kGaveUp) let_land();
+  if (SPLIT) {                             // the other block may still write into this one's memory
+    __syncthreads();
+    cluster_sync();
   }
 }
 
@@ -1024,14 +815,17 @@ constexpr int kMaxRingH = 8192;
 
 struct RingLaunch {
   RingShape shape;
-  int blocks, smem;
-  bool ok;
+  int rows, smem;             // rows: blocks, or clusters of two
 };
+
+// Columns of a row that a block has.
+bool is_split(int64_t H) { return H > kMaxRingH; }
+int block_columns(int64_t H) { return (int)(is_split(H) ? 8 * ceil_div(H, 16) : H); }
 
 // Rows of up to 4096 columns share a block where there are `many`, more than
 // SMs; as many blocks per SM as have 512 threads (128 registers each).
 void block_shape(int64_t H, bool many, RingShape &s, int &per_sm) {
-  s.group = (int)round_up((size_t)ceil_div(H, 8 * V), 32);
+  s.group = (int)round_up((size_t)ceil_div(block_columns(H), 8 * V), 32);
   s.groups = many ? std::max(1, std::min(kMaxGroups, kThreads / s.group)) : 1;
   per_sm = std::min(4, std::max(1, kThreads / (s.group * s.groups)));
 }
@@ -1044,18 +838,22 @@ int most_parts(int64_t T, int64_t H) {
   return (int)std::min<int64_t>(T, 160 * std::max(2, per_sm));
 }
 
-// As many stages as a block's share of the shared memory holds, but no more
-// than a group has rows.
-RingLaunch ring_launch(int64_t T, int64_t H, int row_bytes, int constants) {
+// `row` and `constants`: bytes a column.  As many stages as a block's share of
+// the shared memory holds, but no more than a group has rows.  Fewer blocks per
+// SM where that share would not hold two stages; a block that has the SM for
+// itself holds one at least (8192 columns of 12 bytes and 8 of constants: 160 KB).
+RingLaunch ring_launch(int64_t T, int64_t H, int row, int constants) {
   RingLaunch l{};
-  int per_sm;
+  int per_sm, stages;
+  const int cols = block_columns(H), sms = num_sms() / (is_split(H) ? 2 : 1);
   block_shape(H, T > num_sms(), l.shape, per_sm);
-  l.blocks = (int)std::min<int64_t>({ceil_div(T, l.shape.groups), (int64_t)per_sm * num_sms(), most_parts(T, H)});
-  const int ring = kMaxRingBytes / per_sm - (per_sm - 1) * 10 * 1024 - constants;
-  l.shape.stages = (int)std::min<int64_t>({kMaxStages, ring / (l.shape.groups * row_bytes),
-                                           ceil_div(T, (int64_t)l.blocks * l.shape.groups)});
-  l.smem = std::max(l.shape.stages * l.shape.groups * row_bytes, (int)H * 4) + constants;
-  l.ok = H <= kMaxRingH && ring > 0 && l.shape.stages > 0;
+  for (;; --per_sm) {
+    stages = (kMaxRingBytes / per_sm - (per_sm - 1) * 10 * 1024 - constants * cols) / (l.shape.groups * row * cols);
+    if (stages >= 2 || per_sm == 1) break;
+  }
+  l.rows = (int)std::min<int64_t>({ceil_div(T, l.shape.groups), (int64_t)per_sm * sms, most_parts(T, H)});
+  l.shape.stages = (int)std::min<int64_t>({kMaxStages, stages, ceil_div(T, (int64_t)l.rows * l.shape.groups)});
+  l.smem = std::max(l.shape.stages * l.shape.groups * row * cols, cols * 4) + constants * cols;
   return l;
 }
 
@@ -1070,70 +868,68 @@ bool allow_smem(Kernel kernel, std::atomic<uint64_t> &ready) {
   return true;
 }
 
-// Threads of a wide row: v vectors of 8 columns each, in whole warps.
-struct Shape {
-  int threads, v;
-};
-Shape row_shape(int64_t H, int v, int most) {
-  const int vecs = (int)(H / 8);
-  while (v < 4 && (vecs + v - 1) / v > most) v *= 2;
-  return {(int)round_up((size_t)((vecs + v - 1) / v), 32), v};
+int gate_column_bytes(const moe_norm_args &a) {
+  return a.gate_kind == MOE_GATE_FULL ? (a.gate_dtype == MOE_F32 ? 4 : 2) : 0;
 }
 
-int gate_row_bytes(const moe_norm_args &a) {
-  return a.gate_kind == MOE_GATE_FULL ? (int)a.H * (a.gate_dtype == MOE_F32 ? 4 : 2) : 0;
+template <bool SPLIT, typename Kernel, typename... Args>
+int launch_rows(Kernel kernel, std::atomic<uint64_t> &ready, const RingLaunch &l, cudaStream_t st, const Args &...args) {
+  if (!allow_smem(kernel, ready)) return MOE_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(SPLIT ? 2 * l.rows : l.rows));
+  cfg.blockDim = dim3((unsigned)(l.shape.group * l.shape.groups));
+  cfg.dynamicSmemBytes = (size_t)l.smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename XT, bool SPLIT>
+int forward_rows(const moe_norm_args &a, const RingLaunch &l, cudaStream_t st) {
+  static std::atomic<uint64_t> ready[3];
+  if (a.gate_kind == MOE_GATE_FULL) return launch_rows<SPLIT>(norm_forward_kernel<XT, true, false, SPLIT>, ready[0], l, st, a, l.shape);
+  if (a.b && a.w_post && a.w_pre && a.y)
+    return launch_rows<SPLIT>(norm_forward_kernel<XT, false, true, SPLIT>, ready[1], l, st, a, l.shape);
+  return launch_rows<SPLIT>(norm_forward_kernel<XT, false, false, SPLIT>, ready[2], l, st, a, l.shape);
 }
 
 template <typename XT>
 int forward_launch(const moe_norm_args &a, cudaStream_t st) {
-  const RingLaunch l = ring_launch(a.T, a.H, (int)a.H * ((int)sizeof(XT) + (a.b ? 2 : 0)) + gate_row_bytes(a), 0);
-  if (l.ok) {
-    const int threads = l.shape.group * l.shape.groups;
-    static std::atomic<uint64_t> ready[3];
-    auto run = [&](auto kernel, std::atomic<uint64_t> &r) -> int {
-      return allow_smem(kernel, r) ? launch_pdl(kernel, dim3(l.blocks), dim3(threads), l.smem, st, a, l.shape) : MOE_ERR_CUDA;
-    };
-    const bool all = a.b && a.w_post && a.w_pre && a.y;
-    if (a.gate_kind == MOE_GATE_FULL) return run(norm_forward_kernel<XT, true, false>, ready[0]);
-    return all ? run(norm_forward_kernel<XT, false, true>, ready[1]) : run(norm_forward_kernel<XT, false, false>, ready[2]);
-  }
-  const Shape s = row_shape(a.H, 2, 1024);
-  return launch_pdl(s.v == 2 ? norm_forward_wide_kernel<XT, 2> : norm_forward_wide_kernel<XT, 4>, dim3((unsigned)a.T),
-                    dim3(s.threads), 0, st, a);
+  const RingLaunch l = ring_launch(a.T, a.H, (int)sizeof(XT) + (a.b ? 2 : 0) + gate_column_bytes(a), 0);
+  return is_split(a.H) ? forward_rows<XT, true>(a, l, st) : forward_rows<XT, false>(a, l, st);
+}
+
+template <typename XT, bool SPLIT>
+int backward_rows(const moe_norm_args &a, const moe_norm_grads &g, const RingLaunch &l, int *status, float *parts,
+                  cudaStream_t st) {
+  static std::atomic<uint64_t> ready[3];
+  auto run = [&](auto kernel, std::atomic<uint64_t> &r) { return launch_rows<SPLIT>(kernel, r, l, st, a, g, l.shape, status, parts); };
+  if (a.gate_kind == MOE_GATE_FULL) return run(norm_backward_kernel<XT, true, false, SPLIT>, ready[0]);
+  if (a.b && a.w_post && a.w_pre && g.dy && g.dx && g.db) return run(norm_backward_kernel<XT, false, true, SPLIT>, ready[1]);
+  return run(norm_backward_kernel<XT, false, false, SPLIT>, ready[2]);
 }
 
 template <typename XT>
 int backward_launch(const moe_norm_args &a, const moe_norm_grads &g, cudaStream_t st) {
   int *status = static_cast<int *>(g.workspace);
   float *parts = reinterpret_cast<float *>(static_cast<char *>(g.workspace) + kStatusBytes);
-  const int x = (int)sizeof(XT), H = (int)a.H;
-  const RingLaunch l = ring_launch(a.T, a.H, H * ((a.w_pre ? x + 2 : 0) + (g.dy && x == 2 ? x : 0) + (a.b ? 2 : 0)) + gate_row_bytes(a),
-                                   8 * H);
-  int n = l.blocks, rc;
-  if (l.ok) {
-    const int threads = l.shape.group * l.shape.groups;
-    static std::atomic<uint64_t> ready[3];
-    auto run = [&](auto kernel, std::atomic<uint64_t> &r) -> int {
-      return allow_smem(kernel, r) ? launch_pdl(kernel, dim3(n), dim3(threads), l.smem, st, a, g, l.shape, status, parts)
-                                   : MOE_ERR_CUDA;
-    };
-    const bool all = a.b && a.w_post && a.w_pre && g.dy && g.dx && g.db;
-    if (a.gate_kind == MOE_GATE_FULL)
-      rc = run(norm_backward_kernel<XT, true, false>, ready[0]);
-    else
-      rc = all ? run(norm_backward_kernel<XT, false, true>, ready[1]) : run(norm_backward_kernel<XT, false, false>, ready[2]);
-  } else {
-    if (cudaMemsetAsync(status, 0, 64, st) != cudaSuccess) return MOE_ERR_CUDA;
-    n = std::min(most_parts(a.T, a.H), 2 * num_sms());
-    const Shape s = row_shape(a.H, 2, kBackwardThreads);
-    rc = launch_pdl(s.v == 2 ? norm_backward_wide_kernel<XT, 2> : norm_backward_wide_kernel<XT, 4>, dim3(n),
-                    dim3(s.threads), 0, st, a, g, parts);
-  }
+  const int x = (int)sizeof(XT);
+  const RingLaunch l = ring_launch(
+      a.T, a.H, (a.w_pre ? x + 2 : 0) + (g.dy && x == 2 ? x : 0) + (a.b ? 2 : 0) + gate_column_bytes(a), 8);
+  const int rc = is_split(a.H) ? backward_rows<XT, true>(a, g, l, status, parts, st)
+                               : backward_rows<XT, false>(a, g, l, status, parts, st);
   if (rc != MOE_OK) return rc;
   const bool gate = a.gate_kind == MOE_GATE_CHANNEL && g.dgate;
   if (!g.dw_pre && !g.dw_post && !gate) return MOE_OK;
   return launch_pdl(norm_parts_kernel, dim3((unsigned)ceil_div(a.H, 128), g.dw_post || gate ? 2 : 1), dim3(32 * kPartWarps), 0, st,
-                    a, g, static_cast<const float *>(parts), n);
+                    a, g, static_cast<const float *>(parts), l.rows);
 }
 
 }  // namespace

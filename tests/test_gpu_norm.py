@@ -156,6 +156,18 @@ def test_gates_and_norms(M, gate, gt, sigmoid, post, pre):
     check(M, Case(350, 328, gate=gate, gt=gt, sigmoid=sigmoid, post=post, pre=pre))
 
 
+@pytest.mark.parametrize("gate,gt", [(None, F32), ("token", F32), ("channel", BF16), ("full", F32)])
+@pytest.mark.parametrize("H,xt,post,pre", [(8200, BF16, True, True), (16376, F32, True, True), (16384, BF16, False, True),
+                                           (9000, F32, True, False)])
+def test_rows_split_over_two_blocks(M, H, xt, gate, gt, post, pre):
+    check(M, Case(170, H, xt, gate=gate, gt=gt, sigmoid=True, post=post, pre=pre))
+
+
+@pytest.mark.parametrize("T,H", [(3000, 512), (5000, 248)])
+def test_many_short_rows(M, T, H):
+    check(M, Case(T, H, F32, gate="full", gt=F32))
+
+
 @pytest.mark.parametrize("wt", [BF16, F32])
 @pytest.mark.parametrize("offset", [0.0, 1.0])
 @pytest.mark.parametrize("scale", [0.0, 1.0, -2.5])
@@ -169,6 +181,14 @@ def test_first_norm_alone(M, xt):
     y, n = c.module(M).forward(c.x)
     assert y is c.x
     close("n", n, forward64(c)["n"], c.H, 0)
+    got, want = c.module(M).backward(c.x, None, None, c.dy, c.dn), backward64(c, c.x)
+    for k in want:
+        close(k, got[k], want[k], c.H, c.T)
+
+
+def test_first_norm_alone_of_split_rows(M):
+    c = Case(160, 8208, F32, layer=False)
+    close("n", c.module(M).forward(c.x)[1], forward64(c)["n"], c.H, 0)
     got, want = c.module(M).backward(c.x, None, None, c.dy, c.dn), backward64(c, c.x)
     for k in want:
         close(k, got[k], want[k], c.H, c.T)
