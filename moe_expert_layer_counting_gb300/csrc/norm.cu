@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // blockIdx.y: which sum.  A block has 128 columns, four to a lane, and a warp
 // takes every kPartWarps-th part: a thread's loads (10 for 152 parts) are all
-// in flight at once, and wait for nothing else.
+// in flight at once.
 constexpr int kPartWarps = 16;
 
 __global__ void __launch_bounds__(32 * kPartWarps) norm_parts_kernel(const moe_norm_args a, const moe_norm_grads g,
@@ -747,10 +747,15 @@ __global__ void __launch_bounds__(32 * kPartWarps) norm_parts_kernel(const moe_n
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c4 < H) {
     const float *from = parts + (int64_t)which * H + c4;
-#pragma unroll 10
-    for (int p = warp; p < n; p += kPartWarps) {
-      const float4 v = *reinterpret_cast<const float4 *>(from + (int64_t)p * 2 * H);
-      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    for (int p = warp; p < n; p += 10 * kPartWarps) {
+      float4 v[10];                        // with a test of each, or the last ones' loads would wait for each other
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const int at = p + i * kPartWarps;
+        v[i] = at < n ? *reinterpret_cast<const float4 *>(from + (int64_t)at * 2 * H) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 10; ++i) s = make_float4(s.x + v[i].x, s.y + v[i].y, s.z + v[i].z, s.w + v[i].w);
     }
   }
   red[warp][lane] = s;
