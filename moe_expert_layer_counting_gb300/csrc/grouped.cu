@@ -20,7 +20,7 @@
 // zeroes those rows, and the MMA waits for both CTAs' warps.
 //
 // Roles per CTA (384 threads): warp 0 loads (TMA), warp 1 of the leader issues
-// the MMAs, warp 2 allocates TMEM and zeroes ragged ends, warps 4-11 drain the
+// the MMAs, warp 2 allocates TMEM and zeroes ragged ends, warp 3 hands out wgrad's items, warps 4-11 drain the
 // accumulators (two per TMEM lane quadrant: forward / dgrad 64-byte row pieces
 // from registers, wgrad boxes of 32 rows x 128 bytes through TMA).  Two accumulators
 // alternate, so an item's drain overlaps the next item's MMAs.  Every wait is
@@ -33,8 +33,10 @@
 //                                         (6.0 TB/s)
 //   both (64 experts, 16 384 rows, Zipf)  4.4 GB and 1.0 TFLOP in 761 to 806 us in a burst; at the
 //                                         power limit, back to back, 870 us
-//   wgrad, few rows        HBM, stores    32 experts of 128 rows, BF16: 1.97 GB in 315 us (6.3 TB/s);
-//                                         256 of 31 rows, 1024 x 2048, float32: 366 us (6.0 TB/s)
+//   wgrad, few rows        HBM, stores    32 experts of 128 rows, BF16: 1.97 GB in 308 us (6.4 TB/s);
+//                                         64 of 32 rows, BF16: 522 us (7.3 TB/s); 256 of 31 rows,
+//                                         1024 x 2048, float32: 322 us (6.8 TB/s; zeros alone are
+//                                         written at 7.5, a copy runs at 6.8)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -63,7 +65,8 @@ struct GP {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   static constexpr int kMaxStages = 6;
-  static constexpr int kNumBars = 4 * kMaxStages + 6;
+  static constexpr int kClaims = 4;                    // wgrad: items worked out ahead of the slowest role
+  static constexpr int kNumBars = 4 * kMaxStages + 6 + 4 * kClaims + 1;
 };
 
 // Shared memory of one direction: a ring of slots (stages), staging of the
@@ -75,22 +78,22 @@ struct GP {
 //   up to 320:  one block (A 16 KB, B 20 KB).
 // Six slots: with five, 16 384 rows of one expert (N = 4096, K = 7168) took 539
 // instead of 494 us.  The output goes from registers to memory.
-// wgrad: one block (A 16 KB, B 16 KB).  It stages its output for TMA stores: a
-// 4 KB box per warp for BF16 (two would cost a stage: 348 instead of 312 us for
-// 32 experts of 128 rows), two for float32, whose twice as many boxes bound the
-// drain.  Its items need no table.
+// wgrad: one block (A 16 KB, B 16 KB).  It stages its output for TMA stores, a
+// 4 KB box per warp: two would cost a stage (32 experts of 128 rows, BF16: 333
+// instead of 308 us; 64 of 256 rows, float32: 1220 instead of 1172).
 template <int OP>
 struct Layout {
   static constexpr bool kW = OP >= kWgrad;
   static constexpr int kSlot = kW ? 32768 : 36864;
-  static constexpr int kStages = OP == kWgradF32 ? 5 : 6;
-  static constexpr int kBoxes = OP == kWgradF32 ? 2 : 1;
-  static constexpr int kEpiBytes = kW ? kBoxes * 4096 : 0;       // per epilogue warp
+  static constexpr int kStages = GP::kMaxStages;
+  static constexpr int kEpiBytes = kW ? 4096 : 0;       // per epilogue warp
   static constexpr int kOffEpi = kStages * kSlot;
   static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
+  static constexpr int kOffClaims = kOffTmemPtr + 16;  // wgrad: answers (and one for draining), items
   static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: Lists::first[2][E+1]
-  static constexpr size_t bytes(int E) { return 1024 + kOffTab + (kW ? 0 : (size_t)8 * (E + 1)); }
+  static constexpr int kEnd = kW ? kOffClaims + 16 * (GP::kClaims + 1) + 32 * GP::kClaims : kOffTab;
+  static constexpr size_t bytes(int E) { return 1024 + kEnd + (kW ? 0 : (size_t)8 * (E + 1)); }
 };
 
 // float32 gradients: reduction blocks whose sum the tensor core holds before it
@@ -216,55 +219,147 @@ struct Lists {
   }
 };
 
-// The items at places w, w + step, ... of one cluster, in order.  wgrad: every
-// place has one, expert-major, then 256-row tiles, 256-column tiles fastest (so
-// that the items in flight write whole rows of dw), advanced without divisions.
-template <int OP>
-struct Items {
-  static constexpr bool kW = OP >= kWgrad;
+// forward / dgrad: the items at places w, w + step, ... of one pair.
+struct Places {
   const GArgs &g;
-  const Lists &lists;         // forward / dgrad
+  const Lists &lists;
   int w, step, total;
-  int mt, ct, dm, dc;         // wgrad: tiles of dw, step in (it.m, it.c)
   GItem it;
 
-  __device__ __forceinline__ Items(const GArgs &g, const Lists &lists, int first, int step, int total)
-      : g(g), lists(lists), w(first), step(step), total(total), mt(lists.mt), ct((g.C + GP::kN - 1) / GP::kN), dm(0), dc(0) {
-    if (kW) {
-      it.m = w / ct;
-      it.c = w - it.m * ct;
-      dm = step / ct;
-      dc = step - dm * ct;
-      it.e = it.m / mt;
-      it.m -= it.e * mt;
-      if (w < total) set();
-    } else {
-      it.kb = (g.R + GP::kBK - 1) / GP::kBK;
-      while (w < total && !lists.at(w, it)) w += step;
-    }
-  }
-  __device__ __forceinline__ void set() {
-    it.row0 = __ldg(g.offsets + it.e);
-    it.rows = __ldg(g.offsets + it.e + 1) - it.row0;
-    it.kb = (it.rows + GP::kBK - 1) / GP::kBK;
-    it.per = 1;
-    it.n = min(GP::kN, (g.C - it.c * GP::kN + 31) & ~31);
-    it.n2 = 0;
-  }
   __device__ __forceinline__ bool more() const { return w < total; }
+  __device__ __forceinline__ void find() {
+    while (w < total && !lists.at(w, it)) w += step;
+  }
+  __device__ __forceinline__ void start(bool) {
+    it.kb = (g.R + GP::kBK - 1) / GP::kBK;
+    find();
+  }
   __device__ __forceinline__ void next() {
     w += step;
-    if (kW) {
-      it.c += dc;
-      it.m += dm;
-      if (it.c >= ct) { it.c -= ct; ++it.m; }
-      while (it.m >= mt) { it.m -= mt; ++it.e; }
-      if (w < total) set();
-    } else {
-      while (w < total && !lists.at(w, it)) w += step;
-    }
+    find();
   }
 };
+
+// wgrad: a launch has a pair of CTAs for each item.  A pair works on the one
+// that it was launched for, then on those of pairs that it keeps from being
+// launched (claims): a pair that is quicker does more of them, and they are
+// begun in order.  With fixed shares the SMs that the memory serves last finish
+// last (stores alone: 6.7 instead of 7.5 TB/s; 256 experts of 31 rows, N = 1024,
+// K = 2048, float32: 370 instead of 320 us).  forward and dgrad, whose pairs read
+// the same weights from L2 at the same time, are 2 % slower that way.
+//
+// Warp 3 of the leader claims for both CTAs; each CTA's warp 3 works out the
+// item and puts it into a ring that its roles read.
+struct Ring {
+  uint64_t *claim_full;    // each CTA: an answer has arrived
+  uint64_t *claim_empty;   // leader: the other CTA has read it
+  uint64_t *claim_drain;
+  uint64_t *item_full, *item_empty;
+  unsigned char *answer;   // kClaims + 1 of 16 bytes
+  int4 *items;             // 2 each: (e, m, c, place), (row0, rows, 0, 0); place -1 after the last
+};
+
+struct Claimed {
+  const GArgs &g;
+  const Ring &ring;
+  int w, slot;
+  uint32_t phase;
+  bool wide;               // the role is a warp, not a thread
+  GItem it;
+
+  __device__ __forceinline__ bool more() const { return w >= 0; }
+  __device__ __forceinline__ void start(bool warp_wide) {
+    w = 0;
+    slot = 0;
+    phase = 0;
+    wide = warp_wide;
+    next();
+  }
+  __device__ __forceinline__ void next() {
+    const bool got = mbar_wait_reset(ring.item_full + slot, phase, g.status, kLimit, kWaitArrival, w);
+    if (!(wide ? __all_sync(0xffffffffu, got) : got)) {
+      w = -1;
+      return;
+    }
+    const int4 a = ring.items[2 * slot], b = ring.items[2 * slot + 1];
+    it.e = a.x;
+    it.m = a.y;
+    it.c = a.z;
+    w = a.w;
+    it.row0 = b.x;
+    it.rows = b.y;
+    it.kb = (b.y + GP::kBK - 1) / GP::kBK;
+    it.per = 1;
+    it.n = min(GP::kN, (g.C - a.z * GP::kN + 31) & ~31);
+    it.n2 = 0;
+    if (wide) __syncwarp();
+    if (!wide || (threadIdx.x & 31) == 0) mbar_arrive(ring.item_empty + slot);
+    if (++slot == GP::kClaims) { slot = 0; phase ^= 1; }
+  }
+};
+
+// Short items are claimed as far ahead as the ring holds them; after one of more
+// rows than this (some 20 us) the next is claimed when every role has come to
+// it, or pairs would hold items that are far apart in dw (one expert of 16 384
+// rows: 504 instead of 567 us, of 8192 rows 264 instead of 293; two experts of
+// 4096 rows 270 instead of 264).
+constexpr int kLongRows = 4096;
+
+// One thread of each CTA of a pair.
+__device__ __forceinline__ void claim_items(const GArgs &g, const Ring &ring, int w, int total, int mt, uint32_t rank) {
+  const int ct = (g.C + GP::kN - 1) / GP::kN;
+  int *status = g.status;
+  int slot = 0;
+  uint32_t phase = 0;          // of the slot's answer and item
+  bool ok = true, left = true;
+  for (;;) {
+    // 256-column tiles fastest, so that the items in flight write whole rows of dw
+    int4 a = make_int4(0, w / ct, 0, w), b = make_int4(0, 0, 0, 0);
+    if (w >= total) a.w = -1;
+    if (a.w >= 0) {
+      a.z = w - a.y * ct;
+      a.x = a.y / mt;
+      a.y -= a.x * mt;
+      b.x = __ldg(g.offsets + a.x);
+      b.y = __ldg(g.offsets + a.x + 1) - b.x;
+    }
+    ok = mbar_wait_reset(ring.item_empty + slot, phase ^ 1, status, kLimit, kWaitArrival, w);
+    if (!ok) break;
+    ring.items[2 * slot] = a;
+    ring.items[2 * slot + 1] = b;
+    mbar_arrive(ring.item_full + slot);
+    if (a.w < 0) break;
+    if (b.y > kLongRows) {
+      ok = mbar_wait_reset(ring.item_empty + slot, phase, status, kLimit, kWaitArrival, w);
+      if (!ok) break;
+    }
+    if (rank == 0) {
+      ok = mbar_wait_reset(ring.claim_empty + slot, phase ^ 1, status, kLimit, kWaitArrival, w);
+      if (!ok) break;
+      mbar_arrive_expect_tx(ring.claim_full + slot, 16);
+      mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(ring.claim_full + slot), 1), 16);
+      claim_cluster_pair(ring.answer + 16 * slot, ring.claim_full + slot);
+    }
+    ok = mbar_wait_reset(ring.claim_full + slot, phase, status, kLimit, kWaitArrival, w, rank != 0);
+    if (!ok) break;
+    const int cta = claimed_cta(ring.answer + 16 * slot);
+    fence_proxy_async_shared();                            // the answer's place is written again by the async proxy
+    if (rank != 0) mbar_arrive_done(mapa_shared(smem_u32(ring.claim_empty + slot), 0));
+    left = cta >= 0;
+    w = left ? cta >> 1 : total;
+    if (++slot == GP::kClaims) { slot = 0; phase ^= 1; }
+  }
+  if (rank != 0) return;
+  // after a wait gave up, or with bad offsets (total 0): what is left is claimed
+  // and dropped, so that those pairs need not be launched to give up in turn
+  for (phase = 0; left && (!ok || total == 0); phase ^= 1) {
+    mbar_arrive_expect_tx(ring.claim_drain, 16);
+    claim_cluster(ring.answer + 16 * GP::kClaims, ring.claim_drain);
+    if (!mbar_wait_reset(ring.claim_drain, phase, status, kLimit, kWaitArrival, slot, false)) return;
+    if (claimed_cta(ring.answer + 16 * GP::kClaims) < 0) return;
+    fence_proxy_async_shared();
+  }
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -306,19 +401,18 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], int64_t row0
   }
 }
 
-// wgrad: BOXES boxes of 32 rows (TMEM lanes) x 128 bytes (64 BF16 or 32 float32
+// wgrad: a box of 32 rows (TMEM lanes) x 128 bytes (64 BF16 or 32 float32
 // columns) of dw, from this lane's values `v`, through swizzled staging to a
 // TMA store (`add`: addition), which leaves out what lies outside dw.  dw is
-// written once and streams through L2 (evict first: 1227 instead of 1305 us for
+// written once and streams through L2 (evict first: 1024 instead of 1046 us for
 // 64 experts of 32 rows, N = 4096, K = 7168 in float32).
-template <bool kF32, int BOXES>
-__device__ __forceinline__ void store_boxes(const uint32_t *v, bool add, int row, int col, int e, int C,
-                                            const CUtensorMap *map, int lane, unsigned char *buf) {
-  constexpr int kCols = kF32 ? 32 : 64;
-  if (lane == 0) bulk_wait_read<0>();               // the stores before have read the staging
+template <bool kF32>
+__device__ __forceinline__ void store_box(const uint32_t *v, bool add, int row, int col, int e, const CUtensorMap *map,
+                                          int lane, unsigned char *buf) {
+  if (lane == 0) bulk_wait_read<0>();               // the store before has read the staging
   __syncwarp();
 #pragma unroll
-  for (int p = 0; p < 8 * BOXES; ++p) {
+  for (int p = 0; p < 8; ++p) {
     uint4 piece;
     if (kF32) {
       piece = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
@@ -328,29 +422,25 @@ __device__ __forceinline__ void store_boxes(const uint32_t *v, bool add, int row
       for (int j = 0; j < 4; ++j) w[j] = pack_bf16(__uint_as_float(v[8 * p + 2 * j]), __uint_as_float(v[8 * p + 2 * j + 1]));
       piece = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4 *>(buf + (p >> 3) * 4096 + lane * 128 + (((p & 7) ^ (lane & 7)) << 4)) = piece;
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = piece;
   }
   fence_proxy_async_shared();
   __syncwarp();
   if (lane == 0) {
-#pragma unroll
-    for (int b = 0; b < BOXES; ++b) {
-      if (col + b * kCols >= C) break;
-      if (kF32 && add)
-        tma_add_3d(map, buf + b * 4096, col + b * kCols, row, e);
-      else
-        tma_store_3d(map, buf + b * 4096, col + b * kCols, row, e);
-    }
+    if (kF32 && add)
+      tma_add_3d(map, buf, col, row, e);
+    else
+      tma_store_3d(map, buf, col, row, e);
     bulk_commit();
   }
 }
 
 // This warp's 32 rows x 128 columns of dw from the accumulator; `none`: no
 // rows, zeros.
-template <bool kF32, int BOXES>
+template <bool kF32>
 __device__ __forceinline__ void store_block(uint32_t t_row, bool none, bool add, int row, int col, int e, int C,
                                             const CUtensorMap *map, int lane, unsigned char *buf) {
-  constexpr int kCols = (kF32 ? 32 : 64) * BOXES;
+  constexpr int kCols = kF32 ? 32 : 64;
 #pragma unroll
   for (int c0 = 0; c0 < 128; c0 += kCols) {
     if (col + c0 >= C) break;
@@ -364,7 +454,7 @@ __device__ __forceinline__ void store_block(uint32_t t_row, bool none, bool add,
         tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + h), *reinterpret_cast<uint32_t(*)[32]>(v + h));
       tmem_ld_wait();
     }
-    store_boxes<kF32, BOXES>(v, add, row, col + c0, e, C, map, lane, buf);
+    store_box<kF32>(v, add, row, col + c0, e, map, lane, buf);
   }
 }
 
@@ -384,12 +474,20 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   uint64_t *tmem_empty = tmem_full + 2;                // leader: both CTAs drained the accumulator
   uint64_t *mma_done = tmem_empty + 2;
   uint64_t *never = mma_done + 1;
+  unsigned char *const answers = smem + L::kOffClaims;
+  const Ring ring{never + 1,
+                  never + 1 + GP::kClaims,
+                  never + 1 + 4 * GP::kClaims,
+                  never + 1 + 2 * GP::kClaims,
+                  never + 1 + 3 * GP::kClaims,
+                  answers,
+                  reinterpret_cast<int4 *>(answers + 16 * (GP::kClaims + 1))};
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
   int *tile_first = reinterpret_cast<int *>(smem + L::kOffTab);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int cluster = (int)blockIdx.x >> 1, nclusters = (int)gridDim.x >> 1;
+  const int cluster = (int)blockIdx.x >> 1;
   int *status = g.status;
 
   if (warp == 0) {
@@ -411,6 +509,14 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       }
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
+      for (int c = 0; kW && c < GP::kClaims; ++c) {
+        mbar_init(ring.claim_full + c, 1);
+        mbar_init(ring.claim_empty + c, 1);
+        mbar_init(ring.item_full + c, 1);
+        // roles: loads, ragged ends, epilogue, the leader's MMAs
+        mbar_init(ring.item_empty + c, 2 + GP::kEpiWarps + (rank == 0 ? 1 : 0));
+      }
+      if (kW) mbar_init(ring.claim_drain, 1);
       fence_mbar_init();
     }
     __syncwarp();
@@ -472,7 +578,12 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   }
   if (bad) total = 0;
   const uint32_t tmem_base = *tmem_ptr;
-  Items<OP> items(g, lists, cluster, nclusters, total);
+  auto items = [&] {
+    if constexpr (kW)
+      return Claimed{g, ring};
+    else
+      return Places{g, lists, cluster, (int)gridDim.x >> 1, total};
+  }();
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads (both CTAs), one thread
@@ -484,6 +595,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       uint32_t phase = 0, issued = 0, issued_phase = 0, tails = 0, tail_phase = 0;
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+      items.start(false);
       while (items.more() && ok) {
         const GItem it = items.it;
         if (kW && it.kb == 0) {
@@ -595,6 +707,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       int stage = 0, j = 0;
       uint32_t phase = 0, fixed_phase = 0;
       bool ok = true;
+      items.start(false);
       while (items.more() && ok) {
         const int w = items.w;
         const GItem it = items.it;
@@ -691,6 +804,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
     if (kW) {
       int block = 0;                                           // blocks of the items before, modulo the ring
       uint32_t tail_phase = 0;
+      items.start(true);
       for (; items.more(); items.next()) {
         const GItem it = items.it;
         if (it.kb > 0 && (it.rows & 15) != 0) {
@@ -719,12 +833,16 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         block = (block + it.kb) % L::kStages;
       }
     }
-  } else if (warp >= GP::kFirstEpiWarp) {
+  } else if (warp == 3) {
+    if (kW && elect_one()) claim_items(g, ring, cluster, total, mt, rank);
+    __syncwarp();
+  } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;
     const int ew = warp - GP::kFirstEpiWarp;
     unsigned char *stage_tile = smem + L::kOffEpi + ew * L::kEpiBytes;
     int j = 0;
+    items.start(true);
     while (items.more()) {
       const int w = items.w;
       const GItem it = items.it;
@@ -733,7 +851,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       const int col = it.c * GP::kN + 128 * (ew >> 2);             // wgrad: this warp's columns
       if (kW && it.kb == 0) {                                      // an expert without rows
         if (first < g.M && !g.accumulate)
-          store_block<OP == kWgradF32, L::kBoxes>(0, true, false, first, col, it.e, g.C, &maps.b[1], lane, stage_tile);
+          store_block<OP == kWgradF32>(0, true, false, first, col, it.e, g.C, &maps.b[1], lane, stage_tile);
         continue;
       }
       const uint32_t t_lane = tmem_base + ((uint32_t)(32 * q) << 16);
@@ -773,10 +891,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         if (!got) break;
         if (first < g.M) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 32 * L::kBoxes)
+          for (int c = 0; c < 128; c += 32)
             if (col + c < g.C)
-              store_boxes<true, L::kBoxes>(reinterpret_cast<uint32_t *>(sum) + c, g.accumulate, first, col + c, it.e, g.C,
-                                           &maps.b[1], lane, stage_tile);
+              store_box<true>(reinterpret_cast<uint32_t *>(sum) + c, g.accumulate, first, col + c, it.e, &maps.b[1], lane,
+                              stage_tile);
         }
         continue;
       }
@@ -788,7 +906,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
         if (first < g.M) {
           if (kW) {
-            store_block<OP == kWgradF32, L::kBoxes>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
+            store_block<OP == kWgradF32>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
                                                     &maps.b[1], lane, stage_tile);
           } else {
             const int row0 = it.row0 + part * it.n, rows = part == 0 ? min(it.rows, it.n) : it.rows - it.n;
@@ -862,7 +980,7 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
       return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  const int64_t clusters = std::min<int64_t>(num_sms() / 2, most_items);
+  const int64_t pairs = OP >= kWgrad ? most_items : std::min<int64_t>(num_sms() / 2, most_items);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -871,7 +989,7 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * clusters));
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(GP::kThreads);
   cfg.dynamicSmemBytes = Layout<OP>::bytes(g.E);
   cfg.stream = st;

@@ -155,4 +155,40 @@ __device__ __forceinline__ bool mbar_wait_reset(uint64_t *bar, uint32_t parity, 
   }
 }
 
+// ---------------------------------------------------------------- clusters that have not been launched yet
+// Asks for one: its launch is cancelled and its place left to the caller, or
+// there is none left (nothing is asked after that).  The answer, 16 bytes, is
+// written to `answer` and counted on `bar`, of this CTA or (pair) of both CTAs.
+__device__ __forceinline__ void claim_cluster(void *answer, uint64_t *bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void claim_cluster_pair(void *answer, uint64_t *bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], "
+      "[%1];" ::"r"(smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The index of the claimed cluster's first CTA, or -1.
+__device__ __forceinline__ int claimed_cta(const void *answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return x;
+}
+// Arms a barrier of either CTA of the pair for `bytes` more.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(bytes) : "memory");
+}
+
 }  // namespace mxq
