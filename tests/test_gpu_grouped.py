@@ -133,6 +133,44 @@ def test_long_segment_in_float32(B):
     assert float((dw[0].double() - ref).norm() / ref.norm()) <= 2e-6
 
 
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_weights_of_more_items_than_pairs_of_sms(B, dtype):
+    """Experts of more than 4096 rows, short and empty ones, 280 tiles of dw, two calls at a time on two streams."""
+    counts, N, K = [4100, 0, 3, 70, 0, 5000, 129, 17], 1032, 1544
+    E, P = len(counts), sum(counts)
+    dy, x, off = randn(P, N, seed=3), randn(P, K, seed=4), offsets_of(counts)
+    dws = [torch.full((E, N, K), 3.0, dtype=dtype, device="cuda") for _ in range(2)]
+    spaces, streams = [workspace(B, P, N, K, E) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for dw, ws, stream in zip(dws, spaces, streams):
+            B.moe_grouped_wgrad(dy, x, off, dw, ws, stream=stream)
+    torch.cuda.synchronize()
+    assert all(B.moe_get_device_status(ws) == B.MOE_OK for ws in spaces)
+    for e, (_, _, ref, mag, terms) in enumerate(reference("wgrad", counts, dy, x)):
+        close(dws[0][e], ref, mag, terms)
+    assert torch.equal(dws[0], dws[1])
+
+
+def test_many_items_with_bad_offsets_or_a_wait_that_runs_out(B, monkeypatch):
+    """What is left of the launch is dropped: the call ends, reports, and the next one is right."""
+    E, P, N, K = 400, 800, 256, 264
+    dy, x, ws = randn(P, N, seed=1), randn(P, K, seed=2), workspace(B, P, N, K, E)
+    dw = torch.full((E, N, K), 3.0, dtype=BF16, device="cuda")
+    bad = offsets_of([2] * E).clone()
+    bad[7] = 900
+    B.moe_grouped_wgrad(dy, x, bad, dw, ws)
+    assert B.moe_get_device_status(ws) == B.MOE_ERR_DEVICE_INDEX and bool((dw == 3.0).all())
+    monkeypatch.setenv("MOE_MXQ_DEBUG_INJECT_WAIT", "1")
+    B.moe_grouped_wgrad(dy, x, offsets_of([2] * E), dw, ws)
+    assert B.moe_get_device_status(ws) == B.MOE_ERR_TIMEOUT
+    monkeypatch.delenv("MOE_MXQ_DEBUG_INJECT_WAIT")
+    B.moe_grouped_wgrad(dy, x, offsets_of([2] * E), dw, ws)
+    assert B.moe_get_device_status(ws) == B.MOE_OK
+    for e, (_, _, ref, mag, terms) in enumerate(reference("wgrad", [2] * E, dy, x)):
+        close(dw[e], ref, mag, terms)
+
+
 @pytest.mark.parametrize("first,last", [(0, 9), (6, 0), (5, 4)])
 def test_rows_of_no_expert_are_left_alone(B, first, last):
     """Rows outside [offsets[0], offsets[E]) are not written, whatever they hold (NaN here), and reach no result."""
