@@ -8,10 +8,11 @@
 // tensor by bisection of the tensors' first blocks.  A thread owns 8
 // consecutive values, four neighbours a 32-value group of the 8-bit states.
 // Measured: float32 states, 201 M values in 805 us (7.0 TB/s); 8-bit states,
-// 352 M values in 870 to 912 us (6.2 to 6.5 TB/s, two thirds of the issue slots).
+// 352 M values in 845 us (6.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/moe_adamw.h"
@@ -178,9 +179,20 @@ __device__ __forceinline__ uint2 encode8(const V8 &f, int e) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {              // within 2 units in the last place
+// Within 2 units in the last place; FTZ: a subnormal's root is 0.
+template <bool FTZ>
+__device__ __forceinline__ float sqrt_approx(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  if (FTZ)
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Of a value that is 0 or normal, as its reciprocal is.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -198,7 +210,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
   // a round's loads are issued before the round before is worked on (352 M
   // values with 8-bit states: 871 us instead of 1104; four rounds 1038, fewer
-  // registers for more blocks 1003 or worse)
+  // registers for more blocks 1003 or worse; with a reciprocal for the
+  // quotient, flushing roots, and the tests on values joined over a thread's 8: 845)
   struct Loaded {
     Raw8<PT> p;
     Raw8<GT> g;
@@ -233,6 +246,9 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const Loaded x = ahead;
     if (r + 1 < kRounds) ahead = load(i + 8 * kThreads);
     V8 p, g, m, v, root;
+    // the least v above zero, as its bits less one (0: the largest of all)
+    uint32_t low = 0xffffffffu;
+    constexpr uint32_t kLeastNormal = 0x00800000u - 1u;
     if (!kSmall || live > 0) {
       p = x.p.get();
       g = x.g.get();
@@ -246,9 +262,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const float old = kSmall ? __fmul_rn(v.v[j], v.v[j]) : v.v[j];
         m.v[j] = __fadd_rn(__fmul_rn(m.v[j], a.beta1), __fmul_rn(gj, a.one_minus_beta1));
         v.v[j] = __fadd_rn(__fmul_rn(old, a.beta2), __fmul_rn(__fmul_rn(gj, gj), a.one_minus_beta2));
-        root.v[j] = sqrt_approx(v.v[j]);
-        p.v[j] = p.v[j] * a.keep - a.rate * __fdividef(m.v[j], fmaf(root.v[j], a.root_scale, a.eps));
+        root.v[j] = sqrt_approx<kSmall>(v.v[j]);
+        low = min(low, __float_as_uint(v.v[j]) - 1u);
       }
+      if (kSmall && low < kLeastNormal) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) root.v[j] = __fsqrt_rn(v.v[j]);
+      }
+      // a root is 0 or at least 2^-75, so the sum is 0 or normal
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        p.v[j] = p.v[j] * a.keep - a.rate * (m.v[j] * rcp_approx(fmaf(root.v[j], a.root_scale, a.eps)));
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) p.v[j] = m.v[j] = v.v[j] = root.v[j] = 0.f;
@@ -264,19 +288,22 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       for (int j = 0; j < 8; ++j) {
         m_max = fmaxf(m_max, fabsf(m.v[j]));
         v_max = fmaxf(v_max, v.v[j]);
-        near = min(near, (__float_as_uint(root.v[j]) + 2u) & 0x7ffffu);
+        near = min(near, (__float_as_uint(root.v[j]) + 2u) << 13);
       }
       const int me = ue8m0_exponent<true>(group_max(m_max)), ve = ue8m0_exponent<true>(__fsqrt_rn(group_max(v_max)));
       const uint8_t mb = (uint8_t)(me + 127), vb = (uint8_t)(ve + 127);
-      if (near <= 4u) {
+      if (near < (5u << 13)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) root.v[j] = __fsqrt_rn(v.v[j]);
       }
-      // a root above zero takes at least the smallest code
+      // a root above zero takes at least the smallest code (looked at only where
+      // some v is near or below its square, or subnormal)
       const float least = scale_of(vb) * 0.001953125f;
+      if (low < max(__float_as_uint(1.01f * least * least), kLeastNormal)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (root.v[j] > 0.f) root.v[j] = fmaxf(root.v[j], least);
+        for (int j = 0; j < 8; ++j)
+          if (root.v[j] > 0.f) root.v[j] = fmaxf(root.v[j], least);
+      }
       const uint2 mc = encode8(m, me), vc = encode8(root, ve);
       if (live > 0) {
         store_codes(static_cast<uint8_t *>(t.m) + i, mc, live);
@@ -318,7 +345,7 @@ int launch_some(const moe_adamw_args &a, int from, int to, cudaStream_t st) {
   t.keep = (float)(1.0 - a.lr * a.weight_decay);
   t.rate = (float)(a.lr / (1.0 - std::pow(a.beta1, (double)a.step)));
   t.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, (double)a.step)));
-  t.eps = (float)a.eps;
+  t.eps = a.eps > 0 ? std::max((float)a.eps, 1.17549435e-38f) : 0.f;       // 0 or normal (rcp_approx)
   t.grad_scale = a.grad_scale;
   return launch_pdl(adamw_kernel<PT, GT, kSmall, TENSORS>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t);
 }

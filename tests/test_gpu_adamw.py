@@ -127,6 +127,31 @@ def test_8_bit_states(M, pt, gt, clip):
                 assert np.array_equal(opt.state[name][i].cpu().numpy(), codes), (name, t, n)
 
 
+@pytest.mark.parametrize("low,high", [(-23, 0), (-23, -17), (-21, -18), (-4, 4), (10, 17)])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_gradients_over_the_whole_range(M, bits, low, high):
+    """Magnitudes from 10^low to 10^high in every group, squares that are subnormal or round to 0 among them: the codes
+    bit for bit, and p from m and v as float32 rounds them (a sum of eps alone where v is 0)."""
+    n, eps = 5000, 1e-30
+    rng = np.random.RandomState(7)
+    g = (10.0 ** rng.uniform(low, high, n) * rng.choice([-1.0, 1.0], n)).astype(np.float32)
+    p = torch.zeros(n, device="cuda")
+    b1, b2 = HOW["betas"]
+    opt = M.AdamW([p], state_bits=bits, lr=1e-2, betas=(b1, b2), eps=eps, weight_decay=0.0)
+    opt.step([torch.from_numpy(g).cuda()])
+    m, v = g * np.float32(1 - b1), (g * g) * np.float32(1 - b2)
+    m64, root = m.astype(np.float64), np.sqrt(v.astype(np.float64) / (1 - b2)) + eps
+    want = torch.from_numpy(-1e-2 / (1 - b1) * m64 / root).cuda()
+    close(p, want, want.abs())
+    for name, x, is_root in (("m", m, False), ("v", np.sqrt(v) if bits == 8 else v, True)):
+        if bits == 8:
+            codes, scales = group_codes(x, is_root)
+            assert np.array_equal(opt.state[name + "_scale"][0].cpu().numpy(), scales), name
+            assert np.array_equal(opt.state[name][0].cpu().numpy(), codes), name
+        else:
+            assert np.array_equal(opt.state[name][0].cpu().numpy(), x), name
+
+
 def test_a_small_gradient_beside_a_large_one_does_not_jump(M):
     """8-bit states: sqrt(v) of a value far below its group's largest would round to 0 and the next step divide by
     eps; it is held at the smallest code instead, and no step moves a value by more than a few rates."""
