@@ -8,7 +8,7 @@
 // tensor by bisection of the tensors' first blocks.  A thread owns 8
 // consecutive values, four neighbours a 32-value group of the 8-bit states.
 // Measured: float32 states, 201 M values in 805 us (7.0 TB/s); 8-bit states,
-// 352 M values in 845 us (6.7 TB/s).
+// 352 M values in 843 us (6.7 TB/s), 859 where BF16 gradients meet held roots.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   // a round's loads are issued before the round before is worked on (352 M
   // values with 8-bit states: 871 us instead of 1104; four rounds 1038, fewer
   // registers for more blocks 1003 or worse; with a reciprocal for the
-  // quotient, flushing roots, and the tests on values joined over a thread's 8: 845)
+  // quotient, flushing roots, and the tests on values joined over a thread's 8: 843)
   struct Loaded {
     Raw8<PT> p;
     Raw8<GT> g;
@@ -280,29 +280,28 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (kSmall) {
       // scales: the root of the largest v is the largest root
       float m_max = 0.f, v_max = 0.f;
-      // a code changes where a root passes a multiple of 2^19 units of its last
-      // place; the approximate root decides unless it is that near (about one
-      // value in 100 000)
+      // a code that is not subnormal changes where a root passes an odd multiple
+      // of 2^19 units of its last place; the approximate root decides unless it is
+      // that near (about one value in 200 000; even multiples are the codes
+      // themselves, which a BF16 gradient that equals the held root hits often)
       uint32_t near = 0xffffffffu;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         m_max = fmaxf(m_max, fabsf(m.v[j]));
         v_max = fmaxf(v_max, v.v[j]);
-        near = min(near, (__float_as_uint(root.v[j]) + 2u) << 13);
+        near = min(near, (__float_as_uint(root.v[j]) + 2u + (1u << 19)) << 12);
       }
       const int me = ue8m0_exponent<true>(group_max(m_max)), ve = ue8m0_exponent<true>(__fsqrt_rn(group_max(v_max)));
       const uint8_t mb = (uint8_t)(me + 127), vb = (uint8_t)(ve + 127);
-      if (near < (5u << 13)) {
+      // subnormal codes are below 2^-6 of the scale; a root above zero takes at
+      // least the smallest, 2^-9
+      const float unit = scale_of(vb), subnormal = unit * 0.015625f, least = unit * 0.001953125f;
+      if (near < (5u << 12) || low < max(__float_as_uint(1.01f * subnormal * subnormal), kLeastNormal)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) root.v[j] = __fsqrt_rn(v.v[j]);
-      }
-      // a root above zero takes at least the smallest code (looked at only where
-      // some v is near or below its square, or subnormal)
-      const float least = scale_of(vb) * 0.001953125f;
-      if (low < max(__float_as_uint(1.01f * least * least), kLeastNormal)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
+          root.v[j] = __fsqrt_rn(v.v[j]);
           if (root.v[j] > 0.f) root.v[j] = fmaxf(root.v[j], least);
+        }
       }
       const uint2 mc = encode8(m, me), vc = encode8(root, ve);
       if (live > 0) {
