@@ -8,7 +8,7 @@
 // tensor by bisection of the tensors' first blocks.  A thread owns 8
 // consecutive values, four neighbours a 32-value group of the 8-bit states.
 // Measured: float32 states, 201 M values in 805 us (7.0 TB/s); 8-bit states,
-// 352 M values in 843 us (6.7 TB/s), 859 where BF16 gradients meet held roots.
+// 352 M values in 818 us (6.9 TB/s; 837 as 19 tensors).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,9 +23,13 @@ namespace mxq {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block.  With 8-bit states the arithmetic of one warp hides less
+// behind the others' loads, and blocks that come and go one by one keep the
+// warps of an SM apart: 352 M values in 818 us with 64 threads, 822 with 128, 843
+// with 256, 1105 with 512; float32 states 1403, 1403, 1394 and 1400.
+template <bool kSmall> constexpr int kThreads = kSmall ? 64 : 256;
 constexpr int kRounds = 2;                                   // vectors per thread
-constexpr int64_t kChunk = (int64_t)kThreads * 8 * kRounds;  // values per block
+template <bool kSmall> constexpr int64_t kChunk = (int64_t)kThreads<kSmall> * 8 * kRounds;      // values per block
 
 struct AdamEntry {
   int64_t n;
@@ -197,7 +201,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 template <typename PT, typename GT, bool kSmall, int TENSORS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<TENSORS> a) {
+__global__ void __launch_bounds__(kThreads<kSmall>) adamw_kernel(const __grid_constant__ AdamTable<TENSORS> a) {
   pdl_launch_dependents();
   pdl_wait();
   int lo = 0, hi = a.count;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (a.first[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
   }
   const AdamEntry &t = a.t[lo];
-  const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk;
+  const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - a.first[lo]) * kChunk<kSmall>;
   const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
   // a round's loads are issued before the round before is worked on (352 M
   // values with 8-bit states: 871 us instead of 1104; four rounds 1038, fewer
@@ -240,11 +244,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   int64_t i = base + (int64_t)threadIdx.x * 8;
   Loaded ahead = load(i);
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r, i += 8 * kThreads) {
+  for (int r = 0; r < kRounds; ++r, i += 8 * kThreads<kSmall>) {
     if (kSmall ? i - 8 * (threadIdx.x & 31) >= n : i >= n) break;      // 8-bit states: whole warps go on
     const int live = (int)(n - i < 0 ? 0 : n - i < 8 ? n - i : 8);
     const Loaded x = ahead;
-    if (r + 1 < kRounds) ahead = load(i + 8 * kThreads);
+    if (r + 1 < kRounds) ahead = load(i + 8 * kThreads<kSmall>);
     V8 p, g, m, v, root;
     // the least v above zero, as its bits less one (0: the largest of all)
     uint32_t low = 0xffffffffu;
@@ -333,7 +337,7 @@ int launch_some(const moe_adamw_args &a, int from, int to, cudaStream_t st) {
     if (x.n == 0) continue;
     t.t[t.count] = AdamEntry{x.n, x.p, x.g, x.m, x.v, x.m_scale, x.v_scale, x.copy};
     t.first[t.count++] = (int)blocks;
-    blocks += ceil_div(x.n, kChunk);
+    blocks += ceil_div(x.n, kChunk<kSmall>);
   }
   if (blocks == 0) return MOE_OK;
   t.first[t.count] = (int)blocks;
@@ -346,7 +350,7 @@ int launch_some(const moe_adamw_args &a, int from, int to, cudaStream_t st) {
   t.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, (double)a.step)));
   t.eps = a.eps > 0 ? std::max((float)a.eps, 1.17549435e-38f) : 0.f;       // 0 or normal (rcp_approx)
   t.grad_scale = a.grad_scale;
-  return launch_pdl(adamw_kernel<PT, GT, kSmall, TENSORS>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t);
+  return launch_pdl(adamw_kernel<PT, GT, kSmall, TENSORS>, dim3((unsigned)blocks), dim3(kThreads<kSmall>), 0, st, t);
 }
 
 constexpr int kFew = 40, kMany = 400;       // tensors per launch: 3 KB or 28 KB of kernel parameters
@@ -359,7 +363,7 @@ int step_all(const moe_adamw_args &a, cudaStream_t st) {
     int to = from;
     int64_t blocks = 0;
     while (to < a.n_tensors && to - from < kMany) {
-      const int64_t more = ceil_div(a.tensors[to].n, kChunk);
+      const int64_t more = ceil_div(a.tensors[to].n, kChunk<kSmall>);
       if (to > from && blocks + more > 0x7fffffffLL) break;
       blocks += more;
       ++to;
@@ -403,7 +407,7 @@ extern "C" int moe_adamw_step(const moe_adamw_args *a, cudaStream_t stream) {
     const moe_adamw_tensor &t = a->tensors[i];
     if (t.n < 0) return MOE_ERR_INVALID_ARG;
     if (t.n == 0) continue;
-    if (ceil_div(t.n, kChunk) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (ceil_div(t.n, a->state_bits == 8 ? kChunk<true> : kChunk<false>) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!t.p || !t.g || !t.m || !t.v || (a->state_bits == 8 && (!t.m_scale || !t.v_scale)) ||
         (t.copy && a->p_dtype == MOE_BF16))
       return MOE_ERR_INVALID_ARG;
