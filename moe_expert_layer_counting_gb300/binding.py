@@ -465,11 +465,11 @@ def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, e
         gt, gs = _DTYPES.get(gate.dtype), gate.shape
         if gt is None or len(gs) != 2:
             return None
-        if gs == (T, 1) or gs == (1, H):
-            kind = GATE_TOKEN if gs == (T, 1) else GATE_CHANNEL
-            gr = (gate.data_ptr(), 0) if gate.is_contiguous() else None
+        kind = GATE_TOKEN if gs == (T, 1) else GATE_CHANNEL if gs == (1, H) else GATE_FULL
+        if kind == GATE_FULL:
+            gr = _rows(gate, shape, gate.dtype)
         else:
-            kind, gr = GATE_FULL, _rows(gate, shape, gate.dtype)
+            gr = (gate.data_ptr(), 0) if gate.is_contiguous() else None
         if gr is None:
             return None
     return _NORM_ARGS.pack(_NORM_ARGS.size, xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale, weight_offset, eps,
@@ -489,6 +489,13 @@ def moe_norm_forward(x, b, gate, w_post, w_pre, y, n, residual_scale: float = 1.
     return rc
 
 
+def _column_sum(t, H: int):
+    """Pointer of a contiguous float32 [H] (0 for None); None if it is not one."""
+    if t is None:
+        return 0
+    return t.data_ptr() if t.dtype is torch.float32 and t.shape == (H,) and t.is_contiguous() else None
+
+
 def moe_norm_workspace_size(T: int, H: int) -> int:
     return int(lib.moe_norm_workspace_size(T, H))
 
@@ -499,22 +506,23 @@ def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=
     """Gradients of moe_norm_forward from dy and dn; y is its y (without b: its x).  Outputs that are None are not
     computed; dgate has the gate's shape and type, dw_post and dw_pre are float32 [H]."""
     a = _norm_args(y, b, gate, w_post, w_pre, None, None, residual_scale, weight_offset, eps, gate_sigmoid)
-    shape = y.shape
-    rows = [_NONE if t is None else _rows(t, shape, dtype) for t, dtype in
-            ((dy, y.dtype), (dn, torch.bfloat16), (dx, y.dtype), (db, torch.bfloat16))]
-    if dgate is not None:
-        if gate is None or dgate.dtype is not gate.dtype or dgate.shape != gate.shape:
-            return _invalid("moe_norm_backward", check)
-        rows.append(_rows(dgate, shape, dgate.dtype) if dgate.shape == shape else
-                    (dgate.data_ptr(), 0) if dgate.is_contiguous() else None)
+    shape, dtype = y.shape, y.dtype
+    dyr = _NONE if dy is None else _rows(dy, shape, dtype)
+    dnr = _NONE if dn is None else _rows(dn, shape)
+    dxr = _NONE if dx is None else _rows(dx, shape, dtype)
+    dbr = _NONE if db is None else _rows(db, shape)
+    if dgate is None:
+        dgr = _NONE
+    elif gate is None or dgate.dtype is not gate.dtype or dgate.shape != gate.shape:
+        dgr = None
+    elif dgate.shape == shape:
+        dgr = _rows(dgate, shape, dgate.dtype)
     else:
-        rows.append(_NONE)
-    sums = [0 if t is None else t.data_ptr() if t.dtype is torch.float32 and t.shape == shape[1:] and t.is_contiguous() else None
-            for t in (dw_post, dw_pre)]
-    if a is None or None in rows or None in sums:
+        dgr = (dgate.data_ptr(), 0) if dgate.is_contiguous() else None
+    post, pre = _column_sum(dw_post, shape[1]), _column_sum(dw_pre, shape[1])
+    if None in (a, dyr, dnr, dxr, dbr, dgr, post, pre):
         return _invalid("moe_norm_backward", check)
-    g = _NORM_GRADS.pack(_NORM_GRADS.size, *rows[0], *rows[1], *rows[2], *rows[3], *rows[4], *sums, workspace.data_ptr(),
-                         workspace.nbytes)
+    g = _NORM_GRADS.pack(_NORM_GRADS.size, *dyr, *dnr, *dxr, *dbr, *dgr, post, pre, workspace.data_ptr(), workspace.nbytes)
     rc = lib.moe_norm_backward(a, g, _stream(stream))
     if check:
         _check(rc, "moe_norm_backward")
