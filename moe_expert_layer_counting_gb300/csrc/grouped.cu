@@ -246,9 +246,10 @@ struct Places {
 // wgrad: a launch has a pair of CTAs for each item.  A pair works on the one
 // that it was launched for, then on those of pairs that it keeps from being
 // launched (claims): a pair that is quicker does more of them, and they are
-// begun in order.  With fixed shares the SMs that the memory serves last finish
-// last (stores alone: 6.7 instead of 7.5 TB/s; 256 experts of 31 rows, N = 1024,
-// K = 2048, float32: 370 instead of 320 us).  forward and dgrad, whose pairs read
+// begun in order.  Where all SMs only store, a third of them, whole groups of
+// neighbours, is a fifth slower: with fixed shares of 2.1 GB they end 60 of 325 us
+// after the others (dw's stores alone: 6.7 instead of 7.5 TB/s; 256 experts of 31
+// rows, N = 1024, K = 2048, float32: 370 instead of 322 us).  forward and dgrad, whose pairs read
 // the same weights from L2 at the same time, are 2 % slower that way.
 //
 // Warp 3 of the leader claims for both CTAs; each CTA's warp 3 works out the
