@@ -533,12 +533,13 @@ def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=
 
 def moe_adamw_step(table: np.ndarray, p_dtype: int, g_dtype: int, state_bits: int, lr: float, beta1: float, beta2: float,
                    eps: float, weight_decay: float, step: int, grad_scale: torch.Tensor = None, stream=None,
-                   check=True) -> int:
-    """One step over the tensors of ``table`` (a contiguous array of ADAMW_TENSOR: sizes and device pointers)."""
+                   check=True, address: int = None) -> int:
+    """One step over the tensors of ``table`` (a contiguous array of ADAMW_TENSOR: sizes and device pointers); address:
+    table.ctypes.data, for a caller that keeps it (asking NumPy takes 0.8 us)."""
     if table.dtype != ADAMW_TENSOR or not table.flags.c_contiguous or \
             (grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1)):
         return _invalid("moe_adamw_step", check)
-    a = _ADAMW_ARGS.pack(_ADAMW_ARGS.size, table.size, table.ctypes.data, p_dtype, g_dtype, state_bits,
+    a = _ADAMW_ARGS.pack(_ADAMW_ARGS.size, table.size, address or table.ctypes.data, p_dtype, g_dtype, state_bits,
                          0 if grad_scale is None else grad_scale.data_ptr(), lr, beta1, beta2, eps, weight_decay, step)
     rc = lib.moe_adamw_step(a, _stream(stream))
     if check:

@@ -235,6 +235,7 @@ class AdamW:
         names = ("m", "v", "m_scale", "v_scale") if state_bits == 8 else ("m", "v")
         self.state = {k: list(s) for k, s in zip(names, state)}
         self.table = np.zeros(len(self.params), B.ADAMW_TENSOR)
+        self._address = self.table.ctypes.data
         self.table["n"] = self.sizes = [p.numel() for p in self.params]
         for name, tensors in (("p", self.params), *self.state.items(), ("copy", self.copies)):
             if tensors is None:
@@ -252,5 +253,5 @@ class AdamW:
             raise ValueError("gradients: sizes, types or strides do not fit the parameters")
         self.table["g"] = [g.data_ptr() for g in grads]
         B.moe_adamw_step(self.table, self.p_dtype, B._DTYPES[kind], self.state_bits, self.lr, *self.betas, self.eps,
-                         self.weight_decay, self.steps + 1, grad_scale, stream=stream)
+                         self.weight_decay, self.steps + 1, grad_scale, stream=stream, address=self._address)
         self.steps += 1
