@@ -222,10 +222,10 @@ class AdamW:
         self.state_bits, self.steps = state_bits, step
         if state_bits not in (32, 8):
             raise ValueError("state_bits is 32 or 8")
-        kinds = {p.dtype for p in self.params}
-        if len(kinds) > 1 or not kinds <= set(B._DTYPES):
+        p_kind = self.params[0].dtype if self.params else torch.float32
+        if p_kind not in B._DTYPES or any(p.dtype is not p_kind for p in self.params):
             raise ValueError("parameters are all bf16 or all float32")
-        self.p_dtype = B._DTYPES[kinds.pop()] if kinds else B.F32
+        self.p_dtype = B._DTYPES[p_kind]
         if state is None:
             kind = torch.float32 if state_bits == 32 else torch.uint8
             m, v = ([torch.zeros(p.numel(), dtype=kind, device=p.device) for p in self.params] for _ in range(2))
@@ -240,9 +240,9 @@ class AdamW:
         for name, tensors in (("p", self.params), *self.state.items(), ("copy", self.copies)):
             if tensors is None:
                 continue
-            want = {"p": None, "copy": torch.bfloat16}.get(name, torch.float32 if state_bits == 32 else torch.uint8)
+            kind = {"p": p_kind, "copy": torch.bfloat16}.get(name, torch.float32 if state_bits == 32 else torch.uint8)
             sizes = [-(-n // 32) for n in self.sizes] if name.endswith("scale") else self.sizes
-            if [t.numel() for t in tensors] != sizes or not all(t.is_contiguous() and want in (None, t.dtype) for t in tensors):
+            if len(tensors) != len(sizes) or [t.numel() for t in tensors if t.dtype is kind and t.is_contiguous()] != sizes:
                 raise ValueError(f"{name}: sizes, types or strides do not fit the parameters")
             self.table[name] = [t.data_ptr() for t in tensors]
 
