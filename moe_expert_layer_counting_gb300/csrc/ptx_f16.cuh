@@ -1,7 +1,7 @@
 // ptx_f16.cuh -- inline-PTX wrappers of the BF16 products (grouped.cu) beyond
 // those of ptx.cuh: 3-D TMA loads of a CTA pair, tcgen05.mma kind::f16 with
-// operands of either major, wide TMEM reads, and bounded waits of kernels
-// that reset their own status words.
+// operands of either major, wide TMEM reads, bounded waits of kernels that
+// reset their own status words, and claims of clusters not launched yet.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
