@@ -241,7 +241,6 @@ class AdamW:
         names = ("m", "v", "m_scale", "v_scale") if state_bits == 8 else ("m", "v")
         self.state = {k: list(s) for k, s in zip(names, state)}
         self.table = np.zeros(len(self.params), B.ADAMW_TENSOR)
-        self._address = self.table.ctypes.data
         self.table["n"] = self.sizes = [p.numel() for p in self.params]
         self._look_up()
 
@@ -264,7 +263,11 @@ class AdamW:
                 raise ValueError(f"{name}: sizes, types or strides do not fit the parameters")
             kept += [t.detach() for t in tensors]
             self.table[name] = [t.data_ptr() for t in tensors]
-        self._kept, self._seen = kept, [t.data_ptr() for t in kept]
+        self._kept, self._seen, self._address = kept, [t.data_ptr() for t in kept], self.table.ctypes.data
+
+    def __getstate__(self):
+        """A copy (copy, pickle) has a table and tensors of its own, at addresses that its first step looks up."""
+        return {**self.__dict__, "table": self.table.copy(), "_kept": None, "_seen": None, "_address": None}
 
     def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
         """One step with these gradients (contiguous, all bf16 or all float32), each times grad_scale (a device float)."""

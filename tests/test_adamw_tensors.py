@@ -1,5 +1,8 @@
 """Which tensors a step of AdamW works on: those that its lists hold at that time.  The call into the library is replaced by
 one that keeps the table, so no GPU is needed."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -119,6 +122,29 @@ def test_memory_of_the_old_storage_is_not_handed_on(steps):
     with pytest.raises(ValueError):
         opt.step([torch.zeros(4096)])
     assert np.array_equal(tables[-1]["p"], [old])
+
+
+@pytest.mark.parametrize("copied", [copy.deepcopy, copy.copy, lambda o: pickle.loads(pickle.dumps(o))])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_copied_object_has_a_table_of_its_own(steps, copied, bits):
+    """deepcopy and pickle: the copy's tensors, through the copy's table (the fake call compares its address); copy: the same."""
+    AdamW, tables = steps
+    opt, grads = make(AdamW, bits), tensors(torch.bfloat16)
+    opt.step(grads)
+    other = copied(opt)
+    for which in (other, opt, other):
+        which.step(grads)
+        check(tables[-1], which, grads)
+    assert (other.steps, opt.steps) == (3, 2)
+    other.params = tensors()
+    for which in (other, opt):
+        which.step(grads)
+        check(tables[-1], which, grads)
+    if copied is not copy.copy:
+        assert all(a.data_ptr() != b.data_ptr() for a, b in zip(opt.params, other.params) if a.numel())
+        del opt                                                   # nothing of the original is needed
+        other.step(grads)
+        check(tables[-1], other, grads)
 
 
 @pytest.mark.gpu
