@@ -18,7 +18,7 @@
 // (SPLIT), which add their sums through each other's shared memory (2048 x 16384:
 // 59 and 89 us; held in one block's registers it took 69 and 214).
 // Measured, BF16, channel gate: forward of 8192 x 7168 in 74 us (6.3 TB/s), the
-// gradients in 124 us (5.7 TB/s); 4096 x 7168 in 41 and 69 us, of which ~10 us
+// gradients in 125 us (5.6 TB/s); 4096 x 7168 in 41 and 70 us, of which ~10 us
 // are the first rows' way in, the last ones' way out and the sums of the parts.
 #include <cuda_bf16.h>
 
@@ -595,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sig) gate_t = sigmoid(gate_t);
     }
     const P2 rs = twice(rb * gate_t);
-    const P2 r2 = twice(r), back = twice(-r * r * r * s[1] * inv_h);
+    // r times mean(dn w h); the row's magnitude cancels factor by factor (r cubed
+    // would leave the range of float32 for rows below 1e-13 or above 1e13)
+    const P2 r2 = twice(r), back = twice(-r * (r * s[1] * inv_h));
     P2 d[V][4], q2 = twice(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[i][k] = has_dy ? dy[i].two(k) : twice(0.f);
       if (pre) {
-        // d += r dn w - y r^2 mean(dn w h)
+        // d += r (dn w - h mean(dn w h)), h = y r
         if (kLate) {
           y[i].load(reinterpret_cast<const XT *>(row) + 8 * c);
           dn[i].load(reinterpret_cast<const uint16_t *>(row + src[1].at) + 8 * c);
@@ -613,10 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         get_columns(c_pre, vecs, c, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const P2 m = dn[i].two(k) * r2, f = y[i].two(k);
-          d[i][k] = fma2(m, w[k], d[i][k]);
-          d[i][k] = fma2(f, back, d[i][k]);
-          sum_pre[i][k] = fma2(m, f, sum_pre[i][k]);
+          const P2 g = dn[i].two(k), f = y[i].two(k);
+          d[i][k] = fma2(fma2(f, back, g * w[k]), r2, d[i][k]);
+          sum_pre[i][k] = fma2(g * r2, f, sum_pre[i][k]);
         }
       }
       if (out_dx) {
@@ -685,13 +686,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (token && g.dgate && tid == 0 && rank == 0)
       store1_any(g.dgate, a.gate_dtype, t, (sig ? gate_t * (1.0f - gate_t) : 1.0f) * q[0] * rb);
     if (out_db) {
-      // db = rb (g d w - h mean(g d w h)) = rs d w - b g rb^3 q / H
-      const P2 back_b = twice(post ? -rb * rb * rb * q[0] * gate_t * inv_h : 0.f);
+      // db = rb (g d w - h mean(g d w h)), h = b rb
+      const P2 rb2 = twice(rb), g2 = twice(gate_t), back_b = twice(post ? -rb * (rb * q[0] * gate_t * inv_h) : 0.f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (tid + i * sh.group >= vecs) continue;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[i][k] = fma2(b[i].two(k), back_b, d[i][k] * rs);
+        for (int k = 0; k < 4; ++k) d[i][k] = fma2(b[i].two(k), back_b, d[i][k] * g2) * rb2;
         store_pairs(pb + 8 * i * sh.group, d[i]);
       }
     }
