@@ -686,13 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (token && g.dgate && tid == 0 && rank == 0)
       store1_any(g.dgate, a.gate_dtype, t, (sig ? gate_t * (1.0f - gate_t) : 1.0f) * q[0] * rb);
     if (out_db) {
-      // db = rb (g d w - h mean(g d w h)), h = b rb
-      const P2 rb2 = twice(rb), g2 = twice(gate_t), back_b = twice(post ? -rb * (rb * q[0] * gate_t * inv_h) : 0.f);
+      // db = rb (g d w - h mean(g d w h)), h = b rb; without a norm g d, whatever b is
+      const P2 rb2 = twice(rb), g2 = twice(gate_t), back_b = twice(-rb * (rb * q[0] * gate_t * inv_h));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (tid + i * sh.group >= vecs) continue;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[i][k] = fma2(b[i].two(k), back_b, d[i][k] * g2) * rb2;
+        for (int k = 0; k < 4; ++k) {
+          d[i][k] = d[i][k] * g2;
+          if (post) d[i][k] = fma2(b[i].two(k), back_b, d[i][k]) * rb2;
+        }
         store_pairs(pb + 8 * i * sh.group, d[i]);
       }
     }

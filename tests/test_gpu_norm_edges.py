@@ -35,3 +35,18 @@ def test_gradients_of_rows_far_from_one(M, y_exp, b_exp, H, xt, gate):
     assert {k for k, v in got.items() if v is not None} == set(want)
     for k in want:
         close(k, got[k].reshape(want[k][0].shape), want[k], H, c.T)
+
+
+@pytest.mark.parametrize("gate", [None, "token", "channel", "full"])
+@pytest.mark.parametrize("H,xt", [(264, BF16), (264, F32), (8200, BF16)])
+def test_gradient_of_b_without_a_norm_does_not_read_b(M, H, xt, gate):
+    """u = b: db = g d, finite where b is not; the gate's gradient d b is not finite there."""
+    c = Case(30, H, xt, gate=gate, post=False)
+    y, want = c.x.clone(), backward64(c, c.x)
+    c.b[7, 5], c.b[11, H - 1] = float("inf"), float("nan")
+    got = c.module(M).backward(y, c.b, c.gate, c.dy, c.dn)
+    for k in ("dx", "db", "dw_pre"):
+        close(k, got[k], want[k], H, c.T)
+    if gate == "token":
+        fine = got["dgate"][:, 0].isfinite()
+        assert not bool(fine[7]) and not bool(fine[11]) and int(fine.sum()) == 28
