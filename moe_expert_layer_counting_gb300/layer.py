@@ -148,16 +148,16 @@ class MoELayerBfp8:
 class BlockNorm:
     """The norms around the layer with its gate and residual scale, forward and backward (include/moe_norm.h).
 
-    w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.  The object keeps
-    a workspace for each stream that it is used on.
+    w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.  Each backward call
+    has a workspace of its own, as a captured graph may write one long after its call; the object keeps the last of each
+    stream, for ``device_status``.
     """
 
     def __init__(self, w_post: torch.Tensor = None, w_pre: torch.Tensor = None, residual_scale: float = 1.0,
                  weight_offset: float = 0.0, eps: float = 1e-6, gate_sigmoid: bool = False):
         self.w_post, self.w_pre = w_post, w_pre
         self.how = (residual_scale, weight_offset, eps, gate_sigmoid)
-        self._workspaces = {}                       # stream handle -> (rows it is enough for, tensor)
-        self._outgrown = []                         # kept, as a captured graph may still use one
+        self._last = {}                             # (device, stream handle) -> workspace of the last backward call
 
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
         """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
@@ -194,18 +194,15 @@ class BlockNorm:
         dw_post = None if w_post is None else new(w_post, dtype=torch.float32)
         dw_pre = None if w_pre is None else new(w_pre, dtype=torch.float32)
         handle = B._stream(stream)
-        rows, ws = self._workspaces.get(handle, (-1, None))
-        T, H = y.shape
-        if T > rows:
-            self._outgrown.append(ws)
-            ws = y.new_empty(B.moe_norm_workspace_size(T, H), dtype=torch.uint8)
-            self._workspaces[handle] = (T, ws)
+        key = y.get_device(), handle
+        self._last.pop(key, None)                   # before the next one, which may be the same memory
+        ws = self._last[key] = y.new_empty(B.moe_norm_workspace_size(*y.shape), dtype=torch.uint8)
         B.moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, ws, dx, db, dgate, dw_post, dw_pre, *self.how, handle)
         return {"dx": dx, "db": db, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
 
     def device_status(self, stream=None) -> int:
         """MOE_OK, or what the last backward call on this stream reported."""
-        rows, ws = self._workspaces.get(B._stream(stream), (-1, None))
+        ws = self._last.get((torch.cuda.current_device(), B._stream(stream)))
         return B.MOE_OK if ws is None else B.moe_get_device_status(ws, stream)
 
 
