@@ -30,6 +30,9 @@
  *   - gate_kind: MOE_GATE_TOKEN gate [T], MOE_GATE_CHANNEL gate [H],
  *     MOE_GATE_FULL gate [T][H] (row stride ld_gate).
  *   - Results do not depend on thread timing.
+ *   - Device-side waits give up after ~1 s: the status is then MOE_ERR_TIMEOUT,
+ *     rows of y and n that were not computed are NaN, and gradients undefined.
+ *     The debug hook of moe_get_device_status works here too.
  */
 #ifndef MOE_NORM_H
 #define MOE_NORM_H
@@ -61,6 +64,8 @@ typedef struct moe_norm_args {
     int64_t ldy;
     uint16_t *n;               /* out [T][H]; NULL exactly when w_pre is */
     int64_t ldn;
+    int32_t *status;           /* forward: 64 bytes of device memory, 4-byte aligned, for its device status
+                                  (moe_get_device_status, reset by the call), or NULL; backward has its workspace's */
 } moe_norm_args;
 
 /* y and n as above.  residual_scale, weight_offset and eps are used as given

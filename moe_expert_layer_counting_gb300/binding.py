@@ -101,7 +101,7 @@ class MoeNormArgs(ctypes.Structure):
                 ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
                 ("T", _i64), ("H", _i64), ("x", _p), ("ldx", _i64), ("b", _p), ("ldb", _i64),
                 ("gate", _p), ("ld_gate", _i64), ("w_post", _p), ("w_pre", _p),
-                ("y", _p), ("ldy", _i64), ("n", _p), ("ldn", _i64)]
+                ("y", _p), ("ldy", _i64), ("n", _p), ("ldn", _i64), ("status", _p)]
 
 
 class MoeNormGrads(ctypes.Structure):
@@ -430,7 +430,7 @@ def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
 # ---------------------------------------------------------------- norms around the layer (include/moe_norm.h)
 
 # MoeNormArgs, MoeNormGrads and MoeAdamwArgs as bytes: packing costs a fifth of filling a ctypes structure
-_NORM_ARGS = struct.Struct("@I5i3fqqPqPqPqPPPqPq")
+_NORM_ARGS = struct.Struct("@I5i3fqqPqPqPqPPPqPqP")
 _NORM_GRADS = struct.Struct("@IPqPqPqPqPqPPPN")
 _ADAMW_ARGS = struct.Struct("@IiPiiiP5dq")
 assert (_NORM_ARGS.size, _NORM_GRADS.size, _ADAMW_ARGS.size) == tuple(
@@ -438,7 +438,7 @@ assert (_NORM_ARGS.size, _NORM_GRADS.size, _ADAMW_ARGS.size) == tuple(
 _NONE = (0, 0)
 
 
-def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid):
+def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid, status=0):
     """The bytes of MoeNormArgs for these tensors, or None if a type, shape or stride does not fit."""
     shape = T, H = x.shape
     dtype = x.dtype
@@ -473,15 +473,18 @@ def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, e
         if gr is None:
             return None
     return _NORM_ARGS.pack(_NORM_ARGS.size, xt, wt, gt, kind, 1 if gate_sigmoid else 0, residual_scale, weight_offset, eps,
-                           T, H, *xr, *br, *gr, post, pre, *yr, *nr)
+                           T, H, *xr, *br, *gr, post, pre, *yr, *nr, status)
 
 
 def moe_norm_forward(x, b, gate, w_post, w_pre, y, n, residual_scale: float = 1.0, weight_offset: float = 0.0,
-                     eps: float = 1e-6, gate_sigmoid: bool = False, stream=None, check=True) -> int:
+                     eps: float = 1e-6, gate_sigmoid: bool = False, stream=None, check=True,
+                     status: torch.Tensor = None) -> int:
     """y = residual_scale x + g norm(b; w_post), n = norm(y; w_pre); b, gate, w_post, w_pre, y and n may be None as
-    include/moe_norm.h says.  gate [T, 1], [1, H] or [T, H]; x and y bf16 or float32, b and n bf16."""
-    a = _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid)
-    if a is None:
+    include/moe_norm.h says.  gate [T, 1], [1, H] or [T, H]; x and y bf16 or float32, b and n bf16; status: 64 bytes for
+    moe_get_device_status."""
+    words = 0 if status is None else status.data_ptr()
+    a = _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid, words)
+    if a is None or (status is not None and (status.nbytes < 64 or not status.is_contiguous())):
         return _invalid("moe_norm_forward", check)
     rc = lib.moe_norm_forward(a, _stream(stream))
     if check:

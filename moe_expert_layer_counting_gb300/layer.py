@@ -158,6 +158,7 @@ class BlockNorm:
         self.w_post, self.w_pre = w_post, w_pre
         self.how = (residual_scale, weight_offset, eps, gate_sigmoid)
         self._last = {}                             # (device, stream handle) -> workspace of the last backward call
+        self._status = {}                           # the same -> status words of its forward calls
 
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
         """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
@@ -172,7 +173,12 @@ class BlockNorm:
         n = None
         if self.w_pre is not None:
             n = torch.empty_like(x if b is None else b, dtype=torch.bfloat16, memory_format=flat)
-        B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, stream)
+        handle = B._stream(stream)
+        key = x.get_device(), handle
+        status = self._status.get(key)
+        if status is None:
+            status = self._status[key] = x.new_empty(64, dtype=torch.uint8)
+        B.moe_norm_forward(x, b, gate, self.w_post if b is not None else None, self.w_pre, y, n, *self.how, handle, status=status)
         return (x if y is None else y), n
 
     def backward(self, y: torch.Tensor, b: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, dn: torch.Tensor,
@@ -201,9 +207,10 @@ class BlockNorm:
         return {"dx": dx, "db": db, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
 
     def device_status(self, stream=None) -> int:
-        """MOE_OK, or what the last backward call on this stream reported."""
-        ws = self._last.get((torch.cuda.current_device(), B._stream(stream)))
-        return B.MOE_OK if ws is None else B.moe_get_device_status(ws, stream)
+        """MOE_OK, or what the last backward or else the last forward call on this stream reported (synchronises)."""
+        key = torch.cuda.current_device(), B._stream(stream)
+        words = [w for w in (self._last.get(key), self._status.get(key)) if w is not None]
+        return next((code for code in (B.moe_get_device_status(w, stream) for w in words) if code), B.MOE_OK)
 
 
 class AdamW:

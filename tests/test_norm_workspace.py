@@ -110,3 +110,12 @@ def test_widths_and_lengths_on_one_object():
         norm.backward(x[:T], x[:T], None, x[:T], None)
         held.append(torch.cuda.memory_allocated())
     assert max(held) - min(held) < 1 << 20
+
+
+def test_refused_status_words():
+    """Forward's status words: 4-byte aligned (looked at before anything is enqueued)."""
+    from tests.test_norm_abi import args_of
+    import ctypes
+    B = Hp.lib()
+    for T in (0, 4):
+        assert B.lib.moe_norm_forward(ctypes.byref(args_of(B, T=T, status=0x8002)), None) == B.MOE_ERR_MISALIGNED
