@@ -47,7 +47,7 @@ class TrainableExperts:
     def _sum_slots(self, rows, s):
         """Each token's sum over its slots of its pairs' rows (float32 inside; dropped slots are left out)."""
         T, k = s["row"].shape
-        by_slot = rows[s["row"].clamp(min=0).T.reshape(-1)].view(k, T, -1)
+        by_slot = rows[s["row"].clamp(min=0).T.reshape(-1)].view(k, T, rows.shape[1])
         out = torch.empty(T, rows.shape[1], dtype=torch.bfloat16, device=rows.device)
         B.moe_combine(by_slot, s["row"], out)
         return out

@@ -52,3 +52,13 @@ def test_an_index_that_no_expert_has_is_reported_and_its_pair_dropped(M, bad):
     for a, b in zip(got[1:], dropped[1:]):
         assert torch.equal(a, b)
     assert not bool(got[1][11].any()) and not bool(got[2][11].any()) and not bool(got[3][at].any())
+
+
+def test_no_tokens(M):
+    n, l1, l2, idx, w, db = inputs(0)
+    status, b, dn, dw, dl1, dl2 = step(M, n, l1, l2, idx, w, db)
+    assert status == M.binding.MOE_OK and b.shape == dn.shape == (0, H) and dw.shape == (0, k)
+    assert not bool(dl1.any()) and not bool(dl2.any())
+    dl = torch.ones_like(l1, dtype=torch.float32), torch.ones_like(l2, dtype=torch.float32)
+    step(M, n, l1, l2, idx, w, db, dl, accumulate=True)
+    assert all(bool((t == 1).all()) for t in dl)
