@@ -32,6 +32,10 @@ class TrainableExperts:
                            for _ in range(6)]
         self.permute_workspace = None
 
+    def _check_rows(self, name, t, T):
+        if t.shape != (T, self.H) or t.dtype is not torch.bfloat16 or t.device != self.l1.device:
+            raise ValueError(f"{name} is not [{T}, {self.H}] BF16 on the weights' device")
+
     def _permute(self, topk_idx):
         T, k = topk_idx.shape
         dev = topk_idx.device
@@ -54,8 +58,13 @@ class TrainableExperts:
 
     def forward(self, n: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor):
         """(b [T, H], what backward needs); n [T, H] BF16, topk_idx [T, k] int32, topk_w [T, k] float32."""
+        if topk_idx.dim() != 2 or topk_idx.dtype is not torch.int32 or topk_idx.device != self.l1.device:
+            raise ValueError("topk_idx is not [T, k] int32 on the weights' device")
         T, k = topk_idx.shape
-        offsets, perm, row = self._permute(topk_idx)
+        self._check_rows("n", n, T)
+        if topk_w.shape != (T, k):
+            raise ValueError("topk_w and topk_idx do not fit")
+        offsets, perm, row = self._permute(topk_idx.contiguous())
         # row [T, k]: of each pair; -1 if it was dropped
         s = {"offsets": offsets, "row": row, "token": perm // k, "w": topk_w.reshape(-1)[perm][:, None]}
         s["rows"] = n[s["token"]]
@@ -69,6 +78,7 @@ class TrainableExperts:
 
     def backward(self, db: torch.Tensor, s: dict, dl1: torch.Tensor, dl2: torch.Tensor, accumulate: bool = False):
         """(dn [T, H], dtopk_w [T, k]); the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
+        self._check_rows("db", db, s["row"].shape[0])
         do = db[s["token"]]
         dh = torch.zeros_like(s["h"])
         B.moe_grouped_dgrad(do, self.l2, s["offsets"], dh, self.workspaces[2])

@@ -62,3 +62,17 @@ def test_no_tokens(M):
     dl = torch.ones_like(l1, dtype=torch.float32), torch.ones_like(l2, dtype=torch.float32)
     step(M, n, l1, l2, idx, w, db, dl, accumulate=True)
     assert all(bool((t == 1).all()) for t in dl)
+
+
+def test_strides(M):
+    """Inputs that are parts of wider tensors: the same bits as their copies."""
+    n, l1, l2, idx, w, db = inputs(30)
+    wide = torch.full((30, k + 2), E, dtype=torch.int32, device="cuda")
+    wide[:, 1:1 + k] = idx
+    rows = torch.zeros(30, 2, H, dtype=torch.bfloat16, device="cuda")
+    rows[:, 0], rows[:, 1] = n, db
+    want = step(M, n, l1, l2, idx, w, db)
+    got = step(M, rows[:, 0], l1, l2, wide[:, 1:1 + k], w.T.contiguous().T, rows[:, 1])
+    assert want[0] == got[0] == M.binding.MOE_OK
+    for a, b in zip(want[1:], got[1:]):
+        assert torch.equal(a, b)
