@@ -22,7 +22,9 @@
  * Conventions are those of moe_mxq.h (no allocation, no synchronisation, work
  * enqueued on `stream`, a moe_status returned; nothing is enqueued when the
  * host detects an error).  The table of tensors is read during the call and
- * may be changed or freed after it.  Each tensor is updated in place; tensors
+ * may be changed or freed after it, and the numbers are part of the launch: a
+ * captured one is the same step t, with the same rate and bias correction, at
+ * every replay.  Each tensor is updated in place; tensors
  * do not overlap.  A NaN or an infinity stays in its value (8 bits: an infinity
  * is held as the largest value, and coarsens the other 31 of its group).
  */

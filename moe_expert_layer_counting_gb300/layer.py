@@ -213,6 +213,15 @@ class BlockNorm:
         return next((code for code in (B.moe_get_device_status(w, stream) for w in words) if code), B.MOE_OK)
 
 
+def _capturing(stream) -> bool:
+    if not torch.cuda.is_initialized():
+        return False
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with _on(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class AdamW:
     """AdamW over a list of tensors, all updated by one call (include/moe_adamw.h).
 
@@ -222,7 +231,8 @@ class AdamW:
     (m, v) or (m, v, m_scale, v_scale) as an earlier object's ``state``; they are used in place.
 
     A step updates the tensors that ``params``, ``state`` and ``copies`` hold then, where their values lie then
-    (``p.data = ...`` or another tensor in a list); sizes and types stay.
+    (``p.data = ...`` or another tensor in a list); sizes and types stay.  A step is not for capture into a graph: its number
+    and rate are part of the launch, and every replay would be the same step.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
@@ -275,6 +285,8 @@ class AdamW:
 
     def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
         """One step with these gradients (contiguous, all bf16 or all float32), each times grad_scale (a device float)."""
+        if _capturing(stream):
+            raise RuntimeError("AdamW.step in a graph's capture: every replay would be the same step")
         kind = grads[0].dtype if grads else torch.float32
         if kind not in B._DTYPES or [g.numel() for g in grads if g.dtype is kind and g.is_contiguous()] != self.sizes:
             raise ValueError("gradients: sizes, types or strides do not fit the parameters")

@@ -147,6 +147,44 @@ def test_a_copied_object_has_a_table_of_its_own(steps, copied, bits):
         check(tables[-1], other, grads)
 
 
+def test_a_step_in_a_capture_is_refused(steps, monkeypatch):
+    AdamW, tables = steps
+    opt, grads = make(AdamW, 32), tensors(torch.bfloat16)
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_initialized", lambda: True)
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError):
+            opt.step(grads)
+        assert not tables and opt.steps == 0
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        opt.step(grads)
+    assert len(tables) == opt.steps == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_a_step_in_a_real_capture_is_refused(given):
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    Hp.lib()
+    from moe_expert_layer_counting_gb300 import AdamW
+    p, g = torch.ones(64, device="cuda"), torch.ones(64, device="cuda")
+    opt, graph, side = AdamW([p]), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        g += 1
+        with pytest.raises(RuntimeError):
+            if given:
+                with torch.cuda.stream(torch.cuda.Stream()):       # not the one that captures
+                    opt.step([g], stream=side)
+            else:
+                opt.step([g])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert opt.steps == 0 and bool((p == 1).all()) and bool((g == 2).all())
+    opt.step([g])
+    assert opt.steps == 1 and bool((p < 1).all())
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [8, 32])
 def test_values_of_another_storage_are_updated(bits):
