@@ -161,13 +161,15 @@ class BlockNorm:
         self._status = {}                           # the same -> status words of its forward calls
 
     def forward(self, x: torch.Tensor, b: torch.Tensor = None, gate: torch.Tensor = None, stream=None):
-        """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x)."""
+        """(y, n): the stream after the layer and the next layer's input.  Without b: (x, norm of x).  Without w_pre: n None."""
         if stream is not None:
             with _on(stream):
                 return self._forward(x, b, gate, stream)
         return self._forward(x, b, gate, None)
 
     def _forward(self, x, b, gate, stream):
+        if b is None and gate is None and self.w_pre is None:
+            return x, None                          # nothing to compute
         flat = torch.contiguous_format
         y = torch.empty_like(x, memory_format=flat) if b is not None else None
         n = None
@@ -184,13 +186,16 @@ class BlockNorm:
     def backward(self, y: torch.Tensor, b: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, dn: torch.Tensor,
                  stream=None) -> dict:
         """Gradients dx, db, dgate, dw_post, dw_pre (None where there is nothing to differentiate) from those of
-        forward's y and n (either may be None); y, b and gate are what forward returned and took."""
+        forward's y and n (either may be None); y, b and gate are what forward returned and took.  Without b and dn, dx is dy."""
         if stream is not None:
             with _on(stream):
                 return self._backward(y, b, gate, dy, dn, stream)
         return self._backward(y, b, gate, dy, dn, None)
 
     def _backward(self, y, b, gate, dy, dn, stream):
+        if b is None and gate is None and dn is None:
+            dx = torch.zeros_like(y) if dy is None else dy
+            return {"dx": dx, "db": None, "dgate": None, "dw_post": None, "dw_pre": None}
         new, flat = torch.empty_like, torch.contiguous_format
         w_post = self.w_post if b is not None else None
         w_pre = self.w_pre if dn is not None else None

@@ -119,3 +119,16 @@ def test_refused_status_words():
     B = Hp.lib()
     for T in (0, 4):
         assert B.lib.moe_norm_forward(ctypes.byref(args_of(B, T=T, status=0x8002)), None) == B.MOE_ERR_MISALIGNED
+
+
+def test_calls_with_nothing_to_compute():
+    """Without a layer's answer the stream is x itself: no weight, no n; no dn, and dx is dy.  No GPU is needed."""
+    Hp.lib()
+    from moe_expert_layer_counting_gb300 import BlockNorm
+    x, dy = torch.zeros(3, 64, dtype=torch.bfloat16), torch.ones(3, 64, dtype=torch.bfloat16)
+    assert BlockNorm().forward(x) == (x, None)
+    for w in (None, torch.ones(64)):
+        got = BlockNorm(w_pre=w).backward(x, None, None, dy, None)
+        assert got["dx"] is dy and got["db"] is got["dgate"] is got["dw_post"] is got["dw_pre"] is None
+        got = BlockNorm(w_pre=w).backward(x, None, None, None, None)
+        assert got["dx"].shape == x.shape and got["dx"].dtype is x.dtype and not bool(got["dx"].any())
