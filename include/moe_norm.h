@@ -24,8 +24,9 @@
  *     (enum moe_dtype).  Means, norms and sums are held in float32, and each
  *     output is rounded once: n is the norm of y before its rounding.
  *   - Row strides ldx, ldb, ldy, ldn, ld_gate in elements: multiples of 8, at
- *     least H.  Every row tensor and weight is 16-byte aligned
- *     (MOE_ERR_MISALIGNED).  y may be x, n may be b (each row is read before
+ *     least H.  Every row tensor, weight, channel gate and gradient of a weight
+ *     is 16-byte aligned, a token gate and the gradients of token and channel
+ *     gates as their elements (MOE_ERR_MISALIGNED).  y may be x, n may be b (each row is read before
  *     it is written); no other overlap.
  *   - gate_kind: MOE_GATE_TOKEN gate [T], MOE_GATE_CHANNEL gate [H],
  *     MOE_GATE_FULL gate [T][H] (row stride ld_gate).

@@ -1008,7 +1008,8 @@ extern "C" int moe_norm_backward(const moe_norm_args *a, const moe_norm_grads *g
   int rc = check_norm(a);
   if (rc != MOE_OK) return rc;
   if (!g || g->struct_size != sizeof(moe_norm_grads)) return MOE_ERR_INVALID_ARG;
-  if (!aligned(g->dw_pre, 16) || !aligned(g->dw_post, 16) || !aligned(g->dgate, 4)) return MOE_ERR_MISALIGNED;
+  if (!aligned(g->dw_pre, 16) || !aligned(g->dw_post, 16)) return MOE_ERR_MISALIGNED;
+  if (!aligned(g->dgate, a->gate_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_MISALIGNED;   // stored one by one; a full one below
   if (!g->workspace) return MOE_ERR_INVALID_ARG;
   if (!aligned(g->workspace, 256)) return MOE_ERR_MISALIGNED;
   if (g->workspace_bytes < moe_norm_workspace_size(a->T, a->H)) return MOE_ERR_WORKSPACE_TOO_SMALL;

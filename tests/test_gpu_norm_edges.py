@@ -50,3 +50,19 @@ def test_gradient_of_b_without_a_norm_does_not_read_b(M, H, xt, gate):
     if gate == "token":
         fine = got["dgate"][:, 0].isfinite()
         assert not bool(fine[7]) and not bool(fine[11]) and int(fine.sum()) == 28
+
+
+@pytest.mark.parametrize("kind,gt", [("token", BF16), ("token", F32), ("channel", BF16), ("channel", F32)])
+def test_gates_gradients_aligned_as_their_elements(M, kind, gt):
+    """A token gate and the gradient of a token's or channel's gate may start at any element."""
+    B = M.binding
+    c = Case(33, 264, gate=kind, gt=gt, sigmoid=True)
+    held = torch.full((c.gate.numel() + 2,), 7.0, dtype=gt, device="cuda")
+    dgate = held[1:-1].view(c.gate.shape)
+    if kind == "token":
+        c.gate = torch.cat([c.gate[:1], c.gate])[1:]
+    ws = torch.empty(B.moe_norm_workspace_size(c.T, c.H), dtype=torch.uint8, device="cuda")
+    B.moe_norm_backward(c.x, c.b, c.gate, c.w_post, c.w_pre, c.dy, c.dn, ws, dgate=dgate, residual_scale=c.scale, eps=c.eps,
+                        gate_sigmoid=True)
+    close("dgate", dgate, backward64(c, c.x)["dgate"], c.H, c.T)
+    assert float(held[0]) == float(held[-1]) == 7.0
