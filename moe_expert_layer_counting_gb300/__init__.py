@@ -20,3 +20,4 @@ from .binding import (MoeError, moe_combine, moe_expert_forward, moe_expert_work
                       moe_grouped_workspace_size, moe_grouped_forward, moe_grouped_dgrad, moe_grouped_wgrad,
                       moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_adamw_step)
 from .layer import AdamW, BlockNorm, Bfp8Experts, MoELayer, MoELayerBfp8, QuantizedExperts  # noqa: F401
+from .training import TrainableExperts  # noqa: F401

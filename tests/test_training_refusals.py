@@ -40,3 +40,10 @@ def test_backward(layer, db):
          "h": torch.zeros(T * k, I, dtype=BF16)}
     with pytest.raises(ValueError):
         layer.backward(db, s, torch.zeros(E, 2 * I, H), torch.zeros(E, H, I))
+
+
+def test_the_package_has_it():
+    Hp.lib()
+    import moe_expert_layer_counting_gb300 as M
+    from moe_expert_layer_counting_gb300 import training
+    assert M.TrainableExperts is training.TrainableExperts
