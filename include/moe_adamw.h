@@ -9,8 +9,9 @@
  *   v = beta2 v + (1 - beta2) g^2              c2 = 1 - beta2^t
  *   p = p (1 - lr weight_decay) - (lr / c1) m / (sqrt(v) / sqrt(c2) + eps)
  *
- * in float32, p rounded once to its type, and its BF16 copy (the weights that
- * the next forward pass reads) written in the same pass.
+ * in float32 (the update to within 2^-21 of itself), p rounded once to its
+ * type, and its BF16 copy (the weights that the next forward pass reads)
+ * written in the same pass.
  *
  * States of 8 bits: E4M3 codes with one UE8M0 byte per 32 consecutive values,
  * the format and the rounding rule of mxq_quantize_act (moe_mxq.h).  The
@@ -24,9 +25,9 @@
  * host detects an error).  The table of tensors is read during the call and
  * may be changed or freed after it, and the numbers are part of the launch: a
  * captured one is the same step t, with the same rate and bias correction, at
- * every replay.  Each tensor is updated in place; tensors
- * do not overlap.  A NaN or an infinity stays in its value (8 bits: an infinity
- * is held as the largest value, and coarsens the other 31 of its group).
+ * every replay.  Each tensor is updated in place; tensors do not overlap.  A NaN
+ * or an infinity stays in its value (8 bits: an infinity is held as the largest
+ * value, and coarsens the other 31 of its group).
  */
 #ifndef MOE_ADAMW_H
 #define MOE_ADAMW_H
@@ -57,8 +58,8 @@ typedef struct moe_adamw_args {
     int64_t step;                      /* t, >= 1 */
 } moe_adamw_args;
 
-/* Every pointer is 16-byte aligned except the scales and grad_scale (4 bytes)
- * (MOE_ERR_MISALIGNED).  0 <= beta1, beta2 < 1, eps >= 0, finite lr and
+/* Every pointer is 16-byte aligned except grad_scale (4 bytes) and the scales
+ * (any byte) (MOE_ERR_MISALIGNED).  0 <= beta1, beta2 < 1, eps >= 0, finite lr and
  * weight_decay, otherwise MOE_ERR_INVALID_ARG. */
 MOE_API int moe_adamw_step(const moe_adamw_args *args, cudaStream_t stream);
 

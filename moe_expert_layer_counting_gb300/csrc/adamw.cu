@@ -273,7 +273,10 @@ __global__ void __launch_bounds__(kThreads<kSmall>) adamw_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < 8; ++j) root.v[j] = __fsqrt_rn(v.v[j]);
       }
-      // a root is 0 or at least 2^-75, so the sum is 0 or normal
+      // a root is 0 or at least 2^-75, so the sum is 0 or normal.  An approximate
+      // root (float32 states too), an approximate reciprocal and the products leave
+      // the update within 2^-21 of itself: less than p's own rounding unless p is
+      // smaller than eight updates
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         p.v[j] = p.v[j] * a.keep - a.rate * (m.v[j] * rcp_approx(fmaf(root.v[j], a.root_scale, a.eps)));

@@ -16,7 +16,9 @@
 //     sum_t d b rsqrt(mean b^2 + eps), times a constant of the column.
 // A row of more than 8192 columns is split over the two blocks of a cluster
 // (SPLIT), which add their sums through each other's shared memory (2048 x 16384:
-// 59 and 89 us; held in one block's registers it took 69 and 214).
+// 53 and 84 us; held in one block's registers it took 69 and 214).  One row of
+// those is in work per cluster, and each of its two sums crosses to the other
+// block and is waited for, which the floors (40 and 59 us) have none of.
 // Measured, BF16, channel gate: forward of 8192 x 7168 in 74 us (6.3 TB/s), the
 // gradients in 125 us (5.6 TB/s); 4096 x 7168 in 41 and 70 us, of which ~10 us
 // are the first rows' way in, the last ones' way out and the sums of the parts.
@@ -504,7 +506,9 @@ enum : int { kSumPre = 0, kSumPost = 1 };
 
 // FULL, ALL as above (ALL: and all gradients of rows).  Values stay in
 // registers as they lie in memory: a spilled register goes through the little
-// L1 that the ring leaves, and costs more than unpacking twice.  A float32 dy is
+// L1 that the ring leaves, and costs more than unpacking twice (the form with a
+// float32 stream and a full gate spills 80 bytes all the same: 160 us at 4096 x
+// 7168, floor 95).  A float32 dy is
 // loaded directly, from L2 where its row was brought one row before: with it in
 // the ring, a slot of 7168 columns fits only once.  With a full gate or a
 // float32 stream the row is read again from its slot after the first sum

@@ -270,19 +270,20 @@ class AdamW:
     def _look_up(self):
         """Checks all tensors but the gradients and puts their addresses into the table.
 
-        Views of them are kept, so that no other storage can come to lie at an address in the table: while the tensors'
+        Their storages are kept, so that no other can come to lie at an address in the table: while the tensors'
         addresses are those, the table is theirs.
         """
-        self._seen, kept = None, []
+        self._seen, seen, kept = None, [], []
         for name, tensors in self._lists():
             kind = {"p": _TYPES[self.p_dtype], "copy": torch.bfloat16}.get(
                 name, torch.float32 if self.state_bits == 32 else torch.uint8)
             sizes = [-(-n // 32) for n in self.sizes] if name.endswith("scale") else self.sizes
             if len(tensors) != len(sizes) or [t.numel() for t in tensors if t.dtype is kind and t.is_contiguous()] != sizes:
                 raise ValueError(f"{name}: sizes, types or strides do not fit the parameters")
-            kept += [t.detach() for t in tensors]
-            self.table[name] = [t.data_ptr() for t in tensors]
-        self._kept, self._seen, self._address = kept, [t.data_ptr() for t in kept], self.table.ctypes.data
+            kept += [t.untyped_storage() for t in tensors]
+            self.table[name] = at = [t.data_ptr() for t in tensors]
+            seen += at
+        self._kept, self._seen, self._address = kept, seen, self.table.ctypes.data
 
     def __getstate__(self):
         """A copy (copy, pickle) has a table and tensors of its own, at addresses that its first step looks up."""
