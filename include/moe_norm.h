@@ -32,8 +32,8 @@
  *     MOE_GATE_FULL gate [T][H] (row stride ld_gate).
  *   - Results do not depend on thread timing.
  *   - Device-side waits give up after ~1 s: the status is then MOE_ERR_TIMEOUT,
- *     rows of y and n that were not computed are NaN, and gradients undefined.
- *     The debug hook of moe_get_device_status works here too.
+ *     what was not computed is NaN in y and n (in n the whole row), and gradients
+ *     are undefined.  The debug hook of moe_get_device_status works here too.
  */
 #ifndef MOE_NORM_H
 #define MOE_NORM_H

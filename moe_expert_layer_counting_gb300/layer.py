@@ -150,7 +150,7 @@ class BlockNorm:
 
     w_post (after the layer) and w_pre (before the next one): [H] bf16 or float32, either may be None.  Each backward call
     has a workspace of its own, as a captured graph may write one long after its call; the object keeps the last of each
-    stream, for ``device_status``.
+    stream, and the forward calls' status words, for ``device_status``.  It has to outlive the graphs captured with it.
     """
 
     def __init__(self, w_post: torch.Tensor = None, w_pre: torch.Tensor = None, residual_scale: float = 1.0,
@@ -236,7 +236,8 @@ class AdamW:
     (m, v) or (m, v, m_scale, v_scale) as an earlier object's ``state``; they are used in place.
 
     A step updates the tensors that ``params``, ``state`` and ``copies`` hold then, where their values lie then
-    (``p.data = ...`` or another tensor in a list); sizes and types stay.  A step is not for capture into a graph: its number
+    (``p.data = ...`` or another tensor in a list); sizes and types stay.  The storages that a step worked on are kept until
+    one finds others in their place.  A step is not for capture into a graph: its number
     and rate are part of the launch, and every replay would be the same step.
     """
 
