@@ -39,29 +39,29 @@ def _layer(name, op, T, H, x="bf16", w="f32", add=True, bias=True):
 def listed():
     return [
         # one token of the small-expert decode (top-8 of 256): the eight experts' gate and up weights stream by once
-        _gated("gated, one token", "gated", 8, 512, 2048, 256, keep=False),
+        _gated("gated one token", "gated", 8, 512, 2048, 256, keep=False),
         # gate and up of a skewed training batch (2048 tokens, top-8 of 64), with the rows that the way back needs
-        _gated("gated, skewed", "gated", 16384, 2048, 7168, 64, skew=1.2),
+        _gated("gated skewed", "gated", 16384, 2048, 7168, 64, skew=1.2),
         # the way back over many small experts (1000 tokens, top-8 of 256)
-        _gated("gated gradient, small experts", "gated_grad", 8000, 512, 2048, 256, dropped=5),
+        _gated("gated gradient small experts", "gated_grad", 8000, 512, 2048, 256, dropped=5),
         # the way back of the skewed batch
-        _gated("gated gradient, skewed", "gated_grad", 16384, 2048, 7168, 64, skew=1.2),
+        _gated("gated gradient skewed", "gated_grad", 16384, 2048, 7168, 64, skew=1.2),
         # the tiny layer's down projections: launches and latency
-        _matrices("orthogonalise, tiny layer", "ortho", 8, 256, 128),
+        _matrices("orthogonalise tiny layer", "ortho", 8, 256, 128),
         # gate and up of 64 small experts
-        _matrices("orthogonalise, small experts", "ortho", 64, 1024, 2048),
+        _matrices("orthogonalise small experts", "ortho", 64, 1024, 2048),
         # matrices that no tile divides, BF16 parameters, clipped
-        _matrices("muon, odd matrices", "muon", 8, 1000, 520, p="bf16", g="f32", clip=True),
+        _matrices("muon odd matrices", "muon", 8, 1000, 520, p="bf16", g="f32", clip=True),
         # the down projections of 8 large experts, with float32 masters and their copies
-        _matrices("muon, large experts", "muon", 8, 7168, 2048, p="f32"),
+        _matrices("muon large experts", "muon", 8, 7168, 2048, p="f32"),
         # before a layer while decoding
-        _layer("layer norm, decode", "layer", 8, 2048),
+        _layer("layer norm decode", "layer", 8, 2048),
         # the same in a prefill
-        _layer("layer norm, prefill", "layer", 8192, 7168),
+        _layer("layer norm prefill", "layer", 8192, 7168),
         # its gradients in training, joined with the stream's
         _layer("layer norm gradient", "layer_grad", 4096, 7168),
         # a float32 stream of odd sizes without anything to join
-        _layer("layer norm gradient, f32", "layer_grad", 1000, 1000, x="f32", add=False),
+        _layer("layer norm gradient f32", "layer_grad", 1000, 1000, x="f32", add=False),
     ]
 
 
