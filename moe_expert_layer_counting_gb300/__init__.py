@@ -4,6 +4,8 @@ SwiGLU (.) top-k-weight FP8 epilogue, behind a C ABI (include/moe_mxq.h);
 and its block-FP8 variant (E4M3 weights with 128 x 128 float32 block
 scales, include/moe_bfp8.h); the BF16 products grouped by expert, with their
 gradients, that train the weights both are cast from (include/moe_grouped.h);
+the gated block's gate and up products with their activation in one kernel, and
+the way back (include/moe_gated.h);
 the norms before and after the layer with its gate and residual scale
 (include/moe_norm.h); and AdamW over many tensors, with states in 32 or 8 bits
 (include/moe_adamw.h).
@@ -18,6 +20,7 @@ from .binding import (MoeError, moe_combine, moe_expert_forward, moe_expert_work
                       moe_status_string, moe_version, moe_workspace_size, mxq_quantize_act, mxq_quantize_weight,
                       bfp8_quantize_act, bfp8_quantize_weight, moe_bfp8_workspace_size, moe_forward_bfp8,
                       moe_grouped_workspace_size, moe_grouped_forward, moe_grouped_dgrad, moe_grouped_wgrad,
+                      ACT_SILU, ACT_GELU_TANH, moe_gated_workspace_size, moe_gated_forward, moe_gated_dgrad,
                       moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_adamw_step)
 from .layer import AdamW, BlockNorm, Bfp8Experts, MoELayer, MoELayerBfp8, QuantizedExperts  # noqa: F401
-from .training import TrainableExperts  # noqa: F401
+from .training import GatedFeedForward, TrainableExperts  # noqa: F401

@@ -1,7 +1,7 @@
 """ctypes binding of libmoe_mxq.so -- argument marshalling only.
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
-include/moe_bfp8.h, include/moe_grouped.h,
+include/moe_bfp8.h, include/moe_grouped.h, include/moe_gated.h,
 include/moe_norm.h, include/moe_adamw.h) and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
@@ -45,6 +45,7 @@ PHASE_TOKEN_SCALES, PHASE_GEMM1, PHASE_GEMM2, PHASE_H_SCALES, PHASE_RESET = 1, 2
 SCHEDULE_DEFAULT, SCHEDULE_SEPARATE, SCHEDULE_EXPERT_WAVES = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID, ROUTE_RAW, ROUTE_NO_RENORM = 0, 1, 2, 4
 BFP8_LAYOUT_CANONICAL, BFP8_LAYOUT_TILED = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1                          # enum moe_activation
 BF16, F32 = 0, 1                                         # enum moe_dtype
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
@@ -93,6 +94,13 @@ class MoeBfp8Args(ctypes.Structure):
                 ("topk_idx_out", _p), ("topk_w_out", _p), ("counts_out", _p), ("offsets_out", _p),
                 ("perm_out", _p), ("hq_out", _p), ("hs_out", _p),
                 ("workspace", _p), ("workspace_bytes", _sz), ("weight_layout", _i32), ("phases", _i32)]
+
+
+class MoeGatedArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("E", _i32), ("activation", _i32),
+                ("P", _i64), ("H", _i64), ("I", _i64), ("rows", _p), ("ld_rows", _i64), ("w", _p), ("offsets", _p),
+                ("row_w", _p), ("a", _p), ("ld_a", _i64), ("h", _p), ("ld_h", _i64), ("da", _p), ("ld_da", _i64),
+                ("drow_w", _p), ("workspace", _p), ("workspace_bytes", _sz)]
 
 
 class MoeNormArgs(ctypes.Structure):
@@ -147,6 +155,10 @@ lib.moe_grouped_workspace_size.restype = _sz
 lib.moe_grouped_forward.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _sz, _p]
 lib.moe_grouped_dgrad.argtypes = lib.moe_grouped_forward.argtypes
 lib.moe_grouped_wgrad.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _p, _i32, _i32, _p, _sz, _p]
+lib.moe_gated_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+lib.moe_gated_workspace_size.restype = _sz
+lib.moe_gated_forward.argtypes = [_p, _p]
+lib.moe_gated_dgrad.argtypes = [_p, _p]
 lib.moe_norm_forward.argtypes = [_p, _p]                # packed structures (below) or byref of the ctypes ones
 lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
 lib.moe_norm_workspace_size.restype = _sz
@@ -161,7 +173,7 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_expert_forward",
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
               "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
-              "moe_norm_forward", "moe_norm_backward", "moe_adamw_step"):
+              "moe_gated_forward", "moe_gated_dgrad", "moe_norm_forward", "moe_norm_backward", "moe_adamw_step"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -427,15 +439,76 @@ def moe_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
     return rc
 
 
+# ---------------------------------------------------------------- gated feed-forward block by expert (include/moe_gated.h)
+
+_NONE = (0, 0)
+_GATED_ARGS = struct.Struct("@IiiqqqPqPPPPqPqPqPPN")
+assert _GATED_ARGS.size == ctypes.sizeof(MoeGatedArgs)
+
+
+def _on_current_device(*tensors) -> bool:
+    """Whether all of them (None left out) lie on the current device, whose streams the calls use."""
+    tensors = [t for t in tensors if t is not None]
+    return all(t.is_cuda for t in tensors) and {t.get_device() for t in tensors} <= {torch.cuda.current_device()}
+
+
+def _is_row_values(t, P: int) -> bool:
+    return t is None or (t.dtype is torch.float32 and t.shape == (P,) and t.is_contiguous())
+
+
+def moe_gated_workspace_size(P: int, H: int, I: int, E: int) -> int:
+    return int(lib.moe_gated_workspace_size(P, H, I, E))
+
+
+def _gated(where, rows, w, H, I, offsets, a, h, da, workspace, row_w, drow_w, activation, stream, check):
+    E, P = w.shape[0], rows.shape[0]
+    xr = _rows(rows, (P, H))
+    ar = _NONE if a is None else _rows(a, (P, 2 * I))
+    hr = _NONE if h is None else _rows(h, (P, I))
+    dr = _NONE if da is None else _rows(da, (P, 2 * I))
+    if None in (xr, ar, hr, dr) or not _is_weight(w) or not _is_offsets(offsets, E) or not _is_row_values(row_w, P) or \
+            not _is_row_values(drow_w, P) or not workspace.is_contiguous() or \
+            not _on_current_device(rows, w, offsets, a, h, da, workspace, row_w, drow_w):
+        return _invalid(where, check)
+    args = _GATED_ARGS.pack(_GATED_ARGS.size, E, activation, P, H, I, *xr, w.data_ptr(), offsets.data_ptr(),
+                            0 if row_w is None else row_w.data_ptr(), *ar, *hr, *dr, 0 if drow_w is None else drow_w.data_ptr(),
+                            workspace.data_ptr(), workspace.nbytes)
+    rc = getattr(lib, where)(args, _stream(stream))
+    if check:
+        _check(rc, where)
+    return rc
+
+
+def moe_gated_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, h: torch.Tensor, workspace: torch.Tensor,
+                      a: torch.Tensor = None, row_w: torch.Tensor = None, activation: int = ACT_SILU, stream=None,
+                      check=True) -> int:
+    """h [P, I] = f(gate) up row_w with [gate, up] = a [P, 2I] = x [P, H] @ w[e] [2I, H]^T for the rows
+    offsets[e] .. offsets[e+1] of expert e (bf16); a (what moe_gated_dgrad takes) and row_w [P] float32 may be None."""
+    if w.dim() != 3 or w.shape[1] % 2:
+        return _invalid("moe_gated_forward", check)
+    return _gated("moe_gated_forward", x, w, w.shape[2], w.shape[1] // 2, offsets, a, h, None, workspace, row_w, None,
+                  activation, stream, check)
+
+
+def moe_gated_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, a: torch.Tensor, da: torch.Tensor,
+                    workspace: torch.Tensor, h: torch.Tensor = None, row_w: torch.Tensor = None,
+                    drow_w: torch.Tensor = None, activation: int = ACT_SILU, stream=None, check=True) -> int:
+    """da [P, 2I], the gradient of moe_gated_forward's a, from that of the down product's answer, dy [P, H], and the down
+    weights w [E, H, I]; h [P, I] once more and drow_w [P] float32 (the gradient of row_w) where they are given."""
+    if w.dim() != 3:
+        return _invalid("moe_gated_dgrad", check)
+    return _gated("moe_gated_dgrad", dy, w, w.shape[1], w.shape[2], offsets, a, h, da, workspace, row_w, drow_w, activation,
+                  stream, check)
+
+
 # ---------------------------------------------------------------- norms around the layer (include/moe_norm.h)
 
-# MoeNormArgs, MoeNormGrads and MoeAdamwArgs as bytes: packing costs a fifth of filling a ctypes structure
+# MoeNormArgs, MoeNormGrads and MoeAdamwArgs (above: MoeGatedArgs) as bytes: packing costs a fifth of filling a ctypes structure
 _NORM_ARGS = struct.Struct("@I5i3fqqPqPqPqPPPqPqP")
 _NORM_GRADS = struct.Struct("@IPqPqPqPqPqPPPN")
 _ADAMW_ARGS = struct.Struct("@IiPiiiP5dq")
 assert (_NORM_ARGS.size, _NORM_GRADS.size, _ADAMW_ARGS.size) == tuple(
     ctypes.sizeof(c) for c in (MoeNormArgs, MoeNormGrads, MoeAdamwArgs))
-_NONE = (0, 0)
 
 
 def _norm_args(x, b, gate, w_post, w_pre, y, n, residual_scale, weight_offset, eps, gate_sigmoid, status=0):

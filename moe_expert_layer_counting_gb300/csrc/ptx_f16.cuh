@@ -1,5 +1,5 @@
 // ptx_f16.cuh -- inline-PTX wrappers of the BF16 products (grouped.cu) beyond
-// those of ptx.cuh: 3-D TMA loads of a CTA pair, tcgen05.mma kind::f16 with
+// those of ptx.cuh: 3-D and 5-D TMA loads of a CTA pair, tcgen05.mma kind::f16 with
 // operands of either major, wide TMEM reads, bounded waits of kernels that
 // reset their own status words, and claims of clusters not launched yet.
 #pragma once
@@ -28,6 +28,15 @@ __device__ __forceinline__ void tma_load_3d_2sm(void *dst, const CUtensorMap *ma
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t x,
+                                                int32_t y, int32_t z, int32_t u, int32_t v, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "l"(policy)
       : "memory");
 }
 

@@ -1,8 +1,9 @@
 """The expert layer with BF16 weights, forward and backward: what trains the weights that ``QuantizedExperts`` and
 ``Bfp8Experts`` are cast from.
 
-The products, the permute and the combine are the library's; the gathers of rows and the gated activation between the
-two products are plain torch operations (float32 inside, one rounding to BF16).
+The products, the permute and the combine are the library's; the gathers of rows are torch operations.  The gated
+activation between the two products is one of the products' epilogue (``fused=True``, and ``GatedFeedForward``), or plain
+torch operations between them (float32 inside, one rounding to BF16).
 """
 from __future__ import annotations
 
@@ -18,9 +19,13 @@ class TrainableExperts:
     The layer is that of ``MoELayer`` without its quantisation: h = silu(gate) * up * topk_w for each (token, slot) pair,
     summed over a token's slots after the down product.  topk_idx < 0 marks a dropped pair; an index of E or more is
     reported by status() and its pair dropped.
+
+    fused: the activation inside the products' kernels (include/moe_gated.h), which rounds less on the way: h is that of
+    the unrounded gate and up values, and the gradient of h is not rounded at all.  Without it the results are those of
+    separate operations, each rounded to BF16.
     """
 
-    def __init__(self, l1: torch.Tensor, l2: torch.Tensor):
+    def __init__(self, l1: torch.Tensor, l2: torch.Tensor, fused: bool = False):
         E, twoI, H = l1.shape
         if l2.shape != (E, H, twoI // 2):
             raise ValueError("l1 [E, 2I, H] and l2 [E, H, I] do not fit")
@@ -30,7 +35,8 @@ class TrainableExperts:
         # of the products (the size does not depend on the rows) and of the last permute: status() reads each one's status
         self.workspaces = [torch.zeros(B.moe_grouped_workspace_size(1, H, 2 * self.I, E), dtype=torch.uint8, device=dev)
                            for _ in range(6)]
-        self.permute_workspace = None
+        self.permute_workspace = self.gated_workspace = None
+        self.fused = fused
 
     def _check_rows(self, name, t, T):
         if t.shape != (T, self.H) or t.dtype is not torch.bfloat16 or t.device != self.l1.device:
@@ -47,6 +53,10 @@ class TrainableExperts:
         self.permute_workspace = ws
         B.moe_permute(topk_idx, self.E, counts, offsets, perm, inv_perm, ws)
         return offsets, perm.long(), inv_perm.view(T, k)
+
+    def _gated_workspace(self, P):
+        """A new one for each call: it holds sums, and a captured graph may write it long after the call."""
+        return torch.empty(B.moe_gated_workspace_size(P, self.H, self.I, self.E), dtype=torch.uint8, device=self.l1.device)
 
     def _sum_slots(self, rows, s):
         """Each token's sum over its slots of its pairs' rows (float32 inside; dropped slots are left out)."""
@@ -69,9 +79,17 @@ class TrainableExperts:
         s = {"offsets": offsets, "row": row, "token": perm // k, "w": topk_w.reshape(-1)[perm][:, None]}
         s["rows"] = n[s["token"]]
         s["a"] = torch.zeros(T * k, 2 * self.I, dtype=torch.bfloat16, device=n.device)
-        B.moe_grouped_forward(s["rows"], self.l1, offsets, s["a"], self.workspaces[0])
-        gate, up = s["a"].float().split(self.I, 1)
-        s["h"] = (torch.nn.functional.silu(gate) * up * s["w"]).bfloat16()
+        if self.fused:
+            if topk_w.dtype is not torch.float32 or topk_w.device != self.l1.device:
+                raise ValueError("topk_w is not float32 on the weights' device")
+            h = torch.zeros(T * k, self.I, dtype=torch.bfloat16, device=n.device)
+            ws = self._gated_workspace(T * k)
+            B.moe_gated_forward(s["rows"], self.l1, offsets, h, ws, a=s["a"], row_w=s["w"][:, 0])
+            s["h"], self.gated_workspace = h, ws
+        else:
+            B.moe_grouped_forward(s["rows"], self.l1, offsets, s["a"], self.workspaces[0])
+            gate, up = s["a"].float().split(self.I, 1)
+            s["h"] = (torch.nn.functional.silu(gate) * up * s["w"]).bfloat16()
         o = torch.zeros(T * k, self.H, dtype=torch.bfloat16, device=n.device)
         B.moe_grouped_forward(s["h"], self.l2, offsets, o, self.workspaces[1])
         return self._sum_slots(o, s), s
@@ -80,16 +98,23 @@ class TrainableExperts:
         """(dn [T, H], dtopk_w [T, k]); the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
         self._check_rows("db", db, s["row"].shape[0])
         do = db[s["token"]]
-        dh = torch.zeros_like(s["h"])
-        B.moe_grouped_dgrad(do, self.l2, s["offsets"], dh, self.workspaces[2])
         B.moe_grouped_wgrad(do, s["h"], s["offsets"], dl2, self.workspaces[3], accumulate)
-        gate, up = s["a"].float().split(self.I, 1)
-        sig = torch.sigmoid(gate)
-        act = gate * sig
-        d = dh.float()
-        dw = (d * act * up).sum(1)
-        d = d * s["w"]
-        da = torch.cat([d * up * (sig + act * (1 - sig)), d * act], 1).bfloat16()
+        if self.fused:
+            da = torch.zeros_like(s["a"])
+            dw = torch.zeros(da.shape[0], dtype=torch.float32, device=da.device)
+            ws = self._gated_workspace(da.shape[0])
+            B.moe_gated_dgrad(do, self.l2, s["offsets"], s["a"], da, ws, row_w=s["w"][:, 0], drow_w=dw)
+            self.gated_workspace = ws
+        else:
+            dh = torch.zeros_like(s["h"])
+            B.moe_grouped_dgrad(do, self.l2, s["offsets"], dh, self.workspaces[2])
+            gate, up = s["a"].float().split(self.I, 1)
+            sig = torch.sigmoid(gate)
+            act = gate * sig
+            d = dh.float()
+            dw = (d * act * up).sum(1)
+            d = d * s["w"]
+            da = torch.cat([d * up * (sig + act * (1 - sig)), d * act], 1).bfloat16()
         drows = torch.zeros_like(s["rows"])
         B.moe_grouped_dgrad(da, self.l1, s["offsets"], drows, self.workspaces[4])
         B.moe_grouped_wgrad(da, s["rows"], s["offsets"], dl1, self.workspaces[5], accumulate)
@@ -98,5 +123,67 @@ class TrainableExperts:
 
     def status(self) -> int:
         """MOE_OK, or the first status that the last step's permute or products reported (synchronises)."""
-        used = self.workspaces if self.permute_workspace is None else [self.permute_workspace, *self.workspaces]
+        used = [w for w in (self.permute_workspace, self.gated_workspace) if w is not None] + self.workspaces
         return next((c for c in (B.moe_get_device_status(w) for w in used) if c), B.MOE_OK)
+
+
+class GatedFeedForward:
+    """b = block(n), the gated feed-forward block that every token takes (a shared expert, a dense layer), and its
+    gradients: h = f(n gate^T) (n up^T), b = h l2^T, with l1 [2I, H] (gate rows then up rows) and l2 [H, I] in BF16.
+
+    activation: ACT_SILU or ACT_GELU_TANH (include/moe_gated.h).  Calls run on the current stream; each has outputs and
+    workspaces of its own, of which the object keeps the last for status().
+    """
+
+    def __init__(self, l1: torch.Tensor, l2: torch.Tensor, activation: int = B.ACT_SILU):
+        if l1.dim() != 2 or l1.shape[0] % 2 or l2.shape != (l1.shape[1], l1.shape[0] // 2):
+            raise ValueError("l1 [2I, H] and l2 [H, I] do not fit")
+        if any(t.dtype is not torch.bfloat16 or not t.is_contiguous() for t in (l1, l2)) or l1.device != l2.device:
+            raise ValueError("l1 and l2 are not contiguous BF16 on one device")
+        if activation not in (B.ACT_SILU, B.ACT_GELU_TANH):
+            raise ValueError("activation is ACT_SILU or ACT_GELU_TANH")
+        self.l1, self.l2, self.activation = l1, l2, activation
+        self.H, self.I = l1.shape[1], l2.shape[1]
+        self._used = []
+
+    def _workspaces(self, T, n):
+        """One for a gated call, n - 1 for products."""
+        sizes = [B.moe_gated_workspace_size(T, self.H, self.I, 1)] + [B.moe_grouped_workspace_size(T, self.H, self.I, 1)] * (n - 1)
+        return [torch.empty(size, dtype=torch.uint8, device=self.l1.device) for size in sizes]
+
+    def forward(self, n: torch.Tensor, keep: bool = True):
+        """(b [T, H], what backward needs); n [T, H] BF16.  keep=False: no backward follows, and nothing is kept for it."""
+        self._check(n, n.shape[0] if n.dim() == 2 else -1)
+        T, new = n.shape[0], n.new_empty
+        # [0, T]: all rows are the one expert's
+        offsets = torch.arange(0, T + 1, max(T, 1), dtype=torch.int32, device=n.device) if T else new(2, dtype=torch.int32).zero_()
+        h, b = new(T, self.I), new(T, self.H)
+        a = new(T, 2 * self.I) if keep else None
+        ws = self._workspaces(T, 2)
+        B.moe_gated_forward(n, self.l1[None], offsets, h, ws[0], a=a, activation=self.activation)
+        B.moe_grouped_forward(h, self.l2[None], offsets, b, ws[1])
+        self._used = ws
+        return b, {"n": n, "a": a, "h": h, "offsets": offsets} if keep else None
+
+    def backward(self, db: torch.Tensor, s: dict, dl1: torch.Tensor, dl2: torch.Tensor, accumulate: bool = False):
+        """dn [T, H]; the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
+        n, a, offsets, T = s["n"], s["a"], s["offsets"], s["n"].shape[0]
+        self._check(db, T)
+        if dl1.shape != self.l1.shape or dl2.shape != self.l2.shape:
+            raise ValueError("dl1 and dl2 are not of the weights' shapes")
+        da, dn = torch.empty_like(a), torch.empty_like(n, memory_format=torch.contiguous_format)
+        ws = self._workspaces(T, 4)
+        B.moe_grouped_wgrad(db, s["h"], offsets, dl2[None], ws[1], accumulate)
+        B.moe_gated_dgrad(db, self.l2[None], offsets, a, da, ws[0], activation=self.activation)
+        B.moe_grouped_dgrad(da, self.l1[None], offsets, dn, ws[2])
+        B.moe_grouped_wgrad(da, n, offsets, dl1[None], ws[3], accumulate)
+        self._used = ws
+        return dn
+
+    def _check(self, t, T):
+        if t.shape != (T, self.H) or t.dtype is not torch.bfloat16 or t.device != self.l1.device:
+            raise ValueError(f"rows are not [T, {self.H}] BF16 on the weights' device, or not those of forward")
+
+    def status(self) -> int:
+        """MOE_OK, or the first status that the last forward or backward call's products reported (synchronises)."""
+        return next((c for c in (B.moe_get_device_status(w) for w in self._used) if c), B.MOE_OK)
