@@ -8,7 +8,8 @@ the gated block's gate and up products with their activation in one kernel, and
 the way back (include/moe_gated.h);
 the norms before and after the layer with its gate and residual scale
 (include/moe_norm.h); and AdamW over many tensors, with states in 32 or 8 bits
-(include/moe_adamw.h).
+(include/moe_adamw.h); and Muon over stacks of matrices, with their
+orthogonalisation by Newton-Schulz products (include/moe_muon.h).
 
 ``binding`` holds the thin ctypes layer (same names as the C entry points);
 ``layer.MoELayer`` / ``layer.MoELayerBfp8`` own quantised weights and a
@@ -21,6 +22,7 @@ from .binding import (MoeError, moe_combine, moe_expert_forward, moe_expert_work
                       bfp8_quantize_act, bfp8_quantize_weight, moe_bfp8_workspace_size, moe_forward_bfp8,
                       moe_grouped_workspace_size, moe_grouped_forward, moe_grouped_dgrad, moe_grouped_wgrad,
                       ACT_SILU, ACT_GELU_TANH, moe_gated_workspace_size, moe_gated_forward, moe_gated_dgrad,
-                      moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_adamw_step)
-from .layer import AdamW, BlockNorm, Bfp8Experts, MoELayer, MoELayerBfp8, QuantizedExperts  # noqa: F401
+                      moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_adamw_step, moe_muon_workspace_size,
+                      moe_orthogonalize, moe_muon_step)
+from .layer import AdamW, BlockNorm, Bfp8Experts, MoELayer, MoELayerBfp8, Muon, QuantizedExperts  # noqa: F401
 from .training import GatedFeedForward, TrainableExperts  # noqa: F401

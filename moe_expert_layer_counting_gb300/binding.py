@@ -2,7 +2,7 @@
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
 include/moe_bfp8.h, include/moe_grouped.h, include/moe_gated.h,
-include/moe_norm.h, include/moe_adamw.h) and takes torch tensors for the device buffers; all work runs in the
+include/moe_norm.h, include/moe_adamw.h, include/moe_muon.h) and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
 There is no CPU fallback: importing this module without the built library
@@ -130,6 +130,24 @@ class MoeAdamwArgs(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("step", _i64)]
 
 
+class MoeNewtonSchulz(ctypes.Structure):
+    _fields_ = [("steps", _i32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class MoeMuonArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("p_dtype", _i32), ("g_dtype", _i32), ("nesterov", _i32),
+                ("E", _i64), ("N", _i64), ("K", _i64), ("p", _p), ("g", _p), ("m", _p), ("copy", _p), ("grad_scale", _p),
+                ("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("ns", MoeNewtonSchulz), ("status", _p), ("workspace", _p),
+                ("workspace_bytes", _sz)]
+
+
+class MoeOrthogonalizeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("x_dtype", _i32), ("out_dtype", _i32), ("ns", MoeNewtonSchulz),
+                ("E", _i64), ("N", _i64), ("K", _i64), ("x", _p), ("out", _p), ("status", _p), ("workspace", _p),
+                ("workspace_bytes", _sz)]
+
+
 lib.mxq_quantize_act.argtypes = [_p, _i64, _i64, _p, _p, _p]
 lib.mxq_quantize_weight.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]
 lib.moe_route_topk.argtypes = [_p, _i64, _i32, _i32, _p, _p, _p]
@@ -164,6 +182,10 @@ lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
 lib.moe_norm_workspace_size.restype = _sz
 lib.moe_norm_backward.argtypes = [_p, _p, _p]
 lib.moe_adamw_step.argtypes = [_p, _p]
+lib.moe_muon_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.moe_muon_workspace_size.restype = _sz
+lib.moe_orthogonalize.argtypes = [_p, _p]
+lib.moe_muon_step.argtypes = [_p, _p]
 lib.moe_get_device_status.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_int)]
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
@@ -173,7 +195,8 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_expert_forward",
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
               "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
-              "moe_gated_forward", "moe_gated_dgrad", "moe_norm_forward", "moe_norm_backward", "moe_adamw_step"):
+              "moe_gated_forward", "moe_gated_dgrad", "moe_norm_forward", "moe_norm_backward", "moe_adamw_step",
+              "moe_orthogonalize", "moe_muon_step"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -620,4 +643,69 @@ def moe_adamw_step(table: np.ndarray, p_dtype: int, g_dtype: int, state_bits: in
     rc = lib.moe_adamw_step(a, _stream(stream))
     if check:
         _check(rc, "moe_adamw_step")
+    return rc
+
+
+# ---------------------------------------------------------------- orthogonalised matrices and Muon (include/moe_muon.h)
+
+# MoeMuonArgs and MoeOrthogonalizeArgs as bytes
+_MUON_ARGS = struct.Struct("@IiiiqqqPPPPPddddi4fPPN")
+_ORTHOGONALIZE_ARGS = struct.Struct("@Iiii4fqqqPPPPN")
+assert (_MUON_ARGS.size, _ORTHOGONALIZE_ARGS.size) == (ctypes.sizeof(MoeMuonArgs), ctypes.sizeof(MoeOrthogonalizeArgs))
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _stack(t: torch.Tensor):
+    """(E, N, K) of a matrix or a stack of matrices."""
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape) if t.dim() == 3 else None
+
+
+def _is_like(t, like: torch.Tensor, *dtypes) -> bool:
+    return t is None or (t.dtype in dtypes and t.shape == like.shape and t.is_contiguous())
+
+
+def _is_status(status) -> bool:
+    return status is None or (status.nbytes >= 64 and status.is_contiguous())
+
+
+def moe_muon_workspace_size(E: int, N: int, K: int) -> int:
+    return int(lib.moe_muon_workspace_size(E, N, K))
+
+
+def moe_orthogonalize(x: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, steps: int = 5,
+                      coefficients=NS_COEFFICIENTS, eps: float = 1e-7, stream=None, check=True,
+                      status: torch.Tensor = None) -> int:
+    """out = each matrix of x ([N, K] or [E, N, K]; bf16 or float32, either for out) orthogonalised by Newton-Schulz steps."""
+    shape = _stack(x)
+    if shape is None or not _is_like(x, x, *_DTYPES) or not _is_like(out, x, *_DTYPES) or not workspace.is_contiguous() or \
+            not _is_status(status) or not _on_current_device(x, out, workspace, status):
+        return _invalid("moe_orthogonalize", check)
+    a = _ORTHOGONALIZE_ARGS.pack(_ORTHOGONALIZE_ARGS.size, _DTYPES[x.dtype], _DTYPES[out.dtype], steps, *coefficients, eps, *shape,
+                                 x.data_ptr(), out.data_ptr(), 0 if status is None else status.data_ptr(),
+                                 workspace.data_ptr(), workspace.nbytes)
+    rc = lib.moe_orthogonalize(a, _stream(stream))
+    if check:
+        _check(rc, "moe_orthogonalize")
+    return rc
+
+
+def moe_muon_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, workspace: torch.Tensor, lr: float, momentum: float = 0.95,
+                  weight_decay: float = 0.0, scale: float = 1.0, nesterov: bool = True, steps: int = 5,
+                  coefficients=NS_COEFFICIENTS, eps: float = 1e-7, copy: torch.Tensor = None, grad_scale: torch.Tensor = None,
+                  stream=None, check=True, status: torch.Tensor = None) -> int:
+    """One step of Muon on a matrix or a stack of matrices p (bf16 or float32, in place) with its gradient g (either type)
+    and momentum m (float32, in place); copy: p in bf16 as well; grad_scale: a device float."""
+    shape = _stack(p)
+    if shape is None or not _is_like(p, p, *_DTYPES) or not _is_like(g, p, *_DTYPES) or not _is_like(m, p, torch.float32) or \
+            not _is_like(copy, p, torch.bfloat16) or not workspace.is_contiguous() or not _is_status(status) or \
+            (grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1)) or \
+            not _on_current_device(p, g, m, workspace, copy, grad_scale, status):
+        return _invalid("moe_muon_step", check)
+    a = _MUON_ARGS.pack(_MUON_ARGS.size, _DTYPES[p.dtype], _DTYPES[g.dtype], 1 if nesterov else 0, *shape, p.data_ptr(), g.data_ptr(),
+                        m.data_ptr(), 0 if copy is None else copy.data_ptr(), 0 if grad_scale is None else grad_scale.data_ptr(),
+                        lr, momentum, weight_decay, scale, steps, *coefficients, eps,
+                        0 if status is None else status.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+    rc = lib.moe_muon_step(a, _stream(stream))
+    if check:
+        _check(rc, "moe_muon_step")
     return rc

@@ -98,6 +98,14 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "l"(policy)
                : "memory");
 }
+// As tma_store_3d, of what the next kernel reads.
+__device__ __forceinline__ void tma_store_3d_normal(const CUtensorMap *map, const void *src, int32_t x, int32_t y,
+                                                    int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

@@ -304,3 +304,86 @@ class AdamW:
         B.moe_adamw_step(self.table, self.p_dtype, B._DTYPES[kind], self.state_bits, self.lr, *self.betas, self.eps,
                          self.weight_decay, self.steps + 1, grad_scale, stream=stream, address=self._address)
         self.steps += 1
+
+
+class Muon:
+    """Muon over a list of matrices: a step moves each one by its momentum, orthogonalised (include/moe_muon.h).
+
+    params: contiguous [N, K], or [.., N, K] whose every matrix is orthogonalised for itself (the experts' weights
+    [E, N, K]; gate and up rows apart as a view [2E, I, H]), bf16 or float32 each; other tensors are AdamW's.  copies: a bf16
+    copy of each parameter, written by every step (a list with None where there is none, or None).  adjust sets the length of a
+    step: "rms" lr 0.2 sqrt(max(N, K)), which makes its root mean square that of AdamW's, "shape" lr sqrt(max(1, N / K)),
+    None lr.  state resumes a run: (m,), as an earlier object's ``state``; used in place, float32.
+
+    A step updates the tensors that ``params``, ``state`` and ``copies`` hold then, on the current stream or the given one; its
+    workspace is its own.  Captured into a graph, each replay is a step at the captured rate, with the gradients
+    that then lie there.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.1,
+                 adjust: str = "rms", ns_steps: int = 5, ns_coefficients=B.NS_COEFFICIENTS, eps: float = 1e-7, copies=None,
+                 state=None):
+        self.params, self.copies = list(params), None if copies is None else list(copies)
+        if adjust not in ("rms", "shape", None):
+            raise ValueError('adjust is "rms", "shape" or None')
+        self.lr, self.momentum, self.nesterov, self.weight_decay, self.adjust = lr, momentum, nesterov, weight_decay, adjust
+        self.ns_steps, self.ns_coefficients, self.eps = ns_steps, tuple(ns_coefficients), eps
+        if state is None:
+            state = ([torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format) for p in self.params],)
+        if len(state) != 1:
+            raise ValueError("state is (m,)")
+        self.state = {"m": list(state[0])}
+        self._status = {}                            # (device, stream handle) -> 64 bytes for each parameter
+        self._check()
+
+    def _check(self, grads=None):
+        lists = {"m": (self.state["m"], (torch.float32,)), "copies": (self.copies, (torch.bfloat16,)),
+                 "gradients": (grads, (torch.bfloat16, torch.float32))}
+        for p in self.params:
+            if p.dim() < 2 or p.dtype not in B._DTYPES or not p.is_contiguous():
+                raise ValueError("parameters are contiguous matrices or stacks of them, bf16 or float32")
+        for name, (tensors, kinds) in lists.items():
+            if tensors is None:
+                continue
+            if len(tensors) != len(self.params) or any(
+                    (t is None and name != "copies") or (t is not None and (
+                        t.shape != p.shape or t.dtype not in kinds or not t.is_contiguous() or t.device != p.device))
+                    for t, p in zip(tensors, self.params)):
+                raise ValueError(f"{name}: shapes, types, strides or devices do not fit the parameters")
+
+    def _scale(self, N, K):
+        if self.adjust is None:
+            return 1.0
+        return 0.2 * max(N, K) ** 0.5 if self.adjust == "rms" else max(1.0, N / K) ** 0.5
+
+    def step(self, grads, grad_scale: torch.Tensor = None, stream=None):
+        """One step with these gradients (contiguous, bf16 or float32 each), each times grad_scale (a device float)."""
+        grads = list(grads)
+        self._check(grads)
+        with _on(stream):
+            self._step(grads, grad_scale, B._stream(stream))
+
+    def _step(self, grads, grad_scale, handle):
+        if not self.params:
+            return
+        key = self.params[0].device, handle
+        status = self._status.get(key)
+        if status is None or status.shape[0] != len(self.params):
+            status = self._status[key] = torch.zeros(len(self.params), 64, dtype=torch.uint8, device=self.params[0].device)
+        shapes = [(p.numel() // max(1, p.shape[-2] * p.shape[-1]), *p.shape[-2:]) for p in self.params]
+        nbytes = max((B.moe_muon_workspace_size(*shape) for shape, p in zip(shapes, self.params) if p.numel()), default=0)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.params[0].device)
+        for i, (p, shape) in enumerate(zip(self.params, shapes)):
+            if p.numel():
+                copy = None if self.copies is None or self.copies[i] is None else self.copies[i].view(shape)
+                B.moe_muon_step(p.view(shape), grads[i].view(shape), self.state["m"][i].view(shape), workspace, self.lr,
+                                self.momentum, self.weight_decay, self._scale(*shape[1:]), self.nesterov, self.ns_steps,
+                                self.ns_coefficients, self.eps, copy, grad_scale, handle, status=status[i])
+
+    def device_status(self, stream=None) -> int:
+        """MOE_OK, or the first that the last step on this stream reported (synchronises)."""
+        if not self.params:
+            return B.MOE_OK
+        words = self._status.get((self.params[0].device, B._stream(stream)))
+        return next((code for code in (B.moe_get_device_status(w, stream) for w in ([] if words is None else words)) if code),
+                    B.MOE_OK)
