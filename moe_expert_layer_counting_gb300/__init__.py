@@ -7,7 +7,8 @@ gradients, that train the weights both are cast from (include/moe_grouped.h);
 the gated block's gate and up products with their activation in one kernel, and
 the way back (include/moe_gated.h);
 the norms before and after the layer with its gate and residual scale
-(include/moe_norm.h); and AdamW over many tensors, with states in 32 or 8 bits
+(include/moe_norm.h); layer norm with the stream's addition
+(include/moe_layernorm.h); AdamW over many tensors, with states in 32 or 8 bits
 (include/moe_adamw.h); and Muon over stacks of matrices, with their
 orthogonalisation by Newton-Schulz products (include/moe_muon.h).
 
@@ -22,7 +23,8 @@ from .binding import (MoeError, moe_combine, moe_expert_forward, moe_expert_work
                       bfp8_quantize_act, bfp8_quantize_weight, moe_bfp8_workspace_size, moe_forward_bfp8,
                       moe_grouped_workspace_size, moe_grouped_forward, moe_grouped_dgrad, moe_grouped_wgrad,
                       ACT_SILU, ACT_GELU_TANH, moe_gated_workspace_size, moe_gated_forward, moe_gated_dgrad,
-                      moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_adamw_step, moe_muon_workspace_size,
+                      moe_norm_forward, moe_norm_workspace_size, moe_norm_backward, moe_layernorm_forward,
+                      moe_layernorm_workspace_size, moe_layernorm_backward, moe_adamw_step, moe_muon_workspace_size,
                       moe_orthogonalize, moe_muon_step)
-from .layer import AdamW, BlockNorm, Bfp8Experts, MoELayer, MoELayerBfp8, Muon, QuantizedExperts  # noqa: F401
+from .layer import AdamW, BlockNorm, Bfp8Experts, LayerNorm, MoELayer, MoELayerBfp8, Muon, QuantizedExperts  # noqa: F401
 from .training import GatedFeedForward, TrainableExperts  # noqa: F401

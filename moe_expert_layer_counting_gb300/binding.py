@@ -2,7 +2,7 @@
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
 include/moe_bfp8.h, include/moe_grouped.h, include/moe_gated.h,
-include/moe_norm.h, include/moe_adamw.h, include/moe_muon.h) and takes torch tensors for the device buffers; all work runs in the
+include/moe_norm.h, include/moe_layernorm.h, include/moe_adamw.h, include/moe_muon.h) and takes torch tensors for the device buffers; all work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
 There is no CPU fallback: importing this module without the built library
@@ -119,6 +119,19 @@ class MoeNormGrads(ctypes.Structure):
                 ("workspace", _p), ("workspace_bytes", _sz)]
 
 
+class MoeLayernormArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("x_dtype", _i32), ("w_dtype", _i32), ("eps", ctypes.c_float),
+                ("T", _i64), ("H", _i64), ("x", _p), ("ldx", _i64), ("b", _p), ("ldb", _i64), ("w", _p), ("bias", _p),
+                ("s", _p), ("lds", _i64), ("n", _p), ("ldn", _i64)]
+
+
+class MoeLayernormGrads(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("x_dtype", _i32), ("w_dtype", _i32), ("eps", ctypes.c_float),
+                ("T", _i64), ("H", _i64), ("s", _p), ("lds", _i64), ("w", _p), ("dn", _p), ("ld_dn", _i64),
+                ("ds", _p), ("ld_ds", _i64), ("dx", _p), ("ld_dx", _i64), ("dw", _p), ("dbias", _p), ("workspace", _p),
+                ("workspace_bytes", _sz)]
+
+
 # moe_adamw_tensor, for host tables (numpy structured arrays)
 ADAMW_TENSOR = np.dtype([(f, np.int64) for f in ("n", "p", "g", "m", "v", "m_scale", "v_scale", "copy")])
 
@@ -182,6 +195,10 @@ lib.moe_norm_workspace_size.argtypes = [_i64, _i64]
 lib.moe_norm_workspace_size.restype = _sz
 lib.moe_norm_backward.argtypes = [_p, _p, _p]
 lib.moe_adamw_step.argtypes = [_p, _p]
+lib.moe_layernorm_workspace_size.argtypes = [_i64, _i64]
+lib.moe_layernorm_workspace_size.restype = _sz
+lib.moe_layernorm_forward.argtypes = [_p, _p]
+lib.moe_layernorm_backward.argtypes = [_p, _p]
 lib.moe_muon_workspace_size.argtypes = [_i64, _i64, _i64]
 lib.moe_muon_workspace_size.restype = _sz
 lib.moe_orthogonalize.argtypes = [_p, _p]
@@ -196,7 +213,7 @@ for _name in ("mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_
               "moe_combine", "moe_forward", "moe_get_device_status", "bfp8_quantize_act", "bfp8_quantize_weight",
               "moe_forward_bfp8", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
               "moe_gated_forward", "moe_gated_dgrad", "moe_norm_forward", "moe_norm_backward", "moe_adamw_step",
-              "moe_orthogonalize", "moe_muon_step"):
+              "moe_orthogonalize", "moe_muon_step", "moe_layernorm_forward", "moe_layernorm_backward"):
     getattr(lib, _name).restype = ctypes.c_int
 
 
@@ -625,6 +642,75 @@ def moe_norm_backward(y, b, gate, w_post, w_pre, dy, dn, workspace, dx=None, db=
     rc = lib.moe_norm_backward(a, g, _stream(stream))
     if check:
         _check(rc, "moe_norm_backward")
+    return rc
+
+
+# ---------------------------------------------------------------- layer norm (include/moe_layernorm.h)
+
+# MoeLayernormArgs and MoeLayernormGrads as bytes
+_LAYERNORM_ARGS = struct.Struct("@IiifqqPqPqPPPqPq")
+_LAYERNORM_GRADS = struct.Struct("@IiifqqPqPPqPqPqPPPN")
+assert (_LAYERNORM_ARGS.size, _LAYERNORM_GRADS.size) == (ctypes.sizeof(MoeLayernormArgs), ctypes.sizeof(MoeLayernormGrads))
+
+
+def _column_weights(H: int, *weights):
+    """The type code and pointers of contiguous [H] weights of one type (None: 0); None if they are not."""
+    given = [w for w in weights if w is not None]
+    kind = _DTYPES.get(given[0].dtype) if given else F32
+    if kind is None or any(w.dtype is not given[0].dtype or w.shape != (H,) or not w.is_contiguous() for w in given):
+        return None
+    return kind, [0 if w is None else w.data_ptr() for w in weights]
+
+
+def moe_layernorm_forward(x: torch.Tensor, b: torch.Tensor, w: torch.Tensor, bias: torch.Tensor, s: torch.Tensor, n: torch.Tensor,
+                          eps: float = 1e-5, stream=None, check=True) -> int:
+    """s = x + b, n = the layer norm of s with w and bias ([H], either type); b and s (both), w and bias may be None.  x and s
+    [T, H] bf16 or float32, b and n bf16."""
+    dtype, xt = x.dtype, _DTYPES.get(x.dtype)
+    shape = tuple(x.shape)
+    ok = xt is not None and x.dim() == 2
+    columns = _column_weights(shape[1], w, bias) if ok else None
+    if columns is None:
+        return _invalid("moe_layernorm_forward", check)
+    xr, nr = _rows(x, shape, dtype), _rows(n, shape)
+    br = _NONE if b is None else _rows(b, shape)
+    sr = _NONE if s is None else _rows(s, shape, dtype)
+    if None in (xr, nr, br, sr) or not _on_current_device(x, b, w, bias, s, n):
+        return _invalid("moe_layernorm_forward", check)
+    a = _LAYERNORM_ARGS.pack(_LAYERNORM_ARGS.size, xt, columns[0], eps, *shape, *xr, *br, *columns[1], *sr, *nr)
+    rc = lib.moe_layernorm_forward(a, _stream(stream))
+    if check:
+        _check(rc, "moe_layernorm_forward")
+    return rc
+
+
+def moe_layernorm_workspace_size(T: int, H: int) -> int:
+    return int(lib.moe_layernorm_workspace_size(T, H))
+
+
+def moe_layernorm_backward(s: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, ds: torch.Tensor, workspace: torch.Tensor,
+                           dx: torch.Tensor = None, dw: torch.Tensor = None, dbias: torch.Tensor = None, eps: float = 1e-5,
+                           stream=None, check=True) -> int:
+    """Gradients of moe_layernorm_forward from dn and (or None) ds; s is its s (without b: its x).  Outputs that are None
+    are not computed; dx is of s's type, dw and dbias float32 [H]."""
+    dtype, xt = s.dtype, _DTYPES.get(s.dtype)
+    shape = tuple(s.shape)
+    ok = xt is not None and s.dim() == 2
+    columns = _column_weights(shape[1], w) if ok else None
+    if columns is None:
+        return _invalid("moe_layernorm_backward", check)
+    sr, dnr = _rows(s, shape, dtype), _rows(dn, shape)
+    dsr = _NONE if ds is None else _rows(ds, shape, dtype)
+    dxr = _NONE if dx is None else _rows(dx, shape, dtype)
+    pw, pb = _column_sum(dw, shape[1]), _column_sum(dbias, shape[1])
+    if None in (sr, dnr, dsr, dxr, pw, pb) or not workspace.is_contiguous() or \
+            not _on_current_device(s, w, dn, ds, workspace, dx, dw, dbias):
+        return _invalid("moe_layernorm_backward", check)
+    a = _LAYERNORM_GRADS.pack(_LAYERNORM_GRADS.size, xt, columns[0], eps, *shape, *sr, columns[1][0], *dnr, *dsr, *dxr, pw, pb,
+                              workspace.data_ptr(), workspace.nbytes)
+    rc = lib.moe_layernorm_backward(a, _stream(stream))
+    if check:
+        _check(rc, "moe_layernorm_backward")
     return rc
 
 

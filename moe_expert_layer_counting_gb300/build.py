@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mxq.so")
 SOURCES = ["quant.cu", "route.cu", "permute.cu", "permute_noalloc.cu", "gemm.cu", "gemm2sm.cu", "combine.cu", "api.cu", "bfp8.cu",
            "grouped.cu", "gated.cu", "norm.cu", "adamw.cu",
-           "muon.cu"]
+           "muon.cu", "layernorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

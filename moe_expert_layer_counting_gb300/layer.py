@@ -218,6 +218,38 @@ class BlockNorm:
         return next((code for code in (B.moe_get_device_status(w, stream) for w in words) if code), B.MOE_OK)
 
 
+class LayerNorm:
+    """Layer norm with the residual stream's addition, forward and backward (include/moe_layernorm.h): s = x + b,
+    n = (s - mean) rsqrt(var + eps) weight + bias.
+
+    weight and bias: [H], both bf16 or both float32, either may be None.  Outputs and the backward call's workspace are new
+    tensors of each call; the object keeps nothing but its weights.
+    """
+
+    def __init__(self, weight: torch.Tensor = None, bias: torch.Tensor = None, eps: float = 1e-5):
+        self.weight, self.bias, self.eps = weight, bias, eps
+
+    def forward(self, x: torch.Tensor, b: torch.Tensor = None, stream=None):
+        """(s, n): the stream with the last layer's answer b (without it: x itself) and its norm, the next layer's input."""
+        with _on(stream):
+            flat = torch.contiguous_format
+            s = None if b is None else torch.empty_like(x, memory_format=flat)
+            n = torch.empty_like(x, dtype=torch.bfloat16, memory_format=flat)
+            B.moe_layernorm_forward(x, b, self.weight, self.bias, s, n, self.eps, B._stream(stream))
+        return (x if s is None else s), n
+
+    def backward(self, s: torch.Tensor, dn: torch.Tensor, ds: torch.Tensor = None, stream=None) -> dict:
+        """Gradients dx (x's and, rounded to its type, b's), dw and dbias (float32; None where there is no weight or bias)
+        from those of forward's n and, where the stream goes on, of its s."""
+        with _on(stream):
+            dx = torch.empty_like(s, memory_format=torch.contiguous_format)
+            dw = None if self.weight is None else torch.empty_like(self.weight, dtype=torch.float32)
+            dbias = None if self.bias is None else torch.empty_like(self.bias, dtype=torch.float32)
+            ws = s.new_empty(B.moe_layernorm_workspace_size(*s.shape), dtype=torch.uint8)
+            B.moe_layernorm_backward(s, self.weight, dn, ds, ws, dx, dw, dbias, self.eps, B._stream(stream))
+        return {"dx": dx, "dw": dw, "dbias": dbias}
+
+
 def _capturing(stream) -> bool:
     if not torch.cuda.is_initialized():
         return False
