@@ -1,19 +1,22 @@
 // layernorm.cu -- layer norm with the residual stream's addition, and its
 // gradients (include/moe_layernorm.h).
 //
-// Both directions are bound by HBM: every value is read once and written once.
-// A group of ceil(H / 512) warps owns a row at a time, a thread two runs of
-// eight columns; groups walk the rows with a stride of all groups.  A thread
-// copies (cp.async) its own columns of the rows to come into its own places in
-// shared memory, so that the ring needs no barrier: it waits for its own copies,
-// takes them into registers, and sends the places' next copies on their way
-// before the row's first sum.  The mean comes first and the squares of what is
-// left after it second, both from registers: two sums a row over the group, in
-// the gradients one and three.  Arithmetic is on pairs (f32x2).
-//
+// Both directions are bound by HBM if the SM keeps up: every value is read once
+// and written once, but a row needs its mean, then the squares of what is left
+// after it (and two sums of gradients), and ~20 operations a value.
+//   - A group of ceil(H / 512) warps owns a row at a time (two in the gradients),
+//     a thread sixteen columns; groups walk the rows with a stride of all groups.
+//   - A thread copies (cp.async) its own columns of the rows to come into its own
+//     places in shared memory: the ring needs no barrier, only a wait for the
+//     thread's own copies, and values are read from it again for each of a row's
+//     steps, so that registers are left for the column sums.
+//   - Arithmetic is on pairs (f32x2).
 // The gradients' column sums are kept in registers over a block's rows, joined
 // over its groups in shared memory, written as one part for each block and
 // summed over the blocks, in a fixed order, by a second kernel.
+// Measured (BF16, H = 7168): s and n of 8192 rows in 75 us (6.3 TB/s), of 4096 in 39;
+// the gradients joined with ds of 8192 rows in 89 us (5.3 TB/s), of 4096 in 51, of which ~14 are the
+// launch's start, its end, and the parts.  float32 rows: 123 us (5.7 TB/s) and 129 (6.4).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -24,13 +27,13 @@
 #include "host_common.h"
 #include "pairs.cuh"
 #include "ptx.cuh"
+#include "row_sums.cuh"
 
 namespace mxq {
 
 namespace {
 
 constexpr int kMostH = 16384;
-constexpr int kBlock = 512;               // threads of a block where a row's group is no larger
 
 struct Rows {
   int64_t T;
@@ -47,86 +50,90 @@ struct Rows {
   float *part;                            // gradients: [blocks][2][H], or NULL
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 16-byte pieces of a run of eight values.
-template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 1 : 2;
+// A thread's columns are runs of eight (BF16 rows) or four (float32 rows) of
+// them, run r of thread t at column run * (r * threads of a group + t): 16 bytes a
+// run of the rows' type, so that a warp's access is 512 bytes without gaps
+// (with runs of eight float32 values: 157 instead of 132 us forward and 201 instead
+// of 129 us for the gradients of 8192 x 7168).
+template <typename XT> constexpr int kRun = 16 / sizeof(XT);
+constexpr int kColumns = 16;              // of a thread
 
-template <typename T>
-__device__ __forceinline__ void take8(const uint4 *place, int threads, P2 (&v)[4]) {
-  const uint4 a = place[0];
-  if (sizeof(T) == 2) {
+// BF16: a run of eight, or of four beside float32 rows.
+template <int RUN>
+__device__ __forceinline__ void copy_run(uint32_t dst, const uint16_t *src) {
+  if (RUN == 8)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int RUN>
+__device__ __forceinline__ void copy_run(uint32_t dst, const float *src) {
+  static_assert(RUN == 4, "16 bytes");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int RUN>
+__device__ __forceinline__ void take(const uint16_t *p, P2 (&v)[RUN / 2]) {
+  if (RUN == 8) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
     v[0] = from_bf16x2(a.x);
     v[1] = from_bf16x2(a.y);
-    v[2] = from_bf16x2(a.z);
-    v[3] = from_bf16x2(a.w);
+    v[2 % (RUN / 2)] = from_bf16x2(a.z);
+    v[3 % (RUN / 2)] = from_bf16x2(a.w);
   } else {
-    const uint4 b = place[threads];
-    v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
-    v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
-    v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
-    v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    v[0] = from_bf16x2(a.x);
+    v[1] = from_bf16x2(a.y);
+  }
+}
+template <int RUN>
+__device__ __forceinline__ void take(const float *p, P2 (&v)[RUN / 2]) {
+#pragma unroll
+  for (int i = 0; i < RUN / 4; ++i) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[i];
+    v[2 * i] = pair(a.x, a.y);
+    v[2 * i + 1] = pair(a.z, a.w);
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void put8(T *p, const P2 (&v)[4]) {
-  if (sizeof(T) == 2) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
-  } else {
-    const float2 a = split(v[0]), b = split(v[1]), c = split(v[2]), d = split(v[3]);
-    reinterpret_cast<float4 *>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+template <int RUN>
+__device__ __forceinline__ void put(uint16_t *p, const P2 (&v)[RUN / 2]) {
+  if (RUN == 8)
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2 % (RUN / 2)]), to_bf16x2(v[3 % (RUN / 2)]));
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
+}
+template <int RUN>
+__device__ __forceinline__ void put(float *p, const P2 (&v)[RUN / 2]) {
+#pragma unroll
+  for (int i = 0; i < RUN / 4; ++i) {
+    const float2 a = split(v[2 * i]), b = split(v[2 * i + 1]);
+    reinterpret_cast<float4 *>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
   }
 }
 
-// Eight values of a weight of either type.
-__device__ __forceinline__ void weight8(const void *w, int dtype, int col, P2 (&v)[4]) {
-  if (dtype == MOE_BF16) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + col));
-    v[0] = from_bf16x2(q.x);
-    v[1] = from_bf16x2(q.y);
-    v[2] = from_bf16x2(q.z);
-    v[3] = from_bf16x2(q.w);
-  } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + col);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = pair(a.x, a.y);
-    v[1] = pair(a.z, a.w);
-    v[2] = pair(b.x, b.y);
-    v[3] = pair(b.z, b.w);
-  }
+// A run of a weight of either type (the same branch for the whole launch).
+template <int RUN>
+__device__ __forceinline__ void weight(const void *w, int dtype, int col, P2 (&v)[RUN / 2]) {
+  if (dtype == MOE_BF16)
+    take<RUN>(static_cast<const uint16_t *>(w) + col, v);
+  else
+    take<RUN>(static_cast<const float *>(w) + col, v);
 }
 
-// Sums over the group, the same bits in every thread.  `red`: of this group and
-// of this place in a row (a place's words are written again only after the row's
-// other sum, whose barrier every reader has passed by then).
 template <int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], int warps, int group, float (*red)[N]) {
-  const int lane = (int)(threadIdx.x & 31);
+__device__ __forceinline__ P2 sum_of(const P2 (&v)[N]) {
+  P2 s = v[0] + v[1];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (warps == 1) return;
-  const int warp = (int)(threadIdx.x >> 5) - group * warps;
-  if (lane == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) red[warp][k] = v[k];
-  named_bar_sync(1 + group, 32 * warps);
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = lane < warps ? red[lane][k] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  for (int i = 2; i < N; i += 2) s = s + (v[i] + v[i + 1]);
+  return s;
 }
 
 __device__ __forceinline__ float both(P2 v) {
@@ -136,216 +143,388 @@ __device__ __forceinline__ float both(P2 v) {
 
 // ---------------------------------------------------------------- forward
 
-template <typename XT, bool ADD>
-__global__ void __launch_bounds__(1024, 1) layernorm_kernel(const Rows z) {
-  constexpr int kP = kPieces<XT>, kPer = 2 * kP + (ADD ? 2 : 0), kDepth = 2;
-  extern __shared__ __align__(16) uint4 ring[];              // [depth][piece][thread]
-  __shared__ float red[2][32][1];
+// How the forward kernel goes about a launch: kRows rows of a group in work
+// together, kSets sets of them in the ring (the next set's sum is added up with
+// this one's squares: one exchange a set, and the sets after it are on their way).
+// A row at a time and a deep ring, but for the shortest rows (BF16 without b), whose
+// sums take longer than their bytes: 8192 x 7168 in 47 us by twos and 55 one by one;
+// with b 84 by twos and 75 one by one.
+//   BIG   rows of more than 8192 columns: 1024 threads of 64 registers, a row at a time, weights from L1.
+template <typename XT, bool ADD, bool BIG>
+struct ForwardRing {
+  static constexpr int kSlot = kColumns * (int)(sizeof(XT) + (ADD ? 2 : 0));       // bytes of a thread's part of a row
+  static constexpr int kThreads = BIG ? 1024 : 512;
+  static constexpr int kRows = BIG || kSlot >= 64 ? 1 : 2;
+  static constexpr int kSets = BIG ? (kSlot > 64 ? 2 : 3) : kSlot > 64 ? 4 : kSlot == 64 ? 6 : 3;
+  static constexpr int kRed = 2 * 128 * 4;                   // bytes of a group's sums
+  static size_t bytes(int threads, int tpr) {
+    return (size_t)kSlot * kRows * kSets * threads + (size_t)(threads / tpr) * kRed;
+  }
+};
+
+template <typename XT, bool ADD, bool BIG>
+__global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layernorm_kernel(const Rows z) {
+  using R = ForwardRing<XT, ADD, BIG>;
+  constexpr int RUN = kRun<XT>, kRuns = kColumns / RUN, kRows = R::kRows, kSets = R::kSets;
+  extern __shared__ __align__(16) unsigned char ring[];      // [kSets][kRows] of [run][thread] of x, the same of b; sums
   const int threads = (int)blockDim.x, tpr = 32 * z.warps;
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
-  const int col[2] = {8 * t, 8 * (tpr + t)};
-  const bool has[2] = {col[0] < z.H, col[1] < z.H};
-  uint4 *mine = ring + threadIdx.x;
-  const uint32_t at = smem_u32(mine);
-  const int64_t first = (int64_t)blockIdx.x * z.groups + group, stride = (int64_t)gridDim.x * z.groups;
+  const int64_t stride = (int64_t)gridDim.x * z.groups;
+  int64_t row = (int64_t)blockIdx.x * z.groups + group;
+  float *red = reinterpret_cast<float *>(ring + kSets * kRows * R::kSlot * threads) + group * (R::kRed / 4);
+  if (z.warps > 1) {
+    for (int i = t; i < R::kRed / 4; i += tpr) red[i] = 0.f;         // of warps that the group has not
+    __syncthreads();
+  }
+  auto col = [&](int r) { return RUN * (r * tpr + t); };
+  const uint32_t at = smem_u32(ring);
+  // where run r of x and b lies in a slot
+  auto of_x = [&](int slot, int r) { return slot * R::kSlot * threads + (r * threads + (int)threadIdx.x) * 16; };
+  auto of_b = [&](int slot, int r) {
+    return (slot * R::kSlot + kColumns * (int)sizeof(XT)) * threads + (r * threads + (int)threadIdx.x) * 2 * RUN;
+  };
   pdl_launch_dependents();
   pdl_wait();
-  auto send = [&](int64_t row, int slot) {
-    if (row < z.T) {
+  auto send = [&](int64_t to_row, int set) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (has[c]) {
-          const XT *x = static_cast<const XT *>(z.x) + row * z.ldx + col[c];
-          const uint32_t to = at + (uint32_t)(slot * kPer * threads) * 16;
+    for (int j = 0; j < kRows; ++j, to_row += stride)
+      if (to_row < z.T) {
 #pragma unroll
-          for (int p = 0; p < kP; ++p) copy16(to + (uint32_t)((c * kP + p) * threads) * 16, reinterpret_cast<const uint4 *>(x) + p);
-          if (ADD) copy16(to + (uint32_t)((2 * kP + c) * threads) * 16, z.b + row * z.ldb + col[c]);
-        }
-    }
+        for (int r = 0; r < kRuns; ++r)
+          if (col(r) < z.H) {
+            copy_run<RUN>(at + of_x(set * kRows + j, r), static_cast<const XT *>(z.x) + to_row * z.ldx + col(r));
+            if (ADD) copy_run<RUN>(at + of_b(set * kRows + j, r), z.b + to_row * z.ldb + col(r));
+          }
+      }
     copies_commit();
   };
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) send(first + d * stride, d);
-  int slot = 0;
-  for (int64_t row = first; row < z.T; row += stride) {
-    copies_wait<kDepth - 1>();
-    P2 v[2][4];
-    const uint4 *place = mine + slot * kPer * threads;
+  for (int i = 0; i < kSets; ++i) send(row + i * kRows * stride, i);
+  P2 w[BIG ? 1 : kRuns][RUN / 2], bias[BIG ? 1 : kRuns][RUN / 2];
+  if (!BIG) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (has[c]) {
-        take8<XT>(place + c * kP * threads, threads, v[c]);
-        if (ADD) {
-          P2 b[4];
-          take8<uint16_t>(place + (2 * kP + c) * threads, threads, b);
+    for (int r = 0; r < kRuns; ++r) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[c][i] = v[c][i] + b[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = twice(0.f);
+      for (int i = 0; i < RUN / 2; ++i) {
+        w[BIG ? 0 : r][i] = twice(1.f);
+        bias[BIG ? 0 : r][i] = twice(0.f);
       }
+      if (z.w && col(r) < z.H) weight<RUN>(z.w, z.w_dtype, col(r), w[BIG ? 0 : r]);
+      if (z.bias && col(r) < z.H) weight<RUN>(z.bias, z.w_dtype, col(r), bias[BIG ? 0 : r]);
     }
-    send(row + kDepth * stride, slot);
-    slot ^= 1;
-    if (ADD && z.s) {
+  }
+  // run r of the row in a slot
+  auto take_run = [&](int slot, int r, P2 (&v)[RUN / 2]) {
+    take<RUN>(reinterpret_cast<const XT *>(ring + of_x(slot, r)), v);
+    if (ADD) {
+      P2 b[RUN / 2];
+      take<RUN>(reinterpret_cast<const uint16_t *>(ring + of_b(slot, r)), b);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (has[c]) put8<XT>(static_cast<XT *>(z.s) + row * z.lds + col[c], v[c]);
+      for (int i = 0; i < RUN / 2; ++i) v[i] = v[i] + b[i];
     }
-    float sum[1] = {both(((v[0][0] + v[0][1]) + (v[0][2] + v[0][3])) + ((v[1][0] + v[1][1]) + (v[1][2] + v[1][3])))};
-    group_sums<1>(sum, z.warps, group, red[0] + (z.warps > 1 ? group * z.warps : 0));
-    const P2 mean = twice(-sum[0] * z.inv_h);
-    P2 sq = twice(0.f);
+  };
+  auto sum_row = [&](int slot) {
+    P2 sum = twice(0.f);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[c][i] = v[c][i] + mean;
-        if (has[c]) sq = fma2(v[c][i], v[c][i], sq);
+    for (int r = 0; r < kRuns; ++r)
+      if (col(r) < z.H) {
+        P2 v[RUN / 2];
+        take_run(slot, r, v);
+        sum = sum + sum_of(v);
       }
-    sum[0] = both(sq);
-    group_sums<1>(sum, z.warps, group, red[1] + (z.warps > 1 ? group * z.warps : 0));
-    const P2 r = twice(rsqrtf(fmaf(sum[0], z.inv_h, z.eps)));
+    return both(sum);
+  };
+  auto join = [&] {
+    if (z.warps > 1)
+      named_bar_sync(1 + group, 32 * z.warps);
+    else
+      __syncwarp();
+  };
+  copies_wait<kSets - 1>();
+  float total[kRows];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (has[c]) {
+  for (int j = 0; j < kRows; ++j) total[j] = row + j * stride < z.T ? sum_row(j) : 0.f;
+  group_sum(total, z.warps, t >> 5, red, join);
+  int set = 0, turn = 0;
+  for (; row < z.T; row += kRows * stride) {
+    const int after = set + 1 == kSets ? 0 : set + 1;
+    P2 v[kRows][kRuns][RUN / 2];
+    float sum[2 * kRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = v[c][i] * r;
-        P2 w[4];
-        if (z.w) {
-          weight8(z.w, z.w_dtype, col[c], w);
+    for (int j = 0; j < kRows; ++j) {
+      const P2 mean = twice(-total[j] * z.inv_h);
+      P2 sq = twice(0.f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[c][i] = v[c][i] * w[i];
+      for (int r = 0; r < kRuns; ++r)
+        if (col(r) < z.H) {
+          P2(&u)[RUN / 2] = v[j][r];
+          take_run(set * kRows + j, r, u);
+          if (ADD && z.s && (j == 0 || row + j * stride < z.T))
+            put<RUN>(static_cast<XT *>(z.s) + (row + j * stride) * z.lds + col(r), u);
+#pragma unroll
+          for (int i = 0; i < RUN / 2; ++i) {
+            u[i] = u[i] + mean;
+            sq = fma2(u[i], u[i], sq);
+          }
         }
-        if (z.bias) {
-          weight8(z.bias, z.w_dtype, col[c], w);
+      sum[j] = both(sq);
+    }
+    copies_wait<kSets - 2>();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[c][i] = v[c][i] + w[i];
+    for (int j = 0; j < kRows; ++j)
+      sum[kRows + j] = row + (kRows + j) * stride < z.T ? sum_row(after * kRows + j) : 0.f;
+    turn ^= 1;                                               // a buffer is written again after the other's barrier
+    group_sum(sum, z.warps, t >> 5, red + turn * 128, join);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      total[j] = sum[kRows + j];
+      if (j > 0 && row + j * stride >= z.T) continue;
+      const P2 rr = twice(rsqrtf(fmaf(sum[j], z.inv_h, z.eps)));
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+        if (col(r) < z.H) {
+          P2(&u)[RUN / 2] = v[j][r];
+          if (BIG) {
+            P2 c[RUN / 2];
+#pragma unroll
+            for (int i = 0; i < RUN / 2; ++i) u[i] = u[i] * rr;
+            if (z.w) {
+              weight<RUN>(z.w, z.w_dtype, col(r), c);
+#pragma unroll
+              for (int i = 0; i < RUN / 2; ++i) u[i] = u[i] * c[i];
+            }
+            if (z.bias) {
+              weight<RUN>(z.bias, z.w_dtype, col(r), c);
+#pragma unroll
+              for (int i = 0; i < RUN / 2; ++i) u[i] = u[i] + c[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < RUN / 2; ++i) u[i] = fma2(u[i] * rr, w[BIG ? 0 : r][i], bias[BIG ? 0 : r][i]);
+          }
+          put<RUN>(z.n + (row + j * stride) * z.ldn + col(r), u);
         }
-        put8<uint16_t>(z.n + row * z.ldn + col[c], v[c]);
-      }
+    }
+    send(row + kSets * kRows * stride, set);
+    set = after;
   }
 }
 
 // ---------------------------------------------------------------- gradients
 
-// BIG: rows of more than 8192 columns, 64 registers a thread.
+// How the gradients' kernel goes about a launch.
+//   kRows  rows of a group in work together: two, so that one's exchange and loads hide behind the other's
+//          arithmetic (a block's 16 warps are all that fit: 32 column sums in registers); one where the ring
+//          does not hold twice two.  4096 x 7168 in 51 us; 80 one by one, 75 with two blocks' worth of warps
+//          at 72 registers.
+//   BIG    rows of more than 8192 columns: 1024 threads of 64 registers, weights from L1, and float32 ds from
+//          memory, as two slots do not fit with them.
 template <typename XT, bool DS, bool BIG>
-__global__ void __launch_bounds__(BIG ? 1024 : kBlock, 1) layernorm_grad_kernel(const Rows z) {
-  constexpr int kP = kPieces<XT>, kPer = 2 * kP + 2 + (DS ? 2 * kP : 0), kDepth = BIG && sizeof(XT) == 4 ? 1 : 2;
-  extern __shared__ __align__(16) uint4 ring[];              // [depth][piece][thread]; at the end [2][H] floats
-  __shared__ float red1[32][1], red3[32][3];
+struct GradRing {
+  static constexpr bool kDs = DS && !(BIG && sizeof(XT) == 4), kSharedW = !BIG;
+  static constexpr int kSlot = kColumns * (int)(sizeof(XT) * (kDs ? 2 : 1) + 2);   // bytes of a thread's part of a row
+  static constexpr int kThreads = BIG ? 1024 : 512, kRows = BIG || kSlot > 96 ? 1 : 2;
+  static constexpr int kRed = 2 * 8 * 32 * 4;                // bytes of a group's sums
+  static size_t bytes(int threads, int tpr) {
+    return (size_t)kSlot * 2 * kRows * threads + (kSharedW ? 4 * kColumns * tpr : 0) + (size_t)(threads / tpr) * kRed;
+  }
+};
+
+template <typename XT, bool DS, bool BIG>
+__global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_grad_kernel(const Rows z) {
+  using R = GradRing<XT, DS, BIG>;
+  constexpr int RUN = kRun<XT>, kRuns = kColumns / RUN, kRows = R::kRows;
+  // [2][kRows] of [run][thread] of s, the same of dn and ds; w [run][thread of a group] in float32; the groups' sums.
+  // At the end [2][H] floats.
+  extern __shared__ __align__(16) unsigned char ring[];
   const int threads = (int)blockDim.x, tpr = 32 * z.warps;
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
-  const int col[2] = {8 * t, 8 * (tpr + t)};
-  const bool has[2] = {col[0] < z.H, col[1] < z.H};
-  uint4 *mine = ring + threadIdx.x;
-  const uint32_t at = smem_u32(mine);
-  const int64_t first = (int64_t)blockIdx.x * z.groups + group, stride = (int64_t)gridDim.x * z.groups;
-  const int of_group = z.warps > 1 ? group * z.warps : 0;
+  const int64_t stride = (int64_t)gridDim.x * z.groups;
+  int64_t row = (int64_t)blockIdx.x * z.groups + group;
+  float *const weights = reinterpret_cast<float *>(ring + 2 * kRows * R::kSlot * threads);
+  float *red = weights + (R::kSharedW ? kColumns * tpr : 0) + group * (R::kRed / 4);
+  const uint32_t at = smem_u32(ring);
+  auto col = [&](int r) { return RUN * (r * tpr + t); };
+  auto of_s = [&](int slot, int r) { return slot * R::kSlot * threads + (r * threads + (int)threadIdx.x) * 16; };
+  auto of_dn = [&](int slot, int r) {
+    return (slot * R::kSlot + kColumns * (int)sizeof(XT)) * threads + (r * threads + (int)threadIdx.x) * 2 * RUN;
+  };
+  auto of_ds = [&](int slot, int r) {
+    return (slot * R::kSlot + kColumns * (int)(sizeof(XT) + 2)) * threads + (r * threads + (int)threadIdx.x) * 16;
+  };
+  if (z.warps > 1)
+    for (int i = t; i < R::kRed / 4; i += tpr) red[i] = 0.f;         // of warps that the group has not
   pdl_launch_dependents();
   pdl_wait();
-  auto send = [&](int64_t row, int slot) {
-    if (row < z.T) {
+  // rows to_row, to_row + stride, .. into half `half` of the ring
+  auto send = [&](int64_t to_row, int half) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (has[c]) {
-          const uint32_t to = at + (uint32_t)(slot * kPer * threads) * 16;
-          const XT *x = static_cast<const XT *>(z.x) + row * z.ldx + col[c];
+    for (int j = 0; j < kRows; ++j, to_row += stride)
+      if (to_row < z.T) {
 #pragma unroll
-          for (int p = 0; p < kP; ++p) copy16(to + (uint32_t)((c * kP + p) * threads) * 16, reinterpret_cast<const uint4 *>(x) + p);
-          copy16(to + (uint32_t)((2 * kP + c) * threads) * 16, z.b + row * z.ldb + col[c]);
-          if (DS) {
-            const XT *ds = static_cast<const XT *>(z.ds) + row * z.ld_ds + col[c];
-#pragma unroll
-            for (int p = 0; p < kP; ++p)
-              copy16(to + (uint32_t)((2 * kP + 2 + c * kP + p) * threads) * 16, reinterpret_cast<const uint4 *>(ds) + p);
+        for (int r = 0; r < kRuns; ++r)
+          if (col(r) < z.H) {
+            const int slot = half * kRows + j;
+            copy_run<RUN>(at + of_s(slot, r), static_cast<const XT *>(z.x) + to_row * z.ldx + col(r));
+            copy_run<RUN>(at + of_dn(slot, r), z.b + to_row * z.ldb + col(r));
+            if (R::kDs) copy_run<RUN>(at + of_ds(slot, r), static_cast<const XT *>(z.ds) + to_row * z.ld_ds + col(r));
           }
-        }
-    }
+      }
     copies_commit();
   };
+  send(row, 0);
+  send(row + kRows * stride, 1);
+  // a group's weights in float32 (1 without w), the same for all groups
+  if (R::kSharedW) {
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) send(first + d * stride, d);
-  P2 dw[2][4], db[2][4];
+    for (int r = 0; r < kRuns; ++r)
+      if (group == 0 && col(r) < z.H) {
+        P2 w[RUN / 2];
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+        for (int i = 0; i < RUN / 2; ++i) w[i] = twice(1.f);
+        if (z.w) weight<RUN>(z.w, z.w_dtype, col(r), w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = twice(0.f);
-  int slot = 0;
-  for (int64_t row = first; row < z.T; row += stride) {
-    copies_wait<kDepth - 1>();
-    P2 v[2][4], d[2][4], ds[DS ? 2 : 1][4];
-    const uint4 *place = mine + slot * kPer * threads;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (has[c]) {
-        take8<XT>(place + c * kP * threads, threads, v[c]);
-        take8<uint16_t>(place + (2 * kP + c) * threads, threads, d[c]);
-        if (DS) take8<XT>(place + (2 * kP + 2 + c * kP) * threads, threads, ds[DS ? c : 0]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = d[c][i] = ds[DS ? c : 0][i] = twice(0.f);
+        for (int i = 0; i < RUN / 4; ++i) {
+          const P2 two[2] = {w[2 * i], w[2 * i + 1]};
+          put<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
+        }
       }
+  }
+  __syncthreads();
+  auto take_w = [&](int r, P2 (&w)[RUN / 2]) {
+    if (R::kSharedW) {
+#pragma unroll
+      for (int i = 0; i < RUN / 4; ++i) {
+        P2 two[2];
+        take<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
+        w[2 * i] = two[0];
+        w[2 * i + 1] = two[1];
+      }
+    } else if (z.w) {
+      weight<RUN>(z.w, z.w_dtype, col(r), w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUN / 2; ++i) w[i] = twice(1.f);
     }
-    send(row + kDepth * stride, slot);
-    if (kDepth == 2) slot ^= 1;
-    float sum[1] = {both(((v[0][0] + v[0][1]) + (v[0][2] + v[0][3])) + ((v[1][0] + v[1][1]) + (v[1][2] + v[1][3])))};
-    group_sums<1>(sum, z.warps, group, red1 + of_group);
-    const P2 mean = twice(-sum[0] * z.inv_h);
-    P2 sq = twice(0.f), sg = twice(0.f), sgv = twice(0.f);
+  };
+  auto join = [&] {
+    if (z.warps > 1)
+      named_bar_sync(1 + group, 32 * z.warps);
+    else
+      __syncwarp();
+  };
+  P2 dw[kRuns][RUN / 2], db[kRuns][RUN / 2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (has[c]) {
-        P2 w[4];
-        if (z.w) weight8(z.w, z.w_dtype, col[c], w);
+  for (int r = 0; r < kRuns; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[c][i] = v[c][i] + mean;
-          const P2 g = z.w ? d[c][i] * w[i] : d[c][i];
-          sq = fma2(v[c][i], v[c][i], sq);
-          sg = sg + g;
-          sgv = fma2(g, v[c][i], sgv);
+    for (int i = 0; i < RUN / 2; ++i) dw[r][i] = db[r][i] = twice(0.f);
+  // a row's sums go through two buffers, each written again after the other's barrier
+  for (int half = 0; row < z.T; half ^= 1) {
+    const bool whole = kRows == 1 || row + stride < z.T;     // both rows are there
+    copies_wait<1>();
+    float sum[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      P2 s = twice(0.f);
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+        if (col(r) < z.H) {
+          P2 v[RUN / 2];
+          take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
+          s = s + sum_of(v);
+        }
+      sum[j] = both(s);
+    }
+    group_sum(sum, z.warps, t >> 5, red, join);
+    P2 mean[kRows], sq[kRows], sg[kRows], sgv[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      mean[j] = twice(-sum[j] * z.inv_h);
+      sq[j] = sg[j] = sgv[j] = twice(0.f);
+    }
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+      if (col(r) < z.H) {
+        P2 w[RUN / 2];
+        take_w(r, w);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          P2 v[RUN / 2], d[RUN / 2];
+          take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
+          take<RUN>(reinterpret_cast<const uint16_t *>(ring + of_dn(half * kRows + j, r)), d);
+#pragma unroll
+          for (int i = 0; i < RUN / 2; ++i) {
+            v[i] = v[i] + mean[j];
+            const P2 g = d[i] * w[i];
+            sq[j] = fma2(v[i], v[i], sq[j]);
+            sg[j] = sg[j] + g;
+            sgv[j] = fma2(g, v[i], sgv[j]);
+          }
         }
       }
-    float sums[3] = {both(sq), both(sg), both(sgv)};
-    group_sums<3>(sums, z.warps, group, red3 + of_group);
-    const float r = rsqrtf(fmaf(sums[0], z.inv_h, z.eps));
+    float sums[kRows][3];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      sums[j][0] = both(sq[j]);
+      sums[j][1] = both(sg[j]);
+      sums[j][2] = both(sgv[j]);
+    }
+    group_sums(sums, z.warps, t >> 5, red + 256, join);
     // dx = ds + r (g - mean(g)) - (v r) (r mean(g v) r): factor by factor, so that no power of a row's magnitude is formed
-    const P2 rr = twice(r), mg = twice(-sums[1] * z.inv_h), mgh = twice(-(sums[2] * r) * z.inv_h);
+    P2 rr[kRows], mg[kRows], mgh[kRows];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (has[c]) {
-        P2 w[4], out[4];
-        if (z.w) weight8(z.w, z.w_dtype, col[c], w);
+    for (int j = 0; j < kRows; ++j) {
+      const float q = rsqrtf(fmaf(sums[j][0], z.inv_h, z.eps));
+      rr[j] = twice(q);
+      mg[j] = twice(-sums[j][1] * z.inv_h);
+      mgh[j] = twice(-(sums[j][2] * q) * z.inv_h);
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const P2 h = v[c][i] * rr;
-          const P2 g = z.w ? d[c][i] * w[i] : d[c][i];
-          dw[c][i] = fma2(d[c][i], h, dw[c][i]);
-          db[c][i] = db[c][i] + d[c][i];
-          const P2 a = fma2(h, mgh, g + mg);
-          out[i] = DS ? fma2(a, rr, ds[DS ? c : 0][i]) : a * rr;
+    for (int r = 0; r < kRuns; ++r)
+      if (col(r) < z.H) {
+        P2 w[RUN / 2];
+        take_w(r, w);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          if (j > 0 && !whole) break;
+          P2 v[RUN / 2], d[RUN / 2], ds[RUN / 2], out[RUN / 2];
+          take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
+          take<RUN>(reinterpret_cast<const uint16_t *>(ring + of_dn(half * kRows + j, r)), d);
+          if (R::kDs)
+            take<RUN>(reinterpret_cast<const XT *>(ring + of_ds(half * kRows + j, r)), ds);
+          else if (DS)
+            take<RUN>(static_cast<const XT *>(z.ds) + (row + j * stride) * z.ld_ds + col(r), ds);
+#pragma unroll
+          for (int i = 0; i < RUN / 2; ++i) {
+            const P2 h = (v[i] + mean[j]) * rr[j];
+            const P2 g = d[i] * w[i];
+            dw[r][i] = fma2(d[i], h, dw[r][i]);
+            db[r][i] = db[r][i] + d[i];
+            const P2 a = fma2(h, mgh[j], g + mg[j]);
+            out[i] = DS ? fma2(a, rr[j], ds[i]) : a * rr[j];
+          }
+          if (z.s) put<RUN>(static_cast<XT *>(z.s) + (row + j * stride) * z.lds + col(r), out);
         }
-        if (z.s) put8<XT>(static_cast<XT *>(z.s) + row * z.lds + col[c], out);
       }
+    row += kRows * stride;
+    send(row + kRows * stride, half);
   }
   if (!z.part) return;
   // the groups' sums, joined in their order
   copies_wait<0>();
   __syncthreads();
   float *sums = reinterpret_cast<float *>(ring);
-  for (int k = 0; k < z.groups; ++k) {
-    if (group == k)
+  for (int n = 0; n < z.groups; ++n) {
+    if (group == n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (has[c])
+      for (int r = 0; r < kRuns; ++r)
+        if (col(r) < z.H)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 *pw = reinterpret_cast<float2 *>(sums + col[c]) + i, *pb = reinterpret_cast<float2 *>(sums + z.H + col[c]) + i;
-            float2 a = split(dw[c][i]), b = split(db[c][i]);
-            if (k > 0) {
+          for (int i = 0; i < RUN / 2; ++i) {
+            float2 *pw = reinterpret_cast<float2 *>(sums + col(r)) + i;
+            float2 *pb = reinterpret_cast<float2 *>(sums + z.H + col(r)) + i;
+            float2 a = split(dw[r][i]), b = split(db[r][i]);
+            if (n > 0) {
               a.x += pw->x;
               a.y += pw->y;
               b.x += pb->x;
@@ -383,10 +562,9 @@ __global__ void __launch_bounds__(256) sum_blocks_kernel(const float *part, int 
 // ---------------------------------------------------------------- host
 
 int warps_of(int64_t H) { return (int)ceil_div(H, 512); }
-int groups_of(int64_t H) { return std::max(1, kBlock / (32 * warps_of(H))); }
-// Blocks of the gradients' kernel: one for each SM, its rows' column sums in its registers.
-constexpr int64_t kMostParts = 256;
-int64_t grad_blocks(int64_t T, int64_t H) { return std::min({kMostParts, (int64_t)num_sms(), ceil_div(T, groups_of(H))}); }
+// Groups of a block of at most `threads`.
+int groups_of(int64_t H, int threads) { return std::max(1, threads / (32 * warps_of(H))); }
+constexpr int64_t kMostParts = 256;       // blocks of the gradients' kernel, one for each SM, at most
 
 int check_rows_of(const void *p, int64_t ld, int64_t H) {
   if (!p || ld < H) return MOE_ERR_INVALID_ARG;
@@ -401,9 +579,10 @@ int check_sizes(int64_t T, int64_t H, int32_t x_dtype, int32_t w_dtype, float ep
   return H % 8 != 0 || H > kMostH || T > 0x7fffffffffLL ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
 }
 
+constexpr int kMostSmem = 227 * 1024;     // of a block
+
 template <auto KERNEL>
-int launch_rows(const Rows &z, int64_t blocks, int pieces_deep, size_t least_smem, cudaStream_t st) {
-  constexpr int kMostSmem = 230 * 1024 - 4096;               // beside the kernels' static words
+int launch_rows(const Rows &z, int64_t blocks, size_t smem, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};                     // devices whose kernel attribute is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -412,9 +591,7 @@ int launch_rows(const Rows &z, int64_t blocks, int pieces_deep, size_t least_sme
     if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess) return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  const int threads = 32 * z.warps * z.groups;
-  const size_t smem = std::max((size_t)pieces_deep * threads * 16, least_smem);
-  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3((unsigned)threads), smem, st, z);
+  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3((unsigned)(32 * z.warps * z.groups)), smem, st, z);
 }
 
 }  // namespace
@@ -442,7 +619,6 @@ extern "C" int moe_layernorm_forward(const moe_layernorm_args *a, cudaStream_t s
   z.T = a->T;
   z.H = (int)a->H;
   z.warps = warps_of(a->H);
-  z.groups = groups_of(a->H);
   z.w_dtype = a->w_dtype;
   z.eps = a->eps;
   z.inv_h = 1.f / (float)a->H;
@@ -456,14 +632,21 @@ extern "C" int moe_layernorm_forward(const moe_layernorm_args *a, cudaStream_t s
   z.lds = a->lds;
   z.n = a->n;
   z.ldn = a->ldn;
-  const int64_t per_sm = z.warps * z.groups > 16 ? 1 : 2;
-  const int64_t blocks = std::min<int64_t>(per_sm * num_sms(), ceil_div(a->T, z.groups));
-  const int deep = 2 * (2 * (a->x_dtype == MOE_BF16 ? 1 : 2) + (a->b ? 2 : 0));
-  if (a->x_dtype == MOE_BF16)
-    return a->b ? launch_rows<layernorm_kernel<uint16_t, true>>(z, blocks, deep, 0, stream)
-                : launch_rows<layernorm_kernel<uint16_t, false>>(z, blocks, deep, 0, stream);
-  return a->b ? launch_rows<layernorm_kernel<float, true>>(z, blocks, deep, 0, stream)
-              : launch_rows<layernorm_kernel<float, false>>(z, blocks, deep, 0, stream);
+  auto launch_as = [&](auto type, auto with_b, auto is_big) {
+    using XT = decltype(type);
+    using R = ForwardRing<XT, decltype(with_b)::value, decltype(is_big)::value>;
+    z.groups = groups_of(a->H, R::kThreads);
+    const int tpr = 32 * z.warps;
+    return launch_rows<layernorm_kernel<XT, decltype(with_b)::value, decltype(is_big)::value>>(
+        z, std::min<int64_t>(num_sms(), ceil_div(a->T, z.groups)), R::bytes(tpr * z.groups, tpr), stream);
+  };
+  auto launch = [&](auto type, auto with_b) {
+    return z.warps > 16 ? launch_as(type, with_b, std::true_type{}) : launch_as(type, with_b, std::false_type{});
+  };
+  using std::true_type;
+  using std::false_type;
+  if (a->x_dtype == MOE_F32) return a->b ? launch(0.f, true_type{}) : launch(0.f, false_type{});
+  return a->b ? launch(uint16_t{0}, true_type{}) : launch(uint16_t{0}, false_type{});
 }
 
 extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t stream) {
@@ -491,7 +674,6 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   z.T = a->T;
   z.H = (int)a->H;
   z.warps = warps_of(a->H);
-  z.groups = groups_of(a->H);
   z.w_dtype = a->w_dtype;
   z.eps = a->eps;
   z.inv_h = 1.f / (float)a->H;
@@ -505,15 +687,22 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   z.s = a->dx;
   z.lds = a->ld_dx;
   z.part = a->dw || a->dbias ? static_cast<float *>(a->workspace) : nullptr;
-  const int64_t blocks = grad_blocks(a->T, a->H);
-  const bool big = z.warps > 16, f32 = a->x_dtype == MOE_F32, add = a->ds != nullptr;
-  const int pieces = 2 * (f32 ? 2 : 1) * (add ? 2 : 1) + 2, deep = pieces * (big && f32 ? 1 : 2);
-  const size_t least = z.part ? (size_t)z.H * 8 : 0;
-  auto launch = [&](auto type, auto with_ds) {
+  int64_t blocks = 0;
+  auto launch_as = [&](auto type, auto with_ds, auto is_big) {
     using XT = decltype(type);
-    constexpr bool kDs = decltype(with_ds)::value;
-    return big ? launch_rows<layernorm_grad_kernel<XT, kDs, true>>(z, blocks, deep, least, stream)
-               : launch_rows<layernorm_grad_kernel<XT, kDs, false>>(z, blocks, deep, least, stream);
+    using R = GradRing<XT, decltype(with_ds)::value, decltype(is_big)::value>;
+    z.groups = groups_of(a->H, R::kThreads);
+    blocks = std::min({kMostParts, (int64_t)num_sms(), ceil_div(a->T, z.groups)});
+    const int tpr = 32 * z.warps;
+    const size_t smem = std::max(R::bytes(tpr * z.groups, tpr), z.part ? (size_t)z.H * 8 : 0);
+    return launch_rows<layernorm_grad_kernel<XT, decltype(with_ds)::value, decltype(is_big)::value>>(z, blocks, smem, stream);
+  };
+  const bool f32 = a->x_dtype == MOE_F32, add = a->ds != nullptr;
+  auto launch = [&](auto type, auto with_ds) {
+    using R = GradRing<decltype(type), decltype(with_ds)::value, false>;
+    const int tpr = 32 * z.warps;
+    const bool big = tpr > R::kThreads || R::bytes(tpr, tpr) > kMostSmem;
+    return big ? launch_as(type, with_ds, std::true_type{}) : launch_as(type, with_ds, std::false_type{});
   };
   using std::true_type;
   using std::false_type;
