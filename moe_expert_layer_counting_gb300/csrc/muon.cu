@@ -15,6 +15,11 @@
 // FP16 iterates.  All singular values of an iterate are below 1.3, so that its
 // range is known and FP16 with a fixed scale of 2^12 (16 at most, 2^-26 the
 // smallest normal value) keeps 11 bits where BF16 keeps 8, at the same rate.
+//
+// Measured: 64 matrices of 1024 x 2048, five iterations: 1.87 to 2.07 ms in a burst (two
+// GPUs; 1.29 to 1.16 PFLOP/s of 7.5 GFLOP a matrix and iteration; the tiles on the
+// diagonal add a tenth to that), 2.25 back to back at the power limit (1.5 GHz); a step of 8 of 7168 x 2048 with
+// float32 masters and copies 2.7 to 3.2 ms, of which 0.5 are the three passes over the values at 7 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,6 +51,7 @@ struct Elementwise {
   float *sums;              // [E][parts]
   uint16_t *x;              // [E][N][ld]
   int *status;
+  int *sync;                // [1 + E] of the products, zeroed by the first kernel
   // the end
   void *p;
   int p_dtype;
@@ -139,6 +145,10 @@ __global__ void __launch_bounds__(256) momentum_kernel(const Elementwise z) {
   pdl_wait();
   const int64_t e = blockIdx.y, size = z.N * z.K;
   if (blockIdx.x == 0 && e == 0 && threadIdx.x < 16) z.status[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    z.sync[1 + e] = 0;
+    if (e == 0) z.sync[0] = 0;
+  }
   const float gs = z.grad_scale ? *z.grad_scale : 1.f;
   const int64_t i0 = (int64_t)blockIdx.x * z.per, i1 = min(i0 + z.per, size);
   float sum = 0.f;
@@ -159,14 +169,16 @@ __global__ void __launch_bounds__(256) scale_kernel(const Elementwise z) {
   __shared__ float red[8];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t e = blockIdx.y, size = z.N * z.K;
+  // backwards: what the kernel before touched last is still in L2
+  const int64_t e = gridDim.y - 1 - blockIdx.y, size = z.N * z.K;
+  const int part = (int)(gridDim.x - 1 - blockIdx.x);
   float sum = 0.f;
   for (int i = threadIdx.x; i < z.parts; i += 256) sum += z.sums[e * z.parts + i];
   sum = block_sum(sum, red);
   // (max written so that a NaN stays one)
   const float norm = sqrtf(sum), by = norm == 0.f ? 0.f : kScale / (norm < z.eps ? z.eps : norm);
   const float gs = z.grad_scale ? *z.grad_scale : 1.f;
-  const int64_t i0 = (int64_t)blockIdx.x * z.per, i1 = min(i0 + z.per, size);
+  const int64_t i0 = (int64_t)part * z.per, i1 = min(i0 + z.per, size);
 #pragma unroll 2
   for (int64_t i = i0 + threadIdx.x * VEC; i < i1; i += 256 * VEC) {
     float u[VEC];
@@ -222,56 +234,54 @@ __global__ void __launch_bounds__(256) update_kernel(const Elementwise z) {
 
 // ---------------------------------------------------------------- products
 
-// D[e] = alpha A[e] B[e]^T + beta on the diagonal, FP16, for a stack: M rows, C
-// columns, sums over R.  Pairs of CTAs (M = 256, N = 256 per item), as
-// grouped_kernel.cuh's weights' gradient: 64 reduction values a stage, two
-// accumulators, boxes of 32 rows x 128 bytes through TMA.
-struct ProductArgs {
-  int E, M, C, R;
-  int symmetric;            // D is: tiles on and above the diagonal, each stored twice
+// All products of a call in one launch.  Products of one kind over the stack are a
+// stage: S = alpha A B^T + beta on the diagonal, and so on; a tile of a stage of
+// one matrix is an item.  Pairs of CTAs (M = 256, N up to 256 per item; 64
+// reduction values a stage of the ring, two accumulators) claim items in
+// order, iteration by iteration, stage by stage.  An item may begin when the
+// stages before it are done with its matrix: each of its tiles has raised
+// the matrix's counter then.  Items are claimed in order and depend on earlier ones only, so
+// that the earliest one in work never waits, whatever part of the grid is
+// resident.  Against a launch for each product: 8 matrices of 256 x 128 in 62 us instead
+// of 85, a step of 8 of 1000 x 520 in 185 instead of 224; large ones the same.
+struct NsStage {
+  int M, C, R;              // rows and columns of the result, length of the sums
+  int a_mn, b_mn;           // the operand's M (N) index is the contiguous one in memory (else the summed one)
+  int symmetric;            // the result is: tiles on and above the diagonal, each stored twice
+  int tn, items;            // columns of a tile; tiles of a matrix
   float alpha, beta;
-  uint16_t *d;
-  int64_t ld, stride;       // of d, for the tiles below the diagonal
+  uint16_t *d;              // symmetric: the result
+  int64_t ld;
+};
+
+// 10 maps of [E][rows][columns]: boxes of 128 rows and of 32 rows x 64 columns, and of 64 x 64.
+struct NsMaps {
+  CUtensorMap x128[2], x32[2], x64[2], s128, s32, q128, q32;
+};
+
+struct NsArgs {
+  NsStage stage[3];         // Gram matrix to S (without c: to Q), Q from S, X from Q and X
+  int E, steps, wide, square;       // wide: N <= K; square: the second stage is there
+  int *ticket, *done;       // next item; [E] warps that are done with a tile
   int inject_wait;
   int *status;
 };
 
-struct ProductMaps {
-  CUtensorMap a, b, d;
-};
-
-struct PL {
+struct NsLayout {
   static constexpr int kStages = 6, kSlot = 32768, kEpiBytes = 4096;
+  static constexpr int kClaims = 2;     // (three: 190 instead of 185 us for a step of 8 matrices of 1000 x 520)
   static constexpr int kOffEpi = kStages * kSlot;
-  static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
-  static constexpr int kNumBars = 2 * kStages + 6;
+  static constexpr int kOffItems = kOffEpi + GP::kEpiWarps * kEpiBytes;
+  static constexpr int kOffBar = kOffItems + 16 * kClaims;
+  static constexpr int kNumBars = 2 * kStages + 6 + 2 * kClaims;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * kNumBars + 63) & ~63;
   static constexpr int kBytes = 1024 + kOffTmemPtr + 64;
 };
-static_assert(PL::kBytes <= 232448, "shared memory of one CTA");
+static_assert(NsLayout::kBytes <= 232448, "shared memory of one CTA");
 
-struct Tile {
-  int e, m, c, n;           // N slots (a multiple of 32)
+struct NsItem {
+  int e, m, c, at;          // at: 3 * iteration + stage; -1 after the last
 };
-
-__device__ __forceinline__ Tile tile_at(const ProductArgs &g, int w, int per, int mt, int ct) {
-  Tile t;
-  t.e = w / per;
-  int i = w - t.e * per;
-  if (g.symmetric) {
-    t.m = 0;
-    while (i >= mt - t.m) {
-      i -= mt - t.m;
-      ++t.m;
-    }
-    t.c = t.m + i;
-  } else {
-    t.m = i / ct;
-    t.c = i - t.m * ct;
-  }
-  t.n = min(GP::kN, (g.C - t.c * GP::kN + 31) & ~31);
-  return t;
-}
 
 // Packed words turned as turn_bf16 turns floats: word i of a lane holds rows 2 i and
 // 2 i + 1 of its column.
@@ -304,34 +314,105 @@ __device__ __forceinline__ uint32_t make_idesc_f16(uint32_t m, uint32_t n, bool 
   return make_idesc_bf16(m, n, a_mn, b_mn) & ~((7u << 7) | (7u << 10));      // A and B: FP16 is 0
 }
 
-// AMN / BMN: the operand's M (N) index is the contiguous one in memory.
-template <bool AMN, bool BMN>
-__global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_constant__ ProductMaps maps,
-                                                                  const ProductArgs g) {
+// Items of a ring that one thread fills and every role of both CTAs reads.
+struct NsItems {
+  const int4 *items;
+  uint64_t *full;
+  uint32_t empty0;          // the leader's barriers, shared::cluster
+  int *status;
+  int slot;
+  uint32_t phase;
+
+  // `wide`: called by a warp, not by a thread
+  __device__ __forceinline__ bool next(NsItem &it, bool wide) {
+    const bool got = mbar_wait_reset(full + slot, phase, status, kLimit, kWaitArrival, slot);
+    if (!(wide ? __all_sync(0xffffffffu, got) : got)) return false;
+    const int4 v = items[slot];
+    it = NsItem{v.x, v.y, v.z, v.w};
+    if (wide) __syncwarp();
+    if (!wide || (threadIdx.x & 31) == 0) mbar_arrive_done(empty0 + 8 * (uint32_t)slot);
+    if (++slot == NsLayout::kClaims) { slot = 0; phase ^= 1; }
+    return it.at >= 0;
+  }
+};
+
+__device__ __forceinline__ void store_cluster_v4(uint32_t addr, int4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Item w of the launch.
+__device__ __forceinline__ int4 ns_item(const NsArgs &g, int64_t w) {
+  const int per[3] = {g.stage[0].items, g.square ? g.stage[1].items : 0, g.stage[2].items};
+  const int64_t iteration = (int64_t)g.E * (per[0] + per[1] + per[2]);
+  const int it = (int)(w / iteration);
+  if (it >= g.steps) return make_int4(0, 0, 0, -1);
+  int64_t r = w - it * iteration;
+  int k = 0;
+  while (k < 2 && r >= (int64_t)g.E * per[k]) {
+    r -= (int64_t)g.E * per[k];
+    ++k;
+  }
+  const NsStage &s = g.stage[k];
+  const int e = (int)(r / per[k]);
+  int i = (int)(r - (int64_t)e * per[k]), m = 0;
+  const int ct = (s.C + s.tn - 1) / s.tn;
+  if (s.symmetric) {
+    // row m of tiles begins at the diagonal
+    const int across = GP::kM / s.tn;
+    while (i >= ct - m * across) {
+      i -= ct - m * across;
+      ++m;
+    }
+    i += m * across;
+  } else {
+    m = i / ct;
+    i -= m * ct;
+  }
+  return make_int4(e, m, i, 3 * it + k);
+}
+
+// As wait_counter, with a quick look before it: the stages of small matrices are a
+// few microseconds apart.
+__device__ __forceinline__ bool ns_wait(const int *counter, int target, int *status, int pos) {
+  for (int i = 0; i < 64; ++i)
+    if (ld_acquire_gpu(counter) >= target) return true;
+  return wait_counter(counter, target, status, kLimit, pos);
+}
+
+// Arrivals at a matrix's counter before stage `at` of it may begin.
+__device__ __forceinline__ int ns_arrivals(const NsArgs &g, int at) {
+  const int it = at / 3, k = at - 3 * it;
+  const int a = g.stage[0].items, b = g.square ? g.stage[1].items : 0, c = g.stage[2].items;
+  return 2 * GP::kEpiWarps * (it * (a + b + c) + (k > 0 ? a : 0) + (k > 1 ? b : 0));
+}
+
+__device__ __forceinline__ int tile_slots(const NsStage &s, int c) { return min(s.tn, (s.C - c * s.tn + 31) & ~31); }
+
+__global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __grid_constant__ NsMaps maps,
+                                                                        const __grid_constant__ NsArgs g) {
+  using L = NsLayout;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + PL::kOffBar);     // leader: both CTAs' copies of a stage
-  uint64_t *empty = full + PL::kStages;                                  // each CTA: stage consumed
-  uint64_t *tmem_full = empty + PL::kStages;                             // each CTA: accumulator ready
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);      // leader: both CTAs' copies of a stage
+  uint64_t *empty = full + L::kStages;                                   // each CTA: stage consumed
+  uint64_t *tmem_full = empty + L::kStages;                              // each CTA: accumulator ready
   uint64_t *tmem_empty = tmem_full + 2;                                  // leader: both CTAs drained it
   uint64_t *mma_done = tmem_empty + 2;
   uint64_t *never = mma_done + 1;
-  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + PL::kOffTmemPtr);
+  uint64_t *item_full = never + 1;                                       // each CTA
+  uint64_t *item_empty = item_full + L::kClaims;                         // leader: both CTAs' roles have read it
+  int4 *ring = reinterpret_cast<int4 *>(smem + L::kOffItems);
+  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int cluster = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
   int *status = g.status;
 
   if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&maps.a);
-      tma_prefetch_desc(&maps.b);
-      tma_prefetch_desc(&maps.d);
-    }
+    if (lane < 10) tma_prefetch_desc(&maps.x128[0] + lane);
   } else if (warp == 2) {
     if (lane == 0) {
-      for (int s = 0; s < PL::kStages; ++s) {
+      for (int s = 0; s < L::kStages; ++s) {
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], 1);
       }
@@ -341,6 +422,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
       }
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
+      for (int c = 0; c < L::kClaims; ++c) {
+        mbar_init(item_full + c, 1);
+        mbar_init(item_empty + c, 2 + 2 * GP::kEpiWarps + 1);      // loads, epilogues, the leader's MMAs
+      }
       fence_mbar_init();
     }
     __syncwarp();
@@ -354,9 +439,8 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t tmem_base = *tmem_ptr;
-  const int mt = (g.M + GP::kM - 1) / GP::kM, ct = (g.C + GP::kN - 1) / GP::kN;
-  const int per = g.symmetric ? mt * (mt + 1) / 2 : mt * ct;
-  const int total = g.E * per, blocks = (g.R + GP::kBK - 1) / GP::kBK;
+  NsItems items{ring, item_full, mapa_shared(smem_u32(item_empty), 0), status, 0, 0};
+  NsItem it;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads (both CTAs), one thread
@@ -366,38 +450,48 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(full), 0);
       const uint64_t policy = l2_policy(false);
-      fence_proxy_async_global();       // what the kernel before stored from registers is read by TMA
-      for (int w = cluster; w < total && ok; w += step) {
-        const Tile t = tile_at(g, w, per, mt, ct);
-        const int row = t.m * GP::kM + (int)rank * 128, col = t.c * GP::kN + (int)rank * (t.n >> 1);
-        for (int kb = 0; kb < blocks; ++kb) {
-          unsigned char *a = smem + stage * PL::kSlot, *b = a + GP::kATile;
+      while (ok && items.next(it, false)) {
+        const int iteration = it.at / 3, k = it.at - 3 * iteration, x = iteration & 1;
+        const NsStage &s = g.stage[k];
+        const int n = tile_slots(s, it.c), half = n >> 1, blocks = (s.R + GP::kBK - 1) / GP::kBK;
+        const int row = it.m * GP::kM + (int)rank * 128, col = it.c * s.tn + (int)rank * half;
+        // a: Gram matrix X, square S, product Q or (tall) X; b: X, S, X or (tall) Q
+        const bool is_x_a = k == 0 || (k == 2 && !g.wide), is_x_b = k == 0 || (k == 2 && g.wide);
+        const CUtensorMap *a_map = is_x_a ? (s.a_mn ? &maps.x64[x] : &maps.x128[x]) : k == 1 ? &maps.s128 : &maps.q128;
+        const CUtensorMap *b_map = is_x_b ? (s.b_mn ? &maps.x64[x] : half > 64 ? &maps.x128[x] : &maps.x32[x])
+                                   : k == 1 ? (half > 64 ? &maps.s128 : &maps.s32)
+                                            : (half > 64 ? &maps.q128 : &maps.q32);
+        // rows of a box of b, and boxes
+        const int b_box = s.b_mn ? 64 : half > 64 ? 128 : 32, b_boxes = (half + b_box - 1) / b_box;
+        const uint32_t bytes = (uint32_t)(GP::kATile + b_boxes * b_box * GP::kBK * 2);
+        ok = ns_wait(g.done + it.e, ns_arrivals(g, it.at), status, it.at);
+        fence_proxy_async_global();       // what was stored from registers is read by TMA
+        for (int kb = 0; kb < blocks && ok; ++kb) {
+          unsigned char *a = smem + stage * L::kSlot, *b = a + GP::kATile;
           const uint32_t bar = full0 + 8 * (uint32_t)stage;
           const int k0 = kb * GP::kBK;
-          if (!mbar_wait_reset(&empty[stage], phase ^ 1, status, kLimit, kWaitProducerEmpty, kb)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * PL::kSlot);
-          if (AMN) {
+          ok = mbar_wait_reset(&empty[stage], phase ^ 1, status, kLimit, kWaitProducerEmpty, kb);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+          if (s.a_mn) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_3d_2sm(a + j * GP::kHalfBox, &maps.a, bar, row + 64 * j, k0, t.e, policy);
+            for (int j = 0; j < 2; ++j) tma_load_3d_2sm(a + j * GP::kHalfBox, a_map, bar, row + 64 * j, k0, it.e, policy);
           } else {
-            tma_load_3d_2sm(a, &maps.a, bar, k0, row, t.e, policy);
+            tma_load_3d_2sm(a, a_map, bar, k0, row, it.e, policy);
           }
-          if (BMN) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_3d_2sm(b + j * GP::kHalfBox, &maps.b, bar, col + 64 * j, k0, t.e, policy);
-          } else {
-            tma_load_3d_2sm(b, &maps.b, bar, k0, col, t.e, policy);
+          for (int j = 0; j < b_boxes; ++j) {
+            if (s.b_mn)
+              tma_load_3d_2sm(b + j * GP::kHalfBox, b_map, bar, col + 64 * j, k0, it.e, policy);
+            else
+              tma_load_3d_2sm(b + j * b_box * GP::kBK * 2, b_map, bar, k0, col + b_box * j, it.e, policy);
           }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == PL::kStages) { stage = 0; phase ^= 1; }
+          if (++stage == L::kStages) { stage = 0; phase ^= 1; }
         }
       }
       // no CTA leaves with copies in flight (as in grouped_kernel)
-      for (int s = 0; s < PL::kStages; ++s)
+      for (int s = 0; s < L::kStages; ++s)
         if (rank == 0 && (issued & (1u << s)))
           mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
       if (*reinterpret_cast<volatile int *>(status + 1) != 0) {
@@ -409,70 +503,94 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader), one thread
     if (rank == 0 && elect_one()) {
-      constexpr uint64_t kAStep = (AMN ? 2048 : 32) >> 4, kBStep = (BMN ? 2048 : 32) >> 4;
-      const uint64_t a_desc = make_smem_desc(smem_u32(smem), AMN ? GP::kHalfBox : 16, 1024, kSwizzle128B);
-      const uint64_t b_desc = make_smem_desc(smem_u32(smem) + GP::kATile, BMN ? GP::kHalfBox : 16, 1024, kSwizzle128B);
+      const uint32_t base = smem_u32(smem);
+      // K-major operands and M- / N-major ones
+      const uint64_t desc_k = make_smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t desc_mn = make_smem_desc(base, GP::kHalfBox, 1024, kSwizzle128B);
       int stage = 0, j = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int w = cluster; w < total && ok; w += step, ++j) {
-        const Tile t = tile_at(g, w, per, mt, ct);
+      for (; ok && items.next(it, false); ++j) {
+        const NsStage &s = g.stage[it.at % 3];
+        const int n = tile_slots(s, it.c), blocks = (s.R + GP::kBK - 1) / GP::kBK;
         const int acc = j & 1;
-        if (!mbar_wait_reset(&tmem_empty[acc], ((uint32_t)(j >> 1) & 1u) ^ 1u, status, kLimit, kWaitMmaTmemEmpty, w)) break;
+        ok = mbar_wait_reset(&tmem_empty[acc], ((uint32_t)(j >> 1) & 1u) ^ 1u, status, kLimit, kWaitMmaTmemEmpty, it.at);
+        if (!ok) break;
         tc_fence_after();
-        if (g.inject_wait == 1 && j == 0 && !mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, w)) break;
-        const uint32_t idesc = make_idesc_f16(GP::kM, (uint32_t)t.n, AMN, BMN);
+        if (g.inject_wait == 1 && j == 0 && !mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, it.at)) break;
+        const uint32_t idesc = make_idesc_f16(GP::kM, (uint32_t)n, s.a_mn, s.b_mn);
         const uint32_t d = tmem_base + (uint32_t)(acc * GP::kN);
+        const uint64_t a_step = (s.a_mn ? 2048 : 32) >> 4, b_step = (s.b_mn ? 2048 : 32) >> 4;
+        const uint64_t a_desc = s.a_mn ? desc_mn : desc_k, b_desc = (s.b_mn ? desc_mn : desc_k) + (GP::kATile >> 4);
         for (int kb = 0; kb < blocks; ++kb) {
-          if (!mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb)) {
-            ok = false;
-            break;
-          }
-          const uint64_t ad = a_desc + (uint64_t)((stage * PL::kSlot) >> 4);
-          const uint64_t bd = b_desc + (uint64_t)((stage * PL::kSlot) >> 4);
-          const int left = g.R - kb * GP::kBK;
+          ok = mbar_wait_reset(&full[stage], phase, status, kLimit, kWaitMmaFull, kb);
+          if (!ok) break;
+          const uint64_t ad = a_desc + (uint64_t)((stage * L::kSlot) >> 4);
+          const uint64_t bd = b_desc + (uint64_t)((stage * L::kSlot) >> 4);
+          const int left = s.R - kb * GP::kBK;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            if (16 * kk < left) tc_mma_2sm_f16(d, ad + kk * kAStep, bd + kk * kBStep, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+            if (16 * kk < left) tc_mma_2sm_f16(d, ad + kk * a_step, bd + kk * b_step, idesc, kb > 0 || kk > 0 ? 1u : 0u);
           tc_commit_2sm(&empty[stage], 3);
-          if (++stage == PL::kStages) { stage = 0; phase ^= 1; }
+          if (++stage == L::kStages) { stage = 0; phase ^= 1; }
         }
-        if (!ok) break;
-        tc_commit_2sm(&tmem_full[acc], 3);
+        if (ok) tc_commit_2sm(&tmem_full[acc], 3);
       }
       tc_commit_2sm(mma_done, 1);
       mbar_wait_reset(mma_done, 0, status, kLimit, kWaitMmaDone, 0, false);
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ claims (leader), one thread
+    if (rank == 0 && elect_one()) {
+      const uint32_t ring1 = mapa_shared(smem_u32(ring), 1), full1 = mapa_shared(smem_u32(item_full), 1);
+      int slot = 0;
+      uint32_t phase = 0;
+      for (;;) {
+        if (!mbar_wait_reset(item_empty + slot, phase ^ 1, status, kLimit, kWaitArrival, slot)) break;
+        const int4 v = ns_item(g, (int64_t)(uint32_t)atomicAdd(g.ticket, 1));
+        ring[slot] = v;
+        store_cluster_v4(ring1 + 16 * (uint32_t)slot, v);
+        mbar_arrive(item_full + slot);
+        mbar_arrive_cluster(full1 + 8 * (uint32_t)slot);
+        if (v.w < 0) break;
+        if (++slot == L::kClaims) { slot = 0; phase ^= 1; }
+      }
+    }
+    __syncwarp();
   } else if (warp >= GP::kFirstEpiWarp) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, ew = warp - GP::kFirstEpiWarp;
-    unsigned char *buf = smem + PL::kOffEpi + ew * PL::kEpiBytes;
-    int j = 0;
-    for (int w = cluster; w < total; w += step, ++j) {
-      const Tile t = tile_at(g, w, per, mt, ct);
+    unsigned char *buf = smem + L::kOffEpi + ew * L::kEpiBytes;
+    for (int j = 0; items.next(it, true); ++j) {
+      const int iteration = it.at / 3, k = it.at - 3 * iteration;
+      const NsStage &s = g.stage[k];
+      const CUtensorMap *d_map = k == 2 ? &maps.x32[(iteration + 1) & 1] : k == 1 || !g.square ? &maps.q32 : &maps.s32;
       const int acc = j & 1;
       if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_full[acc], (uint32_t)(j >> 1) & 1u, status, kLimit,
-                                                   kWaitEpiTmemFull, w)))
+                                                   kWaitEpiTmemFull, it.at)))
         break;
       tc_fence_after();
-      const int row0 = t.m * GP::kM + (int)rank * 128 + 32 * q, col0 = t.c * GP::kN + 128 * (ew >> 2);
-      const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN + 128 * (ew >> 2));
-      if (row0 < g.M) {
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
-          if (col0 + c0 >= g.C) break;
+      // this warp's columns of the tile: 128, or 64 (of narrow tiles the first warps' alone)
+      const int wide = s.tn > 128 ? 128 : 64, c_first = wide * (ew >> 2);
+      const int row0 = it.m * GP::kM + (int)rank * 128 + 32 * q;
+      const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN);
+      const bool mirrored = s.symmetric && it.c * s.tn >= (it.m + 1) * GP::kM;
+      if (row0 < s.M) {
+        for (int c0 = c_first; c0 < min(c_first + wide, s.tn); c0 += 64) {
+          const int col0 = it.c * s.tn + c0;
+          if (col0 >= s.C) break;
           uint32_t v[64];
 #pragma unroll
           for (int h = 0; h < 64; h += 32)
             tmem_ld_32x32b_x32(t_row + (uint32_t)(c0 + h), *reinterpret_cast<uint32_t(*)[32]>(v + h));
           tmem_ld_wait();
-          const int diagonal = row0 + lane - (col0 + c0);               // this lane's column on the diagonal
+          const int diagonal = row0 + lane - col0;                      // this lane's column on the diagonal
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float x = fmaf(g.alpha, __uint_as_float(v[2 * i]), diagonal == 2 * i ? g.beta : 0.f);
-            const float y = fmaf(g.alpha, __uint_as_float(v[2 * i + 1]), diagonal == 2 * i + 1 ? g.beta : 0.f);
+            const float x = fmaf(s.alpha, __uint_as_float(v[2 * i]), diagonal == 2 * i ? s.beta : 0.f);
+            const float y = fmaf(s.alpha, __uint_as_float(v[2 * i + 1]), diagonal == 2 * i + 1 ? s.beta : 0.f);
             p[i] = pack_f16(x, y);
           }
           if (lane == 0) bulk_wait_read<0>();                          // the store before has read the staging
@@ -484,18 +602,18 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d_normal(&maps.d, buf, col0 + c0, row0, t.e);
+            tma_store_3d_normal(d_map, buf, col0, row0, it.e);
             bulk_commit();
           }
-          if (g.symmetric && t.c > t.m) {
+          if (mirrored) {
             // the tile below the diagonal: lanes are columns there
-            uint16_t *out = g.d + t.e * g.stride;
+            uint16_t *out = s.d + (int64_t)it.e * s.M * s.ld;
             const int col = row0 + 8 * (lane >> 3);
 #pragma unroll
             for (int h = 0; h < 32; h += 16)
               turn_words<16>(p + h, lane, [&](int r, const uint4 &piece) {
-                const int row = col0 + c0 + 2 * h + 8 * r + (lane & 7);
-                if (row < g.C && col < g.M) *reinterpret_cast<uint4 *>(out + row * g.ld + col) = piece;
+                const int row = col0 + 2 * h + 8 * r + (lane & 7);
+                if (row < s.C && col < s.M) *reinterpret_cast<uint4 *>(out + row * s.ld + col) = piece;
               });
           }
         }
@@ -503,6 +621,18 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      // published: this warp's part of the tile is in memory
+      if (mirrored) {
+        fence_proxy_async_global();
+        __threadfence();
+        __syncwarp();
+      }
+      if (lane == 0) {
+        bulk_wait<0>();
+        fence_proxy_async_global();
+        __threadfence();
+        atomicAdd(g.done + it.e, 1);
+      }
     }
     if (lane == 0) bulk_wait<0>();
   }
@@ -520,7 +650,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) product_kernel(const __grid_c
 struct Stack {              // of a call's workspace
   int64_t n, ldx, lds;
   int parts;
-  size_t sums, x[2], s, q, total;
+  size_t sums, sync, x[2], s, q, total;
 };
 
 Stack stack_layout(int64_t E, int64_t N, int64_t K) {
@@ -536,6 +666,7 @@ Stack stack_layout(int64_t E, int64_t N, int64_t K) {
     return at;
   };
   w.sums = take((size_t)E * w.parts * 4);
+  w.sync = take((size_t)(E + 1) * 4);
   for (auto &x : w.x) x = take((size_t)E * N * w.ldx * 2);
   w.s = take((size_t)E * w.n * w.lds * 2);
   w.q = take((size_t)E * w.n * w.lds * 2);
@@ -555,27 +686,38 @@ bool encode_f16(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// a [M rows of R, or R rows of M], b [C rows of R, or R rows of C], d [M][C].
-template <bool AMN, bool BMN>
-int launch_product(const uint16_t *a, int64_t lda, const uint16_t *b, int64_t ldb, uint16_t *d, int64_t ldd, int64_t E,
-                   int64_t M, int64_t C, int64_t R, bool symmetric, float alpha, float beta, int *status, cudaStream_t st) {
+// The width of a stage's tiles.  A pair of SMs takes some 0.33 us for 64 reduction values of a 256 x 256 tile, bound by its
+// tensor cores, 0.2 and 0.17 of a tile of 128 and 64 columns, bound by the loads: narrower tiles pay where
+// there are too few for the pairs, or the last round of wide ones is nearly empty.
+void choose_tiles(NsStage &s, int64_t E) {
+  const int64_t pairs = num_sms() / 2, mt = ceil_div(s.M, GP::kM);
+  double best = 0;
+  for (int tn : {256, 128, 64}) {
+    const int64_t ct = ceil_div(s.C, tn), across = GP::kM / tn;
+    int64_t items = 0;
+    for (int64_t m = 0; m < mt; ++m) items += s.symmetric ? ct - m * across : ct;
+    const double rounds = (double)ceil_div(E * items, pairs), each = tn == 256 ? 0.33 : tn == 128 ? 0.2 : 0.17;
+    const double cost = rounds * (ceil_div(s.R, GP::kBK) * each + 0.5);
+    if (tn == 256 || cost < 0.95 * best) {
+      best = cost;
+      s.tn = tn;
+      s.items = (int)items;
+    }
+  }
+}
+
+int launch_newton_schulz(const NsMaps &maps, const NsArgs &g, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(product_kernel<AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(newton_schulz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsLayout::kBytes) != cudaSuccess)
       return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  ProductMaps maps;
-  const bool ok = (AMN ? encode_f16(&maps.a, a, M, R, E, lda, 64, GP::kBK) : encode_f16(&maps.a, a, R, M, E, lda, GP::kBK, 128)) &&
-                  (BMN ? encode_f16(&maps.b, b, C, R, E, ldb, 64, GP::kBK) : encode_f16(&maps.b, b, R, C, E, ldb, GP::kBK, 128)) &&
-                  encode_f16(&maps.d, d, C, M, E, ldd, 64, 32);
-  if (!ok) return MOE_ERR_CUDA;
-  const int64_t mt = ceil_div(M, GP::kM), items = E * (symmetric ? mt * (mt + 1) / 2 : mt * ceil_div(C, GP::kN));
-  if (items > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
-  const ProductArgs g{(int)E, (int)M, (int)C, (int)R, symmetric, alpha, beta, d, ldd, M * ldd, injected_wait(), status};
+  int64_t most = 0;
+  for (const NsStage &s : g.stage) most = std::max<int64_t>(most, (int64_t)g.E * s.items);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -584,13 +726,13 @@ int launch_product(const uint16_t *a, int64_t lda, const uint16_t *b, int64_t ld
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(num_sms() / 2, items)));
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(num_sms() / 2, most)));
   cfg.blockDim = dim3(GP::kThreads);
-  cfg.dynamicSmemBytes = PL::kBytes;
+  cfg.dynamicSmemBytes = NsLayout::kBytes;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, product_kernel<AMN, BMN>, maps, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, newton_schulz_kernel, maps, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, const int32_t *status, const void *workspace,
@@ -614,27 +756,44 @@ int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *
   z.per = (int)round_up(ceil_div(N * K, z.parts), 8 * 256);
   z.ld = w.ldx;
   z.sums = reinterpret_cast<float *>(base + w.sums);
+  z.sync = reinterpret_cast<int *>(base + w.sync);
   uint16_t *x[2] = {reinterpret_cast<uint16_t *>(base + w.x[0]), reinterpret_cast<uint16_t *>(base + w.x[1])};
   uint16_t *s = reinterpret_cast<uint16_t *>(base + w.s), *q = reinterpret_cast<uint16_t *>(base + w.q);
   z.x = x[0];
   const dim3 grid((unsigned)z.parts, (unsigned)E), block(256);
   int rc = launch_pdl(momentum_kernel<VEC>, grid, block, 0, st, z);
   if (rc == MOE_OK) rc = launch_pdl(scale_kernel<VEC>, grid, block, 0, st, z);
-  const bool wide = N <= K;                 // the Gram matrix is that of the rows
-  const float unit = 1.f / kScale, shift = ns.c != 0.f ? ns.b / (2.f * ns.c) : 0.f;
-  const int64_t n = w.n, k = std::max(N, K);
-  for (int i = 0; i < ns.steps && rc == MOE_OK; ++i) {
-    const uint16_t *from = x[i & 1];
-    uint16_t *to = x[(i + 1) & 1], *gram = ns.c != 0.f ? s : q;
-    const float alpha = ns.c != 0.f ? unit : ns.b * unit, beta = kScale * (ns.c != 0.f ? shift : ns.a);
-    rc = wide ? launch_product<false, false>(from, w.ldx, from, w.ldx, gram, w.lds, E, n, n, k, true, alpha, beta, z.status, st)
-              : launch_product<true, true>(from, w.ldx, from, w.ldx, gram, w.lds, E, n, n, k, true, alpha, beta, z.status, st);
-    if (rc == MOE_OK && ns.c != 0.f)
-      rc = launch_product<false, false>(s, w.lds, s, w.lds, q, w.lds, E, n, n, n, true, ns.c * unit,
-                                        kScale * (ns.a - ns.b * shift * 0.5f), z.status, st);
-    if (rc == MOE_OK)
-      rc = wide ? launch_product<false, true>(q, w.lds, from, w.ldx, to, w.ldx, E, N, K, n, false, unit, 0.f, z.status, st)
-                : launch_product<false, false>(from, w.ldx, q, w.lds, to, w.ldx, E, N, K, n, false, unit, 0.f, z.status, st);
+  if (rc == MOE_OK && ns.steps > 0) {
+    const bool wide = N <= K, square = ns.c != 0.f;                    // wide: the Gram matrix is that of the rows
+    const float unit = 1.f / kScale, shift = square ? ns.b / (2.f * ns.c) : 0.f;
+    const int n = (int)w.n, k = (int)std::max(N, K);
+    NsMaps maps;
+    bool ok = true;
+    for (int i = 0; i < 2; ++i)
+      ok = ok && encode_f16(&maps.x128[i], x[i], K, N, E, w.ldx, GP::kBK, 128) && encode_f16(&maps.x32[i], x[i], K, N, E, w.ldx, 64, 32) &&
+           encode_f16(&maps.x64[i], x[i], K, N, E, w.ldx, 64, 64);
+    ok = ok && encode_f16(&maps.s128, s, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.s32, s, n, n, E, w.lds, 64, 32) &&
+         encode_f16(&maps.q128, q, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.q32, q, n, n, E, w.lds, 64, 32);
+    if (!ok) return MOE_ERR_CUDA;
+    NsArgs g{};
+    g.stage[0] = {n, n, k, !wide, !wide, 1, 0, 0, square ? unit : ns.b * unit, kScale * (square ? shift : ns.a), square ? s : q, w.lds};
+    g.stage[1] = {n, n, n, 0, 0, 1, 0, 0, ns.c * unit, kScale * (ns.a - ns.b * shift * 0.5f), q, w.lds};
+    g.stage[2] = {(int)N, (int)K, n, 0, wide, 0, 0, 0, unit, 0.f, nullptr, 0};
+    int64_t items = 0;
+    for (NsStage &stage : g.stage) {
+      choose_tiles(stage, E);
+      items += E * stage.items;
+    }
+    if (items * ns.steps > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
+    g.E = (int)E;
+    g.steps = ns.steps;
+    g.wide = wide;
+    g.square = square;
+    g.ticket = z.sync;
+    g.done = z.sync + 1;
+    g.inject_wait = injected_wait();
+    g.status = z.status;
+    rc = launch_newton_schulz(maps, g, st);
   }
   if (rc != MOE_OK) return rc;
   z.x = x[ns.steps & 1];
