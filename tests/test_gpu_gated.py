@@ -133,6 +133,46 @@ def test_forward(B, case, activation):
     check_forward(h, a, x, w, row_w, counts, activation)
 
 
+FEW = [
+    # counts, first, rows behind the last, I, H
+    ([1], 0, 0, 8, 8), ([2], 0, 0, 40, 264), ([1], 0, 1, 512, 2048), ([3, 5], 0, 0, 72, 136), ([0, 8, 0], 0, 0, 24, 520),
+    ([1] * 8, 0, 0, 512, 2048), ([0, 1, 0, 4, 0], 2, 1, 136, 4104), ([0, 0, 0], 3, 4, 16, 64), ([0] * 1020 + [1, 0, 2, 1], 1, 2, 16, 64),
+    ([7, 0], 1, 0, 64, 7168), ([0, 2, 2, 2, 0, 2], 0, 0, 33 * 8, 256),
+]
+
+
+@pytest.mark.parametrize("case", range(len(FEW)))
+@pytest.mark.parametrize("activation", [0, 1])
+def test_few_rows(B, case, activation):
+    """Up to eight rows, of any number of experts; the others keep what they held."""
+    counts, first, behind, I, H = FEW[case]
+    E, n = len(counts), sum(counts)
+    P = first + n + behind
+    x, w = randn(P, H, seed=1), randn(E, 2 * I, H, seed=2, scale=1.5 * H ** -0.5)
+    own = torch.zeros(P, dtype=torch.bool, device="cuda")
+    own[first:first + n] = True
+    x[~own] = float("nan")
+    row_w = randn(P, seed=3, dtype=F32) if case % 2 else None
+    wide_x = torch.full((P, H + 8), float("nan"), dtype=BF16, device="cuda")
+    wide_x[:, :H] = x
+    h, a = torch.full((P, I), 7.0, dtype=BF16, device="cuda"), torch.full((P, 2 * I), 7.0, dtype=BF16, device="cuda")
+    ws = workspace(B, P, H, I, E)
+    ws.fill_(255)
+    B.moe_gated_forward(wide_x[:, :H], w, offsets_of(counts, first), h, ws, a=a if case % 3 else None, row_w=row_w, activation=activation)
+    assert B.moe_get_device_status(ws) == B.MOE_OK
+    check_forward(h, a if case % 3 else None, x, w, row_w, counts, activation, first)
+    assert bool((h[~own] == 7).all()) and bool((a[~own if case % 3 else own | True] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [[0, 5, 3, 8], [0, 4, 8, 9], [-1, 4, 8, 8], [0, -3, 8, 8]])
+def test_few_rows_with_bad_offsets(B, bad):
+    offsets = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    x, w, h = randn(8, 64), randn(3, 80, 64), torch.full((8, 40), 7.0, dtype=BF16, device="cuda")
+    ws = workspace(B, 8, 64, 40, 3)
+    B.moe_gated_forward(x, w, offsets, h, ws)
+    assert B.moe_get_device_status(ws) == B.MOE_ERR_DEVICE_INDEX and bool((h == 7).all())
+
+
 @pytest.mark.parametrize("case", range(len(CASES)))
 @pytest.mark.parametrize("activation", [0, 1])
 def test_back(B, case, activation):
