@@ -488,8 +488,15 @@ assert _GATED_ARGS.size == ctypes.sizeof(MoeGatedArgs)
 
 def _on_current_device(*tensors) -> bool:
     """Whether all of them (None left out) lie on the current device, whose streams the calls use."""
-    tensors = [t for t in tensors if t is not None]
-    return all(t.is_cuda for t in tensors) and {t.get_device() for t in tensors} <= {torch.cuda.current_device()}
+    device = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()                   # -1: of the CPU
+            if d != device:
+                if device is not None or d < 0 or d != torch.cuda.current_device():
+                    return False
+                device = d
+    return True
 
 
 def _is_row_values(t, P: int) -> bool:
@@ -653,23 +660,23 @@ _LAYERNORM_GRADS = struct.Struct("@IiifqqPqPPqPqPqPPPN")
 assert (_LAYERNORM_ARGS.size, _LAYERNORM_GRADS.size) == (ctypes.sizeof(MoeLayernormArgs), ctypes.sizeof(MoeLayernormGrads))
 
 
-def _column_weights(H: int, *weights):
-    """The type code and pointers of contiguous [H] weights of one type (None: 0); None if they are not."""
-    given = [w for w in weights if w is not None]
-    kind = _DTYPES.get(given[0].dtype) if given else F32
-    if kind is None or any(w.dtype is not given[0].dtype or w.shape != (H,) or not w.is_contiguous() for w in given):
-        return None
-    return kind, [0 if w is None else w.data_ptr() for w in weights]
+def _column_weights(H: int, w, bias=None):
+    """(type code, pointers) of contiguous [H] weights of one type (None: 0); None if they are not."""
+    dtype = torch.float32 if w is None and bias is None else (bias if w is None else w).dtype
+    kind = _DTYPES.get(dtype)
+    for t in (w, bias):
+        if t is not None and (t.dtype is not dtype or t.shape != (H,) or not t.is_contiguous()):
+            return None
+    return None if kind is None else (kind, 0 if w is None else w.data_ptr(), 0 if bias is None else bias.data_ptr())
 
 
 def moe_layernorm_forward(x: torch.Tensor, b: torch.Tensor, w: torch.Tensor, bias: torch.Tensor, s: torch.Tensor, n: torch.Tensor,
                           eps: float = 1e-5, stream=None, check=True) -> int:
     """s = x + b, n = the layer norm of s with w and bias ([H], either type); b and s (both), w and bias may be None.  x and s
     [T, H] bf16 or float32, b and n bf16."""
-    dtype, xt = x.dtype, _DTYPES.get(x.dtype)
-    shape = tuple(x.shape)
-    ok = xt is not None and x.dim() == 2
-    columns = _column_weights(shape[1], w, bias) if ok else None
+    dtype, shape = x.dtype, x.shape
+    xt = _DTYPES.get(dtype)
+    columns = _column_weights(shape[1], w, bias) if xt is not None and len(shape) == 2 else None
     if columns is None:
         return _invalid("moe_layernorm_forward", check)
     xr, nr = _rows(x, shape, dtype), _rows(n, shape)
@@ -677,7 +684,7 @@ def moe_layernorm_forward(x: torch.Tensor, b: torch.Tensor, w: torch.Tensor, bia
     sr = _NONE if s is None else _rows(s, shape, dtype)
     if None in (xr, nr, br, sr) or not _on_current_device(x, b, w, bias, s, n):
         return _invalid("moe_layernorm_forward", check)
-    a = _LAYERNORM_ARGS.pack(_LAYERNORM_ARGS.size, xt, columns[0], eps, *shape, *xr, *br, *columns[1], *sr, *nr)
+    a = _LAYERNORM_ARGS.pack(_LAYERNORM_ARGS.size, xt, columns[0], eps, *shape, *xr, *br, *columns[1:], *sr, *nr)
     rc = lib.moe_layernorm_forward(a, _stream(stream))
     if check:
         _check(rc, "moe_layernorm_forward")
@@ -693,10 +700,9 @@ def moe_layernorm_backward(s: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, d
                            stream=None, check=True) -> int:
     """Gradients of moe_layernorm_forward from dn and (or None) ds; s is its s (without b: its x).  Outputs that are None
     are not computed; dx is of s's type, dw and dbias float32 [H]."""
-    dtype, xt = s.dtype, _DTYPES.get(s.dtype)
-    shape = tuple(s.shape)
-    ok = xt is not None and s.dim() == 2
-    columns = _column_weights(shape[1], w) if ok else None
+    dtype, shape = s.dtype, s.shape
+    xt = _DTYPES.get(dtype)
+    columns = _column_weights(shape[1], w) if xt is not None and len(shape) == 2 else None
     if columns is None:
         return _invalid("moe_layernorm_backward", check)
     sr, dnr = _rows(s, shape, dtype), _rows(dn, shape)
@@ -706,7 +712,7 @@ def moe_layernorm_backward(s: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, d
     if None in (sr, dnr, dsr, dxr, pw, pb) or not workspace.is_contiguous() or \
             not _on_current_device(s, w, dn, ds, workspace, dx, dw, dbias):
         return _invalid("moe_layernorm_backward", check)
-    a = _LAYERNORM_GRADS.pack(_LAYERNORM_GRADS.size, xt, columns[0], eps, *shape, *sr, columns[1][0], *dnr, *dsr, *dxr, pw, pb,
+    a = _LAYERNORM_GRADS.pack(_LAYERNORM_GRADS.size, xt, columns[0], eps, *shape, *sr, columns[1], *dnr, *dsr, *dxr, pw, pb,
                               workspace.data_ptr(), workspace.nbytes)
     rc = lib.moe_layernorm_backward(a, _stream(stream))
     if check:

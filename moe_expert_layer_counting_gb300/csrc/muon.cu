@@ -645,6 +645,366 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
   }
 }
 
+// ---------------------------------------------------------------- small matrices
+
+// A matrix whose shorter side is at most 128 and whose other is at most 8 * 384: the whole
+// call in one launch, momentum to update, a cluster of 1, 2, 4 or 8 CTAs for each matrix.
+// The iterate X [n][k] lies in shared memory in FP16, cut along k over the
+// cluster; S and Q [n][n] are in every CTA.  One copy of X serves as both operands
+// of X X^T (summed along its rows) and as the right one of Q X (summed across
+// them): the MMA reads either from the same 128-byte-swizzled blocks of 64
+// columns.  Of X X^T each CTA has the part of its columns; the parts are added in
+// float32 through the cluster's shared memory, a share of the rows by each CTA,
+// which hands its rows of S to all.  A stage is then an MMA of a few hundred
+// nanoseconds, a commit and a pass from TMEM back to shared memory, where the
+// kernel above needs a trip through L2 between any two: 4 us an iteration of 128 x 256
+// instead of 10.
+struct SmallArgs {
+  Elementwise z;
+  int n, k, kc;             // kc: columns of a CTA, a multiple of 64
+  int steps, square;
+  float gram_alpha, gram_beta, square_alpha, square_beta;
+  int inject_wait;
+};
+
+struct SmallLayout {
+  static constexpr int kMostN = 128, kMostColumns = 384, kThreads = 256;
+  static constexpr int kBlock = kMostN * 128;                       // 64 columns of FP16
+  static constexpr int kOffS = kMostColumns / 64 * kBlock, kOffQ = kOffS + 2 * kBlock;
+  static constexpr int kOffPart = kOffQ + 2 * kBlock;               // [128][128] float32
+  static constexpr int kOffBar = kOffPart + kMostN * kMostN * 4;
+  static constexpr int kOffSums = kOffBar + 32;                     // 8 of this block's warps, 8 of the cluster's CTAs
+  static constexpr int kBytes = 1024 + kOffSums + 64;
+};
+static_assert(SmallLayout::kBytes <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ float4 load_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+
+// 16 bytes of columns col .. col + 7 of row r in blocks of 64 columns.
+__device__ __forceinline__ int small_place(int r, int col) {
+  return (col >> 6) * SmallLayout::kBlock + r * 128 + ((((col >> 3) & 7) ^ (r & 7)) << 4);
+}
+
+// Rows r .. r + 7 of X, columns col .. col + 7 of the matrix, of what is orthogonalised (0 past the matrix' ends), all
+// loads before their use.  VEC 8: what is contiguous in memory in runs of 8, aligned to 16 bytes.
+template <int VEC, bool WIDE>
+__device__ __forceinline__ void small_values(const SmallArgs &g, int64_t base, int r, int col, float gs, bool fresh,
+                                             float (&u)[8][8]) {
+  float m[8][8];
+#pragma unroll
+  for (int a = 0; a < 8; ++a)
+#pragma unroll
+    for (int b = 0; b < 8; ++b) u[a][b] = m[a][b] = 0.f;
+  // line a of the run's other direction, element b along the run
+  auto at = [&](int a, int b) {
+    return WIDE ? base + (int64_t)(r + a) * g.k + col + b : base + (int64_t)(col + a) * g.n + r + b;
+  };
+  auto inside = [&](int a, int b) { return WIDE ? r + a < g.n && col + b < g.k : r + b < g.n && col + a < g.k; };
+#pragma unroll
+  for (int a = 0; a < 8; ++a) {
+    if (VEC == 8) {
+      if (!inside(a, 0)) continue;
+      load_values<8>(g.z.g, g.z.g_dtype, at(a, 0), u[a]);
+      if (g.z.m) load_values<8>(g.z.m, MOE_F32, at(a, 0), m[a]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        if (inside(a, b)) {
+          float one[1];
+          load_values<1>(g.z.g, g.z.g_dtype, at(a, b), one);
+          u[a][b] = one[0];
+          if (g.z.m) {
+            load_values<1>(g.z.m, MOE_F32, at(a, b), one);
+            m[a][b] = one[0];
+          }
+        }
+    }
+  }
+  if (!g.z.m) return;
+#pragma unroll
+  for (int a = 0; a < 8; ++a) {
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const float d = g.z.gain * (u[a][b] * gs);
+      if (fresh) m[a][b] = fmaf(g.z.mu, m[a][b], d);
+      u[a][b] = g.z.nesterov ? fmaf(g.z.mu, m[a][b], d) : m[a][b];
+    }
+    if (!fresh) continue;
+    if (VEC == 8) {
+      if (inside(a, 0)) store_values<8>(g.z.m, MOE_F32, at(a, 0), m[a]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        if (inside(a, b)) {
+          const float one[1] = {m[a][b]};
+          store_values<1>(g.z.m, MOE_F32, at(a, b), one);
+        }
+    }
+  }
+}
+
+// WIDE: rows of X are rows in memory (else columns).
+template <int VEC, bool WIDE>
+__global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(const __grid_constant__ SmallArgs g) {
+  using L = SmallLayout;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sx = smem, *ss = smem + L::kOffS, *sq = smem + L::kOffQ, *part = smem + L::kOffPart;
+  uint64_t *done = reinterpret_cast<uint64_t *>(smem + L::kOffBar), *never = done + 1;
+  uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(done + 2);
+  float *sums = reinterpret_cast<float *>(smem + L::kOffSums), *cluster_sums = sums + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), ctas = (int)cluster_size();
+  const int64_t e = blockIdx.x / ctas;
+  int *status = g.z.status;
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(done, 1);
+      mbar_init(never, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(tmem_ptr, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 16) status[threadIdx.x] = 0;
+  const uint32_t tmem_base = *tmem_ptr, smem_base = smem_u32(smem);
+  const int64_t base = e * (int64_t)g.n * g.k;
+  const int first = rank * g.kc, across = g.kc / 8;            // this CTA's columns, eight at a time
+  const float gs = g.z.grad_scale ? *g.z.grad_scale : 1.f;
+
+  // Momentum and norm, blocks of 8 x 8 values; threads next to each other take what lies next to each other in memory.
+  // A block's values are those of the same thread both times.
+  const int down = (g.n + 7) / 8;
+  auto block_at = [&](int i, int &r, int &c) {
+    r = 8 * (WIDE ? i / across : i % down);
+    c = 8 * (WIDE ? i % across : i / down);
+  };
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < down * across; i += L::kThreads) {
+    int r, c;
+    block_at(i, r, c);
+    float u[8][8];
+    small_values<VEC, WIDE>(g, base, r, first + c, gs, true, u);
+#pragma unroll
+    for (int j = 0; j < 64; ++j) sum = fmaf(u[j >> 3][j & 7], u[j >> 3][j & 7], sum);
+  }
+  sum = block_sum(sum, sums);
+  if ((int)threadIdx.x < ctas) store_cluster_f32(mapa_shared(smem_u32(cluster_sums + rank), threadIdx.x), sum);
+  // rows past the last are zero
+  for (int i = threadIdx.x; i < (L::kMostN - 8 * down) * across; i += L::kThreads)
+    *reinterpret_cast<uint4 *>(sx + small_place(8 * down + i / across, 8 * (i % across))) = make_uint4(0, 0, 0, 0);
+  cluster_sync();
+  sum = 0.f;
+  for (int c = 0; c < ctas; ++c) sum += cluster_sums[c];
+  const float norm = sqrtf(sum), by = norm == 0.f ? 0.f : kScale / (norm < g.z.eps ? g.z.eps : norm);
+  for (int i = threadIdx.x; i < down * across; i += L::kThreads) {
+    int r, c;
+    block_at(i, r, c);
+    float u[8][8];
+    small_values<VEC, WIDE>(g, base, r, first + c, gs, false, u);
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      uint32_t w[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        w[b] = WIDE ? pack_f16(u[a][2 * b] * by, u[a][2 * b + 1] * by) : pack_f16(u[2 * b][a] * by, u[2 * b + 1][a] * by);
+      *reinterpret_cast<uint4 *>(sx + small_place(r + a, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+
+  const int n16 = (g.n + 15) & ~15;
+  const uint32_t t_x = tmem_base + L::kMostN;                   // S and Q in columns 0 .. 127, X behind them
+  uint32_t phase = 0;
+  // what a stage writes is ordered before its MMAs, and these before what follows
+  auto multiply = [&](auto issue) {
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && elect_one()) {
+      tc_fence_after();
+      issue();
+      tc_commit(done);
+    }
+    __syncwarp();
+    mbar_wait_reset(done, phase, status, kLimit, kWaitMmaDone, (int)phase);
+    phase ^= 1;
+    tc_fence_after();
+  };
+  // desc of an operand summed along its rows (K-major) or, X, across them
+  auto desc_k = [&](int off) { return make_smem_desc(smem_base + (uint32_t)off, 16, 1024, kSwizzle128B); };
+  const int q = warp & 3, row = 32 * q + lane;                  // this thread's TMEM lane: a row of S, Q and X
+  const uint32_t t_lane = (uint32_t)(32 * q) << 16;
+  // a row's 32 columns from TMEM column `from`: factor, diagonal, FP16, into blocks at `to`
+  auto take_square = [&](float alpha, float beta, unsigned char *to) {
+    uint32_t v[2][32];
+    const int c1 = 32 * (warp >> 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c1 + 64 * h < n16) tmem_ld_32x32b_x32(tmem_base + t_lane + (uint32_t)(c1 + 64 * h), v[h]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c0 = c1 + 64 * h;
+      if (c0 >= n16) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 8 * j + 2 * i;
+          const float a = __uint_as_float(v[h][8 * j + 2 * i]), b = __uint_as_float(v[h][8 * j + 2 * i + 1]);
+          w[i] = pack_f16(c < n16 ? fmaf(alpha, a, c == row && row < g.n ? beta : 0.f) : 0.f,
+                          c < n16 ? fmaf(alpha, b, c + 1 == row && row < g.n ? beta : 0.f) : 0.f);
+        }
+        *reinterpret_cast<uint4 *>(to + small_place(row, c0 + 8 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+
+  for (int it = 0; it < g.steps; ++it) {
+    // S = X X^T + shift (without a square: Q)
+    multiply([&] {
+      if (g.inject_wait == 1 && it == 0) mbar_wait_reset(never, 0, status, kInjectedLimit, kWaitInjected, 0);
+      const uint32_t idesc = make_idesc_f16(128, (uint32_t)n16, false, false);
+      for (int b = 0; b < g.kc / 64; ++b) {
+        const uint64_t d = desc_k(b * L::kBlock);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tmem_base, d + 2 * kk, d + 2 * kk, idesc, b > 0 || kk > 0 ? 1u : 0u);
+      }
+    });
+    unsigned char *gram = g.square ? ss : sq;
+    if (ctas == 1) {
+      take_square(g.gram_alpha, g.gram_beta, gram);
+    } else {
+      // this CTA's part, 16 bytes at place c ^ (row & 7) of a row's 32
+      for (int c0 = 32 * (warp >> 2); c0 < n16; c0 += 64) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem_base + t_lane + (uint32_t)c0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4 *>(part + row * 512 + (((c0 / 4 + j) ^ (row & 7)) << 4)) =
+              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      cluster_sync();
+      const int share = L::kMostN / ctas;
+      for (int i = threadIdx.x; i < share * (n16 / 8); i += L::kThreads) {
+        const int r = rank * share + i / (n16 / 8), c = i % (n16 / 8);
+        float4 a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          a[k] = b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < ctas) {
+            const uint32_t from = mapa_shared(smem_u32(part) + (uint32_t)(r * 512), (uint32_t)k);
+            a[k] = load_cluster_v4(from + (uint32_t)(((2 * c) ^ (r & 7)) << 4));
+            b[k] = load_cluster_v4(from + (uint32_t)(((2 * c + 1) ^ (r & 7)) << 4));
+          }
+        }
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          t[0] += a[k].x; t[1] += a[k].y; t[2] += a[k].z; t[3] += a[k].w;
+          t[4] += b[k].x; t[5] += b[k].y; t[6] += b[k].z; t[7] += b[k].w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = fmaf(g.gram_alpha, t[j], 8 * c + j == r && r < g.n ? g.gram_beta : 0.f);
+        const int4 w = make_int4((int)pack_f16(t[0], t[1]), (int)pack_f16(t[2], t[3]), (int)pack_f16(t[4], t[5]), (int)pack_f16(t[6], t[7]));
+        for (int k = 0; k < ctas; ++k)
+          store_cluster_v4(mapa_shared(smem_u32(gram) + (uint32_t)small_place(r, 8 * c), (uint32_t)k), w);
+      }
+      cluster_sync();
+    }
+    if (g.square) {
+      multiply([&] {
+        const uint32_t idesc = make_idesc_f16(128, (uint32_t)n16, false, false);
+        for (int kk = 0; 16 * kk < n16; ++kk) {
+          const uint64_t d = desc_k(L::kOffS + (kk >> 2) * L::kBlock) + 2 * (kk & 3);
+          tc_mma_f16(tmem_base, d, d, idesc, kk > 0 ? 1u : 0u);
+        }
+      });
+      take_square(g.square_alpha, g.square_beta, sq);
+    }
+    // X = Q X
+    multiply([&] {
+      for (int c0 = 0; c0 < g.kc; c0 += 256) {
+        const uint32_t idesc = make_idesc_f16(128, (uint32_t)min(256, g.kc - c0), false, true);
+        const uint64_t x = make_smem_desc(smem_base + (uint32_t)(c0 / 64 * L::kBlock), L::kBlock, 1024, kSwizzle128B);
+        for (int kk = 0; 16 * kk < n16; ++kk)
+          tc_mma_f16(t_x + (uint32_t)c0, desc_k(L::kOffQ + (kk >> 2) * L::kBlock) + 2 * (kk & 3), x + 128 * kk, idesc, kk > 0 ? 1u : 0u);
+      }
+    });
+    const float unit = 1.f / kScale;
+    for (int c1 = 32 * (warp >> 2); c1 < g.kc; c1 += 128) {
+      uint32_t v[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (c1 + 64 * h < g.kc) tmem_ld_32x32b_x32(t_x + t_lane + (uint32_t)(c1 + 64 * h), v[h]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c0 = c1 + 64 * h;
+        if (c0 >= g.kc) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack_f16(unit * __uint_as_float(v[h][8 * j + 2 * i]), unit * __uint_as_float(v[h][8 * j + 2 * i + 1]));
+          *reinterpret_cast<uint4 *>(sx + small_place(row, c0 + 8 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // p = keep p - rate X, and its copy: runs of RUN values of memory, next to each other for threads next to each other
+  constexpr int RUN = VEC;
+  const float out = (g.z.update ? -g.z.rate : 1.f) * (1.f / kScale);
+  const int mine = min(g.kc, g.k - first), lines = WIDE ? g.n : mine, runs = ((WIDE ? mine : g.n) + RUN - 1) / RUN;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < lines * runs; i += L::kThreads) {
+    const int line = i / runs, at_run = (i - line * runs) * RUN;
+    const int64_t at = base + (WIDE ? (int64_t)line * g.k + first + at_run : (int64_t)(first + line) * g.n + at_run);
+    float x[RUN], y[RUN];
+    if (g.z.update) load_values<RUN>(g.z.p, g.z.p_dtype, at, y);
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) {
+      const int r = WIDE ? line : at_run + j, c = WIDE ? at_run + j : line;
+      x[j] = __half2float(*reinterpret_cast<const __half *>(sx + small_place(r, c & ~7) + 2 * (c & 7)));
+      y[j] = g.z.update ? fmaf(out, x[j], g.z.keep * y[j]) : out * x[j];
+    }
+    store_values<RUN>(g.z.p, g.z.p_dtype, at, y);
+    if (g.z.copy) store_values<RUN>(g.z.copy, MOE_BF16, at, y);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 struct Stack {              // of a call's workspace
@@ -749,6 +1109,58 @@ int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, co
   return bytes < moe_muon_workspace_size(E, N, K) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
+// CTAs for a matrix of the small path, or 0: it is not one.  Clusters that fill the GPU once at most, as an exchange over
+// the cluster takes 8 of an iteration's 12 us: one matrix of 128 x 2048 in 75 us and 104 by the products' kernel, 64 of them
+// in 390 and 207.  Matrices of one CTA in any number: 64 of 128 x 128 in 27 and 71 us, 200 of 64 x 256 in 49 and 95.
+int small_cluster(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns) {
+  const int64_t n = std::min(N, K), k = std::max(N, K);
+  if (n > SmallLayout::kMostN || k > 8 * SmallLayout::kMostColumns || ns.steps == 0) return 0;
+  int ctas = 1;
+  while (ceil_div(k, ctas) > SmallLayout::kMostColumns) ctas *= 2;
+  return ctas == 1 || E * ctas <= num_sms() ? ctas : 0;
+}
+
+template <int VEC, bool WIDE>
+int run_small(const Elementwise &z, const moe_newton_schulz &ns, int ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(small_muon_kernel<VEC, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallLayout::kBytes) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  SmallArgs g{};
+  g.z = z;
+  g.n = (int)std::min(z.N, z.K);
+  g.k = (int)std::max(z.N, z.K);
+  g.kc = (int)round_up(ceil_div(g.k, ctas), 64);
+  g.steps = ns.steps;
+  g.square = ns.c != 0.f;
+  const float unit = 1.f / kScale, shift = g.square ? ns.b / (2.f * ns.c) : 0.f;
+  g.gram_alpha = g.square ? unit : ns.b * unit;
+  g.gram_beta = kScale * (g.square ? shift : ns.a);
+  g.square_alpha = ns.c * unit;
+  g.square_beta = kScale * (ns.a - ns.b * shift * 0.5f);
+  g.inject_wait = injected_wait();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(z.E * ctas));
+  cfg.blockDim = dim3(SmallLayout::kThreads);
+  cfg.dynamicSmemBytes = SmallLayout::kBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, small_muon_kernel<VEC, WIDE>, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 template <int VEC>
 int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *base, cudaStream_t st) {
   const int64_t E = z.E, N = z.N, K = z.K;
@@ -803,6 +1215,9 @@ int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *
 int run_stack(const Elementwise &z, const moe_newton_schulz &ns, void *workspace, cudaStream_t st) {
   const Stack w = stack_layout(z.E, z.N, z.K);
   const bool vec = z.K % 8 == 0 && aligned(z.g, 16) && aligned(z.m, 16) && aligned(z.p, 16) && aligned(z.copy, 16);
+  if (const int ctas = small_cluster(z.E, z.N, z.K, ns))
+    return z.N <= z.K ? (vec ? run_small<8, true>(z, ns, ctas, st) : run_small<1, true>(z, ns, ctas, st))
+                      : (vec ? run_small<8, false>(z, ns, ctas, st) : run_small<1, false>(z, ns, ctas, st));
   return vec ? run_stack<8>(z, ns, w, static_cast<char *>(workspace), st)
              : run_stack<1>(z, ns, w, static_cast<char *>(workspace), st);
 }

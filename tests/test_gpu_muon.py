@@ -83,7 +83,8 @@ def ortho(B, x, dtype=BF16, **how):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 7), (2, 5, 3), (3, 2, 300), (2, 64, 64), (2, 256, 128), (1, 300, 1000), (1, 1000, 300), (5, 40, 72),
-          (1, 257, 513), (2, 520, 264), (1, 31, 4100), (1, 1024, 2048), (1, 2050, 700), (90, 16, 24), (3, 513, 513)]
+          (1, 257, 513), (2, 520, 264), (1, 31, 4100), (2, 128, 384), (2, 385, 128), (1, 127, 3070), (3, 800, 24), (1, 129, 129),
+          (2, 2000, 128), (1, 17, 1600), (1, 1024, 2048), (1, 2050, 700), (90, 16, 24), (3, 513, 513)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -104,7 +105,7 @@ def test_matrix_in_place_and_repeats(B):
 
 @pytest.mark.parametrize("how", [dict(steps=0), dict(steps=1), dict(steps=8), dict(coefficients=(1.5, -0.5, 0.0), steps=12),
                                  dict(coefficients=(1.875, -1.25, 0.375), steps=7), dict(eps=1.0)])
-@pytest.mark.parametrize("shape", [(2, 96, 160), (2, 160, 96)])
+@pytest.mark.parametrize("shape", [(2, 96, 160), (2, 160, 96), (2, 96, 800), (2, 160, 240), (2, 240, 160)])
 def test_other_polynomials(B, shape, how):
     x = randn(*shape, seed=5, scale=1e-3, dtype=F32)
     check(ortho(B, x, F32, **how), x, **how)
@@ -129,8 +130,9 @@ def test_far_scales(B, scale):
     check(ortho(B, x * scale, F32, eps=0.0), x * scale, eps=0.0)
 
 
-def test_zeros_infinities_and_nan_stay_in_their_matrix(B):
-    x = randn(5, 72, 136, seed=8)
+@pytest.mark.parametrize("shape", [(5, 72, 136), (5, 72, 1360), (5, 200, 136)])
+def test_zeros_infinities_and_nan_stay_in_their_matrix(B, shape):
+    x = randn(*shape, seed=8)
     want = ortho(B, x)
     y = x.clone()
     y[1] = 0
@@ -151,7 +153,7 @@ def emulate(p, g, m, clip, lr, mu, wd, scale, nesterov):
     return p.double() * (1 - lr * wd) - lr * scale * o, m, lr * scale * o, worst
 
 
-@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 65, 33), (3, 128, 72), (2, 72, 264)])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 65, 33), (3, 128, 72), (2, 72, 264), (2, 100, 900), (2, 901, 100), (2, 136, 264), (2, 265, 133)])
 @pytest.mark.parametrize("ptype,gtype,nesterov", [(F32, BF16, True), (BF16, F32, False), (BF16, BF16, True), (F32, F32, True)])
 def test_step(B, shape, ptype, gtype, nesterov):
     from moe_expert_layer_counting_gb300 import Muon
@@ -177,11 +179,11 @@ def test_step(B, shape, ptype, gtype, nesterov):
 def test_several_parameters(B):
     """Matrices, stacks and a stack of stacks in one object, against one object each."""
     from moe_expert_layer_counting_gb300 import Muon
-    shapes = [(40, 24), (3, 16, 72), (2, 2, 33, 20), (0, 8, 8)]
+    shapes = [(40, 24), (3, 16, 72), (2, 2, 33, 20), (0, 8, 8), (2, 200, 136)]
     make = lambda: [randn(*s, seed=i, scale=0.02, dtype=F32) for i, s in enumerate(shapes)]      # noqa: E731
     grads = [randn(*s, seed=9 + i, scale=1e-3) for i, s in enumerate(shapes)]
     together, apart = make(), make()
-    copies = [None, torch.zeros(shapes[1], dtype=BF16, device="cuda"), None, None]
+    copies = [None, torch.zeros(shapes[1], dtype=BF16, device="cuda"), None, None, None]
     opt = Muon(together, lr=0.01, copies=copies)
     singles = [Muon([p], lr=0.01) for p in apart]
     for _ in range(3):
@@ -207,9 +209,9 @@ def test_state_resumes(B):
     assert torch.equal(p, q) and torch.equal(whole.state["m"][0], second.state["m"][0])
 
 
-def test_streams_and_graphs(B):
+@pytest.mark.parametrize("shape", [(2, 300, 136), (3, 100, 40), (2, 64, 1000)])
+def test_streams_and_graphs(B, shape):
     from moe_expert_layer_counting_gb300 import Muon
-    shape = (2, 300, 136)
     grads = [randn(*shape, seed=i, scale=1e-3) for i in range(3)]
     p = randn(*shape, seed=9, scale=0.02, dtype=F32)
     start = p.clone()
@@ -239,7 +241,7 @@ def test_streams_and_graphs(B):
     assert torch.equal(q, want)
 
 
-@pytest.mark.parametrize("shape", [(2, 300, 136), (1, 136, 300)])
+@pytest.mark.parametrize("shape", [(2, 300, 136), (1, 136, 300), (2, 72, 40), (1, 100, 2000)])
 def test_a_wait_that_runs_out_is_reported(B, monkeypatch, shape):
     x, out = randn(*shape), torch.zeros(shape, dtype=BF16, device="cuda")
     ws = torch.empty(B.moe_muon_workspace_size(*shape), dtype=torch.uint8, device="cuda")
