@@ -269,11 +269,11 @@ struct NsArgs {
 
 struct NsLayout {
   static constexpr int kStages = 6, kSlot = 32768, kEpiBytes = 4096;
-  static constexpr int kClaims = 2;     // (three: 190 instead of 185 us for a step of 8 matrices of 1000 x 520)
+  static constexpr int kClaims = 2, kAhead = 5;     // items in the ring; blocks before an item's last that the next is claimed
   static constexpr int kOffEpi = kStages * kSlot;
   static constexpr int kOffItems = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffBar = kOffItems + 16 * kClaims;
-  static constexpr int kNumBars = 2 * kStages + 6 + 2 * kClaims;
+  static constexpr int kNumBars = 2 * kStages + 7 + 2 * kClaims;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * kNumBars + 63) & ~63;
   static constexpr int kBytes = 1024 + kOffTmemPtr + 64;
 };
@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
   uint64_t *never = mma_done + 1;
   uint64_t *item_full = never + 1;                                       // each CTA
   uint64_t *item_empty = item_full + L::kClaims;                         // leader: both CTAs' roles have read it
+  uint64_t *want = item_empty + L::kClaims;                              // leader: its loads are nearly done
   int4 *ring = reinterpret_cast<int4 *>(smem + L::kOffItems);
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -422,6 +423,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
       }
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
+      mbar_init(want, 1);
       for (int c = 0; c < L::kClaims; ++c) {
         mbar_init(item_full + c, 1);
         mbar_init(item_empty + c, 2 + 2 * GP::kEpiWarps + 1);      // loads, epilogues, the leader's MMAs
@@ -485,6 +487,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
             else
               tma_load_3d_2sm(b + j * b_box * GP::kBK * 2, b_map, bar, k0, col + b_box * j, it.e, policy);
           }
+          if (rank == 0 && kb == max(0, blocks - L::kAhead)) mbar_arrive(want);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == L::kStages) { stage = 0; phase ^= 1; }
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
     if (rank == 0 && elect_one()) {
       const uint32_t ring1 = mapa_shared(smem_u32(ring), 1), full1 = mapa_shared(smem_u32(item_full), 1);
       int slot = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, wanted = 0;
       for (;;) {
         if (!mbar_wait_reset(item_empty + slot, phase ^ 1, status, kLimit, kWaitArrival, slot)) break;
         const int4 v = ns_item(g, (int64_t)(uint32_t)atomicAdd(g.ticket, 1));
@@ -555,6 +558,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
         mbar_arrive_cluster(full1 + 8 * (uint32_t)slot);
         if (v.w < 0) break;
         if (++slot == L::kClaims) { slot = 0; phase ^= 1; }
+        // the next when this one's loads are nearly done: a pair that held one more would keep it from pairs that wait for
+        // nothing (one matrix of 2048 x 2048 in 393 us instead of 242, of 512 x 512 in 132 instead of 90)
+        if (!mbar_wait_reset(want, wanted, status, kLimit, kWaitArrival, slot)) break;
+        wanted ^= 1;
       }
     }
     __syncwarp();
@@ -1046,9 +1053,10 @@ bool encode_f16(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The width of a stage's tiles.  A pair of SMs takes some 0.33 us for 64 reduction values of a 256 x 256 tile, bound by its
-// tensor cores, 0.2 and 0.17 of a tile of 128 and 64 columns, bound by the loads: narrower tiles pay where
-// there are too few for the pairs, or the last round of wide ones is nearly empty.
+// The width of a stage's tiles.  64 reduction values of a tile of 256, 128 or 64 columns keep a pair's tensor cores busy
+// for 0.27, 0.14 or 0.07 us and bring 64, 48 or 40 KB to it, at 13.5 TB/s from L2 over all pairs that work and no more
+// than 0.12 KB/ns for one SM; an item's start and end take some 3 us that the next one's loads do not hide in a chain of
+// short stages.
 void choose_tiles(NsStage &s, int64_t E) {
   const int64_t pairs = num_sms() / 2, mt = ceil_div(s.M, GP::kM);
   double best = 0;
@@ -1056,9 +1064,10 @@ void choose_tiles(NsStage &s, int64_t E) {
     const int64_t ct = ceil_div(s.C, tn), across = GP::kM / tn;
     int64_t items = 0;
     for (int64_t m = 0; m < mt; ++m) items += s.symmetric ? ct - m * across : ct;
-    const double rounds = (double)ceil_div(E * items, pairs), each = tn == 256 ? 0.33 : tn == 128 ? 0.2 : 0.17;
-    const double cost = rounds * (ceil_div(s.R, GP::kBK) * each + 0.5);
-    if (tn == 256 || cost < 0.95 * best) {
+    const double work = (double)std::min(pairs, E * items), kb = tn == 256 ? 64 : tn == 128 ? 48 : 40;
+    const double block = std::max({0.27 * tn / 256, kb / 2 / 120, kb * work / 13.5e3});
+    const double cost = (double)ceil_div(E * items, pairs) * (ceil_div(s.R, GP::kBK) * block + 0.5) + 3;
+    if (tn == 256 || cost < 0.97 * best) {
       best = cost;
       s.tn = tn;
       s.items = (int)items;
