@@ -24,9 +24,11 @@
  *   - E >= 0 (0: a no-op), 1 <= N, K < 2^20, steps 0 .. 64.  All tensors are contiguous
  *     and aligned to their elements; 16-byte alignment and K a multiple of 8 are faster.
  *   - The iterates are held in FP16 with a fixed scale of 2^12, their sums in float32: eleven bits
- *     where BF16 has eight.  For matrices of independent values the result is off by
- *     1e-3 to 3e-3 in norm (BF16 iterates: 1e-2 to 2e-2), for ones of a few large and many
- *     small singular values by up to 1.5e-2 (BF16: up to 1.2e-1).
+ *     where BF16 has eight.  The polynomial enlarges what lies in directions of small singular values by up
+ *     to a^steps, a rounding as well: in norm the result is off by 1e-3 to 3e-3 for matrices of independent
+ *     values (BF16 iterates: 1e-2 to 2e-2), by up to 1.5e-2 for ones of a few large and many small singular
+ *     values (0.12), by 0.05 for rank 16, 0.08 for rank 4 and 0.15 for rank 1, all of it in directions that the
+ *     matrix lacks (0.4, 0.6 and 1.2, and as much as that from rounding such a matrix to BF16 alone).
  *     Momentum, norm and update are computed in float32; squares that overflow float32
  *     (values of 1e18 and more) give a norm of infinity.
  *   - c is 0, or |b / (2 c)| at most 8; a, b, c at most 64 in magnitude (otherwise MOE_ERR_INVALID_ARG):

@@ -56,7 +56,10 @@ EXPORTED = ["mxq_quantize_act", "mxq_quantize_weight", "moe_route_topk", "moe_ro
             "moe_workspace_size", "moe_forward", "moe_get_device_status", "moe_status_string", "moe_version",
             "bfp8_quantize_act", "bfp8_quantize_weight", "moe_bfp8_workspace_size", "moe_forward_bfp8",
             "moe_grouped_workspace_size", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
-            "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward", "moe_adamw_step"]
+            "moe_gated_workspace_size", "moe_gated_forward", "moe_gated_dgrad",
+            "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward",
+            "moe_layernorm_forward", "moe_layernorm_workspace_size", "moe_layernorm_backward", "moe_adamw_step",
+            "moe_muon_workspace_size", "moe_orthogonalize", "moe_muon_step"]
 
 
 class MoeExpertArgs(ctypes.Structure):
