@@ -539,9 +539,11 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
   for (int i = threadIdx.x; i < z.H / 2; i += threads) part[i] = reinterpret_cast<const float4 *>(sums)[i];
 }
 
-// Sums over the blocks' parts: 32 lanes a column each, 8 warps share the parts.
-__global__ void __launch_bounds__(256) sum_blocks_kernel(const float *part, int blocks, int H, float *dw, float *dbias) {
-  __shared__ float red[8][32];
+// Sums over the blocks' parts: 32 lanes a column each, kSumWarps warps share the parts, all loads of a thread in flight.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(32 * kSumWarps) sum_blocks_kernel(const float *part, int blocks, int H, float *dw, float *dbias) {
+  __shared__ float red[kSumWarps][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -549,12 +551,12 @@ __global__ void __launch_bounds__(256) sum_blocks_kernel(const float *part, int 
   float sum = 0.f;
   if (i < 2 * H)
 #pragma unroll 8
-    for (int b = warp; b < blocks; b += 8) sum += part[(int64_t)b * 2 * H + i];
+    for (int b = warp; b < blocks; b += kSumWarps) sum += part[(int64_t)b * 2 * H + i];
   red[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || i >= 2 * H) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) sum += red[k][lane];
+  for (int k = 1; k < kSumWarps; ++k) sum += red[k][lane];
   float *out = i < H ? dw : dbias;
   if (out) out[i < H ? i : i - H] = sum;
 }
@@ -709,6 +711,6 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   rc = f32 ? (add ? launch(0.f, true_type{}) : launch(0.f, false_type{}))
            : (add ? launch(uint16_t{0}, true_type{}) : launch(uint16_t{0}, false_type{}));
   if (rc != MOE_OK || !z.part) return rc;
-  return launch_pdl(sum_blocks_kernel, dim3((unsigned)ceil_div(2 * z.H, 32)), dim3(256), 0, stream, z.part, (int)blocks, z.H, a->dw,
+  return launch_pdl(sum_blocks_kernel, dim3((unsigned)ceil_div(2 * z.H, 32)), dim3(32 * kSumWarps), 0, stream, z.part, (int)blocks, z.H, a->dw,
                     a->dbias);
 }
