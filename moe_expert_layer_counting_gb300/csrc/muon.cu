@@ -269,7 +269,7 @@ struct NsArgs {
 
 struct NsLayout {
   static constexpr int kStages = 6, kSlot = 32768, kEpiBytes = 4096;
-  static constexpr int kClaims = 2, kAhead = 5;     // items in the ring; blocks before an item's last that the next is claimed
+  static constexpr int kClaims = 2, kAhead = 8;     // items in the ring; blocks before an item's last that the next is claimed
   static constexpr int kOffEpi = kStages * kSlot;
   static constexpr int kOffItems = kOffEpi + GP::kEpiWarps * kEpiBytes;
   static constexpr int kOffBar = kOffItems + 16 * kClaims;
@@ -281,7 +281,9 @@ static_assert(NsLayout::kBytes <= 232448, "shared memory of one CTA");
 
 struct NsItem {
   int e, m, c, at;          // at: 3 * iteration + stage; -1 after the last
+  bool ready;               // the matrix is known to be ready
 };
+constexpr int kNsReady = 1 << 16;          // in the ring: beside at
 
 // Packed words turned as turn_bf16 turns floats: word i of a lane holds rows 2 i and
 // 2 i + 1 of its column.
@@ -328,7 +330,7 @@ struct NsItems {
     const bool got = mbar_wait_reset(full + slot, phase, status, kLimit, kWaitArrival, slot);
     if (!(wide ? __all_sync(0xffffffffu, got) : got)) return false;
     const int4 v = items[slot];
-    it = NsItem{v.x, v.y, v.z, v.w};
+    it = NsItem{v.x, v.y, v.z, v.w < 0 ? -1 : v.w & (kNsReady - 1), (v.w & kNsReady) != 0};
     if (wide) __syncwarp();
     if (!wide || (threadIdx.x & 31) == 0) mbar_arrive_done(empty0 + 8 * (uint32_t)slot);
     if (++slot == NsLayout::kClaims) { slot = 0; phase ^= 1; }
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
         // rows of a box of b, and boxes
         const int b_box = s.b_mn ? 64 : half > 64 ? 128 : 32, b_boxes = (half + b_box - 1) / b_box;
         const uint32_t bytes = (uint32_t)(GP::kATile + b_boxes * b_box * GP::kBK * 2);
-        ok = ns_wait(g.done + it.e, ns_arrivals(g, it.at), status, it.at);
+        if (!it.ready) ok = ns_wait(g.done + it.e, ns_arrivals(g, it.at), status, it.at);
         fence_proxy_async_global();       // what was stored from registers is read by TMA
         for (int kb = 0; kb < blocks && ok; ++kb) {
           unsigned char *a = smem + stage * L::kSlot, *b = a + GP::kATile;
@@ -551,7 +553,10 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
       uint32_t phase = 0, wanted = 0;
       for (;;) {
         if (!mbar_wait_reset(item_empty + slot, phase ^ 1, status, kLimit, kWaitArrival, slot)) break;
-        const int4 v = ns_item(g, (int64_t)(uint32_t)atomicAdd(g.ticket, 1));
+        int4 v = ns_item(g, (int64_t)(uint32_t)atomicAdd(g.ticket, 1));
+        // one look at the matrix's counter: if it is ready, the loads need not look (they are ordered after this one, through
+        // the ring)
+        if (v.w >= 0 && ld_acquire_gpu(g.done + v.x) >= ns_arrivals(g, v.w)) v.w |= kNsReady;
         ring[slot] = v;
         store_cluster_v4(ring1 + 16 * (uint32_t)slot, v);
         mbar_arrive(item_full + slot);
