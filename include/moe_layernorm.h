@@ -22,8 +22,8 @@
  *     (enum moe_dtype), dw and dbias float32.  Means and sums are held in float32, the variance
  *     is that of the values less their mean; each output is rounded once: n is the norm of s before its rounding.
  *   - Row strides in elements: multiples of 8, at least H.  Pointers are 16-byte
- *     aligned, the workspace 256-byte (MOE_ERR_MISALIGNED).  s may be x, n may be b (or x, s: of the
- *     same type), dx may be ds, s or dn of the same type; no other overlap.
+ *     aligned, the workspace 256-byte (MOE_ERR_MISALIGNED).  s may be x, n may be b (without b: x),
+ *     dx may be ds, s or dn, each of the same type and with the same stride; no other overlap.
  *   - A row's n, s and dx depend on that row only.
  *   - Results do not depend on thread timing.
  */

@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   auto desc_k = [&](int off) { return make_smem_desc(smem_base + (uint32_t)off, 16, 1024, kSwizzle128B); };
   const int q = warp & 3, row = 32 * q + lane;                  // this thread's TMEM lane: a row of S, Q and X
   const uint32_t t_lane = (uint32_t)(32 * q) << 16;
-  // a row's 32 columns from TMEM column `from`: factor, diagonal, FP16, into blocks at `to`
+  // S or Q from TMEM: factor, diagonal, FP16, into blocks at `to`
   auto take_square = [&](float alpha, float beta, unsigned char *to) {
     uint32_t v[2][32];
     const int c1 = 32 * (warp >> 2);
@@ -1210,7 +1210,8 @@ int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *
       choose_tiles(stage, E);
       items += E * stage.items;
     }
-    if (items * ns.steps > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // tickets and a matrix's arrivals (16 a tile) are ints
+    if (items * ns.steps >= 1 << 27) return MOE_ERR_UNSUPPORTED_SHAPE;
     g.E = (int)E;
     g.steps = ns.steps;
     g.wide = wide;
