@@ -36,11 +36,13 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int p
 // ---------------------------------------------------------------- few rows
 
 // forward of up to kFewRows rows: products of matrices and a few vectors, bound by the weights' way from HBM.
-// A warp takes one gate row and its up row whole, all their loads in flight at
-// once, and the rows of x that belong to the expert from L1: every SM has work, where
-// the tensor cores' tiles of 256 weight rows are fewer than SMs, and no pair of SMs
-// is waited for.  Which calls: see few_rows_win().
-constexpr int kFewRows = 8, kFewWarps = 8;
+// A block takes eight columns of h, so eight gate and the eight up rows, its warps a share of the sums each. Every SM has
+// work, where the tiles of 256 weight rows are fewer than SMs, and no pair of SMs is waited for.
+// A warp's mma (m16n8k16: the one whose operands are registers, as the weights go through once) has the gate rows as rows
+// 0 to 7, the up rows as 8 to 15 and the rows of x as columns, so that a lane ends with gate and up of the same
+// values. The sum's order is free, so that a lane's 16 bytes of a row are two mma's operands as they are loaded.
+// Which calls: see few_rows_win().
+constexpr int kFewRows = 16, kFewWarps = 8;
 
 __device__ __forceinline__ uint4 load_once(const uint16_t *p) {
   uint4 v;
@@ -50,14 +52,11 @@ __device__ __forceinline__ uint4 load_once(const uint16_t *p) {
   return v;
 }
 
-__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
-    sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
-  }
-  return sum;
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t gate0, uint32_t up0, uint32_t gate1, uint32_t up1, uint32_t x0,
+                                         uint32_t x1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(gate0), "r"(up0), "r"(gate1), "r"(up1), "r"(x0), "r"(x1));
 }
 
 struct FewArgs {
@@ -69,55 +68,69 @@ struct FewArgs {
   GatedArgs gated;
 };
 
-// Column i of rows row0 .. row0 + rows - 1 (at most ROWS) of expert e.
-template <int ROWS>
-__device__ __forceinline__ void few_rows(const FewArgs &g, int e, int row0, int rows, int i, int lane) {
-  constexpr int kUnroll = ROWS == 1 ? 8 : ROWS == 2 ? 4 : 2;
-  const uint16_t *gate = g.w + ((int64_t)e * 2 * g.gated.I + i) * g.H, *up = gate + (int64_t)g.gated.I * g.H;
-  const uint16_t *x[ROWS];
+// Columns i0 .. i0 + 7 of rows row0 .. row0 + rows - 1 (at most 8 TILES) of expert e, by a block; red [warps][4 TILES][32].
+template <int TILES>
+__device__ __forceinline__ void few_rows(const FewArgs &g, int e, int row0, int rows, int i0, float *red) {
+  constexpr int kUnroll = TILES == 1 ? 6 : 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int of = lane >> 2;                            // the lane's weight row, and its row of x in each tile
+  const int64_t first = 32 * warp + 8 * (lane & 3);
+  const uint16_t *gate = g.w + ((int64_t)e * 2 * g.gated.I + i0 + of) * g.H, *up = gate + (int64_t)g.gated.I * g.H;
+  const uint16_t *x[TILES];
+  float d[TILES][4];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) x[r] = g.x + (int64_t)(row0 + min(r, rows - 1)) * g.ldx;
-  float a[ROWS], b[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) a[r] = b[r] = 0.f;
-  for (int64_t k0 = 8 * lane; k0 < g.H; k0 += 256 * kUnroll) {
-    uint4 wg[kUnroll], wu[kUnroll];
+  for (int t = 0; t < TILES; ++t) {
+    x[t] = g.x + (int64_t)(row0 + min(8 * t + of, rows - 1)) * g.ldx;
+    d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+  }
+  for (int64_t base = 0; base < g.H; base += 32 * kFewWarps * kUnroll) {
+    uint4 wg[kUnroll], wu[kUnroll], v[kUnroll][TILES];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
+      const int64_t k = base + first + 32 * kFewWarps * j;
       wg[j] = wu[j] = make_uint4(0, 0, 0, 0);
-      if (k0 + 256 * j < g.H) {
-        wg[j] = load_once(gate + k0 + 256 * j);
-        wu[j] = load_once(up + k0 + 256 * j);
+      if (k < g.H) {
+        wg[j] = load_once(gate + k);
+        wu[j] = load_once(up + k);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int64_t k = base + first + 32 * kFewWarps * j;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        v[j][t] = make_uint4(0, 0, 0, 0);
+        if (k < g.H) v[j][t] = __ldg(reinterpret_cast<const uint4 *>(x[t] + k));
       }
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
-      if (k0 + 256 * j < g.H)
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x[r] + k0 + 256 * j));
-          a[r] = dot8(wg[j], v, a[r]);
-          b[r] = dot8(wu[j], v, b[r]);
-        }
+      for (int t = 0; t < TILES; ++t) {
+        mma_16x8(d[t], wg[j].x, wu[j].x, wg[j].y, wu[j].y, v[j][t].x, v[j][t].y);
+        mma_16x8(d[t], wg[j].z, wu[j].z, wg[j].w, wu[j].w, v[j][t].z, v[j][t].w);
+      }
   }
-  float ga = 0.f, gb = 0.f;            // lane r: row r's
+  // of a tile: d[0], d[1] gate row `of` with rows 2 (lane % 4) and the next of x; d[2], d[3] the up row
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
+  for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a[r] += __shfl_xor_sync(0xffffffffu, a[r], o);
-      b[r] += __shfl_xor_sync(0xffffffffu, b[r], o);
-    }
-    if (lane == r) {
-      ga = a[r];
-      gb = b[r];
-    }
+    for (int c = 0; c < 4; ++c) red[(warp * 4 * TILES + 4 * t + c) * 32 + lane] = d[t][c];
+  __syncthreads();
+  if (warp >= 2 * TILES) return;             // warp: of a tile's gates, the first or the second (of an inlined call: on)
+  const int t = warp >> 1, c = warp & 1;
+  const int r = 8 * t + 2 * (lane & 3) + c, i = i0 + of;
+  if (r >= rows) return;
+  float ga = 0.f, gb = 0.f;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) {
+    ga += red[(w * 4 * TILES + 4 * t + c) * 32 + lane];
+    gb += red[(w * 4 * TILES + 4 * t + 2 + c) * 32 + lane];
   }
-  if (lane >= rows) return;            // (of an inlined call: on to the warp's next column)
-  const int64_t row = row0 + lane;
-  const float v = g.gated.row_w ? __ldg(g.gated.row_w + row) : 1.f;
+  const int64_t row = row0 + r;
+  const float scale = g.gated.row_w ? __ldg(g.gated.row_w + row) : 1.f;
   float dq;
-  const float h = ga * gate_sigmoid(g.gated.activation, ga, dq) * gb * v;
+  const float h = ga * gate_sigmoid(g.gated.activation, ga, dq) * gb * scale;
   reinterpret_cast<__nv_bfloat16 *>(g.gated.h)[row * g.gated.ld_h + i] = __float2bfloat16_rn(h);
   if (g.gated.a) {
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.gated.a) + row * g.gated.ld_a + i;
@@ -129,7 +142,7 @@ __device__ __forceinline__ void few_rows(const FewArgs &g, int e, int row0, int 
 __global__ void __launch_bounds__(32 * kFewWarps, 2) gated_few_kernel(const FewArgs g) {
   __shared__ int expert[kFewRows], runs;
   __shared__ int4 run[kFewRows];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float red[2][kFewWarps * 4 * (kFewRows / 8) * 32];        // a unit writes one while the last's is read
   if (threadIdx.x < kFewRows) expert[threadIdx.x] = -1;
   __syncthreads();
   pdl_launch_dependents();
@@ -164,18 +177,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) gated_few_kernel(const FewA
     runs = n;
   }
   __syncthreads();
-  const int total = runs * g.gated.I;
-  for (int u = (int)blockIdx.x * kFewWarps + warp; u < total; u += (int)gridDim.x * kFewWarps) {
-    const int n = u / g.gated.I, i = u - n * g.gated.I;
+  const int across = g.gated.I / 8, total = runs * across;
+  int turn = 0;
+  for (int u = (int)blockIdx.x; u < total; u += (int)gridDim.x, turn ^= 1) {
+    const int n = u / across, i0 = 8 * (u - n * across);
     const int e = run[n].x, row0 = run[n].y, rows = run[n].z;
-    if (rows == 1)
-      few_rows<1>(g, e, row0, rows, i, lane);
-    else if (rows == 2)
-      few_rows<2>(g, e, row0, rows, i, lane);
-    else if (rows <= 4)
-      few_rows<4>(g, e, row0, rows, i, lane);
+    if (rows <= 8)
+      few_rows<1>(g, e, row0, rows, i0, red[turn]);
     else
-      few_rows<8>(g, e, row0, rows, i, lane);
+      few_rows<2>(g, e, row0, rows, i0, red[turn]);
   }
 }
 
@@ -214,12 +224,13 @@ bool encode_gated_weights(CUtensorMap *map, const uint16_t *w, uint64_t H, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few rows, here against the tensor cores' kernel (I x H, us, graph replay): one dense block 512 x 2048, one row 4.3 and
-// 8.8, eight rows 8.2 and 8.8; 2048 x 7168, one row 14.4 and 18.2, two 15.2, four 17.9, eight 25 and 18.2 (arithmetic); 8
-// rows of 8 of 256 experts, 512 x 2048, 10.7 and 12.1, 2048 x 7168 (470 MB of weights) 89 and 73 (fewer bytes in flight).
+// Few rows, here against the tensor cores' tiles (I x H, us, graph replay): one dense block 512 x 2048, one row 4.4 and 8.8,
+// eight 5.2 and 8.8, sixteen 6.1 and 8.8; 2048 x 7168 11.5, 12.4, 13.9 and 18.2; 4096 x 8192 (134 MB of weights) 23, 24,
+// 26.3 and 25.6. 8 rows of 8 of 256 experts, 512 x 2048, 9.9 and 11.9, of 64, 2048 x 7168 (470 MB), 70.4 and 70.8;
+// 16 of 16, 512 x 2048 (67 MB), 17.0 and 16.5. So up to eight rows always, more while their weights are few.
 bool few_rows_win(const moe_gated_args *a) {
   const int64_t most = std::min<int64_t>(a->P, a->E);           // experts with rows
-  return a->P <= kFewRows && (a->E > 1 || a->P <= 2) && most * 4 * a->I * a->H <= (96LL << 20);
+  return a->P <= 8 || (a->P <= kFewRows && most * 4 * a->I * a->H <= (64LL << 20));
 }
 
 template <int OP>
@@ -231,8 +242,8 @@ int gated_product(const moe_gated_args *a, cudaStream_t st) {
   if (!kBack && few_rows_win(a)) {
     const FewArgs few{a->rows, a->w, a->ld_rows, a->H, a->offsets, (int)a->P, (int)a->E, reinterpret_cast<int *>(a->workspace),
                       {(int)a->I, a->activation, a->row_w, a->a, a->ld_a, a->h, a->ld_h, nullptr, 0, nullptr}};
-    const int64_t units = std::min<int64_t>(a->P, a->E) * a->I;
-    return launch_pdl(gated_few_kernel, dim3((unsigned)std::min<int64_t>(2 * num_sms(), ceil_div(units, kFewWarps))),
+    const int64_t units = std::min<int64_t>(a->P, a->E) * (a->I / 8);
+    return launch_pdl(gated_few_kernel, dim3((unsigned)std::min<int64_t>(2 * num_sms(), units)),
                       dim3(32 * kFewWarps), 0, st, few);
   }
   GMaps maps;

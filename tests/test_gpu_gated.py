@@ -164,6 +164,54 @@ def test_few_rows(B, case, activation):
     assert bool((h[~own] == 7).all()) and bool((a[~own if case % 3 else own | True] == 7).all())
 
 
+MORE = [
+    # counts, first, rows behind the last, I, H: runs of more than eight rows, a warp's share of the sum that ends inside or
+    # is empty, several rounds of columns
+    ([9], 0, 0, 8, 8), ([16], 0, 0, 40, 248), ([3, 10, 0, 2], 0, 1, 72, 1000), ([1] * 16, 0, 0, 512, 1032), ([12], 2, 2, 2048, 1544),
+    ([8, 8], 0, 0, 136, 40), ([0, 15, 1], 0, 0, 24, 2056), ([0] * 500 + [11], 3, 0, 16, 264), ([1], 0, 7, 4096, 6152), ([5], 0, 0, 4104, 1288),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MORE)))
+def test_up_to_sixteen_rows(B, case):
+    """As above, on both sides of eight rows, and bit by bit the same from a second call."""
+    counts, first, behind, I, H = MORE[case]
+    E, n, activation = len(counts), sum(counts), case % 2
+    P = first + n + behind
+    x, w = randn(P, H, seed=11), randn(E, 2 * I, H, seed=12, scale=1.5 * H ** -0.5)
+    own = torch.zeros(P, dtype=torch.bool, device="cuda")
+    own[first:first + n] = True
+    x[~own] = float("nan")
+    row_w, got = randn(P, seed=13, dtype=F32) if case % 3 else None, []
+    for _ in range(2):
+        wide = [torch.full((P, k + 8 * (1 + case % 2)), 7.0, dtype=BF16, device="cuda") for k in (I, 2 * I)]
+        h, a = wide[0][:, :I], wide[1][:, :2 * I]
+        ws = workspace(B, P, H, I, E)
+        B.moe_gated_forward(x, w, offsets_of(counts, first), h, ws, a=a, row_w=row_w, activation=activation)
+        assert B.moe_get_device_status(ws) == B.MOE_OK
+        check_forward(h, a, x, w, row_w, counts, activation, first)
+        assert bool((h[~own] == 7).all()) and bool((a[~own] == 7).all())
+        assert bool((wide[0][:, I:] == 7).all()) and bool((wide[1][:, 2 * I:] == 7).all())
+        got.append((h, a))
+    assert all(torch.equal(u, v) for u, v in zip(*got))
+
+
+@pytest.mark.parametrize("rows", [5, 12])
+def test_few_rows_infinities_and_nan_stay_in_their_row_and_column(B, rows):
+    x, w = randn(rows, 264, seed=1), randn(1, 144, 264, seed=2, scale=0.1)
+    offsets, ws = offsets_of([rows]), workspace(B, rows, 264, 72, 1)
+    fine, h = (torch.empty(rows, 72, dtype=BF16, device="cuda") for _ in range(2))
+    B.moe_gated_forward(x, w, offsets, fine, ws)
+    x[3, 7], x[4, 263] = float("nan"), float("inf")
+    w[0, 72 + 10, 100] = float("nan")
+    B.moe_gated_forward(x, w, offsets, h, ws)
+    good = torch.ones(rows, 72, dtype=torch.bool, device="cuda")
+    good[[3, 4]] = False
+    good[:, 10] = False
+    assert torch.equal(h[good], fine[good]) and bool(h[3].isnan().all()) and bool(h[:, 10].isnan().all())
+    assert bool(((~h[4].isfinite()) | (h[4] == 0)).all())
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 8], [0, 4, 8, 9], [-1, 4, 8, 8], [0, -3, 8, 8]])
 def test_few_rows_with_bad_offsets(B, bad):
     offsets = torch.tensor(bad, dtype=torch.int32, device="cuda")
