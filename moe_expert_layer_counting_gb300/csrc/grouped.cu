@@ -35,8 +35,7 @@ int rows_product(const uint16_t *in, int64_t ld_in, const uint16_t *w, const int
   g.out = out;
   g.inject_wait = injected_wait();
   g.status = reinterpret_cast<int *>(workspace);
-  const int64_t tiles = std::min<int64_t>(P, P / GP::kN + E);      // most row tiles of any offsets
-  return launch_grouped<OP>(maps, g, tiles * ceil_div(M, GP::kM), st);
+  return launch_grouped<OP>(maps, g, most_row_items(g), st);
 }
 
 }  // namespace
