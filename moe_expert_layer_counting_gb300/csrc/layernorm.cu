@@ -5,7 +5,8 @@
 // and written once, but a row needs its mean, then the squares of what is left
 // after it (and two sums of gradients), and ~20 operations a value.
 //   - A group of ceil(H / 512) warps owns a row at a time (two in the gradients),
-//     a thread sixteen columns; groups walk the rows with a stride of all groups.
+//     a thread sixteen columns; groups walk the rows with a stride of all groups.  Of rows of up to 192 columns
+//     a warp owns two or four (see lanes_of).
 //   - A thread copies (cp.async) its own columns of the rows to come into its own
 //     places in shared memory: the ring needs no barrier, only a wait for the
 //     thread's own copies, and values are read from it again for each of a row's
@@ -37,7 +38,7 @@ constexpr int kMostH = 16384;
 
 struct Rows {
   int64_t T;
-  int H, warps, groups;                   // warps of a group, groups of a block
+  int H, warps, lanes, groups;            // warps of a group (a part of one: 1) and its threads, groups of a block
   int w_dtype;
   float eps, inv_h;
   const void *x, *w, *bias;
@@ -141,7 +142,21 @@ __device__ __forceinline__ float both(P2 v) {
   return f.x + f.y;
 }
 
+// Sums over the `lanes` (8 or 16) threads that own a row, in each of them.
+template <int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int lanes) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+    if (o < lanes)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+
 // ---------------------------------------------------------------- forward
+
+// Kinds of a launch: kShort rows of up to 192 columns, which a part of a warp owns; kBig of more than 8192 (or what the
+// rings of the others do not hold).
+enum : int { kShort, kMiddle, kBig };
 
 // How the forward kernel goes about a launch: kRows rows of a group in work
 // together, kSets sets of them in the ring (the next set's sum is added up with
@@ -150,28 +165,31 @@ __device__ __forceinline__ float both(P2 v) {
 // sums take longer than their bytes: 8192 x 7168 in 47 us by twos and 55 one by one;
 // with b 84 by twos and 75 one by one.
 //   BIG   rows of more than 8192 columns: 1024 threads of 64 registers, a row at a time, weights from L1.
-template <typename XT, bool ADD, bool BIG>
+template <typename XT, bool ADD, int KIND>
 struct ForwardRing {
+  static constexpr bool BIG = KIND == kBig;
   static constexpr int kSlot = kColumns * (int)(sizeof(XT) + (ADD ? 2 : 0));       // bytes of a thread's part of a row
   static constexpr int kThreads = BIG ? 1024 : 512;
   static constexpr int kRows = BIG || kSlot >= 64 ? 1 : 2;
   static constexpr int kSets = BIG ? (kSlot > 64 ? 2 : 3) : kSlot > 64 ? 4 : kSlot == 64 ? 6 : 3;
   static constexpr int kRed = 2 * 128 * 4;                   // bytes of a group's sums
   static size_t bytes(int threads, int tpr) {
-    return (size_t)kSlot * kRows * kSets * threads + (size_t)(threads / tpr) * kRed;
+    return (size_t)kSlot * kRows * kSets * threads + (tpr > 32 ? (size_t)(threads / tpr) * kRed : 0);
   }
 };
 
-template <typename XT, bool ADD, bool BIG>
-__global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layernorm_kernel(const Rows z) {
-  using R = ForwardRing<XT, ADD, BIG>;
+template <typename XT, bool ADD, int KIND>
+__global__ void __launch_bounds__(ForwardRing<XT, ADD, KIND>::kThreads, 1) layernorm_kernel(const Rows z) {
+  using R = ForwardRing<XT, ADD, KIND>;
+  constexpr bool BIG = KIND == kBig, SHORT = KIND == kShort;
   constexpr int RUN = kRun<XT>, kRuns = kColumns / RUN, kRows = R::kRows, kSets = R::kSets;
   extern __shared__ __align__(16) unsigned char ring[];      // [kSets][kRows] of [run][thread] of x, the same of b; sums
-  const int threads = (int)blockDim.x, tpr = 32 * z.warps;
+  const int threads = (int)blockDim.x, tpr = z.lanes;
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
   const int64_t stride = (int64_t)gridDim.x * z.groups;
   int64_t row = (int64_t)blockIdx.x * z.groups + group;
-  float *red = reinterpret_cast<float *>(ring + kSets * kRows * R::kSlot * threads) + group * (R::kRed / 4);
+  const int sub = SHORT ? ((int)threadIdx.x & 31) / tpr : 0;           // of the warp's groups, whose rows follow one another
+  float *red = reinterpret_cast<float *>(ring + kSets * kRows * R::kSlot * threads) + (SHORT ? 0 : group * (R::kRed / 4));
   if (z.warps > 1) {
     for (int i = t; i < R::kRed / 4; i += tpr) red[i] = 0.f;         // of warps that the group has not
     __syncthreads();
@@ -244,9 +262,15 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layern
   float total[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) total[j] = row + j * stride < z.T ? sum_row(j) : 0.f;
-  group_sum(total, z.warps, t >> 5, red, join);
+  auto row_sum = [&](auto &v, float *where) {
+    if (SHORT)
+      lanes_sum(v, tpr);
+    else
+      group_sum(v, z.warps, t >> 5, where, join);
+  };
+  row_sum(total, red);
   int set = 0, turn = 0;
-  for (; row < z.T; row += kRows * stride) {
+  for (; row - sub < z.T; row += kRows * stride) {
     const int after = set + 1 == kSets ? 0 : set + 1;
     P2 v[kRows][kRuns][RUN / 2];
     float sum[2 * kRows];
@@ -259,7 +283,7 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layern
         if (col(r) < z.H) {
           P2(&u)[RUN / 2] = v[j][r];
           take_run(set * kRows + j, r, u);
-          if (ADD && z.s && (j == 0 || row + j * stride < z.T))
+          if (ADD && z.s && ((j == 0 && !SHORT) || row + j * stride < z.T))
             put<RUN>(static_cast<XT *>(z.s) + (row + j * stride) * z.lds + col(r), u);
 #pragma unroll
           for (int i = 0; i < RUN / 2; ++i) {
@@ -274,11 +298,11 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layern
     for (int j = 0; j < kRows; ++j)
       sum[kRows + j] = row + (kRows + j) * stride < z.T ? sum_row(after * kRows + j) : 0.f;
     turn ^= 1;                                               // a buffer is written again after the other's barrier
-    group_sum(sum, z.warps, t >> 5, red + turn * 128, join);
+    row_sum(sum, red + turn * 128);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       total[j] = sum[kRows + j];
-      if (j > 0 && row + j * stride >= z.T) continue;
+      if ((j > 0 || SHORT) && row + j * stride >= z.T) continue;
       const P2 rr = twice(rsqrtf(fmaf(sum[j], z.inv_h, z.eps)));
 #pragma unroll
       for (int r = 0; r < kRuns; ++r)
@@ -319,30 +343,33 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, BIG>::kThreads, 1) layern
 //          at 72 registers.
 //   BIG    rows of more than 8192 columns: 1024 threads of 64 registers, weights from L1, and float32 ds from
 //          memory, as two slots do not fit with them.
-template <typename XT, bool DS, bool BIG>
+template <typename XT, bool DS, int KIND>
 struct GradRing {
+  static constexpr bool BIG = KIND == kBig;
   static constexpr bool kDs = DS && !(BIG && sizeof(XT) == 4), kSharedW = !BIG;
   static constexpr int kSlot = kColumns * (int)(sizeof(XT) * (kDs ? 2 : 1) + 2);   // bytes of a thread's part of a row
   static constexpr int kThreads = BIG ? 1024 : 512, kRows = BIG || kSlot > 96 ? 1 : 2;
   static constexpr int kRed = 2 * 8 * 32 * 4;                // bytes of a group's sums
   static size_t bytes(int threads, int tpr) {
-    return (size_t)kSlot * 2 * kRows * threads + (kSharedW ? 4 * kColumns * tpr : 0) + (size_t)(threads / tpr) * kRed;
+    return (size_t)kSlot * 2 * kRows * threads + (kSharedW ? 4 * kColumns * tpr : 0) + (tpr > 32 ? (size_t)(threads / tpr) * kRed : 0);
   }
 };
 
-template <typename XT, bool DS, bool BIG>
-__global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_grad_kernel(const Rows z) {
-  using R = GradRing<XT, DS, BIG>;
+template <typename XT, bool DS, int KIND>
+__global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm_grad_kernel(const Rows z) {
+  using R = GradRing<XT, DS, KIND>;
+  constexpr bool SHORT = KIND == kShort;
   constexpr int RUN = kRun<XT>, kRuns = kColumns / RUN, kRows = R::kRows;
   // [2][kRows] of [run][thread] of s, the same of dn and ds; w [run][thread of a group] in float32; the groups' sums.
   // At the end [2][H] floats.
   extern __shared__ __align__(16) unsigned char ring[];
-  const int threads = (int)blockDim.x, tpr = 32 * z.warps;
+  const int threads = (int)blockDim.x, tpr = z.lanes;
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
   const int64_t stride = (int64_t)gridDim.x * z.groups;
   int64_t row = (int64_t)blockIdx.x * z.groups + group;
   float *const weights = reinterpret_cast<float *>(ring + 2 * kRows * R::kSlot * threads);
-  float *red = weights + (R::kSharedW ? kColumns * tpr : 0) + group * (R::kRed / 4);
+  const int sub = SHORT ? ((int)threadIdx.x & 31) / tpr : 0;           // of the warp's groups, whose rows follow one another
+  float *red = weights + (R::kSharedW ? kColumns * tpr : 0) + (SHORT ? 0 : group * (R::kRed / 4));
   const uint32_t at = smem_u32(ring);
   auto col = [&](int r) { return RUN * (r * tpr + t); };
   auto of_s = [&](int slot, int r) { return slot * R::kSlot * threads + (r * threads + (int)threadIdx.x) * 16; };
@@ -419,8 +446,9 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
 #pragma unroll
     for (int i = 0; i < RUN / 2; ++i) dw[r][i] = db[r][i] = twice(0.f);
   // a row's sums go through two buffers, each written again after the other's barrier
-  for (int half = 0; row < z.T; half ^= 1) {
+  for (int half = 0; row - sub < z.T; half ^= 1) {
     const bool whole = kRows == 1 || row + stride < z.T;     // both rows are there
+    const bool any = !SHORT || row < z.T;                    // the first is
     copies_wait<1>();
     float sum[kRows];
 #pragma unroll
@@ -435,7 +463,10 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
         }
       sum[j] = both(s);
     }
-    group_sum(sum, z.warps, t >> 5, red, join);
+    if (SHORT)
+      lanes_sum(sum, tpr);
+    else
+      group_sum(sum, z.warps, t >> 5, red, join);
     P2 mean[kRows], sq[kRows], sg[kRows], sgv[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
@@ -469,7 +500,12 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
       sums[j][1] = both(sg[j]);
       sums[j][2] = both(sgv[j]);
     }
-    group_sums(sums, z.warps, t >> 5, red + 256, join);
+    if (SHORT) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) lanes_sum(sums[j], tpr);
+    } else {
+      group_sums(sums, z.warps, t >> 5, red + 256, join);
+    }
     // dx = ds + r (g - mean(g)) - (v r) (r mean(g v) r): factor by factor, so that no power of a row's magnitude is formed
     P2 rr[kRows], mg[kRows], mgh[kRows];
 #pragma unroll
@@ -486,7 +522,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
         take_w(r, w);
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          if (j > 0 && !whole) break;
+          if (j > 0 ? !whole : !any) break;
           P2 v[RUN / 2], d[RUN / 2], ds[RUN / 2], out[RUN / 2];
           take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
           take<RUN>(reinterpret_cast<const uint16_t *>(ring + of_dn(half * kRows + j, r)), d);
@@ -510,12 +546,23 @@ __global__ void __launch_bounds__(GradRing<XT, DS, BIG>::kThreads, 1) layernorm_
     send(row + kRows * stride, half);
   }
   if (!z.part) return;
-  // the groups' sums, joined in their order
+  // a warp's groups' sums, then the groups' (warps') in their order
+  if (SHORT)
+    for (int o = tpr; o < 32; o <<= 1)
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+        for (int i = 0; i < RUN / 2; ++i) {
+          const float2 a = split(dw[r][i]), b = split(db[r][i]);
+          dw[r][i] = dw[r][i] + pair(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o));
+          db[r][i] = db[r][i] + pair(__shfl_xor_sync(0xffffffffu, b.x, o), __shfl_xor_sync(0xffffffffu, b.y, o));
+        }
   copies_wait<0>();
   __syncthreads();
   float *sums = reinterpret_cast<float *>(ring);
-  for (int n = 0; n < z.groups; ++n) {
-    if (group == n)
+  const int part_of = SHORT ? (int)threadIdx.x >> 5 : group;
+  for (int n = 0; n < (SHORT ? threads / 32 : z.groups); ++n) {
+    if (part_of == n && sub == 0)
 #pragma unroll
       for (int r = 0; r < kRuns; ++r)
         if (col(r) < z.H)
@@ -564,8 +611,9 @@ __global__ void __launch_bounds__(32 * kSumWarps) sum_blocks_kernel(const float 
 // ---------------------------------------------------------------- host
 
 int warps_of(int64_t H) { return (int)ceil_div(H, 512); }
-// Groups of a block of at most `threads`.
-int groups_of(int64_t H, int threads) { return std::max(1, threads / (32 * warps_of(H))); }
+// Threads of a group.  Forward with b and gradients with ds, BF16, against a warp a row: 262 144 x 64 25 and 73 us (forward),
+// 170 000 x 192 46 and 51, 59 and 65; 131 072 x 256 would be 48 and 46, 55 and 53.
+int lanes_of(int64_t H) { return H <= 128 ? 8 : H <= 192 ? 16 : 32 * warps_of(H); }
 constexpr int64_t kMostParts = 256;       // blocks of the gradients' kernel, one for each SM, at most
 
 int check_rows_of(const void *p, int64_t ld, int64_t H) {
@@ -593,7 +641,7 @@ int launch_rows(const Rows &z, int64_t blocks, size_t smem, cudaStream_t st) {
     if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess) return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3((unsigned)(32 * z.warps * z.groups)), smem, st, z);
+  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3((unsigned)(z.lanes * z.groups)), smem, st, z);
 }
 
 }  // namespace
@@ -621,6 +669,7 @@ extern "C" int moe_layernorm_forward(const moe_layernorm_args *a, cudaStream_t s
   z.T = a->T;
   z.H = (int)a->H;
   z.warps = warps_of(a->H);
+  z.lanes = lanes_of(a->H);
   z.w_dtype = a->w_dtype;
   z.eps = a->eps;
   z.inv_h = 1.f / (float)a->H;
@@ -634,16 +683,17 @@ extern "C" int moe_layernorm_forward(const moe_layernorm_args *a, cudaStream_t s
   z.lds = a->lds;
   z.n = a->n;
   z.ldn = a->ldn;
-  auto launch_as = [&](auto type, auto with_b, auto is_big) {
+  auto launch_as = [&](auto type, auto with_b, auto kind) {
     using XT = decltype(type);
-    using R = ForwardRing<XT, decltype(with_b)::value, decltype(is_big)::value>;
-    z.groups = groups_of(a->H, R::kThreads);
-    const int tpr = 32 * z.warps;
-    return launch_rows<layernorm_kernel<XT, decltype(with_b)::value, decltype(is_big)::value>>(
-        z, std::min<int64_t>(num_sms(), ceil_div(a->T, z.groups)), R::bytes(tpr * z.groups, tpr), stream);
+    using R = ForwardRing<XT, decltype(with_b)::value, decltype(kind)::value>;
+    z.groups = std::max(1, R::kThreads / z.lanes);
+    return launch_rows<layernorm_kernel<XT, decltype(with_b)::value, decltype(kind)::value>>(
+        z, std::min<int64_t>(num_sms(), ceil_div(a->T, z.groups)), R::bytes(z.lanes * z.groups, z.lanes), stream);
   };
   auto launch = [&](auto type, auto with_b) {
-    return z.warps > 16 ? launch_as(type, with_b, std::true_type{}) : launch_as(type, with_b, std::false_type{});
+    if (z.lanes < 32) return launch_as(type, with_b, std::integral_constant<int, kShort>{});
+    return z.warps > 16 ? launch_as(type, with_b, std::integral_constant<int, kBig>{})
+                        : launch_as(type, with_b, std::integral_constant<int, kMiddle>{});
   };
   using std::true_type;
   using std::false_type;
@@ -676,6 +726,7 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   z.T = a->T;
   z.H = (int)a->H;
   z.warps = warps_of(a->H);
+  z.lanes = lanes_of(a->H);
   z.w_dtype = a->w_dtype;
   z.eps = a->eps;
   z.inv_h = 1.f / (float)a->H;
@@ -690,21 +741,21 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   z.lds = a->ld_dx;
   z.part = a->dw || a->dbias ? static_cast<float *>(a->workspace) : nullptr;
   int64_t blocks = 0;
-  auto launch_as = [&](auto type, auto with_ds, auto is_big) {
+  auto launch_as = [&](auto type, auto with_ds, auto kind) {
     using XT = decltype(type);
-    using R = GradRing<XT, decltype(with_ds)::value, decltype(is_big)::value>;
-    z.groups = groups_of(a->H, R::kThreads);
+    using R = GradRing<XT, decltype(with_ds)::value, decltype(kind)::value>;
+    z.groups = std::max(1, R::kThreads / z.lanes);
     blocks = std::min({kMostParts, (int64_t)num_sms(), ceil_div(a->T, z.groups)});
-    const int tpr = 32 * z.warps;
-    const size_t smem = std::max(R::bytes(tpr * z.groups, tpr), z.part ? (size_t)z.H * 8 : 0);
-    return launch_rows<layernorm_grad_kernel<XT, decltype(with_ds)::value, decltype(is_big)::value>>(z, blocks, smem, stream);
+    const size_t smem = std::max(R::bytes(z.lanes * z.groups, z.lanes), z.part ? (size_t)z.H * 8 : 0);
+    return launch_rows<layernorm_grad_kernel<XT, decltype(with_ds)::value, decltype(kind)::value>>(z, blocks, smem, stream);
   };
   const bool f32 = a->x_dtype == MOE_F32, add = a->ds != nullptr;
   auto launch = [&](auto type, auto with_ds) {
-    using R = GradRing<decltype(type), decltype(with_ds)::value, false>;
-    const int tpr = 32 * z.warps;
-    const bool big = tpr > R::kThreads || R::bytes(tpr, tpr) > kMostSmem;
-    return big ? launch_as(type, with_ds, std::true_type{}) : launch_as(type, with_ds, std::false_type{});
+    using R = GradRing<decltype(type), decltype(with_ds)::value, kMiddle>;
+    if (z.lanes < 32) return launch_as(type, with_ds, std::integral_constant<int, kShort>{});
+    const bool big = z.lanes > R::kThreads || R::bytes(z.lanes, z.lanes) > kMostSmem;
+    return big ? launch_as(type, with_ds, std::integral_constant<int, kBig>{})
+               : launch_as(type, with_ds, std::integral_constant<int, kMiddle>{});
   };
   using std::true_type;
   using std::false_type;

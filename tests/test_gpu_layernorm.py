@@ -117,6 +117,54 @@ def test_backward(B, T, H, dtype):
         assert all(v is None or torch.equal(v, again[k]) for k, v in out.items())
 
 
+SHORT = [(1, 128), (2, 120), (3, 136), (7, 256), (63, 72), (65, 64), (2500, 24), (9729, 128), (20001, 64), (4867, 248), (40000, 8), (19457, 104)]
+
+
+@pytest.mark.parametrize("T,H", SHORT)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_short_rows(B, T, H, dtype):
+    """Several rows of a warp: numbers of rows around one, two and more rounds of all groups, and between them."""
+    from moe_expert_layer_counting_gb300 import LayerNorm
+    wide = lambda t: torch.cat([t, torch.full_like(t[:, :8], float("nan"))], 1)[:, :H]       # noqa: E731
+    x, b = wide(randn(T, H, seed=1, scale=1.5, dtype=dtype, shift=0.3)), wide(randn(T, H, seed=2, scale=2.0))
+    dn, ds = wide(randn(T, H, seed=3, scale=0.1)), wide(randn(T, H, seed=4, scale=0.1, dtype=dtype))
+    w, bias = randn(H, seed=5, dtype=F32, shift=1.0), randn(H, seed=6)
+    ws = torch.empty(B.moe_layernorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    for other in (b, None):
+        keep = torch.full((T + 1, H + 8), 7.0, dtype=dtype, device="cuda"), torch.full((T + 1, H + 8), 7.0, dtype=BF16, device="cuda")
+        s, n = (t[:T, :H] for t in keep)
+        B.moe_layernorm_forward(x, other, w, bias.float(), s if other is not None else None, n)
+        check_forward(s, n, x, other, w, bias.float(), 1e-5)
+        assert all(bool((t[T] == 7).all()) and bool((t[:, H:] == 7).all()) for t in keep)
+    norm = LayerNorm(w, bias.float(), eps=1e-5)
+    for stream in (ds, None):
+        keep = torch.full((T + 1, H + 8), 7.0, dtype=dtype, device="cuda")
+        out = {"dx": keep[:T, :H], "dw": torch.empty(H, device="cuda"), "dbias": torch.empty(H, device="cuda")}
+        B.moe_layernorm_backward(x, w, dn, stream, ws, out["dx"], out["dw"], out["dbias"])
+        check_backward(out, x, w, dn, stream, 1e-5)
+        assert bool((keep[T] == 7).all()) and bool((keep[:, H:] == 7).all())
+        again = norm.backward(x.contiguous(), dn.contiguous(), None if stream is None else stream.contiguous())
+        assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("H", [64, 200])
+def test_short_rows_infinities_and_nan_stay_in_their_row(B, H):
+    from moe_expert_layer_counting_gb300 import LayerNorm
+    x, b, dn = randn(130, H, seed=1), randn(130, H, seed=2), randn(130, H, seed=3)
+    norm = LayerNorm(randn(H, seed=4), randn(H, seed=5))
+    s, n = norm.forward(x, b)
+    dx = norm.backward(s, dn)["dx"]
+    y, d = x.clone(), dn.clone()
+    y[3, 5], y[129, 0], d[20, 7] = float("nan"), float("inf"), float("nan")
+    s2, n2 = norm.forward(y, b)
+    dx2 = norm.backward(s2, d)["dx"]
+    fine = torch.ones(130, dtype=torch.bool, device="cuda")
+    fine[[3, 129]] = False
+    assert torch.equal(n2[fine], n[fine]) and bool(n2[~fine].isnan().all())
+    fine[20] = False
+    assert torch.equal(dx2[fine], dx[fine]) and bool(dx2[~fine].isnan().all())
+
+
 @pytest.mark.parametrize("shift", [0.0, 1e3])
 def test_rows_far_from_zero(B, shift):
     """A mean far above the spread: the variance is that of the differences, not of squares that cancel."""
