@@ -695,11 +695,6 @@ struct SmallLayout {
 };
 static_assert(SmallLayout::kBytes <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ float4 load_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void store_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -850,6 +845,13 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   }
 
   const int n16 = (g.n + 15) & ~15;
+  const int share = (n16 + ctas - 1) / ctas;                    // rows of S that a CTA adds up
+  // of S the rows that no CTA adds up, which no result depends on
+  if (ctas > 1)
+    for (int i = threadIdx.x; i < 2 * (L::kMostN - n16) * 8; i += L::kThreads) {
+      const int at = (i & 1) * L::kBlock + (n16 * 8 + (i >> 1)) * 16;
+      *reinterpret_cast<uint4 *>(ss + at) = *reinterpret_cast<uint4 *>(sq + at) = make_uint4(0, 0, 0, 0);
+    }
   const uint32_t t_x = tmem_base + L::kMostN;                   // S and Q in columns 0 .. 127, X behind them
   uint32_t phase = 0;
   // what a stage writes is ordered before its MMAs, and these before what follows
@@ -913,28 +915,37 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
     if (ctas == 1) {
       take_square(g.gram_alpha, g.gram_beta, gram);
     } else {
-      // this CTA's part, 16 bytes at place c ^ (row & 7) of a row's 32
+      // this CTA's part of each row to the CTA that adds it up: [CTA][row of the share], 16 bytes at place c ^ (row & 7) of a
+      // row's 32
+      const int owner = row / share, mine = row - owner * share;
+      const uint32_t to = mapa_shared(smem_u32(part) + (uint32_t)((rank * share + mine) * 512), (uint32_t)min(owner, ctas - 1));
       for (int c0 = 32 * (warp >> 2); c0 < n16; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tmem_base + t_lane + (uint32_t)c0, v);
         tmem_ld_wait();
+        if (row < n16)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4 *>(part + row * 512 + (((c0 / 4 + j) ^ (row & 7)) << 4)) =
-              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            const int4 w = make_int4((int)v[4 * j], (int)v[4 * j + 1], (int)v[4 * j + 2], (int)v[4 * j + 3]);
+            const int at = ((c0 / 4 + j) ^ (row & 7)) << 4;
+            if (owner == rank)
+              *reinterpret_cast<int4 *>(part + row * 512 + at) = w;      // rank * share + mine is row
+            else
+              store_cluster_v4(to + (uint32_t)at, w);
+          }
       }
       cluster_sync();
-      const int share = L::kMostN / ctas;
       for (int i = threadIdx.x; i < share * (n16 / 8); i += L::kThreads) {
         const int r = rank * share + i / (n16 / 8), c = i % (n16 / 8);
+        if (r >= n16) break;
         float4 a[8], b[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           a[k] = b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k < ctas) {
-            const uint32_t from = mapa_shared(smem_u32(part) + (uint32_t)(r * 512), (uint32_t)k);
-            a[k] = load_cluster_v4(from + (uint32_t)(((2 * c) ^ (r & 7)) << 4));
-            b[k] = load_cluster_v4(from + (uint32_t)(((2 * c + 1) ^ (r & 7)) << 4));
+            const unsigned char *from = part + (k * share + i / (n16 / 8)) * 512;
+            a[k] = *reinterpret_cast<const float4 *>(from + (((2 * c) ^ (r & 7)) << 4));
+            b[k] = *reinterpret_cast<const float4 *>(from + (((2 * c + 1) ^ (r & 7)) << 4));
           }
         }
         float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
