@@ -670,9 +670,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
 // cluster; S and Q [n][n] are in every CTA.  One copy of X serves as both operands
 // of X X^T (summed along its rows) and as the right one of Q X (summed across
 // them): the MMA reads either from the same 128-byte-swizzled blocks of 64
-// columns.  Of X X^T each CTA has the part of its columns; the parts are added in
-// float32 through the cluster's shared memory, a share of the rows by each CTA,
-// which hands its rows of S to all.  A stage is then an MMA of a few hundred
+// columns.  Of X X^T each CTA has the part of its columns; it writes each row's part into
+// the shared memory of the CTA that adds this row up in float32, which
+// hands its rows of S to all (parts that are read from there instead: 75 instead of 60 us for 128 x 2048).  A stage is then an MMA of a few hundred
 // nanoseconds, a commit and a pass from TMEM back to shared memory, where the
 // kernel above needs a trip through L2 between any two: 4 us an iteration of 128 x 256
 // instead of 10.
@@ -1146,8 +1146,8 @@ int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, co
 }
 
 // CTAs for a matrix of the small path, or 0: it is not one.  Clusters that fill the GPU once at most, as an exchange over
-// the cluster takes 8 of an iteration's 12 us: one matrix of 128 x 2048 in 75 us and 104 by the products' kernel, 64 of them
-// in 390 and 207.  Matrices of one CTA in any number: 64 of 128 x 128 in 27 and 71 us, 200 of 64 x 256 in 49 and 95.
+// the cluster takes 4 of an iteration's 9 us: one matrix of 128 x 2048 in 60 us and 104 by the products' kernel, 16 of them in
+// 120, 64 (four rounds of clusters) in 207 by the products'.  Matrices of one CTA in any number: 64 of 128 x 128 in 27 and 71 us, 200 of 64 x 256 in 49 and 95.
 int small_cluster(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns) {
   const int64_t n = std::min(N, K), k = std::max(N, K);
   if (n > SmallLayout::kMostN || k > 8 * SmallLayout::kMostColumns || ns.steps == 0) return 0;
