@@ -676,6 +676,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
 // nanoseconds, a commit and a pass from TMEM back to shared memory, where the
 // kernel above needs a trip through L2 between any two: 4 us an iteration of 128 x 256
 // instead of 10.
+// What FP16 leaves of the diagonals of S and Q is not lost here: rounded, they would be off by the same in every row of
+// a matrix of few rows (562 x 39: 7.5e-4 of the result instead of 3.3e-3, 128 x 384 7.5e-4 instead of 1.2e-3, for 3 to 8 % of
+// the time).
 struct SmallArgs {
   Elementwise z;
   int n, k, kc;             // kc: columns of a CTA, a multiple of 64
@@ -691,7 +694,8 @@ struct SmallLayout {
   static constexpr int kOffPart = kOffQ + 2 * kBlock;               // [128][128] float32
   static constexpr int kOffBar = kOffPart + kMostN * kMostN * 4;
   static constexpr int kOffSums = kOffBar + 32;                     // 8 of this block's warps, 8 of the cluster's CTAs
-  static constexpr int kBytes = 1024 + kOffSums + 64;
+  static constexpr int kOffDiag = kOffSums + 64;                    // [2][128] float32: of S, of Q
+  static constexpr int kBytes = 1024 + kOffDiag + 2 * kMostN * 4;
 };
 static_assert(SmallLayout::kBytes <= 232448, "shared memory of one CTA");
 
@@ -778,6 +782,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   uint64_t *done = reinterpret_cast<uint64_t *>(smem + L::kOffBar), *never = done + 1;
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(done + 2);
   float *sums = reinterpret_cast<float *>(smem + L::kOffSums), *cluster_sums = sums + 8;
+  float *of_s = reinterpret_cast<float *>(smem + L::kOffDiag), *of_q = of_s + L::kMostN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank(), ctas = (int)cluster_size();
   const int64_t e = blockIdx.x / ctas;
@@ -822,6 +827,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   }
   sum = block_sum(sum, sums);
   if ((int)threadIdx.x < ctas) store_cluster_f32(mapa_shared(smem_u32(cluster_sums + rank), threadIdx.x), sum);
+  if (threadIdx.x < 2 * L::kMostN) of_s[threadIdx.x] = 0.f;
   // rows past the last are zero
   for (int i = threadIdx.x; i < (L::kMostN - 8 * down) * across; i += L::kThreads)
     *reinterpret_cast<uint4 *>(sx + small_place(8 * down + i / across, 8 * (i % across))) = make_uint4(0, 0, 0, 0);
@@ -873,8 +879,14 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   auto desc_k = [&](int off) { return make_smem_desc(smem_base + (uint32_t)off, 16, 1024, kSwizzle128B); };
   const int q = warp & 3, row = 32 * q + lane;                  // this thread's TMEM lane: a row of S, Q and X
   const uint32_t t_lane = (uint32_t)(32 * q) << 16;
+  // What FP16 leaves of a diagonal's value x.  Of S: what it adds to Q's diagonal.  Of Q: the factor of X's row that stands
+  // for it, as the other values of a row add up to little beside it.
+  auto left = [&](float x, bool of_square) {
+    const float h = __half2float(__float2half_rn(x));
+    return of_square ? 2.f * g.square_alpha * h * (x - h) : h == 0.f ? 1.f : __fdividef(x, h);
+  };
   // S or Q from TMEM: factor, diagonal, FP16, into blocks at `to`
-  auto take_square = [&](float alpha, float beta, unsigned char *to) {
+  auto take_square = [&](float alpha, float beta, unsigned char *to, float *diag, bool of_square) {
     uint32_t v[2][32];
     const int c1 = 32 * (warp >> 2);
 #pragma unroll
@@ -885,18 +897,26 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
     for (int h = 0; h < 2; ++h) {
       const int c0 = c1 + 64 * h;
       if (c0 >= n16) break;
+      const float add = c0 == 32 * q && row < g.n ? beta : 0.f;
+      float mine = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = c0 + 8 * j + 2 * i;
-          const float a = __uint_as_float(v[h][8 * j + 2 * i]), b = __uint_as_float(v[h][8 * j + 2 * i + 1]);
-          w[i] = pack_f16(c < n16 ? fmaf(alpha, a, c == row && row < g.n ? beta : 0.f) : 0.f,
-                          c < n16 ? fmaf(alpha, b, c + 1 == row && row < g.n ? beta : 0.f) : 0.f);
+          float x[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool on = 8 * j + 2 * i + k == lane;           // the diagonal, in the 32 columns from 32 q
+            x[k] = c < n16 ? fmaf(alpha, __uint_as_float(v[h][8 * j + 2 * i + k]), on ? add : 0.f) : 0.f;
+            if (on) mine = x[k];
+          }
+          w[i] = pack_f16(x[0], x[1]);
         }
         *reinterpret_cast<uint4 *>(to + small_place(row, c0 + 8 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if (c0 == 32 * q && row < g.n) diag[row] = left(mine, of_square);
     }
   };
 
@@ -913,12 +933,12 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
     });
     unsigned char *gram = g.square ? ss : sq;
     if (ctas == 1) {
-      take_square(g.gram_alpha, g.gram_beta, gram);
+      take_square(g.gram_alpha, g.gram_beta, gram, g.square ? of_s : of_q, g.square);
     } else {
       // this CTA's part of each row to the CTA that adds it up: [CTA][row of the share], 16 bytes at place c ^ (row & 7) of a
       // row's 32
-      const int owner = row / share, mine = row - owner * share;
-      const uint32_t to = mapa_shared(smem_u32(part) + (uint32_t)((rank * share + mine) * 512), (uint32_t)min(owner, ctas - 1));
+      const int owner = row / share;
+      const uint32_t to = mapa_shared(smem_u32(part) + (uint32_t)((rank * share + row - owner * share) * 512), (uint32_t)min(owner, ctas - 1));
       for (int c0 = 32 * (warp >> 2); c0 < n16; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tmem_base + t_lane + (uint32_t)c0, v);
@@ -929,7 +949,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
             const int4 w = make_int4((int)v[4 * j], (int)v[4 * j + 1], (int)v[4 * j + 2], (int)v[4 * j + 3]);
             const int at = ((c0 / 4 + j) ^ (row & 7)) << 4;
             if (owner == rank)
-              *reinterpret_cast<int4 *>(part + row * 512 + at) = w;      // rank * share + mine is row
+              *reinterpret_cast<int4 *>(part + row * 512 + at) = w;      // its place is row
             else
               store_cluster_v4(to + (uint32_t)at, w);
           }
@@ -954,8 +974,18 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
           t[0] += a[k].x; t[1] += a[k].y; t[2] += a[k].z; t[3] += a[k].w;
           t[4] += b[k].x; t[5] += b[k].y; t[6] += b[k].z; t[7] += b[k].w;
         }
+        float mine = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = fmaf(g.gram_alpha, t[j], 8 * c + j == r && r < g.n ? g.gram_beta : 0.f);
+        for (int j = 0; j < 8; ++j) {
+          const bool on = 8 * c + j == r && r < g.n;
+          t[j] = fmaf(g.gram_alpha, t[j], on ? g.gram_beta : 0.f);
+          if (on) mine = t[j];
+        }
+        if (r >> 3 == c && r < g.n) {
+          const float d = left(mine, g.square);
+          float *at = (g.square ? of_s : of_q) + r;
+          for (int k = 0; k < ctas; ++k) store_cluster_f32(mapa_shared(smem_u32(at), (uint32_t)k), d);
+        }
         const int4 w = make_int4((int)pack_f16(t[0], t[1]), (int)pack_f16(t[2], t[3]), (int)pack_f16(t[4], t[5]), (int)pack_f16(t[6], t[7]));
         for (int k = 0; k < ctas; ++k)
           store_cluster_v4(mapa_shared(smem_u32(gram) + (uint32_t)small_place(r, 8 * c), (uint32_t)k), w);
@@ -970,7 +1000,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
           tc_mma_f16(tmem_base, d, d, idesc, kk > 0 ? 1u : 0u);
         }
       });
-      take_square(g.square_alpha, g.square_beta, sq);
+      take_square(g.square_alpha, g.square_beta + of_s[row], sq, of_q, false);
     }
     // X = Q X
     multiply([&] {
@@ -981,7 +1011,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
           tc_mma_f16(t_x + (uint32_t)c0, desc_k(L::kOffQ + (kk >> 2) * L::kBlock) + 2 * (kk & 3), x + 128 * kk, idesc, kk > 0 ? 1u : 0u);
       }
     });
-    const float unit = 1.f / kScale;
+    const float unit = of_q[row] / kScale;
     for (int c1 = 32 * (warp >> 2); c1 < g.kc; c1 += 128) {
       uint32_t v[2][32];
 #pragma unroll
@@ -1145,15 +1175,18 @@ int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, co
   return bytes < moe_muon_workspace_size(E, N, K) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
-// CTAs for a matrix of the small path, or 0: it is not one.  Clusters that fill the GPU once at most, as an exchange over
-// the cluster takes 4 of an iteration's 9 us: one matrix of 128 x 2048 in 60 us and 104 by the products' kernel, 16 of them in
-// 120, 64 (four rounds of clusters) in 207 by the products'.  Matrices of one CTA in any number: 64 of 128 x 128 in 27 and 71 us, 200 of 64 x 256 in 49 and 95.
+// CTAs for a matrix of the small path, or 0: it is not one.  Matrices of one CTA in any number: 64 of 128 x 128 in 28 us, by
+// the products' kernel 71, 200 of 64 x 256 in 53 and 95.  Clusters, whose exchange takes 4 of an iteration's 9 us, in as
+// many rounds as pay: of two CTAs three (128 of 128 x 768 in 147 and 161, 200 of 40 x 600 in 103 and 182); of more, one, or two
+// where n is at most 64 and the products' tiles are mostly empty (32 of 64 x 2048 in 109 and 122, 64 of 897 x 32 in 60 and
+// 105; 20 of 128 x 2048 129 and 123, 64 of 64 x 2048, in four rounds, 183 and 173).
 int small_cluster(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns) {
   const int64_t n = std::min(N, K), k = std::max(N, K);
   if (n > SmallLayout::kMostN || k > 8 * SmallLayout::kMostColumns || ns.steps == 0) return 0;
   int ctas = 1;
   while (ceil_div(k, ctas) > SmallLayout::kMostColumns) ctas *= 2;
-  return ctas == 1 || E * ctas <= num_sms() ? ctas : 0;
+  const int rounds = ctas == 2 ? 3 : n <= 64 ? 2 : 1;
+  return ctas == 1 || E * ctas <= rounds * num_sms() ? ctas : 0;
 }
 
 template <int VEC, bool WIDE>
