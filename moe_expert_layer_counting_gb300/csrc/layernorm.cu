@@ -39,6 +39,7 @@ constexpr int kMostH = 16384;
 struct Rows {
   int64_t T;
   int H, warps, lanes, groups;            // warps of a group (a part of one: 1) and its threads, groups of a block
+  int half;                               // gradients, kPair: columns of a cluster's first block
   int w_dtype;
   float eps, inv_h;
   const void *x, *w, *bias;
@@ -154,9 +155,13 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N], int lanes) {
 
 // ---------------------------------------------------------------- forward
 
-// Kinds of a launch: kShort rows of up to 192 columns, which a part of a warp owns; kBig of more than 8192 (or what the
-// rings of the others do not hold).
-enum : int { kShort, kMiddle, kBig };
+// Kinds of a launch: kShort rows of up to 192 columns, which a part of a warp owns; of more than 8192 columns kBig (forward) and
+// kPair (gradients).
+enum : int { kShort, kMiddle, kBig, kPair };
+
+__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 
 // How the forward kernel goes about a launch: kRows rows of a group in work
 // together, kSets sets of them in the ring (the next set's sum is added up with
@@ -341,35 +346,61 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, KIND>::kThreads, 1) layer
 //          arithmetic (a block's 16 warps are all that fit: 32 column sums in registers); one where the ring
 //          does not hold twice two.  4096 x 7168 in 51 us; 80 one by one, 75 with two blocks' worth of warps
 //          at 72 registers.
-//   BIG    rows of more than 8192 columns: 1024 threads of 64 registers, weights from L1, and float32 ds from
-//          memory, as two slots do not fit with them.
+//   kPair  rows of more than 8192 columns: a cluster of two blocks owns a row, half the columns each, and every
+//          sum is joined through both blocks' shared memory (2048 x 16384, BF16 with ds, in MEASURED; one block of 1024 threads
+//          of 64 registers, a row at a time, 100).
 template <typename XT, bool DS, int KIND>
 struct GradRing {
-  static constexpr bool BIG = KIND == kBig;
-  static constexpr bool kDs = DS && !(BIG && sizeof(XT) == 4), kSharedW = !BIG;
-  static constexpr int kSlot = kColumns * (int)(sizeof(XT) * (kDs ? 2 : 1) + 2);   // bytes of a thread's part of a row
-  static constexpr int kThreads = BIG ? 1024 : 512, kRows = BIG || kSlot > 96 ? 1 : 2;
+  static constexpr int kSlot = kColumns * (int)(sizeof(XT) * (DS ? 2 : 1) + 2);    // bytes of a thread's part of a row
+  static constexpr int kThreads = 512, kRows = kSlot > 96 ? 1 : 2;
   static constexpr int kRed = 2 * 8 * 32 * 4;                // bytes of a group's sums
   static size_t bytes(int threads, int tpr) {
-    return (size_t)kSlot * 2 * kRows * threads + (kSharedW ? 4 * kColumns * tpr : 0) + (tpr > 32 ? (size_t)(threads / tpr) * kRed : 0);
+    return (size_t)kSlot * 2 * kRows * threads + 4 * kColumns * tpr + (tpr > 32 ? (size_t)(threads / tpr) * kRed : 0);
   }
 };
+
+// Sums of N values over both blocks of a cluster, up to 16 warps each, the same bits in every thread; red [2 blocks][N][16] of
+// each block, written again after another sum in another place.
+template <int N>
+__device__ __forceinline__ void pair_sum(float (&v)[N], uint32_t rank, float *red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (lane < 2) {
+    const uint32_t to = mapa_shared(smem_u32(red + (int)rank * N * 16 + warp), (uint32_t)lane);
+#pragma unroll
+    for (int k = 0; k < N; ++k) store_cluster(to + 64 * k, v[k]);
+  }
+  cluster_sync();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = red[((lane >> 4) * N + k) * 16 + (lane & 15)];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
 
 template <typename XT, bool DS, int KIND>
 __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm_grad_kernel(const Rows z) {
   using R = GradRing<XT, DS, KIND>;
-  constexpr bool SHORT = KIND == kShort;
+  constexpr bool SHORT = KIND == kShort, PAIR = KIND == kPair;
   constexpr int RUN = kRun<XT>, kRuns = kColumns / RUN, kRows = R::kRows;
+  // this block's columns: H from the first on
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int first = PAIR && rank ? z.half : 0, H = !PAIR ? z.H : rank ? z.H - z.half : z.half;
+  const int64_t owner = PAIR ? blockIdx.x >> 1 : blockIdx.x, owners = PAIR ? gridDim.x >> 1 : gridDim.x;
   // [2][kRows] of [run][thread] of s, the same of dn and ds; w [run][thread of a group] in float32; the groups' sums.
   // At the end [2][H] floats.
   extern __shared__ __align__(16) unsigned char ring[];
   const int threads = (int)blockDim.x, tpr = z.lanes;
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
-  const int64_t stride = (int64_t)gridDim.x * z.groups;
-  int64_t row = (int64_t)blockIdx.x * z.groups + group;
+  const int64_t stride = owners * z.groups;
+  int64_t row = owner * z.groups + group;
   float *const weights = reinterpret_cast<float *>(ring + 2 * kRows * R::kSlot * threads);
   const int sub = SHORT ? ((int)threadIdx.x & 31) / tpr : 0;           // of the warp's groups, whose rows follow one another
-  float *red = weights + (R::kSharedW ? kColumns * tpr : 0) + (SHORT ? 0 : group * (R::kRed / 4));
+  float *red = weights + kColumns * tpr + (SHORT ? 0 : group * (R::kRed / 4));
   const uint32_t at = smem_u32(ring);
   auto col = [&](int r) { return RUN * (r * tpr + t); };
   auto of_s = [&](int slot, int r) { return slot * R::kSlot * threads + (r * threads + (int)threadIdx.x) * 16; };
@@ -390,11 +421,11 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
       if (to_row < z.T) {
 #pragma unroll
         for (int r = 0; r < kRuns; ++r)
-          if (col(r) < z.H) {
+          if (col(r) < H) {
             const int slot = half * kRows + j;
-            copy_run<RUN>(at + of_s(slot, r), static_cast<const XT *>(z.x) + to_row * z.ldx + col(r));
-            copy_run<RUN>(at + of_dn(slot, r), z.b + to_row * z.ldb + col(r));
-            if (R::kDs) copy_run<RUN>(at + of_ds(slot, r), static_cast<const XT *>(z.ds) + to_row * z.ld_ds + col(r));
+            copy_run<RUN>(at + of_s(slot, r), static_cast<const XT *>(z.x) + to_row * z.ldx + first + col(r));
+            copy_run<RUN>(at + of_dn(slot, r), z.b + to_row * z.ldb + first + col(r));
+            if (DS) copy_run<RUN>(at + of_ds(slot, r), static_cast<const XT *>(z.ds) + to_row * z.ld_ds + first + col(r));
           }
       }
     copies_commit();
@@ -402,36 +433,30 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
   send(row, 0);
   send(row + kRows * stride, 1);
   // a group's weights in float32 (1 without w), the same for all groups
-  if (R::kSharedW) {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r)
-      if (group == 0 && col(r) < z.H) {
-        P2 w[RUN / 2];
-#pragma unroll
-        for (int i = 0; i < RUN / 2; ++i) w[i] = twice(1.f);
-        if (z.w) weight<RUN>(z.w, z.w_dtype, col(r), w);
-#pragma unroll
-        for (int i = 0; i < RUN / 4; ++i) {
-          const P2 two[2] = {w[2 * i], w[2 * i + 1]};
-          put<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
-        }
-      }
-  }
-  __syncthreads();
-  auto take_w = [&](int r, P2 (&w)[RUN / 2]) {
-    if (R::kSharedW) {
-#pragma unroll
-      for (int i = 0; i < RUN / 4; ++i) {
-        P2 two[2];
-        take<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
-        w[2 * i] = two[0];
-        w[2 * i + 1] = two[1];
-      }
-    } else if (z.w) {
-      weight<RUN>(z.w, z.w_dtype, col(r), w);
-    } else {
+  for (int r = 0; r < kRuns; ++r)
+    if (group == 0 && col(r) < H) {
+      P2 w[RUN / 2];
 #pragma unroll
       for (int i = 0; i < RUN / 2; ++i) w[i] = twice(1.f);
+      if (z.w) weight<RUN>(z.w, z.w_dtype, first + col(r), w);
+#pragma unroll
+      for (int i = 0; i < RUN / 4; ++i) {
+        const P2 two[2] = {w[2 * i], w[2 * i + 1]};
+        put<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
+      }
+    }
+  if (PAIR)
+    cluster_sync();                    // and the other block's sums are zeroed
+  else
+    __syncthreads();
+  auto take_w = [&](int r, P2 (&w)[RUN / 2]) {
+#pragma unroll
+    for (int i = 0; i < RUN / 4; ++i) {
+      P2 two[2];
+      take<4>(weights + ((r * RUN / 4 + i) * tpr + t) * 4, two);
+      w[2 * i] = two[0];
+      w[2 * i + 1] = two[1];
     }
   };
   auto join = [&] {
@@ -456,7 +481,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
       P2 s = twice(0.f);
 #pragma unroll
       for (int r = 0; r < kRuns; ++r)
-        if (col(r) < z.H) {
+        if (col(r) < H) {
           P2 v[RUN / 2];
           take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
           s = s + sum_of(v);
@@ -465,6 +490,8 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
     }
     if (SHORT)
       lanes_sum(sum, tpr);
+    else if constexpr (PAIR)
+      pair_sum(sum, rank, red);
     else
       group_sum(sum, z.warps, t >> 5, red, join);
     P2 mean[kRows], sq[kRows], sg[kRows], sgv[kRows];
@@ -475,7 +502,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
     }
 #pragma unroll
     for (int r = 0; r < kRuns; ++r)
-      if (col(r) < z.H) {
+      if (col(r) < H) {
         P2 w[RUN / 2];
         take_w(r, w);
 #pragma unroll
@@ -503,6 +530,13 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
     if (SHORT) {
 #pragma unroll
       for (int j = 0; j < kRows; ++j) lanes_sum(sums[j], tpr);
+    } else if constexpr (PAIR) {
+      float all[3 * kRows];
+#pragma unroll
+      for (int k = 0; k < 3 * kRows; ++k) all[k] = sums[k / 3][k % 3];
+      pair_sum(all, rank, red + 256);
+#pragma unroll
+      for (int k = 0; k < 3 * kRows; ++k) sums[k / 3][k % 3] = all[k];
     } else {
       group_sums(sums, z.warps, t >> 5, red + 256, join);
     }
@@ -517,7 +551,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
     }
 #pragma unroll
     for (int r = 0; r < kRuns; ++r)
-      if (col(r) < z.H) {
+      if (col(r) < H) {
         P2 w[RUN / 2];
         take_w(r, w);
 #pragma unroll
@@ -526,10 +560,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
           P2 v[RUN / 2], d[RUN / 2], ds[RUN / 2], out[RUN / 2];
           take<RUN>(reinterpret_cast<const XT *>(ring + of_s(half * kRows + j, r)), v);
           take<RUN>(reinterpret_cast<const uint16_t *>(ring + of_dn(half * kRows + j, r)), d);
-          if (R::kDs)
-            take<RUN>(reinterpret_cast<const XT *>(ring + of_ds(half * kRows + j, r)), ds);
-          else if (DS)
-            take<RUN>(static_cast<const XT *>(z.ds) + (row + j * stride) * z.ld_ds + col(r), ds);
+          if (DS) take<RUN>(reinterpret_cast<const XT *>(ring + of_ds(half * kRows + j, r)), ds);
 #pragma unroll
           for (int i = 0; i < RUN / 2; ++i) {
             const P2 h = (v[i] + mean[j]) * rr[j];
@@ -539,7 +570,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
             const P2 a = fma2(h, mgh[j], g + mg[j]);
             out[i] = DS ? fma2(a, rr[j], ds[i]) : a * rr[j];
           }
-          if (z.s) put<RUN>(static_cast<XT *>(z.s) + (row + j * stride) * z.lds + col(r), out);
+          if (z.s) put<RUN>(static_cast<XT *>(z.s) + (row + j * stride) * z.lds + first + col(r), out);
         }
       }
     row += kRows * stride;
@@ -565,11 +596,11 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
     if (part_of == n && sub == 0)
 #pragma unroll
       for (int r = 0; r < kRuns; ++r)
-        if (col(r) < z.H)
+        if (col(r) < H)
 #pragma unroll
           for (int i = 0; i < RUN / 2; ++i) {
             float2 *pw = reinterpret_cast<float2 *>(sums + col(r)) + i;
-            float2 *pb = reinterpret_cast<float2 *>(sums + z.H + col(r)) + i;
+            float2 *pb = reinterpret_cast<float2 *>(sums + H + col(r)) + i;
             float2 a = split(dw[r][i]), b = split(db[r][i]);
             if (n > 0) {
               a.x += pw->x;
@@ -582,8 +613,11 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
           }
     __syncthreads();
   }
-  float4 *part = reinterpret_cast<float4 *>(z.part + (int64_t)blockIdx.x * 2 * z.H);
-  for (int i = threadIdx.x; i < z.H / 2; i += threads) part[i] = reinterpret_cast<const float4 *>(sums)[i];
+  float *part = z.part + owner * 2 * z.H + first;
+  for (int i = threadIdx.x; i < H / 2; i += threads) {
+    const int of = i < H / 4 ? 0 : 1;                          // dw, dbias
+    reinterpret_cast<float4 *>(part + (int64_t)of * z.H)[i - of * (H / 4)] = reinterpret_cast<const float4 *>(sums)[i];
+  }
 }
 
 // Sums over the blocks' parts: 32 lanes a column each, kSumWarps warps share the parts, all loads of a thread in flight.
@@ -632,7 +666,7 @@ int check_sizes(int64_t T, int64_t H, int32_t x_dtype, int32_t w_dtype, float ep
 constexpr int kMostSmem = 227 * 1024;     // of a block
 
 template <auto KERNEL>
-int launch_rows(const Rows &z, int64_t blocks, size_t smem, cudaStream_t st) {
+int launch_rows(const Rows &z, int64_t blocks, size_t smem, cudaStream_t st, int cluster = 1) {
   static std::atomic<uint64_t> ready{0};                     // devices whose kernel attribute is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -641,7 +675,21 @@ int launch_rows(const Rows &z, int64_t blocks, size_t smem, cudaStream_t st) {
     if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess) return MOE_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3((unsigned)(z.lanes * z.groups)), smem, st, z);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)(z.lanes * z.groups));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, KERNEL, z) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -725,8 +773,10 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   Rows z{};
   z.T = a->T;
   z.H = (int)a->H;
-  z.warps = warps_of(a->H);
-  z.lanes = lanes_of(a->H);
+  const bool pair = a->H > 8192;
+  z.half = pair ? (int)round_up(ceil_div(a->H, 2), 8) : 0;
+  z.warps = warps_of(pair ? z.half : a->H);
+  z.lanes = lanes_of(pair ? z.half : a->H);
   z.w_dtype = a->w_dtype;
   z.eps = a->eps;
   z.inv_h = 1.f / (float)a->H;
@@ -740,28 +790,27 @@ extern "C" int moe_layernorm_backward(const moe_layernorm_grads *a, cudaStream_t
   z.s = a->dx;
   z.lds = a->ld_dx;
   z.part = a->dw || a->dbias ? static_cast<float *>(a->workspace) : nullptr;
-  int64_t blocks = 0;
+  int64_t parts = 0;
   auto launch_as = [&](auto type, auto with_ds, auto kind) {
     using XT = decltype(type);
     using R = GradRing<XT, decltype(with_ds)::value, decltype(kind)::value>;
     z.groups = std::max(1, R::kThreads / z.lanes);
-    blocks = std::min({kMostParts, (int64_t)num_sms(), ceil_div(a->T, z.groups)});
-    const size_t smem = std::max(R::bytes(z.lanes * z.groups, z.lanes), z.part ? (size_t)z.H * 8 : 0);
-    return launch_rows<layernorm_grad_kernel<XT, decltype(with_ds)::value, decltype(kind)::value>>(z, blocks, smem, stream);
+    constexpr int cluster = decltype(kind)::value == kPair ? 2 : 1;
+    parts = std::min({kMostParts, (int64_t)num_sms() / cluster, ceil_div(a->T, z.groups)});
+    const size_t smem = std::max(R::bytes(z.lanes * z.groups, z.lanes), z.part ? (size_t)(pair ? z.half : z.H) * 8 : 0);
+    return launch_rows<layernorm_grad_kernel<XT, decltype(with_ds)::value, decltype(kind)::value>>(z, cluster * parts, smem, stream, cluster);
   };
   const bool f32 = a->x_dtype == MOE_F32, add = a->ds != nullptr;
   auto launch = [&](auto type, auto with_ds) {
-    using R = GradRing<decltype(type), decltype(with_ds)::value, kMiddle>;
-    if (z.lanes < 32) return launch_as(type, with_ds, std::integral_constant<int, kShort>{});
-    const bool big = z.lanes > R::kThreads || R::bytes(z.lanes, z.lanes) > kMostSmem;
-    return big ? launch_as(type, with_ds, std::integral_constant<int, kBig>{})
-               : launch_as(type, with_ds, std::integral_constant<int, kMiddle>{});
+    if (pair) return launch_as(type, with_ds, std::integral_constant<int, kPair>{});
+    return z.lanes < 32 ? launch_as(type, with_ds, std::integral_constant<int, kShort>{})
+                        : launch_as(type, with_ds, std::integral_constant<int, kMiddle>{});
   };
   using std::true_type;
   using std::false_type;
   rc = f32 ? (add ? launch(0.f, true_type{}) : launch(0.f, false_type{}))
            : (add ? launch(uint16_t{0}, true_type{}) : launch(uint16_t{0}, false_type{}));
   if (rc != MOE_OK || !z.part) return rc;
-  return launch_pdl(sum_blocks_kernel, dim3((unsigned)ceil_div(2 * z.H, 32)), dim3(32 * kSumWarps), 0, stream, z.part, (int)blocks, z.H, a->dw,
+  return launch_pdl(sum_blocks_kernel, dim3((unsigned)ceil_div(2 * z.H, 32)), dim3(32 * kSumWarps), 0, stream, z.part, (int)parts, z.H, a->dw,
                     a->dbias);
 }

@@ -147,6 +147,43 @@ def test_short_rows(B, T, H, dtype):
         assert all(torch.equal(out[k], again[k]) for k in out)
 
 
+@pytest.mark.parametrize("T,H", [(1, 8200), (2, 8208), (75, 12288), (77, 9000), (153, 16376), (400, 16384), (310, 10240)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_long_rows(B, T, H, dtype):
+    """Rows that two SMs share: numbers of rows around one, two and more rounds, columns that do not divide into two equal
+    halves of eight, outputs in place of inputs, and the same bits again."""
+    from moe_expert_layer_counting_gb300 import LayerNorm
+    wide = lambda t: torch.cat([t, torch.full_like(t[:, :8], float("nan"))], 1)[:, :H]       # noqa: E731
+    s, dn, ds = wide(randn(T, H, seed=1, scale=1.5, dtype=dtype, shift=0.3)), wide(randn(T, H, seed=2, scale=0.1)), \
+        wide(randn(T, H, seed=3, scale=0.1, dtype=dtype))
+    ws = torch.empty(B.moe_layernorm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    for w, stream in ((randn(H, seed=5, dtype=F32, shift=1.0), ds), (randn(H, seed=6), None), (None, ds)):
+        keep = torch.full((T + 1, H + 8), 7.0, dtype=dtype, device="cuda")
+        out = {"dx": keep[:T, :H], "dw": None if w is None else torch.empty(H, device="cuda"), "dbias": torch.empty(H, device="cuda")}
+        B.moe_layernorm_backward(s, w, dn, stream, ws, out["dx"], out["dw"], out["dbias"])
+        check_backward(out, s, w, dn, stream, 1e-5)
+        assert bool((keep[T] == 7).all()) and bool((keep[:, H:] == 7).all())
+        place = s.clone()
+        B.moe_layernorm_backward(place, w, dn, stream, ws, place)
+        assert torch.equal(place, out["dx"])
+        again = LayerNorm(w, torch.zeros(H, device="cuda") if w is None or w.dtype == F32 else torch.zeros_like(w)).backward(s, dn, stream)
+        assert all(v is None or torch.equal(v, again[k]) for k, v in out.items())
+
+
+def test_long_rows_infinities_and_nan_stay_in_their_row(B):
+    from moe_expert_layer_counting_gb300 import LayerNorm
+    s, dn = randn(200, 9000, seed=1), randn(200, 9000, seed=2)
+    norm = LayerNorm(randn(9000, seed=3), None)
+    dx = norm.backward(s, dn)["dx"]
+    y, d = s.clone(), dn.clone()
+    y[3, 5], y[79, 8999], d[152, 4600], d[199, 0] = float("nan"), float("inf"), float("nan"), float("-inf")
+    dx2 = norm.backward(y, d)["dx"]
+    fine = torch.ones(200, dtype=torch.bool, device="cuda")
+    fine[[3, 79, 152, 199]] = False
+    # row 199: mean(g) and mean(g h) are infinite, so that g - mean(g) - h mean(g h) is infinite or, where they cancel, NaN
+    assert torch.equal(dx2[fine], dx[fine]) and bool(dx2[[3, 79, 152]].isnan().all()) and not bool(dx2[199].isfinite().any())
+
+
 @pytest.mark.parametrize("H", [64, 200])
 def test_short_rows_infinities_and_nan_stay_in_their_row(B, H):
     from moe_expert_layer_counting_gb300 import LayerNorm
