@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(ForwardRing<XT, ADD, KIND>::kThreads, 1) layer
 //          does not hold twice two.  4096 x 7168 in 51 us; 80 one by one, 75 with two blocks' worth of warps
 //          at 72 registers.
 //   kPair  rows of more than 8192 columns: a cluster of two blocks owns a row, half the columns each, and every
-//          sum is joined through both blocks' shared memory (2048 x 16384, BF16 with ds, in MEASURED; one block of 1024 threads
-//          of 64 registers, a row at a time, 100).
+//          sum is joined through both blocks' shared memory, in one exchange a round, with the sums of the rows after
+//          it (2048 x 16384, BF16 with ds, in 76 us; with two exchanges 83; one block of 1024 threads of 64 registers, a row at a time, 100).
 template <typename XT, bool DS, int KIND>
 struct GradRing {
   static constexpr int kSlot = kColumns * (int)(sizeof(XT) * (DS ? 2 : 1) + 2);    // bytes of a thread's part of a row
@@ -470,12 +470,7 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
   for (int r = 0; r < kRuns; ++r)
 #pragma unroll
     for (int i = 0; i < RUN / 2; ++i) dw[r][i] = db[r][i] = twice(0.f);
-  // a row's sums go through two buffers, each written again after the other's barrier
-  for (int half = 0; row - sub < z.T; half ^= 1) {
-    const bool whole = kRows == 1 || row + stride < z.T;     // both rows are there
-    const bool any = !SHORT || row < z.T;                    // the first is
-    copies_wait<1>();
-    float sum[kRows];
+  auto sum_rows = [&](int half, float *sum) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       P2 s = twice(0.f);
@@ -488,12 +483,25 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
         }
       sum[j] = both(s);
     }
-    if (SHORT)
-      lanes_sum(sum, tpr);
-    else if constexpr (PAIR)
-      pair_sum(sum, rank, red);
-    else
-      group_sum(sum, z.warps, t >> 5, red, join);
+  };
+  float sum[kRows];
+  if constexpr (PAIR) {
+    copies_wait<1>();
+    sum_rows(0, sum);
+    pair_sum(sum, rank, red + 256);
+  }
+  // a row's sums go through two buffers, each written again after the other's barrier
+  for (int half = 0; row - sub < z.T; half ^= 1) {
+    const bool whole = kRows == 1 || row + stride < z.T;     // both rows are there
+    const bool any = !SHORT || row < z.T;                    // the first is
+    if constexpr (!PAIR) {
+      copies_wait<1>();
+      sum_rows(half, sum);
+      if (SHORT)
+        lanes_sum(sum, tpr);
+      else
+        group_sum(sum, z.warps, t >> 5, red, join);
+    }
     P2 mean[kRows], sq[kRows], sg[kRows], sgv[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
@@ -531,12 +539,17 @@ __global__ void __launch_bounds__(GradRing<XT, DS, KIND>::kThreads, 1) layernorm
 #pragma unroll
       for (int j = 0; j < kRows; ++j) lanes_sum(sums[j], tpr);
     } else if constexpr (PAIR) {
-      float all[3 * kRows];
+      // with the next rows' sums, so that a round has one exchange
+      float all[4 * kRows];
 #pragma unroll
       for (int k = 0; k < 3 * kRows; ++k) all[k] = sums[k / 3][k % 3];
-      pair_sum(all, rank, red + 256);
+      copies_wait<0>();
+      sum_rows(half ^ 1, all + 3 * kRows);
+      pair_sum(all, rank, red + 256 * half);
 #pragma unroll
       for (int k = 0; k < 3 * kRows; ++k) sums[k / 3][k % 3] = all[k];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) sum[j] = all[3 * kRows + j];
     } else {
       group_sums(sums, z.warps, t >> 5, red + 256, join);
     }
