@@ -694,6 +694,27 @@ def moe_layernorm_forward(x: torch.Tensor, b: torch.Tensor, w: torch.Tensor, bia
     return rc
 
 
+def layernorm_forward(x: torch.Tensor, b: torch.Tensor, w: torch.Tensor, bias: torch.Tensor, eps: float, stream=None) -> tuple:
+    """(s, n) of moe_layernorm_forward, new tensors (s is x without b); what is new needs no check, a third of the call."""
+    dtype, shape = x.dtype, x.shape
+    xt = _DTYPES.get(dtype)
+    columns = _column_weights(shape[1], w, bias) if xt is not None and len(shape) == 2 else None
+    xr, br = None if columns is None else _rows(x, shape, dtype), _NONE if b is None else _rows(b, shape)
+    if xr is None or br is None or not _on_current_device(x, b, w, bias):
+        _invalid("moe_layernorm_forward", True)
+    n = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    if b is None:
+        s, sr = x, _NONE
+    else:
+        s = torch.empty(shape, dtype=dtype, device=x.device)
+        sr = s.data_ptr(), shape[1]
+    a = _LAYERNORM_ARGS.pack(_LAYERNORM_ARGS.size, xt, columns[0], eps, *shape, *xr, *br, *columns[1:], *sr, n.data_ptr(), shape[1])
+    rc = lib.moe_layernorm_forward(a, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_layernorm_forward")
+    return s, n
+
+
 def moe_layernorm_workspace_size(T: int, H: int) -> int:
     return int(lib.moe_layernorm_workspace_size(T, H))
 
@@ -721,6 +742,29 @@ def moe_layernorm_backward(s: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, d
     if check:
         _check(rc, "moe_layernorm_backward")
     return rc
+
+
+def layernorm_backward(s: torch.Tensor, w: torch.Tensor, bias: torch.Tensor, dn: torch.Tensor, ds: torch.Tensor, eps: float,
+                       stream=None) -> tuple:
+    """(dx, dw, dbias) of moe_layernorm_backward, new tensors (dw and dbias None without w or bias)."""
+    dtype, shape = s.dtype, s.shape
+    xt = _DTYPES.get(dtype)
+    columns = _column_weights(shape[1], w, bias) if xt is not None and len(shape) == 2 else None
+    sr, dnr = None if columns is None else _rows(s, shape, dtype), _rows(dn, shape)
+    dsr = _NONE if ds is None else _rows(ds, shape, dtype)
+    if sr is None or dnr is None or dsr is None or not _on_current_device(s, w, bias, dn, ds):
+        _invalid("moe_layernorm_backward", True)
+    device, H, size = s.device, shape[1], lib.moe_layernorm_workspace_size(*shape)
+    dx = torch.empty(shape, dtype=dtype, device=device)
+    dw = None if w is None else torch.empty(H, dtype=torch.float32, device=device)
+    dbias = None if bias is None else torch.empty(H, dtype=torch.float32, device=device)
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    a = _LAYERNORM_GRADS.pack(_LAYERNORM_GRADS.size, xt, columns[0], eps, *shape, *sr, columns[1], *dnr, *dsr, dx.data_ptr(), H,
+                              0 if w is None else dw.data_ptr(), 0 if bias is None else dbias.data_ptr(), ws.data_ptr(), size)
+    rc = lib.moe_layernorm_backward(a, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_layernorm_backward")
+    return dx, dw, dbias
 
 
 # ---------------------------------------------------------------- AdamW over many tensors (include/moe_adamw.h)

@@ -233,15 +233,8 @@ class LayerNorm:
         """(s, n): the stream with the last layer's answer b (without it: x itself) and its norm, the next layer's input."""
         if stream is not None:
             with _on(stream):
-                return self._forward(x, b, stream)
-        return self._forward(x, b, None)
-
-    def _forward(self, x, b, stream):
-        new, flat = torch.empty_like, torch.contiguous_format
-        s = None if b is None else new(x, memory_format=flat)
-        n = new(x if b is None else b, dtype=torch.bfloat16, memory_format=flat)
-        B.moe_layernorm_forward(x, b, self.weight, self.bias, s, n, self.eps, stream)
-        return (x if s is None else s), n
+                return B.layernorm_forward(x, b, self.weight, self.bias, self.eps, stream)
+        return B.layernorm_forward(x, b, self.weight, self.bias, self.eps)
 
     def backward(self, s: torch.Tensor, dn: torch.Tensor, ds: torch.Tensor = None, stream=None) -> dict:
         """Gradients dx (x's and, rounded to its type, b's), dw and dbias (float32; None where there is no weight or bias)
@@ -252,12 +245,7 @@ class LayerNorm:
         return self._backward(s, dn, ds, None)
 
     def _backward(self, s, dn, ds, stream):
-        new = torch.empty_like
-        dx = new(s, memory_format=torch.contiguous_format)
-        dw = None if self.weight is None else new(self.weight, dtype=torch.float32)
-        dbias = None if self.bias is None else new(self.bias, dtype=torch.float32)
-        ws = s.new_empty(B.moe_layernorm_workspace_size(*s.shape), dtype=torch.uint8)
-        B.moe_layernorm_backward(s, self.weight, dn, ds, ws, dx, dw, dbias, self.eps, stream)
+        dx, dw, dbias = B.layernorm_backward(s, self.weight, self.bias, dn, ds, self.eps, stream)
         return {"dx": dx, "dw": dw, "dbias": dbias}
 
 
