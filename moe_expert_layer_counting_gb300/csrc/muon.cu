@@ -1132,16 +1132,21 @@ void choose_tiles(NsStage &s, int64_t E) {
   }
 }
 
-int launch_newton_schulz(const NsMaps &maps, const NsArgs &g, cudaStream_t st) {
+// The kernel's shared memory is allowed on the current device.
+bool newton_schulz_ready() {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     if (cudaFuncSetAttribute(newton_schulz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsLayout::kBytes) != cudaSuccess)
-      return MOE_ERR_CUDA;
+      return false;
     ready.fetch_or(bit, std::memory_order_release);
   }
+  return true;
+}
+
+int launch_newton_schulz(const NsMaps &maps, const NsArgs &g, cudaStream_t st) {
   int64_t most = 0;
   for (const NsStage &s : g.stage) most = std::max<int64_t>(most, (int64_t)g.E * s.items);
   cudaLaunchAttribute attr[2];
@@ -1230,53 +1235,60 @@ int run_small(const Elementwise &z, const moe_newton_schulz &ns, int ctas, cudaS
   return cudaLaunchKernelEx(&cfg, small_muon_kernel<VEC, WIDE>, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The stages of a stack's products and their tensor maps, and the kernel made ready: all that a call can be refused for, so that
+// nothing is enqueued before.
+int plan_newton_schulz(const Elementwise &z, const moe_newton_schulz &ns, const Stack &w, uint16_t *const (&x)[2], uint16_t *s,
+                       uint16_t *q, NsMaps &maps, NsArgs &g) {
+  const int64_t E = z.E, N = z.N, K = z.K;
+  const bool wide = N <= K, square = ns.c != 0.f;                    // wide: the Gram matrix is that of the rows
+  const float unit = 1.f / kScale, shift = square ? ns.b / (2.f * ns.c) : 0.f;
+  const int n = (int)w.n, k = (int)std::max(N, K);
+  g.stage[0] = {n, n, k, !wide, !wide, 1, 0, 0, square ? unit : ns.b * unit, kScale * (square ? shift : ns.a), square ? s : q, w.lds};
+  g.stage[1] = {n, n, n, 0, 0, 1, 0, 0, ns.c * unit, kScale * (ns.a - ns.b * shift * 0.5f), q, w.lds};
+  g.stage[2] = {(int)N, (int)K, n, 0, wide, 0, 0, 0, unit, 0.f, nullptr, 0};
+  int64_t items = 0;
+  for (NsStage &stage : g.stage) {
+    choose_tiles(stage, E);
+    items += E * stage.items;
+  }
+  // tickets and a matrix's arrivals (16 a tile) are ints
+  if (items * ns.steps >= 1 << 27) return MOE_ERR_UNSUPPORTED_SHAPE;
+  bool ok = true;
+  for (int i = 0; i < 2; ++i)
+    ok = ok && encode_f16(&maps.x128[i], x[i], K, N, E, w.ldx, GP::kBK, 128) && encode_f16(&maps.x32[i], x[i], K, N, E, w.ldx, 64, 32) &&
+         encode_f16(&maps.x64[i], x[i], K, N, E, w.ldx, 64, 64);
+  ok = ok && encode_f16(&maps.s128, s, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.s32, s, n, n, E, w.lds, 64, 32) &&
+       encode_f16(&maps.q128, q, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.q32, q, n, n, E, w.lds, 64, 32);
+  if (!ok || !newton_schulz_ready()) return MOE_ERR_CUDA;
+  g.E = (int)E;
+  g.steps = ns.steps;
+  g.wide = wide;
+  g.square = square;
+  g.ticket = z.sync;
+  g.done = z.sync + 1;
+  g.inject_wait = injected_wait();
+  g.status = z.status;
+  return MOE_OK;
+}
+
 template <int VEC>
 int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *base, cudaStream_t st) {
-  const int64_t E = z.E, N = z.N, K = z.K;
   z.parts = w.parts;
-  z.per = (int)round_up(ceil_div(N * K, z.parts), 8 * 256);
+  z.per = (int)round_up(ceil_div(z.N * z.K, z.parts), 8 * 256);
   z.ld = w.ldx;
   z.sums = reinterpret_cast<float *>(base + w.sums);
   z.sync = reinterpret_cast<int *>(base + w.sync);
-  uint16_t *x[2] = {reinterpret_cast<uint16_t *>(base + w.x[0]), reinterpret_cast<uint16_t *>(base + w.x[1])};
+  uint16_t *const x[2] = {reinterpret_cast<uint16_t *>(base + w.x[0]), reinterpret_cast<uint16_t *>(base + w.x[1])};
   uint16_t *s = reinterpret_cast<uint16_t *>(base + w.s), *q = reinterpret_cast<uint16_t *>(base + w.q);
+  NsMaps maps;
+  NsArgs g{};
+  int rc = ns.steps > 0 ? plan_newton_schulz(z, ns, w, x, s, q, maps, g) : MOE_OK;
+  if (rc != MOE_OK) return rc;
   z.x = x[0];
-  const dim3 grid((unsigned)z.parts, (unsigned)E), block(256);
-  int rc = launch_pdl(momentum_kernel<VEC>, grid, block, 0, st, z);
+  const dim3 grid((unsigned)z.parts, (unsigned)z.E), block(256);
+  rc = launch_pdl(momentum_kernel<VEC>, grid, block, 0, st, z);
   if (rc == MOE_OK) rc = launch_pdl(scale_kernel<VEC>, grid, block, 0, st, z);
-  if (rc == MOE_OK && ns.steps > 0) {
-    const bool wide = N <= K, square = ns.c != 0.f;                    // wide: the Gram matrix is that of the rows
-    const float unit = 1.f / kScale, shift = square ? ns.b / (2.f * ns.c) : 0.f;
-    const int n = (int)w.n, k = (int)std::max(N, K);
-    NsMaps maps;
-    bool ok = true;
-    for (int i = 0; i < 2; ++i)
-      ok = ok && encode_f16(&maps.x128[i], x[i], K, N, E, w.ldx, GP::kBK, 128) && encode_f16(&maps.x32[i], x[i], K, N, E, w.ldx, 64, 32) &&
-           encode_f16(&maps.x64[i], x[i], K, N, E, w.ldx, 64, 64);
-    ok = ok && encode_f16(&maps.s128, s, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.s32, s, n, n, E, w.lds, 64, 32) &&
-         encode_f16(&maps.q128, q, n, n, E, w.lds, GP::kBK, 128) && encode_f16(&maps.q32, q, n, n, E, w.lds, 64, 32);
-    if (!ok) return MOE_ERR_CUDA;
-    NsArgs g{};
-    g.stage[0] = {n, n, k, !wide, !wide, 1, 0, 0, square ? unit : ns.b * unit, kScale * (square ? shift : ns.a), square ? s : q, w.lds};
-    g.stage[1] = {n, n, n, 0, 0, 1, 0, 0, ns.c * unit, kScale * (ns.a - ns.b * shift * 0.5f), q, w.lds};
-    g.stage[2] = {(int)N, (int)K, n, 0, wide, 0, 0, 0, unit, 0.f, nullptr, 0};
-    int64_t items = 0;
-    for (NsStage &stage : g.stage) {
-      choose_tiles(stage, E);
-      items += E * stage.items;
-    }
-    // tickets and a matrix's arrivals (16 a tile) are ints
-    if (items * ns.steps >= 1 << 27) return MOE_ERR_UNSUPPORTED_SHAPE;
-    g.E = (int)E;
-    g.steps = ns.steps;
-    g.wide = wide;
-    g.square = square;
-    g.ticket = z.sync;
-    g.done = z.sync + 1;
-    g.inject_wait = injected_wait();
-    g.status = z.status;
-    rc = launch_newton_schulz(maps, g, st);
-  }
+  if (rc == MOE_OK && ns.steps > 0) rc = launch_newton_schulz(maps, g, st);
   if (rc != MOE_OK) return rc;
   z.x = x[ns.steps & 1];
   return launch_pdl(update_kernel<VEC>, grid, block, 0, st, z);
