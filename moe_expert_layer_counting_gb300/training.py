@@ -35,7 +35,8 @@ class TrainableExperts:
         # of the products (the size does not depend on the rows) and of the last permute: status() reads each one's status
         self.workspaces = [torch.zeros(B.moe_grouped_workspace_size(1, H, 2 * self.I, E), dtype=torch.uint8, device=dev)
                            for _ in range(6)]
-        self.permute_workspace = self.gated_workspace = None
+        self.permute_workspace = None
+        self.gated_workspaces = {}                  # of the last forward and of the last backward call's gated product
         self.fused = fused
 
     def _check_rows(self, name, t, T):
@@ -85,7 +86,7 @@ class TrainableExperts:
             h = torch.zeros(T * k, self.I, dtype=torch.bfloat16, device=n.device)
             ws = self._gated_workspace(T * k)
             B.moe_gated_forward(s["rows"], self.l1, offsets, h, ws, a=s["a"], row_w=s["w"][:, 0])
-            s["h"], self.gated_workspace = h, ws
+            s["h"], self.gated_workspaces["forward"] = h, ws
         else:
             B.moe_grouped_forward(s["rows"], self.l1, offsets, s["a"], self.workspaces[0])
             gate, up = s["a"].float().split(self.I, 1)
@@ -104,7 +105,7 @@ class TrainableExperts:
             dw = torch.zeros(da.shape[0], dtype=torch.float32, device=da.device)
             ws = self._gated_workspace(da.shape[0])
             B.moe_gated_dgrad(do, self.l2, s["offsets"], s["a"], da, ws, row_w=s["w"][:, 0], drow_w=dw)
-            self.gated_workspace = ws
+            self.gated_workspaces["backward"] = ws
         else:
             dh = torch.zeros_like(s["h"])
             B.moe_grouped_dgrad(do, self.l2, s["offsets"], dh, self.workspaces[2])
@@ -122,8 +123,8 @@ class TrainableExperts:
         return self._sum_slots(drows, s), dtopk_w
 
     def status(self) -> int:
-        """MOE_OK, or the first status that the last step's permute or products reported (synchronises)."""
-        used = [w for w in (self.permute_workspace, self.gated_workspace) if w is not None] + self.workspaces
+        """MOE_OK, or the first status that the last forward and backward call's permute and products reported (synchronises)."""
+        used = ([] if self.permute_workspace is None else [self.permute_workspace]) + [*self.gated_workspaces.values()] + self.workspaces
         return next((c for c in (B.moe_get_device_status(w) for w in used) if c), B.MOE_OK)
 
 

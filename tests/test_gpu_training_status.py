@@ -1,0 +1,69 @@
+"""What the training objects report of a device-side wait that ran out in one of a step's calls, when the calls after it were
+fine: the first code is the step's.
+
+Only the call under test has its wait injected (the host reads the variable as it enqueues), so that no other workspace holds a
+code."""
+import os
+
+import pytest
+import torch
+
+from tests import helpers as Hp
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    Hp.lib()
+    import moe_expert_layer_counting_gb300 as package
+    return package
+
+
+def randn(*shape, seed=0, scale=1.0, dtype=BF16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def inject(monkeypatch, B, name):
+    """Every call of this entry point enqueues a kernel whose first wait runs out."""
+    call = getattr(B, name)
+
+    def injected(*args, **kwargs):
+        os.environ["MOE_MXQ_DEBUG_INJECT_WAIT"] = "1"
+        try:
+            return call(*args, **kwargs)
+        finally:
+            del os.environ["MOE_MXQ_DEBUG_INJECT_WAIT"]
+
+    monkeypatch.setattr(B, name, injected)
+
+
+def experts_step(M, T=60, E=2, H=128, I=64, k=2):
+    layer = M.TrainableExperts(randn(E, 2 * I, H, scale=0.1), randn(E, H, I, scale=0.1), fused=True)
+    idx = torch.arange(T * k, dtype=torch.int32, device="cuda").view(T, k) % E
+    w = torch.full((T, k), 0.5, device="cuda")
+    dl1, dl2 = torch.zeros(E, 2 * I, H, device="cuda"), torch.zeros(E, H, I, device="cuda")
+
+    def forward():
+        return layer.forward(randn(T, H, seed=1), idx, w)[1]
+
+    return layer, forward, lambda kept: layer.backward(randn(T, H, seed=2), kept, dl1, dl2)
+
+
+@pytest.mark.parametrize("name", ["moe_gated_forward", "moe_gated_dgrad"])
+def test_fused_experts_report_either_gated_call(M, monkeypatch, name):
+    from moe_expert_layer_counting_gb300 import binding as B
+    layer, forward, backward = experts_step(M)
+    with monkeypatch.context() as m:
+        inject(m, B, name)
+        backward(forward())
+    assert layer.status() == B.MOE_ERR_TIMEOUT
+    kept = forward()
+    assert layer.status() == (B.MOE_OK if name == "moe_gated_forward" else B.MOE_ERR_TIMEOUT)
+    backward(kept)
+    assert layer.status() == B.MOE_OK
