@@ -133,7 +133,7 @@ class GatedFeedForward:
     gradients: h = f(n gate^T) (n up^T), b = h l2^T, with l1 [2I, H] (gate rows then up rows) and l2 [H, I] in BF16.
 
     activation: ACT_SILU or ACT_GELU_TANH (include/moe_gated.h).  Calls run on the current stream; each has outputs and
-    workspaces of its own, of which the object keeps the last for status().
+    workspaces of its own, of which the object keeps the last forward and the last backward call's for status().
     """
 
     def __init__(self, l1: torch.Tensor, l2: torch.Tensor, activation: int = B.ACT_SILU):
@@ -145,7 +145,7 @@ class GatedFeedForward:
             raise ValueError("activation is ACT_SILU or ACT_GELU_TANH")
         self.l1, self.l2, self.activation = l1, l2, activation
         self.H, self.I = l1.shape[1], l2.shape[1]
-        self._used = []
+        self._used = {"forward": [], "backward": []}
 
     def _workspaces(self, T, n):
         """One for a gated call, n - 1 for products."""
@@ -163,7 +163,7 @@ class GatedFeedForward:
         ws = self._workspaces(T, 2)
         B.moe_gated_forward(n, self.l1[None], offsets, h, ws[0], a=a, activation=self.activation)
         B.moe_grouped_forward(h, self.l2[None], offsets, b, ws[1])
-        self._used = ws
+        self._used["forward"] = ws
         return b, {"n": n, "a": a, "h": h, "offsets": offsets} if keep else None
 
     def backward(self, db: torch.Tensor, s: dict, dl1: torch.Tensor, dl2: torch.Tensor, accumulate: bool = False):
@@ -178,7 +178,7 @@ class GatedFeedForward:
         B.moe_gated_dgrad(db, self.l2[None], offsets, a, da, ws[0], activation=self.activation)
         B.moe_grouped_dgrad(da, self.l1[None], offsets, dn, ws[2])
         B.moe_grouped_wgrad(da, n, offsets, dl1[None], ws[3], accumulate)
-        self._used = ws
+        self._used["backward"] = ws
         return dn
 
     def _check(self, t, T):
@@ -186,5 +186,6 @@ class GatedFeedForward:
             raise ValueError(f"rows are not [T, {self.H}] BF16 on the weights' device, or not those of forward")
 
     def status(self) -> int:
-        """MOE_OK, or the first status that the last forward or backward call's products reported (synchronises)."""
-        return next((c for c in (B.moe_get_device_status(w) for w in self._used) if c), B.MOE_OK)
+        """MOE_OK, or the first status that the last forward and backward call's products reported (synchronises)."""
+        used = self._used["forward"] + self._used["backward"]
+        return next((c for c in (B.moe_get_device_status(w) for w in used) if c), B.MOE_OK)

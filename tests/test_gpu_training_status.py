@@ -67,3 +67,22 @@ def test_fused_experts_report_either_gated_call(M, monkeypatch, name):
     assert layer.status() == (B.MOE_OK if name == "moe_gated_forward" else B.MOE_ERR_TIMEOUT)
     backward(kept)
     assert layer.status() == B.MOE_OK
+
+
+@pytest.mark.parametrize("name", ["moe_gated_forward", "moe_gated_dgrad"])
+def test_a_gated_block_reports_either_gated_call(M, monkeypatch, name):
+    from moe_expert_layer_counting_gb300 import binding as B
+    T, H, I = 60, 128, 64
+    block = M.GatedFeedForward(randn(2 * I, H, scale=0.1), randn(H, I, scale=0.1))
+    dl1, dl2 = torch.zeros(2 * I, H, device="cuda"), torch.zeros(H, I, device="cuda")
+
+    def step():
+        kept = block.forward(randn(T, H, seed=1))[1]
+        block.backward(randn(T, H, seed=2), kept, dl1, dl2)
+
+    with monkeypatch.context() as m:
+        inject(m, B, name)
+        step()
+    assert block.status() == B.MOE_ERR_TIMEOUT
+    step()
+    assert block.status() == B.MOE_OK
