@@ -348,7 +348,7 @@ class Muon:
 
     A step updates the tensors that ``params``, ``state`` and ``copies`` hold then, on the current stream or the given one; its
     workspace is its own.  Captured into a graph, each replay is a step at the captured rate, with the gradients
-    that then lie there.
+    that then lie there; the object holds the replays' status words and has to outlive the graph.
     """
 
     def __init__(self, params, lr: float = 1e-3, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.1,
@@ -365,7 +365,11 @@ class Muon:
             raise ValueError("state is (m,)")
         self.state = {"m": list(state[0])}
         self._status = {}                            # (device, stream handle) -> 64 bytes for each parameter
+        # the same of captured steps, whatever stream they are replayed on; the last is in use, graphs captured before the
+        # parameters changed write the others
+        self._captured = []
         self._check()
+        self._captured_status()
 
     def _check(self, grads=None):
         lists = {"m": (self.state["m"], (torch.float32,)), "copies": (self.copies, (torch.bfloat16,)),
@@ -394,13 +398,29 @@ class Muon:
         with _on(stream):
             self._step(grads, grad_scale, B._stream(stream))
 
+    def _words(self):
+        return torch.zeros(len(self.params), 64, dtype=torch.uint8, device=self.params[0].device)
+
+    def _captured_status(self):
+        """The words of captured steps, which only a call outside of captures can make: zeroed before a graph's first replay."""
+        if not self.params:
+            return None
+        last = self._captured[-1] if self._captured else None
+        if last is None or last.shape[0] != len(self.params) or last.device != self.params[0].device:
+            if _capturing(None):
+                raise RuntimeError("Muon.step in a graph's capture: the parameters changed, and a step without capture has to come first")
+            self._captured.append(self._words())
+        return self._captured[-1]
+
     def _step(self, grads, grad_scale, handle):
         if not self.params:
             return
-        key = self.params[0].device, handle
-        status = self._status.get(key)
-        if status is None or status.shape[0] != len(self.params):
-            status = self._status[key] = torch.zeros(len(self.params), 64, dtype=torch.uint8, device=self.params[0].device)
+        status = self._captured_status()
+        if not _capturing(None):
+            key = self.params[0].device, handle
+            status = self._status.get(key)
+            if status is None or status.shape[0] != len(self.params):
+                status = self._status[key] = self._words()
         shapes = [(p.numel() // max(1, p.shape[-2] * p.shape[-1]), *p.shape[-2:]) for p in self.params]
         nbytes = max((B.moe_muon_workspace_size(*shape) for shape, p in zip(shapes, self.params) if p.numel()), default=0)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.params[0].device)
@@ -412,9 +432,9 @@ class Muon:
                                 self.ns_coefficients, self.eps, copy, grad_scale, handle, status=status[i])
 
     def device_status(self, stream=None) -> int:
-        """MOE_OK, or the first that the last step on this stream reported (synchronises)."""
+        """MOE_OK, or the first that the last step on this stream or the last replay of captured ones reported (synchronises)."""
         if not self.params:
             return B.MOE_OK
-        words = self._status.get((self.params[0].device, B._stream(stream)))
-        return next((code for code in (B.moe_get_device_status(w, stream) for w in ([] if words is None else words)) if code),
-                    B.MOE_OK)
+        device = self.params[0].device
+        words = [t for t in (self._status.get((device, B._stream(stream))), *self._captured) if t is not None and t.device == device]
+        return next((code for t in words for code in (B.moe_get_device_status(w, stream) for w in t) if code), B.MOE_OK)

@@ -86,3 +86,50 @@ def test_a_gated_block_reports_either_gated_call(M, monkeypatch, name):
     assert block.status() == B.MOE_ERR_TIMEOUT
     step()
     assert block.status() == B.MOE_OK
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 136), (2, 72, 40)])
+def test_muon_reports_replayed_steps(M, monkeypatch, shape):
+    """A captured step's code is its last replay's, whatever stream the replay ran on, and none before the first replay."""
+    from moe_expert_layer_counting_gb300 import binding as B
+    p, g = randn(*shape, seed=9, scale=0.02, dtype=torch.float32), randn(*shape, seed=1, scale=1e-3)
+    opt = M.Muon([p.clone(), p], lr=0.01)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph in graphs:
+        with monkeypatch.context() as m:
+            if graph is graphs[0]:
+                inject(m, B, "moe_muon_step")
+            with torch.cuda.graph(graph):
+                opt.step([g, g])
+        assert opt.device_status() == B.MOE_OK
+    graphs[0].replay()
+    assert opt.device_status() == B.MOE_ERR_TIMEOUT
+    opt.step([g, g])                                        # an eager step's words are its own
+    assert opt.device_status() == B.MOE_ERR_TIMEOUT
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert opt.device_status() == opt.device_status(side) == B.MOE_OK
+
+
+def test_muon_with_more_parameters_is_captured_after_a_step(M):
+    """The words of captured steps are made outside of a capture, one for each parameter; graphs of before keep theirs."""
+    p, g = randn(2, 72, 40, scale=0.02, dtype=torch.float32), randn(2, 72, 40, seed=1, scale=1e-3)
+    opt, graph = M.Muon([p], lr=0.01), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step([g])
+    opt.params.append(p.clone())
+    opt.state["m"].append(torch.zeros_like(p))
+    before = [t.clone() for t in (*opt.params, *opt.state["m"])]
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            opt.step([g, g])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, (*opt.params, *opt.state["m"])))
+    opt.step([g, g])
+    graph.replay()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        opt.step([g, g])
+    assert opt.device_status() == 0
