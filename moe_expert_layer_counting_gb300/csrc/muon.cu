@@ -1246,13 +1246,14 @@ int plan_newton_schulz(const Elementwise &z, const moe_newton_schulz &ns, const 
   g.stage[0] = {n, n, k, !wide, !wide, 1, 0, 0, square ? unit : ns.b * unit, kScale * (square ? shift : ns.a), square ? s : q, w.lds};
   g.stage[1] = {n, n, n, 0, 0, 1, 0, 0, ns.c * unit, kScale * (ns.a - ns.b * shift * 0.5f), q, w.lds};
   g.stage[2] = {(int)N, (int)K, n, 0, wide, 0, 0, 0, unit, 0.f, nullptr, 0};
-  int64_t items = 0;
+  int64_t items = 0;                       // of a matrix, all iterations
   for (NsStage &stage : g.stage) {
     choose_tiles(stage, E);
-    items += E * stage.items;
+    items += (int64_t)ns.steps * stage.items;
   }
-  // tickets and a matrix's arrivals (16 a tile) are ints
-  if (items * ns.steps >= 1 << 27) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // Tickets (each pair draws one past the last) are 32 bits, a matrix's arrivals an int.  With up to 40 steps no stack that fits
+  // 288 GB reaches either: 12 bytes a value, 256 values a tile at the least in stacks that long.
+  if (E * items + num_sms() > 0xffffffffLL || 2 * GP::kEpiWarps * items > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED_SHAPE;
   bool ok = true;
   for (int i = 0; i < 2; ++i)
     ok = ok && encode_f16(&maps.x128[i], x[i], K, N, E, w.ldx, GP::kBK, 128) && encode_f16(&maps.x32[i], x[i], K, N, E, w.ldx, 64, 32) &&

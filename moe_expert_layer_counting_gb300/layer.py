@@ -369,6 +369,7 @@ class Muon:
         # parameters changed write the others
         self._captured = []
         self._check()
+        self._stacks()
         self._captured_status()
 
     def _check(self, grads=None):
@@ -377,6 +378,8 @@ class Muon:
         for p in self.params:
             if p.dim() < 2 or p.dtype not in B._DTYPES or not p.is_contiguous():
                 raise ValueError("parameters are contiguous matrices or stacks of them, bf16 or float32")
+            if p.device != self.params[0].device:
+                raise ValueError("parameters are on one device")
         for name, (tensors, kinds) in lists.items():
             if tensors is None:
                 continue
@@ -385,6 +388,14 @@ class Muon:
                         t.shape != p.shape or t.dtype not in kinds or not t.is_contiguous() or t.device != p.device))
                     for t, p in zip(tensors, self.params)):
                 raise ValueError(f"{name}: shapes, types, strides or devices do not fit the parameters")
+
+    def _stacks(self):
+        """(shape [E, N, K], workspace bytes) of each parameter; of one without values no bytes."""
+        shapes = [(p.numel() // max(1, p.shape[-2] * p.shape[-1]), *p.shape[-2:]) for p in self.params]
+        sizes = [B.moe_muon_workspace_size(*shape) if p.numel() else 0 for shape, p in zip(shapes, self.params)]
+        if any(not size and p.numel() for size, p in zip(sizes, self.params)):
+            raise ValueError("a parameter has more matrices, rows or columns than a step takes")
+        return list(zip(shapes, sizes))
 
     def _scale(self, N, K):
         if self.adjust is None:
@@ -395,8 +406,9 @@ class Muon:
         """One step with these gradients (contiguous, bf16 or float32 each), each times grad_scale (a device float)."""
         grads = list(grads)
         self._check(grads)
+        stacks = self._stacks()                      # nothing is refused after the first parameter has moved
         with _on(stream):
-            self._step(grads, grad_scale, B._stream(stream))
+            self._step(grads, stacks, grad_scale, B._stream(stream))
 
     def _words(self):
         return torch.zeros(len(self.params), 64, dtype=torch.uint8, device=self.params[0].device)
@@ -412,7 +424,7 @@ class Muon:
             self._captured.append(self._words())
         return self._captured[-1]
 
-    def _step(self, grads, grad_scale, handle):
+    def _step(self, grads, stacks, grad_scale, handle):
         if not self.params:
             return
         status = self._captured_status()
@@ -421,10 +433,8 @@ class Muon:
             status = self._status.get(key)
             if status is None or status.shape[0] != len(self.params):
                 status = self._status[key] = self._words()
-        shapes = [(p.numel() // max(1, p.shape[-2] * p.shape[-1]), *p.shape[-2:]) for p in self.params]
-        nbytes = max((B.moe_muon_workspace_size(*shape) for shape, p in zip(shapes, self.params) if p.numel()), default=0)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.params[0].device)
-        for i, (p, shape) in enumerate(zip(self.params, shapes)):
+        workspace = torch.empty(max(size for _, size in stacks), dtype=torch.uint8, device=self.params[0].device)
+        for i, (p, (shape, _)) in enumerate(zip(self.params, stacks)):
             if p.numel():
                 copy = None if self.copies is None or self.copies[i] is None else self.copies[i].view(shape)
                 B.moe_muon_step(p.view(shape), grads[i].view(shape), self.state["m"][i].view(shape), workspace, self.lr,
