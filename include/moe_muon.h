@@ -31,9 +31,9 @@
  *     matrix lacks (0.4, 0.6 and 1.2, and as much as that from rounding such a matrix to BF16 alone).
  *     Momentum, norm and update are computed in float32; squares that overflow float32
  *     (values of 1e18 and more) give a norm of infinity.
- *   - c is 0, or |b / (2 c)| at most 8; a, b, c at most 64 in magnitude (otherwise MOE_ERR_INVALID_ARG):
- *     the iterates and their polynomials have to stay below 16 in magnitude, as they do for
- *     polynomials that map [0, 1] into [0, 1.3].
+ *   - c is 0, or |b / (2 c)| at most 8; a, b, c at most 64 and a + b t + c t^2 at most 15.9 in magnitude for
+ *     t in [0, 1] (otherwise MOE_ERR_INVALID_ARG).  The later iterates and their polynomials have to stay below 16
+ *     in magnitude too, as they do for polynomials x (a + b x^2 + c x^4) that map [0, 1] into [0, 1.3].
  *   - A matrix's results depend on that matrix only: one with infinities or NaN
  *     does not change another; a matrix of zeros gives zeros.
  *   - moe_orthogonalize's out may be x if their types are the same; no other overlap.

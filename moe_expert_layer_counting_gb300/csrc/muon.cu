@@ -1166,6 +1166,14 @@ int launch_newton_schulz(const NsMaps &maps, const NsArgs &g, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, newton_schulz_kernel, maps, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The largest |a + b t + c t^2| of t in [0, 1], where the first iteration's Gram matrix has its eigenvalues: Q's entries are
+// no larger, and its diagonal is a where the matrix has nothing.  FP16 with kScale ends at 15.99, and Q's own rounding is 2^-11 of that.
+double largest_factor(const moe_newton_schulz &ns) {
+  const double a = ns.a, b = ns.b, c = ns.c, t = c != 0.0 ? -b / (2.0 * c) : 0.0;
+  const double inside = t > 0.0 && t < 1.0 ? std::fabs(a + t * (b + c * t)) : 0.0;
+  return std::max({std::fabs(a), std::fabs(a + b + c), inside});
+}
+
 int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, const int32_t *status, const void *workspace,
                 size_t bytes) {
   if (E < 0 || N <= 0 || K <= 0 || ns.steps < 0 || ns.steps > 64) return MOE_ERR_INVALID_ARG;
@@ -1173,6 +1181,7 @@ int check_stack(int64_t E, int64_t N, int64_t K, const moe_newton_schulz &ns, co
     if (!(std::fabs(f) <= 64.f)) return MOE_ERR_INVALID_ARG;
   if (!(ns.eps >= 0.f) || std::isinf(ns.eps) || (ns.c != 0.f && !(std::fabs(ns.b) <= 16.f * std::fabs(ns.c))))
     return MOE_ERR_INVALID_ARG;
+  if (largest_factor(ns) > 15.9) return MOE_ERR_INVALID_ARG;
   if (N >= (1 << 20) || K >= (1 << 20) || E > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (E == 0) return MOE_OK;
   if (!workspace) return MOE_ERR_INVALID_ARG;
