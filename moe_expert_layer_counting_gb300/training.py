@@ -12,6 +12,15 @@ import torch
 from . import binding as B
 
 
+def _check_gradients(dl1, dl2, l1, l2, accumulate):
+    """Of a backward call, before its first product writes dl2 or adds to it."""
+    kinds = (torch.float32,) if accumulate else (torch.bfloat16, torch.float32)
+    for name, d, w in (("dl1", dl1, l1), ("dl2", dl2, l2)):
+        if d.shape != w.shape or d.dtype not in kinds or d.device != w.device or not d.is_contiguous() or d.data_ptr() % 16:
+            raise ValueError(f"{name} is not contiguous {'float32' if accumulate else 'BF16 or float32'} of the weight's shape, "
+                             "on its device, aligned to 16 bytes")
+
+
 class TrainableExperts:
     """b = layer(n, topk_idx, topk_w) and its gradients, with the layer's weights l1 [E, 2I, H] (gate rows then up rows)
     and l2 [E, H, I] in BF16.
@@ -98,6 +107,7 @@ class TrainableExperts:
     def backward(self, db: torch.Tensor, s: dict, dl1: torch.Tensor, dl2: torch.Tensor, accumulate: bool = False):
         """(dn [T, H], dtopk_w [T, k]); the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
         self._check_rows("db", db, s["row"].shape[0])
+        _check_gradients(dl1, dl2, self.l1, self.l2, accumulate)
         do = db[s["token"]]
         B.moe_grouped_wgrad(do, s["h"], s["offsets"], dl2, self.workspaces[3], accumulate)
         if self.fused:
@@ -170,8 +180,7 @@ class GatedFeedForward:
         """dn [T, H]; the weights' gradients go to dl1 and dl2 (BF16, or float32, then also added to)."""
         n, a, offsets, T = s["n"], s["a"], s["offsets"], s["n"].shape[0]
         self._check(db, T)
-        if dl1.shape != self.l1.shape or dl2.shape != self.l2.shape:
-            raise ValueError("dl1 and dl2 are not of the weights' shapes")
+        _check_gradients(dl1, dl2, self.l1, self.l2, accumulate)
         da, dn = torch.empty_like(a), torch.empty_like(n, memory_format=torch.contiguous_format)
         ws = self._workspaces(T, 4)
         B.moe_grouped_wgrad(db, s["h"], offsets, dl2[None], ws[1], accumulate)
