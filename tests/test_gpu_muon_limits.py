@@ -27,3 +27,15 @@ def test_largest_factors(B, shape, how):
     x = T.randn(*shape, seed=5, scale=1e-3, dtype=F32)
     T.check(T.ortho(B, x, F32, steps=1, **how), x, steps=1, **how)
     assert bool((T.ortho(B, torch.zeros_like(x), **how) == 0).all())
+
+
+@pytest.mark.parametrize("rank,most", [(1, 0.15), (4, 0.08), (16, 0.05)])
+@pytest.mark.parametrize("shape", [(64, 200), (128, 384), (2000, 128), (256, 640), (520, 264), (1024, 2048)])
+def test_matrices_of_low_rank(B, shape, rank, most):
+    """As the gradient of an expert with few tokens: the polynomial enlarges what the roundings leave in the directions that
+    the matrix lacks."""
+    N, K = shape
+    x = (T.randn(N, rank, seed=1, dtype=F32) @ T.randn(rank, K, seed=2, dtype=F32))[None]
+    got = T.ortho(B, x, F32)
+    T.check(got, x)
+    assert T.error(got[0], T.orthogonal(x[0])) <= most + 0.005
