@@ -2,7 +2,10 @@
 
 Every function has the name of the C entry point it calls (include/moe_mxq.h,
 include/moe_bfp8.h, include/moe_grouped.h, include/moe_gated.h,
-include/moe_norm.h, include/moe_layernorm.h, include/moe_adamw.h, include/moe_muon.h) and takes torch tensors for the device buffers; all work runs in the
+include/moe_norm.h, include/moe_layernorm.h, include/moe_adamw.h,
+include/moe_muon.h) and takes torch tensors for the device buffers, outputs
+among them; layernorm_forward and layernorm_backward are the two calls of that
+name with new outputs, which LayerNorm makes.  All work runs in the
 library's CUDA kernels on the given (default: current) stream.  PyTorch is
 used for device memory and streams only.  A non-zero status raises MoeError.
 There is no CPU fallback: importing this module without the built library

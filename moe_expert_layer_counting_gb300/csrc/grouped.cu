@@ -35,7 +35,7 @@ int rows_product(const uint16_t *in, int64_t ld_in, const uint16_t *w, const int
   g.out = out;
   g.inject_wait = injected_wait();
   g.status = reinterpret_cast<int *>(workspace);
-  return launch_grouped<OP>(maps, g, most_row_items<OP>(g), st);
+  return launch_grouped<OP>(maps, g, most_row_items(g), st);
 }
 
 }  // namespace

@@ -177,23 +177,17 @@ constexpr int kGroup = 8;
 
 __device__ __forceinline__ int tiles_of(int rows) { return rows <= 320 ? (rows > 0) : rows <= 576 ? 2 : (rows + 255) / 256; }
 
-// Rows of a tile, as their log2: 256, or 128 or 64 where all tiles are in work at once all the same (so that a tile's loads, and
-// above all its drain by eight warps, are shorter): one expert of 256 rows, N = 4096, K = 7168, forward 37 -> 28 us, gated 41 -> 30,
-// gated gradient 47 -> 29; of 1024 rows, 1024 x 2048: 16 -> 12, 20 -> 13.5, 26 -> 14.5.  Finer tiles in two rounds lose
-// (512 rows of 4096 x 7168 by 64: 50 us, by 128: 30, by 256: 38).  Called by a warp; which launches look: see most_row_items().
-__device__ __forceinline__ int log_rows(const int32_t *offsets, int E, int mt, int pairs, int lane) {
-  int n128 = 0, n64 = 0;
-#pragma unroll 4
-  for (int e = lane; e < E; e += 32) {
-    const int rows = __ldg(offsets + e + 1) - __ldg(offsets + e);
-    n128 += (rows + 127) >> 7;
-    n64 += (rows + 63) >> 6;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    n128 += __shfl_xor_sync(0xffffffffu, n128, o);
-    n64 += __shfl_xor_sync(0xffffffffu, n64, o);
-  }
+// Rows of a tile, as their log2: 256, or 128 or 64 where all tiles (n128, n64 of a warp's lanes together) are in work at once all
+// the same, so that a tile's loads, and above all its drain by eight warps, are shorter: one expert of 256 rows, N = 4096,
+// K = 7168, forward 37 -> 28 us, gated 41 -> 30, gated gradient 47 -> 29; of 1024 rows, 1024 x 2048: 16 -> 12, 20 -> 13.5,
+// 26 -> 14.5.  Finer tiles in two rounds lose (512 rows of 4096 x 7168 by 64: 50 us, by 128: 30, by 256: 38), and so do plain
+// ones of experts that are short already (up to `least` rows each: 19 of up to 75, 512 columns from sums of 1232, 9.1 us whole
+// and 9.6 cut).  Of 1040 products of 65 to 9000 rows of up to 256 experts the choice takes 0.944 of the time without it in the mean,
+// 215 of them under 0.9; 16 are over 1.1, most of few columns (one expert of 5701 rows, 64 columns from sums of 1016: 15 and 23 us).
+__device__ __forceinline__ int log_rows(int n64, int n128, int longest, int least, int mt, int pairs) {
+  n64 = __reduce_add_sync(0xffffffffu, n64);
+  n128 = __reduce_add_sync(0xffffffffu, n128);
+  if (__reduce_max_sync(0xffffffffu, longest) <= least) return 8;
   return (int64_t)n64 * mt <= pairs ? 6 : (int64_t)n128 * mt <= pairs ? 7 : 8;
 }
 
@@ -562,14 +556,21 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       // a lane takes a run of experts, so that its loads are all in flight
       int *first = tile_first + warp * (g.E + 1);
       const int per = (g.E + 31) / 32, e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
-      auto fill = [&](auto tiles) {
-        auto tiles_in_list = [&](int e) {
-          const int n = bad ? 0 : tiles(__ldg(g.offsets + e + 1) - __ldg(g.offsets + e));
-          return (n > 1) == (warp == 0) ? n : 0;
-        };
-        int sum = 0;
+      int sum = 0, n64 = 0, n128 = 0, longest = 0;
+      auto in_list = [&](int n) { return !bad && (n > 1) == (warp == 0) ? n : 0; };
+      auto rows_of = [&](int e) { return __ldg(g.offsets + e + 1) - __ldg(g.offsets + e); };
 #pragma unroll 8
-        for (int e = e0; e < e1; ++e) sum += tiles_in_list(e);
+      for (int e = e0; e < e1; ++e) {
+        const int rows = rows_of(e);
+        sum += in_list(tiles_of(rows));
+        n64 += (rows + 63) >> 6;
+        n128 += (rows + 127) >> 7;
+        longest = max(longest, rows);
+      }
+      constexpr int kLeast = OP == kForward || OP == kDgrad ? 96 : 64;
+      const int log = g.may_split && !bad ? log_rows(n64, n128, longest, kLeast, mt, (int)gridDim.x >> 1) : 8;
+      // the same tiles again, with their places: first[e] is the first of e
+      auto fill = [&](auto tiles) {
         int upto = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -579,15 +580,18 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         int at = upto - sum;
         for (int e = e0; e < e1; ++e) {
           first[e] = at;
-          at += tiles_in_list(e);
+          at += in_list(tiles(rows_of(e)));
         }
         if (lane == 31) first[g.E] = upto;
       };
-      const int log = g.may_split && !bad ? log_rows(g.offsets, g.E, mt, (int)gridDim.x >> 1, lane) : 8;
-      if (log == 8)
+      if (log == 8) {
         fill([](int rows) { return tiles_of(rows); });
-      else
-        fill([log](int rows) { return (rows + (1 << log) - 1) >> log; });
+      } else {
+        auto cut = [log](int rows) { return (rows + (1 << log) - 1) >> log; };
+        sum = 0;
+        for (int e = e0; e < e1; ++e) sum += in_list(cut(rows_of(e)));
+        fill(cut);
+      }
     }
     __syncthreads();
     lists.items0 = tile_first[g.E] * mt;
@@ -1026,17 +1030,10 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
   return cudaLaunchKernelEx(&cfg, grouped_kernel<OP>, maps, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// forward / dgrad: the most items of any offsets; says whether tiles of fewer rows may pay.  Looking costs 0.2 to 0.4 us of the
-// plain products' 5 to 10, and more pairs on fewer rows leave the next launch fewer free SMs to start on, so that these look only
-// where the experts' tiles are long on average and 256 rows a tile leave most pairs idle: of 520 products of 65 to 9000 rows
-// and up to 256 experts the tiles then take 0.72 to 1.0 of the time where they pay (93 of them by more than a tenth), and 9 us
-// become 7.5 where every launch looked (2706 rows, 72 x 248: 7.4 without, 9.7 with it).  The gated ones drain for longer.
-template <int OP>
+// forward / dgrad: the most items of any offsets; says whether tiles of fewer rows may pay.
 int64_t most_row_items(GArgs &g) {
-  constexpr bool kPlain = OP == kForward || OP == kDgrad;
-  const int64_t mt = ceil_div(g.M, GP::kM), pairs = num_sms() / 2;
-  g.may_split = g.P > 64 && ceil_div(g.P, 128) * mt <= pairs;
-  if (kPlain && (g.P <= 32LL * g.E || 10 * ceil_div(g.P, GP::kN) * mt > 3 * pairs)) g.may_split = 0;
+  const int64_t mt = ceil_div(g.M, GP::kM);
+  g.may_split = g.P > 64 && ceil_div(g.P, 128) * mt <= num_sms() / 2;
   return std::min<int64_t>(g.P, g.P / (g.may_split ? 64 : GP::kN) + g.E) * mt;
 }
 

@@ -420,7 +420,7 @@ class Muon:
         last = self._captured[-1] if self._captured else None
         if last is None or last.shape[0] != len(self.params) or last.device != self.params[0].device:
             if _capturing(None):
-                raise RuntimeError("Muon.step in a graph's capture: the parameters changed, and a step without capture has to come first")
+                raise RuntimeError("Muon in a graph's capture: the object is new, or its parameters changed; make it, or take a step, before")
             self._captured.append(self._words())
         return self._captured[-1]
 

@@ -13,11 +13,13 @@ from tests import helpers as Hp
 pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
-R = 328                          # length of the sums
+R = 328                          # length of the gated products' sums
 
-# counts, columns of the product (gate and up rows for the gated one), height
-PLAIN = [([300, 0, 40, 130], 400, 64), ([70, 64, 65, 129], 136, 64), ([690, 0, 450, 33, 40], 1000, 128), ([0, 1100, 80], 904, 128),
-         ([20] * 12, 400, 256), ([900, 0, 800], 1400, 256), ([2100, 640], 264, 128)]
+# counts, columns of the product, length of its sums, height
+PLAIN = [([300, 0, 40, 130], 400, 584, 64), ([70, 64, 65, 129], 136, 328, 64), ([690, 0, 450, 33, 40], 1000, 584, 128),
+         ([0, 1100, 80], 904, 1032, 128), ([20] * 12, 400, 584, 256), ([900, 0, 800], 1400, 584, 256), ([2100, 640], 264, 520, 128),
+         ([96, 20, 0, 90], 400, 328, 256)]
+# counts, columns (gate and up rows forward), height
 GATED = [([300, 0, 40, 130], 400, 64), ([0, 65, 128, 1, 200], 528, 64), ([700, 0, 500, 33], 1392, 128),
          ([260, 130, 0, 5, 700], 1200, 128), ([400, 0, 300, 20], 4000, 256), ([40] * 9, 2560, 256)]
 
@@ -36,7 +38,7 @@ def up(a, b):
 def height(counts, columns, gated, pairs):
     """csrc/grouped_kernel.cuh: most_row_items() says which launches look, log_rows() what they choose."""
     P, E, mt = sum(counts), len(counts), up(columns, 256)
-    if P <= 64 or up(P, 128) * mt > pairs or (not gated and (P <= 32 * E or 10 * up(P, 256) * mt > 3 * pairs)):
+    if P <= 64 or up(P, 128) * mt > pairs or max(counts) <= (64 if gated else 96):
         return 256
     pairs = min(pairs, min(P, P // 64 + E) * mt)
     return next((t for t in (64, 128) if sum(up(c, t) for c in counts) * mt <= pairs), 256)
@@ -48,13 +50,13 @@ def expect(counts, columns, gated, want):
         assert height(counts, columns, gated, pairs) == want
 
 
-@pytest.mark.parametrize("counts,columns,want", PLAIN)
+@pytest.mark.parametrize("counts,columns,sums,want", PLAIN)
 @pytest.mark.parametrize("op", ["forward", "dgrad"])
-def test_products(B, op, counts, columns, want):
+def test_products(B, op, counts, columns, sums, want):
     expect(counts, columns, False, want)
     E, P = len(counts), sum(counts)
-    N, K = (columns, R) if op == "forward" else (R, columns)
-    x, w = P0.randn(P, R, seed=1), P0.randn(E, N, K, seed=2, scale=0.1)
+    N, K = (columns, sums) if op == "forward" else (sums, columns)
+    x, w = P0.randn(P, sums, seed=1), P0.randn(E, N, K, seed=2, scale=0.1)
     out, ws = torch.full((P + 1, columns), 3.0, dtype=BF16, device="cuda"), P0.workspace(B, P, N, K, E)
     (B.moe_grouped_forward if op == "forward" else B.moe_grouped_dgrad)(x, w, P0.offsets_of(counts), out[:P], ws)
     assert B.moe_get_device_status(ws) == B.MOE_OK and bool((out[P] == 3).all())
