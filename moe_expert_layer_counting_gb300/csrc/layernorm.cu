@@ -15,7 +15,7 @@
 // The gradients' column sums are kept in registers over a block's rows, joined
 // over its groups in shared memory, written as one part for each block and
 // summed over the blocks, in a fixed order, by a second kernel.
-// Measured (BF16, H = 7168): s and n of 8192 rows in 75 us (6.3 TB/s), of 4096 in 39;
+// Measured (BF16, H = 7168): s and n of 8192 rows in 75 to 78 us (6.0 to 6.3 TB/s), of 4096 in 39;
 // the gradients joined with ds of 8192 rows in 89 us (5.3 TB/s), of 4096 in 51, of which ~14 are the
 // launch's start, its end, and the parts.  float32 rows: 123 us (5.7 TB/s) and 129 (6.4).
 #include <cuda_bf16.h>
