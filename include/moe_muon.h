@@ -26,11 +26,11 @@
  *     and aligned to their elements; 16-byte alignment and K a multiple of 8 are faster.
  *   - The iterates are held in FP16 with a fixed scale of 2^12, their sums in float32: eleven bits
  *     where BF16 has eight.  The polynomial enlarges what lies in directions of small singular values by up
- *     to a^steps, a rounding as well: in norm the result is off by 6e-4 to 4e-3 for matrices of independent
- *     values (least with a side of at most 128 and few matrices, most where that side is below 50 and the other
- *     or the stack too long for it; BF16 iterates: 1e-2 to 2e-2), by up to 1.5e-2 for ones of a few large and many
- *     small singular values (0.12), by 0.05 for rank 16, 0.08 for rank 4 and 0.15 for rank 1, all of it in directions
- *     that the matrix lacks (0.4, 0.6 and 1.2; rounding such a matrix itself to BF16 costs 0.25, 0.5 and 1.15).
+ *     to a^steps, a rounding as well: in norm the result is off by 5e-4 to 1.2e-3 for matrices of independent
+ *     values (BF16 iterates: 1e-2 to 2e-2), by up to 1.5e-2 for ones of a few large and many small singular
+ *     values (0.12), by 0.05 for rank 16, 0.08 for rank 4 and 0.15 for rank 1, all of it in directions that the
+ *     matrix lacks (0.4, 0.6 and 1.2; rounding such a matrix itself to BF16 costs 0.25, 0.5 and 1.15).
+ *     What FP16 leaves of the diagonals of the products in between is not lost.
  *     Momentum, norm and update are computed in float32; squares that overflow float32
  *     (values of 1e18 and more) give a norm of infinity.
  *   - c is 0, or |b / (2 c)| at most 8; a, b, c at most 64 and a + b t + c t^2 at most 15.9 in magnitude for

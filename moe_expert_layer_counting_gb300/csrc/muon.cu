@@ -15,6 +15,10 @@
 // FP16 iterates.  All singular values of an iterate are below 1.3, so that its
 // range is known and FP16 with a fixed scale of 2^12 (16 at most, 2^-26 the
 // smallest normal value) keeps 11 bits where BF16 keeps 8, at the same rate.
+// The diagonals of S and Q alone are kept in full (left_of): rounded, they would
+// be off by nearly the same in every row, which is as much as all else together
+// (1024 x 2048: 1.6e-3 of the result instead of 7e-4, 30 x 3383 3.2e-3 instead of
+// 6e-4; the times are the same).
 //
 // Measured: 64 matrices of 1024 x 2048, five iterations: 1.87 to 2.07 ms in a burst (two
 // GPUs; 1.29 to 1.16 PFLOP/s of 7.5 GFLOP a matrix and iteration; the tiles on the
@@ -268,6 +272,8 @@ struct NsArgs {
   NsStage stage[3];         // Gram matrix to S (without c: to Q), Q from S, X from Q and X
   int E, steps, wide, square;       // wide: N <= K; square: the second stage is there
   int *ticket, *done;       // next item; [E] warps that are done with a tile
+  float *of_s, *of_q;       // [E][ld_of]: what FP16 leaves of the diagonals (see left_of)
+  int ld_of;                // a multiple of 64
   int inject_wait;
   int *status;
 };
@@ -277,8 +283,9 @@ struct NsLayout {
   static constexpr int kClaims = 2, kAhead = 8;     // items in the ring; blocks before an item's last that the next is claimed
   static constexpr int kOffEpi = kStages * kSlot;
   static constexpr int kOffItems = kOffEpi + GP::kEpiWarps * kEpiBytes;
-  static constexpr int kOffBar = kOffItems + 16 * kClaims;
-  static constexpr int kNumBars = 2 * kStages + 7 + 2 * kClaims;
+  static constexpr int kOffOf = kOffItems + 16 * kClaims;          // 256 floats: what is left of a diagonal, for a tile's drain
+  static constexpr int kOffBar = kOffOf + 4 * GP::kN;
+  static constexpr int kNumBars = 2 * kStages + 7 + 2 * kClaims + 2;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * kNumBars + 63) & ~63;
   static constexpr int kBytes = 1024 + kOffTmemPtr + 64;
 };
@@ -393,6 +400,20 @@ __device__ __forceinline__ int ns_arrivals(const NsArgs &g, int at) {
   return 2 * GP::kEpiWarps * (it * (a + b + c) + (k > 0 ? a : 0) + (k > 1 ? b : 0));
 }
 
+// What FP16 leaves of a diagonal's value x (both scaled).  Of S: what it adds to Q's diagonal, 2 c h (x - h).  Of Q: the factor of
+// X's row (of tall matrices, column) that stands for it, as the other values of a row add up to little beside it.  A stage's
+// drain writes them, the next one's reads them: the thread of the loads fetches them behind its last load (fetched by the drain's
+// warps, after the accumulator: chains of short stages 5 to 8 % slower; with a wait of these warps for the matrix: 12 %).
+__device__ __forceinline__ float left_of(float x, bool of_square, float square_alpha) {
+  const float h = __half2float(__float2half_rn(x));
+  return of_square ? 2.f * square_alpha * h * (x - h) : h == 0.f ? 1.f : __fdividef(x, h);
+}
+
+// Whether a tile's drain needs values of of_s (its rows', for Q's diagonal) or of of_q (X's rows', of tall matrices columns').
+__device__ __forceinline__ bool needs_of(const NsItem &it, const NsStage &s, int k) {
+  return k == 2 || (k == 1 && it.c * s.tn < (it.m + 1) * GP::kM);
+}
+
 __device__ __forceinline__ int tile_slots(const NsStage &s, int c) { return min(s.tn, (s.C - c * s.tn + 31) & ~31); }
 
 __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __grid_constant__ NsMaps maps,
@@ -410,6 +431,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
   uint64_t *item_full = never + 1;                                       // each CTA
   uint64_t *item_empty = item_full + L::kClaims;                         // leader: both CTAs' roles have read it
   uint64_t *want = item_empty + L::kClaims;                              // leader: its loads are nearly done
+  uint64_t *of_full = want + 1, *of_empty = of_full + 1;                 // each CTA: values for a drain, read by its warps
   int4 *ring = reinterpret_cast<int4 *>(smem + L::kOffItems);
   uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::kOffTmemPtr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -431,6 +453,8 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
       mbar_init(want, 1);
+      mbar_init(of_full, 1);
+      mbar_init(of_empty, GP::kEpiWarps);
       for (int c = 0; c < L::kClaims; ++c) {
         mbar_init(item_full + c, 1);
         mbar_init(item_empty + c, 2 + 2 * GP::kEpiWarps + 1);      // loads, epilogues, the leader's MMAs
@@ -455,7 +479,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
     // ------------------------------------------------------------ loads (both CTAs), one thread
     if (elect_one()) {
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0, ofs = 0;           // ofs: drains' values fetched so far
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(full), 0);
       const uint64_t policy = l2_policy(false);
@@ -499,11 +523,24 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == L::kStages) { stage = 0; phase ^= 1; }
         }
+        if (ok && needs_of(it, s, k)) {
+          // after the tile's loads: the drain before this one may still read its own
+          const bool columns = k == 2 && !g.wide;
+          const uint32_t of_bytes = 4u * (columns ? s.tn : 128);                  // (past a row's end: the next one's)
+          ok = mbar_wait_reset(of_empty, (ofs & 1) ^ 1, status, kLimit, kWaitProducerEmpty, it.at);
+          if (ok) {
+            mbar_arrive_expect_tx(of_full, of_bytes);
+            bulk_load(smem + L::kOffOf, (k == 1 ? g.of_s : g.of_q) + (int64_t)it.e * g.ld_of + (columns ? it.c * s.tn : row), of_bytes,
+                      of_full);
+            ++ofs;
+          }
+        }
       }
       // no CTA leaves with copies in flight (as in grouped_kernel)
       for (int s = 0; s < L::kStages; ++s)
         if (rank == 0 && (issued & (1u << s)))
           mbar_wait_reset(&full[s], (issued_phase >> s) & 1u, status, kLimit, kWaitProducerDrain, s, false);
+      if (ofs > 0) mbar_wait_reset(of_full, (ofs - 1) & 1, status, kLimit, kWaitProducerDrain, 0, false);
       if (*reinterpret_cast<volatile int *>(status + 1) != 0) {
         const long long t0 = clock64();
         while (clock64() - t0 < 200000) __nanosleep(1000);
@@ -579,20 +616,35 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, ew = warp - GP::kFirstEpiWarp;
     unsigned char *buf = smem + L::kOffEpi + ew * L::kEpiBytes;
+    uint32_t ofs = 0;
     for (int j = 0; items.next(it, true); ++j) {
       const int iteration = it.at / 3, k = it.at - 3 * iteration;
       const NsStage &s = g.stage[k];
       const CUtensorMap *d_map = k == 2 ? &maps.x32[(iteration + 1) & 1] : k == 1 || !g.square ? &maps.q32 : &maps.s32;
       const int acc = j & 1;
+      // this warp's rows and columns of the tile: 128 columns, or 64 (of narrow tiles the first warps' alone)
+      const int wide = s.tn > 128 ? 128 : 64, c_first = wide * (ew >> 2);
+      const int row0 = it.m * GP::kM + (int)rank * 128 + 32 * q;
+      const bool mirrored = s.symmetric && it.c * s.tn >= (it.m + 1) * GP::kM, in_rows = row0 + lane < s.M;
+      float beta = s.beta, alpha = s.alpha;
+      const float *of = reinterpret_cast<const float *>(smem + L::kOffOf);
+      const bool of_rows = needs_of(it, s, k) && (k == 1 || g.wide), of_columns = k == 2 && !g.wide;
+      if (of_rows || of_columns) {
+        if (!__all_sync(0xffffffffu, mbar_wait_reset(of_full, ofs & 1, status, kLimit, kWaitEpiTmemFull, it.at))) break;
+        ++ofs;
+      }
+      if (of_rows) {
+        const float left = in_rows ? of[32 * q + lane] : 0.f;
+        if (k == 1) beta += left; else alpha *= left;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(of_empty);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_reset(&tmem_full[acc], (uint32_t)(j >> 1) & 1u, status, kLimit,
                                                    kWaitEpiTmemFull, it.at)))
         break;
       tc_fence_after();
-      // this warp's columns of the tile: 128, or 64 (of narrow tiles the first warps' alone)
-      const int wide = s.tn > 128 ? 128 : 64, c_first = wide * (ew >> 2);
-      const int row0 = it.m * GP::kM + (int)rank * 128 + 32 * q;
       const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * GP::kN);
-      const bool mirrored = s.symmetric && it.c * s.tn >= (it.m + 1) * GP::kM;
+      bool kept = false;                                              // this warp wrote a part of a diagonal
       if (row0 < s.M) {
         for (int c0 = c_first; c0 < min(c_first + wide, s.tn); c0 += 64) {
           const int col0 = it.c * s.tn + c0;
@@ -604,11 +656,30 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
           tmem_ld_wait();
           const int diagonal = row0 + lane - col0;                      // this lane's column on the diagonal
           uint32_t p[32];
+          if (of_columns) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = fmaf(s.alpha, __uint_as_float(v[2 * i]), diagonal == 2 * i ? s.beta : 0.f);
-            const float y = fmaf(s.alpha, __uint_as_float(v[2 * i + 1]), diagonal == 2 * i + 1 ? s.beta : 0.f);
-            p[i] = pack_f16(x, y);
+            for (int i = 0; i < 32; ++i) {
+              const float2 f = *reinterpret_cast<const float2 *>(of + c0 + 2 * i);
+              p[i] = pack_f16(alpha * f.x * __uint_as_float(v[2 * i]), alpha * f.y * __uint_as_float(v[2 * i + 1]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = fmaf(alpha, __uint_as_float(v[2 * i]), diagonal == 2 * i ? beta : 0.f);
+              const float y = fmaf(alpha, __uint_as_float(v[2 * i + 1]), diagonal == 2 * i + 1 ? beta : 0.f);
+              p[i] = pack_f16(x, y);
+            }
+          }
+          if (k < 2 && !mirrored && col0 <= row0 && row0 < col0 + 64) {
+            // the rows' part of the diagonal lies here
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x = diagonal == i ? __uint_as_float(v[i]) : x;
+            const bool of_square = k == 0 && g.square;
+            if (in_rows)
+              (of_square ? g.of_s : g.of_q)[(int64_t)it.e * g.ld_of + row0 + lane] =
+                  left_of(fmaf(alpha, x, beta), of_square, g.stage[1].alpha);
+            kept = true;
           }
           if (lane == 0) bulk_wait_read<0>();                          // the store before has read the staging
           __syncwarp();
@@ -638,8 +709,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_done(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      if (of_columns && lane == 0) mbar_arrive(of_empty);
       // published: this warp's part of the tile is in memory
-      if (mirrored) {
+      if (mirrored || kept) {
         fence_proxy_async_global();
         __threadfence();
         __syncwarp();
@@ -676,9 +748,8 @@ __global__ void __launch_bounds__(GP::kThreads, 1) newton_schulz_kernel(const __
 // nanoseconds, a commit and a pass from TMEM back to shared memory, where the
 // kernel above needs a trip through L2 between any two: 4 us an iteration of 128 x 256
 // instead of 10.
-// What FP16 leaves of the diagonals of S and Q is not lost here: rounded, they would be off by the same in every row of
-// a matrix of few rows (562 x 39: 7.5e-4 of the result instead of 3.3e-3, 128 x 384 7.5e-4 instead of 1.2e-3, for 3 to 8 % of
-// the time).
+// What FP16 leaves of the diagonals costs 3 to 8 % of the time here (562 x 39: 7.5e-4 of the result instead of 3.3e-3, 128 x 384
+// 7.5e-4 instead of 1.2e-3).
 struct SmallArgs {
   Elementwise z;
   int n, k, kc;             // kc: columns of a CTA, a multiple of 64
@@ -879,12 +950,7 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
   auto desc_k = [&](int off) { return make_smem_desc(smem_base + (uint32_t)off, 16, 1024, kSwizzle128B); };
   const int q = warp & 3, row = 32 * q + lane;                  // this thread's TMEM lane: a row of S, Q and X
   const uint32_t t_lane = (uint32_t)(32 * q) << 16;
-  // What FP16 leaves of a diagonal's value x.  Of S: what it adds to Q's diagonal.  Of Q: the factor of X's row that stands
-  // for it, as the other values of a row add up to little beside it.
-  auto left = [&](float x, bool of_square) {
-    const float h = __half2float(__float2half_rn(x));
-    return of_square ? 2.f * g.square_alpha * h * (x - h) : h == 0.f ? 1.f : __fdividef(x, h);
-  };
+  auto left = [&](float x, bool of_square) { return left_of(x, of_square, g.square_alpha); };
   // S or Q from TMEM: factor, diagonal, FP16, into blocks at `to`
   auto take_square = [&](float alpha, float beta, unsigned char *to, float *diag, bool of_square) {
     uint32_t v[2][32];
@@ -1066,9 +1132,9 @@ __global__ void __launch_bounds__(SmallLayout::kThreads, 1) small_muon_kernel(co
 // ---------------------------------------------------------------- host
 
 struct Stack {              // of a call's workspace
-  int64_t n, ldx, lds;
+  int64_t n, ldx, lds, ld_of;
   int parts;
-  size_t sums, sync, x[2], s, q, total;
+  size_t sums, sync, x[2], s, q, of_s, of_q, total;
 };
 
 Stack stack_layout(int64_t E, int64_t N, int64_t K) {
@@ -1091,6 +1157,8 @@ Stack stack_layout(int64_t E, int64_t N, int64_t K) {
   for (auto &x : w.x) x = take((size_t)E * N * w.ldx * 2);
   w.s = take((size_t)E * w.n * w.lds * 2);
   w.q = take((size_t)E * w.n * w.lds * 2);
+  w.ld_of = (int64_t)round_up(w.n, 64);
+  for (auto *of : {&w.of_s, &w.of_q}) *of = take(((size_t)E * w.ld_of + 256) * 4);       // (tiles read to their own ends)
   w.total = off;
   return w;
 }
@@ -1276,6 +1344,7 @@ int plan_newton_schulz(const Elementwise &z, const moe_newton_schulz &ns, const 
   g.square = square;
   g.ticket = z.sync;
   g.done = z.sync + 1;
+  g.ld_of = (int)w.ld_of;
   g.inject_wait = injected_wait();
   g.status = z.status;
   return MOE_OK;
@@ -1292,6 +1361,8 @@ int run_stack(Elementwise z, const moe_newton_schulz &ns, const Stack &w, char *
   uint16_t *s = reinterpret_cast<uint16_t *>(base + w.s), *q = reinterpret_cast<uint16_t *>(base + w.q);
   NsMaps maps;
   NsArgs g{};
+  g.of_s = reinterpret_cast<float *>(base + w.of_s);
+  g.of_q = reinterpret_cast<float *>(base + w.of_q);
   int rc = ns.steps > 0 ? plan_newton_schulz(z, ns, w, x, s, q, maps, g) : MOE_OK;
   if (rc != MOE_OK) return rc;
   z.x = x[0];

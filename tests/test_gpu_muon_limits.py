@@ -39,3 +39,15 @@ def test_matrices_of_low_rank(B, shape, rank, most):
     got = T.ortho(B, x, F32)
     T.check(got, x)
     assert T.error(got[0], T.orthogonal(x[0])) <= most + 0.005
+
+
+@pytest.mark.parametrize("shape", [(30, 3383), (300, 1000), (1000, 300), (31, 4100), (1024, 2048), (2050, 700), (129, 900), (136, 264)])
+def test_products_keep_their_diagonals(B, shape):
+    """As test_gpu_muon.py's test of small matrices, for those that go through the products: the roundings' draw plays no part but
+    for 1.5 times, and a sum's terms add 2^-23 each at most."""
+    x = T.randn(3, *shape, seed=sum(shape), scale=1e-3, dtype=F32)
+    for o, m in list(zip(T.ortho(B, x, F32), x))[:2]:
+        emulated = T.kept_diagonals(m)
+        ref = T.orthogonal(m)
+        bound = 1.5 * T.error(emulated.T if shape[0] > shape[1] else emulated, ref) + max(shape) * 2.0 ** -23
+        assert T.error(o, ref) <= bound, (T.error(o, ref), bound)
