@@ -25,9 +25,9 @@
  * the first bytes of the workspace (moe_get_device_status), reset by each call.
  *
  *   - Rows, weights and outputs are BF16, v and dv float32.  Sums, activations
- *     and products are held in float32 (the tensor core truncates as it adds, in norm 1.1e-9 of a
- *     sum for each of its H terms if their signs differ, up to 4.5e-9 if they have one sign, which shows in dv
- *     alone: 8e-6 and 3e-5 of it at H = 7168); h is that of the unrounded gate and up
+ *     and products are held in float32 (the tensor core truncates as it adds; for dv, where that would
+ *     show, d is summed in parts: dv is off by 5e-7 in norm at H = 2048 and 1.0e-6 at 7168, by up to
+ *     3.5e-6 where all terms of d have one sign); h is that of the unrounded gate and up
  *     values; every output is rounded once.  h of moe_gated_dgrad is that of the
  *     BF16 values a, as is everything else there.
  *   - 0 <= P < 2^31 rows, H and I multiples of 8, 1 <= E <= 1024 experts with any

@@ -262,7 +262,9 @@ int gated_product(const moe_gated_args *a, cudaStream_t st) {
   g.status = reinterpret_cast<int *>(a->workspace);
   float *part = kBack && a->drow_w ? reinterpret_cast<float *>(static_cast<char *>(a->workspace) + kStatusBytes) : nullptr;
   g.gated = {(int)a->I, a->activation, a->row_w, a->a, a->ld_a, a->h, a->ld_h, a->da, a->ld_da, part};
-  const int launched = launch_grouped<OP>(maps, g, most_row_items(g), st);
+  const int64_t items = most_row_items(g);
+  const int launched = part && a->H > kDvBlocks * GP::kBK ? launch_grouped<kBack ? kGatedGradDv : OP>(maps, g, items, st)
+                                                          : launch_grouped<OP>(maps, g, items, st);
   if (launched != MOE_OK || !part) return launched;
   return launch_pdl(sum_parts_kernel, dim3((unsigned)ceil_div(a->P, 256)), dim3(256), 0, st, part,
                     (int)ceil_div(a->I, kPartCols), a->P, a->offsets, (int)a->E, g.status, a->drow_w);

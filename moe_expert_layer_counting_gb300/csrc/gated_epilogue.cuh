@@ -75,21 +75,20 @@ __device__ __forceinline__ void turn_bf16(const V (&v)[N], int lane, Put put) {
   }
 }
 
-// As turn_bf16 for 32 rows, with the values left in float32: t[r][c] is column
-// 8 (l / 8) + c of row 8 r + l % 8.
-__device__ __forceinline__ void turn_f32(const uint32_t (&v)[32], int lane, float (&t)[4][8]) {
+// As turn_bf16 for eight rows, with the values left in float32: t[c] is column 8 (l / 8) + c of row l % 8.
+__device__ __forceinline__ void turn_f32(const uint32_t (&v)[8], int lane, float (&t)[8]) {
   const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0, b2 = (lane & 4) != 0;
-  float w[16][2];
+  float w[4][2];
 #pragma unroll
-  for (int p = 0; p < 16; ++p) {
+  for (int p = 0; p < 4; ++p) {
     const float a = __uint_as_float(v[2 * p]), b = __uint_as_float(v[2 * p + 1]);
     const float got = __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
     w[p][0] = b0 ? got : a;
     w[p][1] = b0 ? b : got;
   }
-  float u[8][4];
+  float u[2][4];
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float got = __shfl_xor_sync(0xffffffffu, b1 ? w[2 * q][i] : w[2 * q + 1][i], 2);
@@ -97,13 +96,11 @@ __device__ __forceinline__ void turn_f32(const uint32_t (&v)[32], int lane, floa
       u[q][2 + i] = b1 ? w[2 * q + 1][i] : got;
     }
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float got = __shfl_xor_sync(0xffffffffu, b2 ? u[2 * r][i] : u[2 * r + 1][i], 4);
-      t[r][i] = b2 ? got : u[2 * r][i];
-      t[r][4 + i] = b2 ? u[2 * r + 1][i] : got;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float got = __shfl_xor_sync(0xffffffffu, b2 ? u[0][i] : u[1][i], 4);
+    t[i] = b2 ? got : u[0][i];
+    t[4 + i] = b2 ? u[1][i] : got;
+  }
 }
 
 // s(q(z)) and q'(z).  GELU's q is taken at |z| <= 12, past which s is 0 or 1 in
@@ -151,65 +148,65 @@ __device__ __forceinline__ void gated_rows(const uint32_t (&v)[32], int64_t row0
   });
 }
 
-// The way back: 32 N slots of dh at this warp's 32 columns from col0.
-__device__ __forceinline__ void gated_grad_rows(const uint32_t (&v)[32], int64_t row0, int rows, int col0, int64_t P,
-                                                const GatedArgs &g, int lane) {
-  const int col = col0 + 8 * (lane >> 3);
-  uint4 gate[4], up[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = 8 * r + (lane & 7);
-    gate[r] = up[r] = make_uint4(0, 0, 0, 0);
+// The way back, for eight N slots (`rows` of them rows, from row0) at this warp's 32 columns from col0: what a lane reads of a,
+// and these slots of dh.
+struct GatedRow {
+  uint4 gate, up;
+
+  __device__ __forceinline__ void take(int64_t row0, int rows, int col0, const GatedArgs &g, int lane) {
+    const int col = col0 + 8 * (lane >> 3), row = lane & 7;
+    gate = up = make_uint4(0, 0, 0, 0);
     if (row < rows && col < g.I) {
       const uint16_t *a = g.a + (row0 + row) * g.ld_a + col;
-      gate[r] = *reinterpret_cast<const uint4 *>(a);
-      up[r] = *reinterpret_cast<const uint4 *>(a + g.I);
+      gate = *reinterpret_cast<const uint4 *>(a);
+      up = *reinterpret_cast<const uint4 *>(a + g.I);
     }
   }
-  float t[4][8];
+};
+
+__device__ __forceinline__ void gated_grad_rows(const uint32_t (&v)[8], const GatedRow &in, int64_t row0, int rows, int col0, int64_t P,
+                                                const GatedArgs &g, int lane) {
+  const int col = col0 + 8 * (lane >> 3), row = lane & 7;
+  const bool mine = row < rows && col < g.I;
+  float t[8];
   turn_f32(v, lane, t);
+  const float w = g.row_w && mine ? __ldg(g.row_w + row0 + row) : 1.f;
+  const uint32_t gw[4] = {in.gate.x, in.gate.y, in.gate.z, in.gate.w};
+  const uint32_t uw[4] = {in.up.x, in.up.y, in.up.z, in.up.w};
+  uint32_t dg[4], du[4], hh[4];
+  float sum = 0.f;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = 8 * r + (lane & 7);
-    const bool mine = row < rows && col < g.I;
-    const float w = g.row_w && mine ? __ldg(g.row_w + row0 + row) : 1.f;
-    const uint32_t gw[4] = {gate[r].x, gate[r].y, gate[r].z, gate[r].w};
-    const uint32_t uw[4] = {up[r].x, up[r].y, up[r].z, up[r].w};
-    uint32_t dg[4], du[4], hh[4];
-    float sum = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    float a[2], b[2], c[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a[2], b[2], c[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float z = __uint_as_float(k == 0 ? gw[i] << 16 : gw[i] & 0xFFFF0000u);
-        const float u = __uint_as_float(k == 0 ? uw[i] << 16 : uw[i] & 0xFFFF0000u);
-        float dq;
-        const float s = gate_sigmoid(g.activation, z, dq);
-        const float f = z * s;
-        const float d = t[r][2 * i + k];
-        sum = fmaf(d * f, u, sum);
-        const float dw = d * w;
-        a[k] = dw * u * fmaf(f * (1.f - s), dq, s);
-        b[k] = dw * f;
-        c[k] = f * u * w;
-      }
-      dg[i] = pack_bf16(a[0], a[1]);
-      du[i] = pack_bf16(b[0], b[1]);
-      hh[i] = pack_bf16(c[0], c[1]);
+    for (int k = 0; k < 2; ++k) {
+      const float z = __uint_as_float(k == 0 ? gw[i] << 16 : gw[i] & 0xFFFF0000u);
+      const float u = __uint_as_float(k == 0 ? uw[i] << 16 : uw[i] & 0xFFFF0000u);
+      float dq;
+      const float s = gate_sigmoid(g.activation, z, dq);
+      const float f = z * s;
+      const float d = t[2 * i + k];
+      sum = fmaf(d * f, u, sum);
+      const float dw = d * w;
+      a[k] = dw * u * fmaf(f * (1.f - s), dq, s);
+      b[k] = dw * f;
+      c[k] = f * u * w;
     }
-    if (mine) {
-      uint16_t *da = g.da + (row0 + row) * g.ld_da + col;
-      *reinterpret_cast<uint4 *>(da) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-      *reinterpret_cast<uint4 *>(da + g.I) = make_uint4(du[0], du[1], du[2], du[3]);
-      if (g.h) *reinterpret_cast<uint4 *>(g.h + (row0 + row) * g.ld_h + col) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-    }
-    if (g.part) {
-      if (!mine) sum = 0.f;              // a row of another expert, or columns past the last
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      if (lane < 8 && row < rows) g.part[(int64_t)(col0 >> 5) * P + row0 + row] = sum;
-    }
+    dg[i] = pack_bf16(a[0], a[1]);
+    du[i] = pack_bf16(b[0], b[1]);
+    hh[i] = pack_bf16(c[0], c[1]);
+  }
+  if (mine) {
+    uint16_t *da = g.da + (row0 + row) * g.ld_da + col;
+    *reinterpret_cast<uint4 *>(da) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+    *reinterpret_cast<uint4 *>(da + g.I) = make_uint4(du[0], du[1], du[2], du[3]);
+    if (g.h) *reinterpret_cast<uint4 *>(g.h + (row0 + row) * g.ld_h + col) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+  }
+  if (g.part) {
+    if (!mine) sum = 0.f;              // a row of another expert, or columns past the last
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane < 8 && row < rows) g.part[(int64_t)(col0 >> 5) * P + row0 + row] = sum;
   }
 }
 

@@ -58,7 +58,7 @@ namespace mxq {
 
 namespace {
 
-enum : int { kForward = 0, kDgrad = 1, kWgrad = 2, kWgradF32 = 3, kGated = 4, kGatedGrad = 5 };
+enum : int { kForward = 0, kDgrad = 1, kWgrad = 2, kWgradF32 = 3, kGated = 4, kGatedGrad = 5, kGatedGradDv = 6 };
 
 struct GP {
   static constexpr int kM = 256;                       // M of a pair's MMA (128 per CTA)
@@ -93,11 +93,16 @@ template <int OP>
 struct Layout {
   static constexpr bool kW = OP == kWgrad || OP == kWgradF32;
   static constexpr bool kAK = OP == kForward || OP == kGated;     // A is K-major
+  static constexpr bool kGrad = OP == kGatedGrad || OP == kGatedGradDv;
   static constexpr int kSlot = kW ? 32768 : 36864;
   static constexpr int kStages = GP::kMaxStages;
+  // the gated gradient's drain is the longest and bound by its instructions' latency: eight warps take 18 us for 256 x 256
+  static constexpr int kEpiWarps = kGrad ? 16 : GP::kEpiWarps;
+  static constexpr int kThreads = 32 * (GP::kFirstEpiWarp + kEpiWarps);
+  static constexpr int kRowStep = (kGrad ? 2 : 8) * kEpiWarps;    // rows of a tile that the warps take at a time, 8 or 32 each
   static constexpr int kEpiBytes = kW ? 4096 : 0;       // per epilogue warp
   static constexpr int kOffEpi = kStages * kSlot;
-  static constexpr int kOffBar = kOffEpi + GP::kEpiWarps * kEpiBytes;
+  static constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiBytes;
   static constexpr int kOffTmemPtr = (kOffBar + 8 * GP::kNumBars + 63) & ~63;
   static constexpr int kOffClaims = kOffTmemPtr + 16;  // wgrad: answers (and one for draining), items
   static constexpr int kOffTab = kOffTmemPtr + 64;     // forward / dgrad: Lists::first[2][E+1]
@@ -114,6 +119,16 @@ struct Layout {
 // experts of 2048 rows 621 instead of 570 us, 16 of 1024 rows 761 instead of 703,
 // 32 of 512 rows 810 instead of 790; one of 16 384 rows 562 instead of 548.
 constexpr int kPartBlocks = 4;
+
+// The gated gradient with dv, whose float32 sums over I show it (dv off by 8e-6 at H = 7168 in one piece, by 3e-5 where all terms
+// have one sign): the same, of 512 terms, which the epilogue adds up in registers and puts back into the last part's
+// accumulator.  A tile's first part is longer, a quarter of it up to 1792 terms, as the tensor cores have no other accumulator
+// while the epilogue works on the tile before.  dv is then off by 5e-7 at H = 2048 and 1.0e-6 at 7168 (3e-6 if of one sign).
+// Against sums in one piece: 16 384 rows of 64 experts, Zipf 1.2, 513 us and 513; experts of 256 rows each, of which those of
+// 257 and more take two tiles where one would use both accumulators, 522 and 456; 4096 rows of one expert 113 and 106.
+constexpr int kDvBlocks = 8;
+__device__ __forceinline__ int dv_lead(int kb) { return max(kDvBlocks, min(28, kb / 4 & ~1)); }
+__device__ __forceinline__ int dv_parts(int kb) { return 1 + (kb - dv_lead(kb) + kDvBlocks - 1) / kDvBlocks; }
 
 constexpr int kSmallB = 2048;       // forward / dgrad: B of one of a slot's two blocks
 
@@ -179,8 +194,8 @@ __device__ __forceinline__ int tiles_of(int rows) { return rows <= 320 ? (rows >
 
 // Rows of a tile, as their log2: 256, or 128 or 64 where all tiles (n128, n64 of a warp's lanes together) are in work at once all
 // the same, so that a tile's loads, and above all its drain by eight warps, are shorter: one expert of 256 rows, N = 4096,
-// K = 7168, forward 37 -> 28 us, gated 41 -> 30, gated gradient 47 -> 29; of 1024 rows, 1024 x 2048: 16 -> 12, 20 -> 13.5,
-// 26 -> 14.5.  Finer tiles in two rounds lose (512 rows of 4096 x 7168 by 64: 50 us, by 128: 30, by 256: 38), and so do plain
+// K = 7168, forward 37 -> 28 us, gated 41 -> 30, gated gradient 47 -> 28; of 1024 rows, 1024 x 2048: 16 -> 12, 20 -> 13.5,
+// 26 -> 13.4.  Finer tiles in two rounds lose (512 rows of 4096 x 7168 by 64: 50 us, by 128: 30, by 256: 38), and so do plain
 // ones of experts that are short already (up to `least` rows each: 19 of up to 75, 512 columns from sums of 1232, 9.1 us whole
 // and 9.6 cut).  Of 1040 products of 65 to 9000 rows of up to 256 experts the choice takes 0.944 of the time without it in the mean,
 // 215 of them under 0.9; 16 are over 1.1, most of few columns (one expert of 5701 rows, 64 columns from sums of 1016: 15 and 23 us).
@@ -465,8 +480,50 @@ __device__ __forceinline__ void store_block(uint32_t t_row, bool none, bool add,
   }
 }
 
+// The parts of a tile's sums, in the accumulators from the j-th use on: added up in registers, in order, and left in the last one's
+// accumulator, complete but not released.  Of a warp: 8 columns from taddr, every STEP while `left` is positive.  A function of its
+// own, as the registers hold little more than the sums.
+template <int STEP>
+__device__ __noinline__ bool collect_parts(uint32_t taddr, int left, int parts, int j, uint64_t *full, uint32_t empty, int *status,
+                                           int w) {
+  float sum[GP::kN / STEP][8];
+#pragma unroll
+  for (auto &run : sum)
+#pragma unroll
+    for (float &value : run) value = 0.f;
+#pragma unroll 1
+  for (; parts > 0; --parts, ++j) {
+    const int acc = j & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait_reset(&full[acc], (uint32_t)(j >> 1) & 1u, status, kLimit, kWaitEpiTmemFull, w)))
+      return false;
+    tc_fence_after();
+    const uint32_t from = taddr + (uint32_t)(acc * GP::kN);
+    const bool last = parts == 1;
+#pragma unroll
+    for (int i = 0; i < GP::kN / STEP; i += 2)
+      if (STEP * i < left) {
+        uint32_t v[2][8];
+        tmem_ld_32x32b_x8(from + (uint32_t)(STEP * i), v[0]);
+        tmem_ld_32x32b_x8(from + (uint32_t)(STEP * i + STEP), v[1]);        // (past the rows: another sum's, not used)
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) sum[i + k][c] += __uint_as_float(v[k][c]);
+          if (last) tmem_st_32x32b_x8(from + (uint32_t)(STEP * (i + k)), sum[i + k]);
+        }
+      }
+    if (last) break;
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_done(empty + 8u * (uint32_t)acc);
+  }
+  tmem_st_wait();
+  return true;
+}
+
 template <int OP>
-__global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_constant__ GMaps maps, const GArgs g) {
+__global__ void __launch_bounds__(Layout<OP>::kThreads, 1) grouped_kernel(const __grid_constant__ GMaps maps, const GArgs g) {
   using L = Layout<OP>;
   constexpr bool kW = L::kW, kAK = L::kAK;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -512,7 +569,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
       }
       for (int a = 0; a < 2; ++a) {
         mbar_init(&tmem_full[a], 1);
-        mbar_init(&tmem_empty[a], 2 * GP::kEpiWarps);
+        mbar_init(&tmem_empty[a], 2 * L::kEpiWarps);
       }
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
@@ -521,7 +578,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         mbar_init(ring.claim_empty + c, 1);
         mbar_init(ring.item_full + c, 1);
         // roles: loads, ragged ends, epilogue, the leader's MMAs
-        mbar_init(ring.item_empty + c, 2 + GP::kEpiWarps + (rank == 0 ? 1 : 0));
+        mbar_init(ring.item_empty + c, 2 + L::kEpiWarps + (rank == 0 ? 1 : 0));
       }
       if (kW) mbar_init(ring.claim_drain, 1);
       fence_mbar_init();
@@ -538,7 +595,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x < 16) status[threadIdx.x] = 0;
   int bad = 0;
-  for (int e = threadIdx.x; e <= g.E; e += GP::kThreads) {
+  for (int e = threadIdx.x; e <= g.E; e += L::kThreads) {
     const int o = __ldg(g.offsets + e);
     const int before = e > 0 ? __ldg(g.offsets + e - 1) : 0;
     bad |= o < before || (int64_t)o > g.P;
@@ -584,7 +641,7 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         }
         if (lane == 31) first[g.E] = upto;
       };
-      if (log == 8) {
+      if (log == 8 && OP != kGatedGradDv) {
         fill([](int rows) { return tiles_of(rows); });
       } else {
         auto cut = [log](int rows) { return (rows + (1 << log) - 1) >> log; };
@@ -767,7 +824,9 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
           const uint32_t d = tmem_base + (uint32_t)(acc * GP::kN), d2 = tmem_base + (uint32_t)(acc2 * GP::kN);
           uint32_t d_now = d;
           for (int kb = 0; kb < it.kb; kb += kPer) {
-            if (OP == kWgradF32 && kb == first + kPartBlocks) { // hand the part over, go on in the other accumulator
+            if ((OP == kWgradF32 && kb == first + kPartBlocks) ||
+                (OP == kGatedGradDv && kb == first + (first == 0 ? dv_lead(it.kb) : kDvBlocks))) {
+              // hand the part over, go on in the other accumulator
               tc_commit_2sm(&tmem_full[acc], 3);
               if (!next_acc(acc)) return false;
               d_now = tmem_base + (uint32_t)(acc * GP::kN);
@@ -926,25 +985,55 @@ __global__ void __launch_bounds__(GP::kThreads, 1) grouped_kernel(const __grid_c
         continue;
       }
       bool got = true;
+      if constexpr (OP == kGatedGradDv) {
+        got = collect_parts<L::kRowStep>(t_lane + (uint32_t)(8 * (ew >> 2)), (first < g.M ? it.rows : 0) - 8 * (ew >> 2),
+                                         dv_parts(it.kb), j, tmem_full, mapa_shared(smem_u32(tmem_empty), 0), status, w);
+        if (!got) break;
+        j += dv_parts(it.kb) - 1;
+      }
       for (int part = 0; part < (it.n2 ? 2 : 1); ++part) {
         const int acc = j & 1;
+        const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
+        if constexpr (L::kGrad) {
+          // eight rows at a time: a loop of few instructions, whose loads are a step ahead
+          const int64_t row0 = it.row0 + part * it.n;
+          const int rows = first >= g.M ? 0 : part == 0 ? min(it.rows, it.n) : it.rows - it.n;
+          int slot = 8 * (ew >> 2);
+          GatedRow a;
+          a.take(row0 + slot, rows - slot, first, g.gated, lane);
+          if (OP == kGatedGradDv)
+            ++j;                                                   // waited for by collect_parts
+          else
+            got = wait_full(acc);
+          if (!got) break;
+#pragma unroll 1
+          while (slot < rows) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(t_row + (uint32_t)slot, v);
+            const GatedRow in = a;
+            const int now = slot;
+            slot += L::kRowStep;
+            a.take(row0 + slot, rows - slot, first, g.gated, lane);
+            tmem_ld_wait();
+            gated_grad_rows(v, in, row0 + now, rows - now, first, g.P, g.gated, lane);
+          }
+          release(acc);
+          continue;
+        }
         got = wait_full(acc);
         if (!got) break;
-        const uint32_t t_row = t_lane + (uint32_t)(acc * GP::kN);
         if (first < g.M) {
           if (kW) {
             store_block<OP == kWgradF32>(t_row + 128 * (ew >> 2), false, g.accumulate, first, col, it.e, g.C,
                                                     &maps.b[1], lane, stage_tile);
           } else {
             const int row0 = it.row0 + part * it.n, rows = part == 0 ? min(it.rows, it.n) : it.rows - it.n;
-            for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 64) {
+            for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += L::kRowStep) {
               uint32_t v[32];
               tmem_ld_32x32b_x32(t_row + (uint32_t)c0, v);
               tmem_ld_wait();
               if constexpr (OP == kGated)
                 gated_rows(v, (int64_t)row0 + c0, rows - c0, first >> 1, g.gated, lane);
-              else if constexpr (OP == kGatedGrad)
-                gated_grad_rows(v, (int64_t)row0 + c0, rows - c0, first, g.P, g.gated, lane);
               else
                 store_rows(v, (int64_t)row0 + c0, rows - c0, first, g, lane);
             }
@@ -1022,7 +1111,7 @@ int launch_grouped(const GMaps &maps, const GArgs &g, int64_t most_items, cudaSt
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(GP::kThreads);
+  cfg.blockDim = dim3(Layout<OP>::kThreads);
   cfg.dynamicSmemBytes = Layout<OP>::bytes(g.E);
   cfg.stream = st;
   cfg.attrs = attr;
