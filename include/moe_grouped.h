@@ -20,8 +20,9 @@
  *     outputs are rounded once to BF16, or stored as float32 (dw only).  The
  *     tensor core truncates as it adds, in norm 1e-9 of a sum for each of its
  *     terms (up to 4.5e-9 if they have one sign): beside a BF16 output's rounding
- *     that counts from some hundred thousand terms on; a float32 dw is summed in parts of 256 rows and is within a float32
- *     product's error (3e-7) at any length.
+ *     that counts from some hundred thousand terms on; a float32 dw is summed in
+ *     parts of 256 rows and is within a float32 product's error (3e-7, 4e-7 if
+ *     they have one sign) at any length.
  *   - P rows in all (0 <= P < 2^31), N and K multiples of 8, 1 <= E <= 1024.
  *     An expert may own any number of rows, none included.
  *   - Row tensors x, y, dx, dy have a row stride in elements (ldx, ldy: a
